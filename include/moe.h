@@ -467,6 +467,141 @@ int moe_attn_prefill(moe_attn *plan, const uint16_t *x, int n_tokens, int seq, i
 int moe_attn_get_device_status(moe_attn *plan, int *status, void *stream);
 void moe_attn_destroy(moe_attn *plan);
 
+/* ---------------------------------------------------------------------------
+ * Serving: the page tables of a paged key/value cache, such a cache held in 8
+ * bits with the attention over it, and the choice of the next token.  One
+ * step of a serving loop is moe_pages_assign, then per layer moe_kv8_append
+ * and moe_kv8_attend, then moe_sample on the logits.  All of it enqueues only,
+ * is graph-capturable and reads lengths on the device; a captured call sees
+ * the lengths of its replay.
+ */
+
+/* Block tables and slot maps from request lengths, and the pages themselves.
+ * P = page_size tokens a page (1..65536); n_seqs requests (0..4096), request b
+ * with cached[b] tokens in the cache and fresh[b] new ones; fresh[b] < 0 marks
+ * a finished request, whose pages go back to the free list first.  cached[b]
+ * below 0 counts as 0.  Int32 device arrays, 4-byte aligned:
+ *   table [n_seqs][table_width]  in/out: page of each P tokens of a request.
+ *                 A request holds h = min(ceil(cached / P), table_width)
+ *                 entries; the entries h .. of its new pages are written, all
+ *                 others are left as they are (a finished request's too).
+ *   free_pages [capacity]  in/out: the free list, a stack of page ids;
+ *                 counts[0] of them are free.  Finished requests' entries
+ *                 (those >= 0) are pushed in order of request, then entry;
+ *                 then pages are popped in that order.  Pushes beyond
+ *                 capacity are dropped.
+ *   counts [1] in, counts_out [2] out (they may be the same array): the number
+ *                 of free pages before and after; counts_out[1] is the number
+ *                 of pages that were wanted but not there (their entries are
+ *                 -1, their tokens' slots too).
+ *   starts [n_seqs + 1] out: index of each request's first new token, and
+ *                 their number; a finished request has none.
+ *   lens [n_seqs] out: cached + fresh, 0 for a finished request.  Must not
+ *                 overlap cached.
+ *   slots [max_tokens] out: page * P + place in the page of new token i, -1
+ *                 for one without a page or past table_width pages, and from
+ *                 starts[n_seqs] on.
+ *   positions [max_tokens] out (may be NULL): its position in its request, -1
+ *                 from starts[n_seqs] on.
+ * MOE_EINVAL on sizes out of range, NULL or misaligned pointers, or a table
+ * of more than 2^31 - 1 entries. */
+int moe_pages_assign(int page_size, int n_seqs, const int32_t *cached, const int32_t *fresh, int32_t *free_pages,
+                     int capacity, const int32_t *counts, int32_t *counts_out, int32_t *table, int table_width,
+                     int32_t *starts, int32_t *lens, int32_t *slots, int32_t *positions, int max_tokens, void *stream);
+
+/* One layer's paged cache in 8 bits: E4M3 codes and one E8M0 scale (value
+ * 2^(s - 127)) for each page of P tokens and kv head, for keys and for values.
+ * Device arrays, borrowed, 16-byte aligned codes:
+ *   k codes uint8 [n_pages][kv_heads][head_dim / 16][P][16]: dims 16 c .. 16 c
+ *           + 15 of a token together
+ *   v codes uint8 [n_pages][kv_heads][P / 16][head_dim][16]: 16 tokens of a
+ *           dim together; token 2 t + e (t < 4, e < 2) of them at byte
+ *           4 t + e, token 8 + 2 t + e at byte 4 t + 2 + e
+ *   k_scales, v_scales uint8 [n_pages][kv_heads]
+ * A slot is page * P + place in the page. */
+typedef struct moe_kv8 moe_kv8;
+/* kv_heads 1..256, q_heads a multiple of it with at most 16 per kv head,
+ * head_dim 64 or 128, page_size 16, 32 or 64, n_pages * page_size at most
+ * 2^31 - 1.  Defaults: full attention, softmax_scale 1 / sqrt(head_dim), no
+ * sinks.  NULL on bad arguments. */
+moe_kv8 *moe_kv8_create(int q_heads, int kv_heads, int head_dim, int page_size, int n_pages);
+/* "sliding_window": 0 (full attention) or the number of most recent tokens a
+ * query sees, itself among them. */
+int moe_kv8_set_i(moe_kv8 *plan, const char *key, long long value);
+/* "softmax_scale": factor of the scores (1e-30 .. 1e30). */
+int moe_kv8_set_f(moe_kv8 *plan, const char *key, double value);
+int moe_kv8_set_cache(moe_kv8 *plan, uint8_t *k, uint8_t *v, uint8_t *k_scales, uint8_t *v_scales);
+/* Per query head a logit that enters the softmax's denominator only (f32
+ * [q_heads], device, borrowed); NULL: none. */
+int moe_kv8_set_sinks(moe_kv8 *plan, const float *sinks);
+/* Device workspace of moe_kv8_attend, whatever the call's sizes: caller-owned,
+ * 256-byte aligned, borrowed (moe_kv8_set_workspace clears its tickets; it
+ * synchronises the device).  Plans whose attends follow one another on one
+ * stream may share it; attends that can overlap on the GPU need one each. */
+size_t moe_kv8_workspace_bytes(const moe_kv8 *plan);
+int moe_kv8_set_workspace(moe_kv8 *plan, void *dev_ptr, size_t bytes);
+/* n_tokens tokens' keys and values (bf16, [n_tokens] rows of [kv_heads]
+ * [head_dim], k_stride / v_stride elements from row to row, a multiple of 8;
+ * 16-byte aligned) into the cache at slots (int32, device).  A slot outside
+ * 0 .. n_pages * P - 1 appends nothing.  Tokens of one page must follow one
+ * another in the call, at ascending consecutive slots (as moe_pages_assign
+ * lays them out); of a page that a call names in any other way, or twice, the
+ * contents are unspecified.  Per page, kv head and side (keys, values), with
+ * the call's first token of the page at place o:
+ *   k   = ceil(log2(amax / 448)) of the new tokens' largest magnitude, which is
+ *         taken as at least 448 * 2^-126 (NaN never raises it; infinity counts
+ *         as the largest finite float); if o > 0 and the page's exponent is
+ *         larger, that one.  o = 0 starts the page: its old exponent is
+ *         forgotten.
+ *   scale byte = k + 127
+ *   code = the E4M3 value nearest to x / 2^k, ties to even; infinities +-448,
+ *         NaN the NaN code
+ *   if the exponent rose, the codes at places 0 .. o - 1 are rounded again,
+ *         nearest, ties to even, from their values at the old exponent.
+ * Codes at places behind the new tokens are left as they are. */
+int moe_kv8_append(moe_kv8 *plan, const uint16_t *k, const uint16_t *v, long long k_stride, long long v_stride,
+                   const int32_t *slots, int n_tokens, void *stream);
+/* Attention of new tokens over the cache (their own keys and values appended
+ * before): q bf16 rows of [q_heads][head_dim], out likewise, q_stride /
+ * out_stride elements from row to row (multiples of 8), 16-byte aligned, not
+ * overlapping.  Sequence b (of 0..4096) has rows starts[b] .. starts[b + 1] - 1
+ * (int32 [n_seqs + 1], device; NULL: row b alone, then n_rows = n_seqs and
+ * max_new = 1), the last of them at position lens[b] - 1; the row at position
+ * p sees the tokens 0 .. p, on a plan with a sliding window the last
+ * sliding_window of those.  Token t is read from page table[b][t / P] (int32
+ * [n_seqs][table_width]); a token whose page is outside 0 .. n_pages - 1 or
+ * past table_width is not seen.  Per head
+ *   out = sum_t p_t v_t,  p = softmax over the seen tokens' softmax_scale q . k_t
+ *                             and the head's sink logit, if the plan has sinks
+ * rounded to bf16; 0 for a row that sees no token.  What a row does not see
+ * does not touch its result, whatever it holds.  max_new: rows of a sequence
+ * that are computed, at most 65535; rows past it, rows of no sequence, and
+ * rows from n_rows on are left as they are.  A sequence of one row among long
+ * prompts is better served by a call of its own kind: the kernel and its split
+ * of the work are chosen by max_new. */
+int moe_kv8_attend(moe_kv8 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
+                   const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
+                   long long out_stride, void *stream);
+void moe_kv8_destroy(moe_kv8 *plan);
+
+/* The next token of each row of logits (fp32, or bf16 with is_bf16 = 1;
+ * [n_rows] rows of vocab values (1..2^24), row_stride elements apart), from
+ * given uniform numbers u[n_rows] in [0, 1).  Per row, with M its largest logit
+ * and t its temperature, a token's weight is w = e^((l - M) / t), 1 for l = M;
+ * NaN and -inf are never chosen.
+ *   1. top_k > 0 keeps the top_k first in descending order of logits (equal
+ *      ones: the lower index first); 0 or less, or vocab and more: all
+ *   2. top_p < 1 keeps the shortest prefix of those, in that order, whose
+ *      weights reach top_p of their sum (at least one token)
+ *   3. min_p (above 1: 1) keeps those with w >= min_p
+ *   4. the token is the first, in order of index, at which the running sum of
+ *      the kept weights exceeds u times their total
+ * t <= 0 (or NaN) takes the first token in descending order.  temperature, top_k,
+ * top_p, min_p: device arrays [n_rows], each may be NULL (1, all, 1, 0).
+ * ids int32 [n_rows]; -1 for a row without a token to choose. */
+int moe_sample(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *ids, void *stream);
+
 /* Text of the last failure on this thread ("" if none) (goosedump gpt_oss.rs:
  * every `ensure!` carries a message). */
 const char *moe_last_error(void);

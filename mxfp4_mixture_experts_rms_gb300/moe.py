@@ -29,7 +29,10 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_plan_set_i", "moe_plan_se
            "moe_locality_record", "moe_locality_attach", "moe_locality_read", "moe_locality_reset",
            "moe_locality_destroy", "moe_attn_create", "moe_attn_set_i", "moe_attn_set_f", "moe_attn_workspace_bytes",
            "moe_attn_set_workspace", "moe_attn_set_cache", "moe_attn_load_weights", "moe_attn_decode", "moe_attn_prefill",
-           "moe_attn_destroy", "moe_attn_get_device_status", "moe_last_error"]
+           "moe_attn_destroy", "moe_attn_get_device_status", "moe_pages_assign", "moe_kv8_create", "moe_kv8_set_i",
+           "moe_kv8_set_f", "moe_kv8_set_cache", "moe_kv8_set_sinks", "moe_kv8_workspace_bytes",
+           "moe_kv8_set_workspace", "moe_kv8_append", "moe_kv8_attend", "moe_kv8_destroy", "moe_sample",
+           "moe_last_error"]
 
 
 class LocalityStats(C.Structure):
@@ -120,12 +123,27 @@ def load(build_if_missing: bool = True):
     L.moe_attn_get_device_status.argtypes = [P, C.POINTER(I), P]
     L.moe_attn_destroy.restype = None
     L.moe_attn_destroy.argtypes = [P]
+    L.moe_pages_assign.argtypes = [I, I, P, P, P, I, P, P, P, I, P, P, P, P, I, P]
+    L.moe_kv8_create.restype = P
+    L.moe_kv8_create.argtypes = [I, I, I, I, I]
+    L.moe_kv8_set_i.argtypes = [P, C.c_char_p, LL]
+    L.moe_kv8_set_f.argtypes = [P, C.c_char_p, D]
+    L.moe_kv8_set_cache.argtypes = [P, P, P, P, P]
+    L.moe_kv8_set_sinks.argtypes = [P, P]
+    L.moe_kv8_workspace_bytes.restype = SZ
+    L.moe_kv8_workspace_bytes.argtypes = [P]
+    L.moe_kv8_set_workspace.argtypes = [P, P, SZ]
+    L.moe_kv8_append.argtypes = [P, P, P, LL, LL, P, I, P]
+    L.moe_kv8_attend.argtypes = [P, P, LL, P, P, P, I, I, I, I, P, LL, P]
+    L.moe_kv8_destroy.restype = None
+    L.moe_kv8_destroy.argtypes = [P]
+    L.moe_sample.argtypes = [P, I, I, I, LL, P, P, P, P, P, P, P]
     L.moe_last_error.restype = C.c_char_p
     L.moe_last_error.argtypes = []
     for name in EXPORTS:
         if name not in ("moe_plan_create", "moe_plan_destroy", "moe_workspace_bytes", "moe_last_error",
                         "moe_locality_create", "moe_locality_destroy", "moe_attn_create", "moe_attn_destroy",
-                        "moe_attn_workspace_bytes"):
+                        "moe_attn_workspace_bytes", "moe_kv8_create", "moe_kv8_destroy", "moe_kv8_workspace_bytes"):
             getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -448,3 +466,119 @@ class AttnPlan:
             self.close()
         except Exception:
             pass
+
+
+def _arg(t, itemsize: int, shape=None, what="tensor", none=False):
+    """Device address of a dense CUDA tensor of `itemsize` bytes an element and
+    (where given) `shape`; None passes where `none` allows it."""
+    if t is None and none:
+        return None
+    if t is None or not t.is_cuda or t.element_size() != itemsize or not t.is_contiguous() or \
+            (shape is not None and tuple(t.shape) != shape):
+        raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {itemsize}-byte elements"
+                                   + (f" and shape {list(shape)}" if shape is not None else "") + " is needed")
+    return t.data_ptr()
+
+
+def _head_rows(t, heads: int, dim: int, what: str):
+    """(address, row stride) of bf16 rows [n][heads][dim], dense but for the stride from row to row."""
+    if not t.is_cuda or t.element_size() != 2 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][{heads}][{dim}] is needed")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != dim and heads > 1):
+        raise MoeError(MOE_EINVAL, f"{what}: the heads of a row must lie side by side")
+    return t.data_ptr(), s0 if t.shape[0] > 1 else max(s0, heads * dim)
+
+
+def pages_assign(page_size: int, cached, fresh, free_pages, counts, counts_out, table, starts, lens, slots, positions=None,
+                 stream=None):
+    """Block tables and slot maps from request lengths (moe_pages_assign): int32 device tensors cached [n],
+    fresh [n] (below 0: finished), free_pages [capacity], counts [>= 1], counts_out [2], table [n][width],
+    starts [n + 1], lens [n], slots [max_tokens], positions [max_tokens] or None."""
+    n, width = table.shape
+    tokens = slots.numel()
+    _check(load().moe_pages_assign(
+        int(page_size), n, _arg(cached, 4, (n,), "cached"), _arg(fresh, 4, (n,), "fresh"), _arg(free_pages, 4, None, "free_pages"),
+        free_pages.numel(), _arg(counts, 4, None, "counts"), _arg(counts_out, 4, (2,), "counts_out"), _arg(table, 4, None, "table"),
+        width, _arg(starts, 4, (n + 1,), "starts"), _arg(lens, 4, (n,), "lens"), _arg(slots, 4, None, "slots"),
+        _arg(positions, 4, (tokens,), "positions", none=True), tokens, _stream_ptr(stream)))
+
+
+class Kv8:
+    """One layer's paged key/value cache in 8 bits (moe_kv8_*): the plan, its workspace, and the arrays of
+    codes and scales k, v [n_pages][kv_heads][page_size * head_dim], k_scale, v_scale [n_pages][kv_heads]
+    (uint8; `cache` = (k, v, k_scale, v_scale) to use given ones).  `workspace`: another plan, used on the
+    same stream, whose workspace this one shares."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, n_pages: int, sliding_window: int = 0,
+                 softmax_scale: float | None = None, sinks=None, cache=None, workspace: "Kv8 | None" = None, device="cuda"):
+        import torch
+        self.L = load()
+        h = self.L.moe_kv8_create(q_heads, kv_heads, head_dim, page_size, n_pages)
+        if not h:
+            raise MoeError(MOE_EINVAL, self.L.moe_last_error().decode())
+        self.h = C.c_void_p(h)
+        self.q_heads, self.kv_heads, self.head_dim, self.page_size, self.n_pages = q_heads, kv_heads, head_dim, page_size, n_pages
+        _check(self.L.moe_kv8_set_i(self.h, b"sliding_window", int(sliding_window)))
+        if softmax_scale is not None:
+            _check(self.L.moe_kv8_set_f(self.h, b"softmax_scale", float(softmax_scale)))
+        codes, scales = (n_pages, kv_heads, page_size * head_dim), (n_pages, kv_heads)
+        if cache is None:
+            cache = [torch.zeros(s, dtype=torch.uint8, device=device) for s in (codes, codes, scales, scales)]
+        self.k, self.v, self.k_scale, self.v_scale = cache
+        _check(self.L.moe_kv8_set_cache(self.h, _arg(self.k, 1, codes, "k"), _arg(self.v, 1, codes, "v"),
+                                        _arg(self.k_scale, 1, scales, "k_scale"), _arg(self.v_scale, 1, scales, "v_scale")))
+        self.sinks = sinks
+        _check(self.L.moe_kv8_set_sinks(self.h, _arg(sinks, 4, (q_heads,), "sinks", none=True)))
+        n = int(self.L.moe_kv8_workspace_bytes(self.h))
+        self.ws = torch.empty(n + 256, dtype=torch.uint8, device=device) if workspace is None else workspace.ws
+        if self.ws.numel() < n + 256:
+            raise MoeError(MOE_ENOMEM, "the shared workspace is too small for this plan")
+        _check(self.L.moe_kv8_set_workspace(self.h, self.ws.data_ptr() + (-self.ws.data_ptr()) % 256, n))
+
+    def append(self, k, v, slots, stream=None):
+        """k, v: bf16 [n][kv_heads][head_dim] (rows may be strided); slots: int32 [n]."""
+        kp, ks = _head_rows(k, self.kv_heads, self.head_dim, "k")
+        vp, vs = _head_rows(v, self.kv_heads, self.head_dim, "v")
+        n = k.shape[0]
+        if v.shape[0] != n:
+            raise MoeError(MOE_EINVAL, "k and v must have the same number of rows")
+        _check(self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, 4, (n,), "slots"), n, _stream_ptr(stream)))
+
+    def attend(self, q, lens, table, out, starts=None, max_new: int = 1, stream=None):
+        """q, out: bf16 [n_rows][q_heads][head_dim] (rows may be strided); lens int32 [n_seqs]; table int32
+        [n_seqs][width]; starts int32 [n_seqs + 1] (None: one row a sequence); max_new: most rows of a sequence."""
+        qp, qs = _head_rows(q, self.q_heads, self.head_dim, "q")
+        op, os_ = _head_rows(out, self.q_heads, self.head_dim, "out")
+        n, width = table.shape
+        if out.shape[0] != q.shape[0]:
+            raise MoeError(MOE_EINVAL, "q and out must have the same number of rows")
+        _check(self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, 4, (n + 1,), "starts", none=True), _arg(lens, 4, (n,), "lens"),
+                                     _arg(table, 4, None, "table"), width, n, int(max_new), q.shape[0], op, os_,
+                                     _stream_ptr(stream)))
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.L.moe_kv8_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """Next tokens (moe_sample): logits [n][vocab] fp32 or bf16 (rows may be strided), u float32 [n] in [0, 1), ids
+    int32 [n]; temperature, top_p, min_p float32 [n] and top_k int32 [n], each may be None."""
+    import torch
+    if not logits.is_cuda or logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or \
+            (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise MoeError(MOE_EINVAL, "logits: a CUDA tensor of fp32 or bf16 rows is needed")
+    n, vocab = logits.shape
+    _check(load().moe_sample(logits.data_ptr(), int(logits.dtype == torch.bfloat16), n, vocab,
+                             logits.stride(0) if n > 1 else vocab, _arg(temperature, 4, (n,), "temperature", none=True),
+                             _arg(top_k, 4, (n,), "top_k", none=True), _arg(top_p, 4, (n,), "top_p", none=True),
+                             _arg(min_p, 4, (n,), "min_p", none=True), _arg(u, 4, (n,), "u"), _arg(ids, 4, (n,), "ids"),
+                             _stream_ptr(stream)))
