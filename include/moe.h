@@ -570,7 +570,9 @@ int moe_kv8_append(moe_kv8 *plan, const uint16_t *k, const uint16_t *v, long lon
  * p sees the tokens 0 .. p, on a plan with a sliding window the last
  * sliding_window of those.  Token t is read from page table[b][t / P] (int32
  * [n_seqs][table_width]); a token whose page is outside 0 .. n_pages - 1 or
- * past table_width is not seen.  Per head
+ * past table_width is not seen.  table_width * page_size is at most 2^30, and
+ * 4 (table_width + 1) n_seqs and 4 (table_width + 1) kv_heads below 2^31.  Per
+ * head
  *   out = sum_t p_t v_t,  p = softmax over the seen tokens' softmax_scale q . k_t
  *                             and the head's sink logit, if the plan has sinks
  * rounded to bf16; 0 for a row that sees no token.  What a row does not see
@@ -582,6 +584,11 @@ int moe_kv8_append(moe_kv8 *plan, const uint16_t *k, const uint16_t *v, long lon
 int moe_kv8_attend(moe_kv8 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
                    const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
                    long long out_stride, void *stream);
+/* Synchronises the stream and returns the status of the plan's workspace in
+ * *status (0 = fine; 1 = a bounded wait of an attend gave up, whose outputs are
+ * void), then clears it; MOE_EDEVICE when it was set (message: status and
+ * detail). */
+int moe_kv8_get_device_status(moe_kv8 *plan, int *status, void *stream);
 void moe_kv8_destroy(moe_kv8 *plan);
 
 /* The next token of each row of logits (fp32, or bf16 with is_bf16 = 1;

@@ -207,6 +207,24 @@ moe_kv8 *moe_kv8_create(int q_heads, int kv_heads, int head_dim, int page_size, 
 
 void moe_kv8_destroy(moe_kv8 *p) { delete p; }
 
+int moe_kv8_get_device_status(moe_kv8 *p, int *status, void *stream) {
+    if (!p || !status) return moe_fail_status(MOE_EINVAL, "NULL argument");
+    if (!p->ws) return moe_fail_status(MOE_ENOTREADY, "moe_kv8_set_workspace has not been called");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t h[2] = {0, 0};
+    cudaError_t e = cudaMemcpyAsync(h, p->ws, sizeof h, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && h[0]) {
+        // a share that gave up may have left its tickets: all of them start over
+        e = cudaMemsetAsync(p->ws, 0, kKv8ClearBytes, st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    if (e != cudaSuccess) return moe_fail_status(MOE_ECUDA, "moe_kv8_get_device_status: %s", cudaGetErrorString(e));
+    *status = h[0];
+    if (h[0]) return moe_fail_status(MOE_EDEVICE, "device status %d (detail %d)", h[0], h[1]);
+    return MOE_OK;
+}
+
 int moe_kv8_set_i(moe_kv8 *p, const char *key, long long v) {
     if (!p || !key) return moe_fail_status(MOE_EINVAL, "NULL argument");
     if (strcmp(key, "sliding_window")) return moe_fail_status(MOE_EINVAL, "unknown integer option '%s'", key);
@@ -244,7 +262,7 @@ int moe_kv8_set_workspace(moe_kv8 *p, void *dev, size_t bytes) {
     if ((uintptr_t)dev & 255u) return moe_fail_status(MOE_EINVAL, "the workspace must be 256-byte aligned");
     const size_t need = kv8_workspace_bytes(p->c.D);
     if (bytes < need) return moe_fail_status(MOE_ENOMEM, "workspace of %zu bytes, %zu needed", bytes, need);
-    const cudaError_t e = cudaMemset(dev, 0, std::min(need, (size_t)8192));  // the tickets
+    const cudaError_t e = cudaMemset(dev, 0, kKv8ClearBytes);
     if (e != cudaSuccess) return moe_fail_status(MOE_ECUDA, "moe_kv8_set_workspace: %s", cudaGetErrorString(e));
     p->ws = static_cast<unsigned char *>(dev);
     return MOE_OK;
@@ -275,6 +293,8 @@ int moe_kv8_attend(moe_kv8 *p, const uint16_t *q, long long q_stride, const int3
     if (n_seqs < 0 || n_seqs > kKv8MaxSeqs) return moe_fail_status(MOE_EINVAL, "n_seqs must be 0..%d", kKv8MaxSeqs);
     if (n_rows < 0 || table_width < 0 || max_new < 0)
         return moe_fail_status(MOE_EINVAL, "n_rows, table_width and max_new must be >= 0");
+    if ((long long)table_width * p->c.P > (1ll << 30) || ((long long)table_width + 1) * 4 * std::max(n_seqs, p->c.KVH) > INT_MAX)
+        return moe_fail_status(MOE_EINVAL, "table_width %d: at most 2^30 tokens, and a table of fewer than 2^29 entries", table_width);
     if (max_new > 65535) return moe_fail_status(MOE_EINVAL, "max_new must be at most 65535");
     if (!starts && (n_rows != n_seqs || max_new != 1))
         return moe_fail_status(MOE_EINVAL, "without starts every sequence has one row: n_rows = n_seqs, max_new = 1");

@@ -50,6 +50,7 @@ __device__ __forceinline__ float pow2i(int e) {
                      : (e >= -149 ? __uint_as_float(1u << (e + 149)) : 0.f);
 }
 
+constexpr size_t kKv8ClearBytes = 8192;  // head of the workspace: status word and detail, tickets (zero between calls)
 constexpr int kKv8MaxSeqs = 4096;
 constexpr int kKv8MaxGroup = 16;  // query heads of one kv head
 

@@ -31,7 +31,8 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_plan_set_i", "moe_plan_se
            "moe_attn_set_workspace", "moe_attn_set_cache", "moe_attn_load_weights", "moe_attn_decode", "moe_attn_prefill",
            "moe_attn_destroy", "moe_attn_get_device_status", "moe_pages_assign", "moe_kv8_create", "moe_kv8_set_i",
            "moe_kv8_set_f", "moe_kv8_set_cache", "moe_kv8_set_sinks", "moe_kv8_workspace_bytes",
-           "moe_kv8_set_workspace", "moe_kv8_append", "moe_kv8_attend", "moe_kv8_destroy", "moe_sample",
+           "moe_kv8_set_workspace", "moe_kv8_append", "moe_kv8_attend", "moe_kv8_destroy", "moe_kv8_get_device_status",
+           "moe_sample",
            "moe_last_error"]
 
 
@@ -135,6 +136,7 @@ def load(build_if_missing: bool = True):
     L.moe_kv8_set_workspace.argtypes = [P, P, SZ]
     L.moe_kv8_append.argtypes = [P, P, P, LL, LL, P, I, P]
     L.moe_kv8_attend.argtypes = [P, P, LL, P, P, P, I, I, I, I, P, LL, P]
+    L.moe_kv8_get_device_status.argtypes = [P, C.POINTER(I), P]
     L.moe_kv8_destroy.restype = None
     L.moe_kv8_destroy.argtypes = [P]
     L.moe_sample.argtypes = [P, I, I, I, LL, P, P, P, P, P, P, P]
@@ -556,6 +558,13 @@ class Kv8:
         _check(self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, 4, (n + 1,), "starts", none=True), _arg(lens, 4, (n,), "lens"),
                                      _arg(table, 4, None, "table"), width, n, int(max_new), q.shape[0], op, os_,
                                      _stream_ptr(stream)))
+
+    def device_status(self, stream=None) -> int:
+        s = C.c_int(0)
+        rc = self.L.moe_kv8_get_device_status(self.h, C.byref(s), _stream_ptr(stream))
+        if rc not in (MOE_OK, MOE_EDEVICE):
+            _check(rc)
+        return s.value
 
     def close(self):
         if getattr(self, "h", None):
