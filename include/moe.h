@@ -570,8 +570,8 @@ int moe_kv8_append(moe_kv8 *plan, const uint16_t *k, const uint16_t *v, long lon
  * p sees the tokens 0 .. p, on a plan with a sliding window the last
  * sliding_window of those.  Token t is read from page table[b][t / P] (int32
  * [n_seqs][table_width]); a token whose page is outside 0 .. n_pages - 1 or
- * past table_width is not seen.  table_width * page_size is at most 2^30, and
- * 4 (table_width + 1) n_seqs and 4 (table_width + 1) kv_heads below 2^31.  Per
+ * past table_width is not seen.  A table holds at most 2^30 tokens a sequence,
+ * and 2^35 - 512 n_seqs kv_heads over all sequences and kv heads.  Per
  * head
  *   out = sum_t p_t v_t,  p = softmax over the seen tokens' softmax_scale q . k_t
  *                             and the head's sink logit, if the plan has sinks

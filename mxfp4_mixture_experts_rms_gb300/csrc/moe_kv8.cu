@@ -293,8 +293,10 @@ int moe_kv8_attend(moe_kv8 *p, const uint16_t *q, long long q_stride, const int3
     if (n_seqs < 0 || n_seqs > kKv8MaxSeqs) return moe_fail_status(MOE_EINVAL, "n_seqs must be 0..%d", kKv8MaxSeqs);
     if (n_rows < 0 || table_width < 0 || max_new < 0)
         return moe_fail_status(MOE_EINVAL, "n_rows, table_width and max_new must be >= 0");
-    if ((long long)table_width * p->c.P > (1ll << 30) || ((long long)table_width + 1) * 4 * std::max(n_seqs, p->c.KVH) > INT_MAX)
-        return moe_fail_status(MOE_EINVAL, "table_width %d: at most 2^30 tokens, and a table of fewer than 2^29 entries", table_width);
+    if ((long long)table_width * p->c.P > (1ll << 30) ||
+        ((long long)table_width * p->c.P / 64 + 2) * 4 * n_seqs * p->c.KVH > INT_MAX)
+        return moe_fail_status(MOE_EINVAL, "table_width %d: at most 2^30 tokens a sequence, and 2^35 token places over "
+                               "all sequences and kv heads", table_width);
     if (max_new > 65535) return moe_fail_status(MOE_EINVAL, "max_new must be at most 65535");
     if (!starts && (n_rows != n_seqs || max_new != 1))
         return moe_fail_status(MOE_EINVAL, "without starts every sequence has one row: n_rows = n_seqs, max_new = 1");

@@ -104,26 +104,42 @@ __global__ void __launch_bounds__(128) moe_kv8_attend_kernel(const Kv8Attend a) 
 // row's values down to 2^-28 of its largest.
 constexpr int kTile = 64;             // tokens of a unit
 constexpr int kRows = 16;             // rows of a unit
-constexpr int kMaxCtas = 256;
+constexpr int kMaxCtas = 160;         // the tickets and partials there are room for
+constexpr int kSmemSeqs = 512;       // sequences whose lengths are held in shared memory
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Warps, and units in each one's ring.  What bounds the kernel is latency at
+// the instructions of a unit, so as many warps as registers and the 227 KB of
+// shared memory allow come before a deeper ring: a warp's own copies are in
+// flight while the others compute.
 template <int D, bool TOP>
 struct Few {
-    // as many as leave room for two or three units of each in the ring
-    static constexpr int kWarps = D == 64 ? (TOP ? 7 : 8) : (TOP ? 5 : 6);
+#ifndef FW
+#define FW 16
+#define FS 1
+#endif
+    static constexpr int kWarps = D == 64 ? (TOP ? 10 : FW) : (TOP ? 8 : 10);
+    static constexpr int kStages = D == 64 ? (TOP ? 2 : FS) : 1;
     static constexpr int kStage = 2 * kTile * D;   // bytes of one unit: keys, values
     static constexpr int kPad = D + 8;             // floats of a partial's row: 64-bit stores on distinct banks
 };
 // A partial: acc [rows][D + 8], then m, l, N [rows] each.
 __host__ __device__ constexpr int partial_floats(int rows, int D) { return rows * (D + 8 + 3); }
 
+template <int D, bool TOP>
+__host__ __device__ constexpr int few_smem() {   // without the sequences
+    return Few<D, TOP>::kWarps * (Few<D, TOP>::kStages * Few<D, TOP>::kStage + partial_floats(TOP ? 16 : 8, D) * 4) +
+           kMaxCtas * (TOP ? 16 : 8) * 4;
+}
+
 struct FewArgs {
     Kv8Attend a;
-    int G, stages, rows8;      // query heads per kv head; ring stages; rows of a partial (8 or 16)
+    int G;                     // query heads per kv head
     int32_t *status;           // [2]
     uint32_t *tickets;         // [kMaxCtas], zero between calls
     float *parts;              // [kMaxCtas][2][partial_floats]
+    int *seqs;                 // [3][n_seqs], or null: in shared memory
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -181,55 +197,117 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// A share's boundary c of n over `units`: the even cut, moved down to its
-// job's first unit where the job is at most 8 units long (a job that one CTA
-// can take at once is not worth joining across two).
 struct Plan {
     const int *cum;          // [n_seqs]: units of the sequences before, per kv head
     const int *lo, *len;     // [n_seqs]: first unit's index in the sequence; tokens of it that can be seen
-    int n_seqs, KVH, G;
-    long long units;
+    int n_seqs, KVH, units;
 };
 
 struct Job {
-    int b, h, rt, n_rt, nt;  // sequence, kv head, row tile of n_rt, units of the job
-    long long u0;            // its first unit
+    int b, h, rt, nt;  // sequence, kv head, row tile, units
+    int u0;            // its first unit
 };
 
 // The job of unit u (0 <= u < units).
-__device__ __forceinline__ void job_of(const Plan &p, const Kv8Attend &a, long long u, Job &j) {
+__device__ __noinline__ Job job_of(const Plan &p, int u) {
+    Job j;
     int lo = 0, hi = p.n_seqs;   // the last sequence with KVH * cum <= u
+    const int uk = u / p.KVH;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)p.cum[mid] * p.KVH <= u) lo = mid;
+        if (p.cum[mid] <= uk) lo = mid;
         else hi = mid;
     }
-    const int per = (lo + 1 < p.n_seqs ? p.cum[lo + 1] : (int)(p.units / p.KVH)) - p.cum[lo];  // units per kv head
+    const int per = (lo + 1 < p.n_seqs ? p.cum[lo + 1] : p.units / p.KVH) - p.cum[lo];  // units per kv head
     j.b = lo;
-    const int off = (int)(u - (long long)p.cum[lo] * p.KVH);   // < 2^31 (checked on the host)
+    const int off = u - p.cum[lo] * p.KVH;
     j.h = off / per;
     j.nt = max(1, (p.len[lo] + kTile - 1) / kTile - p.lo[lo]);
-    j.n_rt = per / j.nt;
-    j.rt = off % per / j.nt;
-    j.u0 = (long long)p.cum[lo] * p.KVH + (long long)j.h * per + (long long)j.rt * j.nt;
+    j.rt = (off - j.h * per) / j.nt;
+    j.u0 = p.cum[lo] * p.KVH + j.h * per + j.rt * j.nt;
+    return j;
+}
+
+// One of the CTA's pieces of a job: partials that lie side by side in it.
+struct Seg {
+    int u0;             // the job's first unit, -1: none
+    int nt, b, h, rt;
+};
+
+// Weights that join n partials of `rows` rows, and their joint m, N and l: a
+// warp a row, a lane a partial.  src(k): partial k.
+template <int W, class F>
+__device__ __forceinline__ void join_rows(F src, int n, int rows, int R, int PAD, float *cw, float *mnl) {
+    const int lane = threadIdx.x & 31;
+    for (int r = threadIdx.x >> 5; r < rows; r += W) {
+        float mm = -INFINITY, NN = -INFINITY, ll = 0.f;
+        for (int k = lane; k < n; k += 32) mm = fmaxf(mm, *(volatile const float *)(src(k) + R * PAD + r));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+        const float ms = mm == -INFINITY ? 0.f : mm;
+        for (int k = lane; k < n; k += 32) {
+            volatile const float *ml = src(k) + R * PAD + r;
+            const float m = ml[0], l = ml[R], nn = m - ms + ml[2 * R];
+            NN = fmaxf(NN, nn);
+            cw[k * R + r] = nn;
+            ll += l * (m == -INFINITY ? 1.f : ex2(m - ms));   // a NaN score's l has no maximum
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            NN = fmaxf(NN, __shfl_xor_sync(0xffffffffu, NN, d));
+            ll += __shfl_xor_sync(0xffffffffu, ll, d);
+        }
+        for (int k = lane; k < n; k += 32) {
+            const float nn = cw[k * R + r];
+            cw[k * R + r] = nn == -INFINITY ? 0.f : ex2(nn - NN);
+        }
+        if (lane == 0) mnl[r] = mm, mnl[kRows + r] = ll, mnl[2 * kRows + r] = NN;
+    }
+}
+template <class F>
+__device__ __forceinline__ float2 join_values(F src, int n, int at, const float *cw, int R) {
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < n; k++) {
+        const float c = cw[k * R];
+        volatile const float *p = src(k) + at;
+        v.x = fmaf(c, p[0], v.x), v.y = fmaf(c, p[1], v.y);
+    }
+    return v;
+}
+
+// What turns a row's accumulator into its output.
+__device__ __forceinline__ float row_factor(float m, float l, float N, const float *sinks, int head) {
+    float den = l, top = m;
+    if (sinks) {
+        const float sk = sinks[head] * kLog2e;
+        top = fmaxf(m, sk);
+        den = top == -INFINITY ? 0.f : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sk - top);
+    }
+    return den == 0.f || N == -INFINITY ? 0.f : ex2(N - 15.f + (m - top)) / den;   // an empty row: 0; NaN stays NaN
 }
 
 // One warp's place in its units: where the next unit's pages come from.
 template <int D, int P, bool TOP>
 __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kernel(const __grid_constant__ FewArgs f) {
-    constexpr int W = Few<D, TOP>::kWarps, NP = kTile / P, NC = D / 16, ST = Few<D, TOP>::kStage, PAD = Few<D, TOP>::kPad;
+    constexpr int W = Few<D, TOP>::kWarps, NP = kTile / P, HP = P == 16 ? 2 : 1, NC = D / 16, ST = Few<D, TOP>::kStage, PAD = Few<D, TOP>::kPad;
+    constexpr int S = Few<D, TOP>::kStages, R = TOP ? 16 : 8, PF = partial_floats(R, D);
+    static_assert(PF * 4 <= S * ST && few_smem<D, TOP>() + kSmemSeqs * 12 <= 230000, "shared memory");
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t bars[W][4];
-    __shared__ uint32_t meta[W][4][NP];           // per stage and page: key exponent byte, value's, 1 if it is there
-    __shared__ int scan[W + 1];
-    __shared__ long long seg_job[2 * W];          // first unit of the job of each warp's partials, -1: none
+    __shared__ __align__(8) uint64_t bars[W][S];
+    __shared__ uint32_t meta[W][S][NP];           // per stage and page: key exponent byte, value's, 1 if it is there
+    __shared__ int scan[W], cuts[2];
+    __shared__ Seg segs[2 * W];                   // head and tail of each warp
+    __shared__ float mnl[3 * kRows];
+    __shared__ int list[2 * W];
     __shared__ int s_last;
     const Kv8Attend &a = f.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int S = f.stages, R = f.rows8, PF = partial_floats(R, D);
     unsigned char *ring = smem_raw + (size_t)warp * S * ST;
     float *part = reinterpret_cast<float *>(smem_raw + (size_t)W * S * ST);   // [W] head partials; tails go over the rings
-    int *cum = reinterpret_cast<int *>(part + (size_t)W * PF), *lo_s = cum + a.n_seqs, *len_s = lo_s + a.n_seqs;
+    float *cw = part + (size_t)W * PF;                                         // [kMaxCtas][R] weights of a join
+    // per sequence; many of them: in the workspace, where every CTA writes the same
+    int *cum = f.seqs ? f.seqs : reinterpret_cast<int *>(cw + kMaxCtas * R), *lo_s = cum + a.n_seqs, *len_s = lo_s + a.n_seqs;
     if (lane == 0)
         for (int s = 0; s < S; s++) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&bars[warp][s])));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -238,16 +316,15 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
 
     // every sequence's units: contiguous shares of sequences per thread, one block scan
     const int per_thr = (a.n_seqs + W * 32 - 1) / (W * 32), sb0 = min(tid * per_thr, a.n_seqs), sb1 = min(sb0 + per_thr, a.n_seqs);
-    int mine = 0;
-    for (int b = sb0; b < sb1; b++) {
+    auto seq_units = [&](int b, int &first, int &seen) {
         int row0, n, pos0;
         kv8_rows(a, b, row0, n, pos0);
-        const int seen = (int)max(0ll, min((long long)a.lens[b], (long long)a.width * P));
-        const int first = a.window > 0 ? max(0, pos0 - a.window + 1) / kTile : 0;
-        const int cnt = n > 0 ? max(1, (seen + kTile - 1) / kTile - first) * ((n * f.G + kRows - 1) / kRows) : 0;
-        lo_s[b] = first, len_s[b] = seen, cum[b] = mine;
-        mine += cnt;
-    }
+        seen = (int)max(0ll, min((long long)a.lens[b], (long long)a.width * P));
+        first = a.window > 0 ? max(0, pos0 - a.window + 1) / kTile : 0;
+        return n > 0 ? max(1, (seen + kTile - 1) / kTile - first) * ((n * f.G + kRows - 1) / kRows) : 0;
+    };
+    int mine = 0, first, seen_b;
+    for (int b = sb0; b < sb1; b++) mine += seq_units(b, first, seen_b);
     int inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -262,32 +339,39 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
         if (w < warp) base += scan[w];
         total += scan[w];
     }
-    for (int b = sb0; b < sb1; b++) cum[b] += base;
+    for (int b = sb0; b < sb1; b++) {   // in the workspace: only these final values are ever written, by every CTA
+        const int cnt = seq_units(b, first, seen_b);
+        cum[b] = base, lo_s[b] = first, len_s[b] = seen_b;
+        base += cnt;
+    }
     __syncthreads();
-    Plan pl{cum, lo_s, len_s, a.n_seqs, a.c.KVH, f.G, (long long)total * a.c.KVH};
-    const int ctas = (int)min((long long)gridDim.x, (pl.units + 3) / 4);
+    const Plan pl{cum, lo_s, len_s, a.n_seqs, a.c.KVH, total * a.c.KVH};
+    const int ctas = min((int)gridDim.x, (pl.units + 3) / 4);
     if ((int)blockIdx.x >= ctas) return;
-    auto cut = [&](int c) {
-        long long u = pl.units * c / ctas;
+    // The CTA's share: the even cuts, each moved down to its job's first unit
+    // where the job is at most 8 units long (a job that one CTA can take at
+    // once is not worth joining across two).
+    if (tid < 2) {
+        int u = (int)((long long)pl.units * (blockIdx.x + tid) / ctas);
         if (u > 0 && u < pl.units) {
-            Job j;
-            job_of(pl, a, u, j);
+            const Job j = job_of(pl, u);
             if (j.nt <= 8) u = j.u0;
         }
-        return u;
-    };
-    const long long c0 = cut(blockIdx.x), c1 = cut(blockIdx.x + 1);
-    const long long u0 = c0 + (c1 - c0) * warp / W, u1 = c0 + (c1 - c0) * (warp + 1) / W;
+        cuts[tid] = u;
+    }
+    if (tid < 2 * W) segs[tid].u0 = -1;
+    __syncthreads();
+    const int c0 = cuts[0], c1 = cuts[1];
+    const int u0 = c0 + (c1 - c0) * warp / W, u1 = c0 + (c1 - c0) * (warp + 1) / W;   // c1 - c0 < 2^31 / 16 (host)
 
     // the issuing side: place of the next unit to copy, its pages read one unit ahead
-    Job ij;
-    ij.nt = 1, ij.u0 = 0, ij.b = 0, ij.h = 0;
-    long long iu = u0;
+    Job ij = {0, 0, 0, 1, 0};
+    int iu = u0;
     int pg = -1;
     auto fetch_page = [&]() {   // lane p < NP: page of the unit iu
         pg = -1;
         if (iu < u1 && lane < NP) {
-            const int tile = lo_s[ij.b] + (int)(iu - ij.u0);
+            const int tile = lo_s[ij.b] + iu - ij.u0;
             const int t0 = tile * kTile + lane * P;
             if (t0 < len_s[ij.b]) pg = __ldg(a.table + (size_t)ij.b * a.width + t0 / P);
         }
@@ -317,12 +401,11 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
         }
         pend_stage = stage;
         iu++;
-        if (iu < u1 && iu >= ij.u0 + ij.nt) job_of(pl, a, iu, ij);
+        if (iu < u1 && iu == ij.u0 + ij.nt) ij = job_of(pl, iu);
         fetch_page();
     };
-    if (lane < 2) seg_job[2 * warp + lane] = -1;
     if (u0 < u1) {
-        job_of(pl, a, u0, ij);
+        ij = job_of(pl, u0);
         fetch_page();
     }
     bool fine = true;
@@ -330,34 +413,23 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
     for (; filled < S && u0 + filled < u1; filled++) issue(filled);
 
     // the computing side
-    float acc[D / 8][4], m[2], l[2], N[2];
+    // values: up to 8 rows transposed (16 dims x 8 rows a tile: dims g, g + 8 of rows 2 t4, 2 t4 + 1), else 16
+    // rows x 8 dims (rows g, g + 8, dims 2 t4, 2 t4 + 1)
+    constexpr int NA = TOP ? D / 8 : D / 16;
+    float acc[NA][4], m[2], l[2], N[2];
     const float sc = a.scale * kLog2e;
     int up[2] = {0, 0};   // the rows' queries carry 2^up
     uint32_t qf[NC][4];
-    Job j = ij;
+    Job j = ij;               // of the unit at hand (the issuing side is at it or ahead)
+    bool begun = false;
     int pos[2] = {0, 0}, pmin = 0, pmax = 0;
-    long long seg0 = u0;     // first unit of the running segment
-    float *tail = nullptr;
-    auto store_partial = [&](float *p) {
-#pragma unroll
-        for (int r = 0; r < (TOP ? 2 : 1); r++) {
-            const float ls = quad_sum(l[r]);
-            float *row = p + (g + 8 * r) * PAD;
-#pragma unroll
-            for (int d = 0; d < D / 8; d++)
-                *reinterpret_cast<float2 *>(row + 8 * d + 2 * t4) = make_float2(acc[d][2 * r], acc[d][2 * r + 1]);
-            if (t4 == 0) {
-                float *ml = p + R * PAD + (g + 8 * r);
-                ml[0] = m[r], ml[R] = ls, ml[2 * R] = N[r];
-            }
-        }
-    };
-    for (long long u = u0; u < u1 && fine; u++) {
-        const int i = (int)(u - u0), stage = i % S;
-        if (u == u0 || u == j.u0 + j.nt) {
+    int seg0 = u0;           // first unit of the running segment
+    for (int u = u0; u < u1 && fine; u++) {
+        const int i = u - u0, stage = i % S;
+        if (!begun) {
             // a new job: its rows' queries, scaled per row into fp16
-            job_of(pl, a, u, j);
-            seg0 = u;
+            j = iu > u && ij.u0 <= u ? ij : job_of(pl, u);
+            begun = true, seg0 = u;
             int row0, n, pos0;
             kv8_rows(a, j.b, row0, n, pos0);
             pmin = pos0 + j.rt * kRows / f.G;
@@ -389,315 +461,327 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                 }
             }
 #pragma unroll
-            for (int d = 0; d < D / 8; d++) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
+            for (int d = 0; d < NA; d++) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
         }
         if (pend_stage == stage) flush();
         __syncwarp();
         fine = bar_wait(smem_u32(&bars[warp][stage]), (uint32_t)(i / S) & 1, f.status, 90);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
-        const int t0 = (lo_s[j.b] + (int)(u - j.u0)) * kTile, seen = len_s[j.b];
-        uint32_t mt[NP];
-        bool whole = t0 + kTile <= seen && t0 + kTile - 1 <= pmin && (a.window == 0 || t0 > pmax - a.window);
+        const int seen = len_s[j.b];
+        // 32 tokens at a time
+#pragma unroll 1
+        for (int hf = 0; hf < 2; hf++) {
+            const int t0 = (lo_s[j.b] + u - j.u0) * kTile + 32 * hf;
+            uint32_t mt[HP];
+            bool whole = t0 + 32 <= seen && t0 + 31 <= pmin && (a.window == 0 || t0 > pmax - a.window);
 #pragma unroll
-        for (int p = 0; p < NP; p++) {
-            mt[p] = meta[warp][stage][p];
-            whole = whole && (mt[p] >> 16);
-        }
-        const uint32_t kb = smem_u32(ring + stage * ST), vb = kb + kTile * D;
-        // scores: 8 token octets x (rows g: c0, c1; rows g + 8: c2, c3)
-        float s[8][4];
+            for (int p = 0; p < HP; p++) {
+                mt[p] = meta[warp][stage][P == 64 ? 0 : hf * HP + p];
+                whole = whole && (mt[p] >> 16);
+            }
+            // where this half's tokens begin in the unit: pages hold keys [D / 16][P][16], values [P / 16][D][16]
+            const uint32_t kb = smem_u32(ring + stage * ST) + (P == 64 ? hf * 512 : hf * 32 * D);
+            const uint32_t vb = smem_u32(ring + stage * ST) + kTile * D + hf * 32 * D;
+            // scores: 4 token octets x (rows g: c0, c1; rows g + 8: c2, c3)
+            float s[4][4];
 #pragma unroll
-        for (int n = 0; n < 8; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int n = 0; n < 4; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; c++)
-#pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-                // 32 tokens (lane: one) of dims 16 c ..: pages hold [D / 16][P][16]
-                const int tok = 32 * hf + lane;
+            for (int c = 0; c < NC; c++) {
                 uint32_t w[4];
-                ldsm4(w, kb + (tok / P) * (P * D) + c * (P * 16) + (tok % P) * 16);
+                ldsm4(w, kb + (lane / P) * (P * D) + c * (P * 16) + (lane % P) * 16);
 #pragma unroll
                 for (int n = 0; n < 4; n++) {
                     uint32_t b0, b1;
                     e4m3x4_to_f16(w[n], b0, b1);
-                    mma_f16(s[4 * hf + n], qf[c], b0, b1);
+                    mma_f16(s[n], qf[c], b0, b1);
                 }
             }
-        uint32_t keep[4] = {0, 0, 0, 0};    // where not whole, per 16 tokens: bytes of the thread's value words some row sees
-        uint32_t vis[2] = {0, 0};           // and the tokens that each row sees: bit 2 n + e
+            // byte 2 (n & 1) + e of a thread's value word is token 8 (n & 1) + 2 t4 + e of its 16
+            auto sees = [&](int t, int p) { return t <= p && (a.window == 0 || t > p - a.window); };
+            auto there = [&](int n, int t) { return t < seen && (mt[n * HP / 4] >> 16); };
+            bool odd = false;
+            if (!whole) {
+                uint32_t keep[2] = {0, 0};   // value bytes that some row sees
 #pragma unroll
-        for (int r = 0; r < (TOP ? 2 : 1); r++)
+                for (int n = 0; n < 4; n++)
 #pragma unroll
-            for (int n = 0; n < 8; n++) {
-                const float k = pow2i((int)(mt[n * 8 / P] & 255u) - 127 - up[r]) * sc;
-                s[n][2 * r] *= k, s[n][2 * r + 1] *= k;
-            }
-        if (!whole) {
+                    for (int e = 0; e < 2; e++) {
+                        const int t = t0 + 8 * n + 2 * t4 + e;
 #pragma unroll
-            for (int n = 0; n < 8; n++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int t = t0 + 8 * n + 2 * t4 + e;
-                    const bool there = t < seen && (mt[n * 8 / P] >> 16);
-#pragma unroll
-                    for (int r = 0; r < (TOP ? 2 : 1); r++) {
-                        if (there && t <= pos[r] && (a.window == 0 || t > pos[r] - a.window)) vis[r] |= 1u << (2 * n + e);
-                        else s[n][2 * r + e] = -INFINITY;
+                        for (int r = 0; r < (TOP ? 2 : 1); r++)
+                            if (!(there(n, t) && sees(t, pos[r]))) s[n][2 * r + e] = -INFINITY;
+                        if (there(n, t) && t <= pmax && (a.window == 0 || t > pmin - a.window)) keep[n / 2] |= 0xFFu << (16 * (n & 1) + 8 * e);
                     }
-                    // token 8 (n & 1) + 2 t4 + e of its 16: byte 2 (n & 1) + e of the thread's word
-                    if (there && t <= pmax && (a.window == 0 || t > pmin - a.window)) keep[n / 2] |= 0xFFu << (8 * (2 * (n & 1) + e));
+                // values that no row sees to zero: nothing they hold may meet a weight of 0
+                uint32_t nan = 0;
+                for (int x = lane; x < 8 * D; x += 32) {   // words of [2][D][16]: word x & 3 is that of the lanes t4 = x & 3
+                    const uint32_t at = vb + 4 * x, k = x >= 4 * D ? keep[1] : keep[0];
+                    uint32_t w;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                    w &= k;
+                    nan |= ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
                 }
-        }
-        bool moved = false;
-        float corr[2] = {1.f, 1.f}, fac[2][NP];
-#pragma unroll
-        for (int r = 0; r < (TOP ? 2 : 1); r++) {
-            float mx = -INFINITY, pmx[NP];
-#pragma unroll
-            for (int p = 0; p < NP; p++) {
-                float pm = -INFINITY;
-#pragma unroll
-                for (int n = p * (8 / NP); n < (p + 1) * (8 / NP); n++) pm = fmaxf(pm, fmaxf(s[n][2 * r], s[n][2 * r + 1]));
-                pmx[p] = pm, mx = fmaxf(mx, pm);
+                // a NaN that only some rows see: those rows' values apart (below)
+                odd = __any_sync(0xffffffffu, nan != 0 && pmin != pmax);
             }
-            mx = quad_max(mx);
-            const float mn = fmaxf(m[r], mx), ms = mn == -INFINITY ? 0.f : mn;
-            const float was = N[r] + (m[r] - ms);                    // the old reference, over the new m
-            float mvr = -INFINITY;   // over the new m, as scores may be too large for an exponent beside them
+            bool moved = false;
+            float corr[2] = {1.f, 1.f};
 #pragma unroll
-            for (int p = 0; p < NP; p++) mvr = fmaxf(mvr, pmx[p] - ms + (float)((int)((mt[p] >> 8) & 255u) - 127));
-            const float Nn = fmaxf(was, quad_max(mvr)), Ns = Nn == -INFINITY ? 0.f : Nn;
-            l[r] *= ex2(m[r] - ms);
-            corr[r] = ex2(was - Ns);
-            moved |= Nn != was;
-            m[r] = mn, N[r] = Nn;
+            for (int r = 0; r < (TOP ? 2 : 1); r++) {
+                float mx = -INFINITY, pmx[HP], ks[HP];   // ks > 0: a hidden token's -inf stays
 #pragma unroll
-            for (int p = 0; p < NP; p++) fac[r][p] = ex2(fminf((float)((int)((mt[p] >> 8) & 255u) - 112) - Ns, 126.f));
-            float sum = 0.f;
+                for (int p = 0; p < HP; p++) {
+                    ks[p] = fmaxf(pow2i((int)(mt[p] & 255u) - 127 - up[r]) * sc, 1e-37f);
+                    float pm = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < 8; n++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const float p = ex2(s[n][2 * r + e] - ms);
-                    sum += p;
-                    s[n][2 * r + e] = p * fac[r][n * 8 / P];
+                    for (int n = p * (4 / HP); n < (p + 1) * (4 / HP); n++) pm = fmaxf(pm, fmaxf(s[n][2 * r], s[n][2 * r + 1]));
+                    pmx[p] = pm * ks[p], mx = fmaxf(mx, pmx[p]);
                 }
-            l[r] += sum;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
+                mx = quad_max(mx);
+                const float mn = fmaxf(m[r], mx), ms = mn == -INFINITY ? 0.f : mn;
+                const float was = N[r] + (m[r] - ms);    // the old reference, over the new m
+                float mv = -INFINITY;                    // over the new m, as scores may be too large for an exponent beside them
 #pragma unroll
-            for (int d = 0; d < D / 8; d++) {
-                acc[d][0] *= corr[0], acc[d][1] *= corr[0];
-                if (TOP) acc[d][2] *= corr[1], acc[d][3] *= corr[1];
-            }
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; kk++) {
-            const uint32_t pf[4] = {pack_f16(s[2 * kk][0], s[2 * kk][1]), TOP ? pack_f16(s[2 * kk][2], s[2 * kk][3]) : 0u,
-                                    pack_f16(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                                    TOP ? pack_f16(s[2 * kk + 1][2], s[2 * kk + 1][3]) : 0u};
-            const uint32_t blk = vb + (16 * kk / P) * (P * D) + (16 * kk % P) * D;   // [D][16] of these 16 tokens
-#pragma unroll
-            for (int q = 0; q < D / 32; q++) {
-                uint32_t w[4];
-                ldsm4(w, blk + (32 * q + lane) * 16);
+                for (int p = 0; p < HP; p++) mv = fmaxf(mv, pmx[p] - ms + (float)((int)((mt[p] >> 8) & 255u) - 127));
+                if (HP > 1) mv = quad_max(mv);
+                else mv = mx - ms + (float)((int)((mt[0] >> 8) & 255u) - 127);
+                const float Nn = fmaxf(was, mv), Ns = Nn == -INFINITY ? 0.f : Nn;
+                l[r] *= ex2(m[r] - ms);
+                corr[r] = ex2(was - Ns);
+                moved |= Nn != was;
+                m[r] = mn, N[r] = Nn;
+                float sum = 0.f;
 #pragma unroll
                 for (int n = 0; n < 4; n++) {
-                    uint32_t b0, b1;
-                    if (!whole) {
-                        w[n] &= keep[kk];
-                        // a NaN that only later rows see must not reach the others as 0 * NaN
-                        const uint32_t nan = pmin == pmax ? 0 : ((w[n] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                        if (__any_sync(0xffffffffu, nan != 0)) {
-                            const uint32_t all = (nan >> 7) * 255u;
-                            uint32_t seen1[4];
+                    const int p = n * HP / 4;
+                    const float fac = ex2(fminf((float)((int)((mt[p] >> 8) & 255u) - 112) - Ns, 126.f));
 #pragma unroll
-                            for (int x = 0; x < 4; x++) {
-                                const uint32_t bits = vis[x & 1] >> (4 * kk + 2 * (x >> 1));
-                                seen1[x] = (bits & 1u) * 0x3C00u | (bits >> 1 & 1u) * 0x3C000000u;
-                            }
-                            float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                            e4m3x4_to_f16(all & 0x38383838u, b0, b1);   // ones where the value is NaN
-                            mma_f16(hit, seen1, b0, b1);
+                    for (int e = 0; e < 2; e++) {
+                        const float w = ex2(fmaf(s[n][2 * r + e], ks[p], -ms));
+                        sum += w;
+                        s[n][2 * r + e] = w * fac;
+                    }
+                }
+                l[r] += sum;
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+                const float c0 = TOP ? corr[0] : __shfl_sync(0xffffffffu, corr[0], 8 * t4);
+                const float c1 = TOP ? c0 : __shfl_sync(0xffffffffu, corr[0], 8 * t4 + 4);
 #pragma unroll
-                            for (int x = 0; x < 4; x++)
-                                if (hit[x] > 0.f) acc[4 * q + n][x] = NAN;
-                            w[n] &= ~all;
+                for (int d = 0; d < NA; d++) {
+                    acc[d][0] *= c0, acc[d][1] *= c1;
+                    acc[d][2] *= TOP ? corr[1] : c0, acc[d][3] *= TOP ? corr[1] : c1;
+                }
+            }
+            uint32_t pf[2][TOP ? 4 : 2];   // weights: rows as an A fragment, or as a B fragment
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++)
+#pragma unroll
+                for (int x = 0; x < (TOP ? 4 : 2); x++) {
+                    const float *sp = TOP ? s[2 * kk + (x >> 1)] + 2 * (x & 1) : s[2 * kk + x];
+                    pf[kk][x] = pack_f16(sp[0], sp[1]);
+                }
+            // value words wl, wh of dims g, g + 8 of a 16-dim tile
+            auto times = [&](int kk, uint32_t wl, uint32_t wh, float (&lo)[4], float (&hi)[4]) {
+                uint32_t v[4];
+                e4m3x4_to_f16(wl, v[0], v[2]);
+                e4m3x4_to_f16(wh, v[1], v[3]);
+                if constexpr (TOP) {
+                    mma_f16(lo, pf[kk], v[0], v[2]);
+                    mma_f16(hi, pf[kk], v[1], v[3]);
+                } else {
+                    mma_f16(lo, v, pf[kk][0], pf[kk][1]);
+                }
+            };
+            if (!odd) {
+#pragma unroll
+                for (int kk = 0; kk < 2; kk++)
+#pragma unroll
+                    for (int q = 0; q < D / 32; q++) {
+                        uint32_t w[4];
+                        ldsm4(w, vb + kk * (16 * D) + (32 * q + lane) * 16);
+#pragma unroll
+                        for (int n = 0; n < 2; n++) {
+                            constexpr int F = TOP ? 2 : 1;
+                            times(kk, w[2 * n], w[2 * n + 1], acc[F * (2 * q + n)], acc[F * (2 * q + n) + F - 1]);
                         }
                     }
-                    e4m3x4_to_f16(w[n], b0, b1);
-                    mma_f16(acc[4 * q + n], pf, b0, b1);
+            } else {
+                // one position's rows at a time, with only the values that they see
+                __syncwarp();
+#pragma unroll 1
+                for (int p = pmin; p <= pmax; p++) {
+                    uint32_t keep[2] = {0, 0};
+#pragma unroll
+                    for (int n = 0; n < 4; n++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+                            if (sees(t0 + 8 * n + 2 * t4 + e, p)) keep[n / 2] |= 0xFFu << (16 * (n & 1) + 8 * e);
+                    // rows of the accumulator's columns (transposed: 2 t4, 2 t4 + 1; else g, g + 8)
+                    const int p0 = TOP ? pos[0] : __shfl_sync(0xffffffffu, pos[0], 8 * t4);
+                    const int p1 = TOP ? pos[1] : __shfl_sync(0xffffffffu, pos[0], 8 * t4 + 4);
+#pragma unroll
+                    for (int q = 0; q < D / 16; q++) {
+                        float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                        for (int kk = 0; kk < 2; kk++) {
+                            uint32_t w[2];
+#pragma unroll
+                            for (int y = 0; y < 2; y++) {
+                                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[y]) : "r"(vb + kk * (16 * D) + (16 * q + 8 * y + g) * 16 + 4 * t4) : "memory");
+                                w[y] &= keep[kk];
+                            }
+                            times(kk, w[0], w[1], x[0], x[1]);
+                        }
+#pragma unroll
+                        for (int y = 0; y < (TOP ? 2 : 1); y++)
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                if ((TOP ? (e >> 1 ? p1 : p0) : (e & 1 ? p1 : p0)) == p) acc[(TOP ? 2 : 1) * q + y][e] += x[y][e];
+                    }
                 }
             }
         }
         __syncwarp();
         if (u + S < u1) issue(stage);
         if (u + 1 == j.u0 + j.nt || u + 1 == u1) {
-            if (seg0 == j.u0 && u + 1 == j.u0 + j.nt) {
+            begun = false;
+            const bool begins = seg0 == j.u0, ends = u + 1 == j.u0 + j.nt;
+            if (begins && ends) {
                 // the whole job was this warp's
                 int row0, n, pos0;
                 kv8_rows(a, j.b, row0, n, pos0);
+                float k[2];
 #pragma unroll
-                for (int r = 0; r < (TOP ? 2 : 1); r++) {
-                    const int rr = j.rt * kRows + g + 8 * r;
-                    const float ls = quad_sum(l[r]);
+                for (int r = 0; r < (TOP ? 2 : 1); r++)
+                    k[r] = row_factor(m[r], quad_sum(l[r]), N[r], a.sinks, j.h * f.G + (j.rt * kRows + g + 8 * r) % f.G);
+                if (!TOP) {
+                    k[1] = __shfl_sync(0xffffffffu, k[0], 8 * t4 + 4);
+                    k[0] = __shfl_sync(0xffffffffu, k[0], 8 * t4);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const int rr = j.rt * kRows + (TOP ? g + 8 * r : 2 * t4 + r);
                     if (rr >= n * f.G) continue;
-                    const int head = j.h * f.G + rr % f.G;
-                    float den = ls, top = m[r];
-                    if (a.sinks) {
-                        const float sk = a.sinks[head] * kLog2e;
-                        top = fmaxf(top, sk);
-                        den = top == -INFINITY ? 0.f : ls * ex2(m[r] - top) + ex2(sk - top);
-                    }
-                    // an empty row: 0; NaN stays NaN
-                    const float k = den == 0.f || N[r] == -INFINITY ? 0.f : ex2(N[r] - 15.f + (m[r] - top)) / den;
-                    uint16_t *o = a.out + (long long)(row0 + rr / f.G) * a.o_stride + head * D + 2 * t4;
+                    __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(a.out) + (long long)(row0 + rr / f.G) * a.o_stride +
+                                       (j.h * f.G + rr % f.G) * D + (TOP ? 2 * t4 : g);
 #pragma unroll
-                    for (int d = 0; d < D / 8; d++) {
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[d][2 * r] * k, acc[d][2 * r + 1] * k);
-                        *reinterpret_cast<__nv_bfloat162 *>(o + 8 * d) = v;
+                    for (int d = 0; d < NA; d++) {
+                        if (TOP) {
+                            *reinterpret_cast<__nv_bfloat162 *>(o + 8 * d) = __floats2bfloat162_rn(acc[d][2 * r] * k[r], acc[d][2 * r + 1] * k[r]);
+                        } else {
+                            o[16 * d] = __float2bfloat16_rn(acc[d][r] * k[r]);
+                            o[16 * d + 8] = __float2bfloat16_rn(acc[d][2 + r] * k[r]);
+                        }
                     }
                 }
             } else {
-                const bool head_seg = seg0 != j.u0;
-                if (!head_seg || u + 1 == u1) {
-                    // the warp's last segment: over its ring, once that is drained (below)
-                    tail = reinterpret_cast<float *>(ring);
-                } else {
-                    store_partial(part + (size_t)warp * PF);
-                    if (lane == 0) seg_job[2 * warp] = j.u0;
+                // a head of more to come goes to its own place, the last segment over
+                // the ring, whose copies have all landed and been read
+                const bool last = u + 1 == u1;
+                float *to = last ? reinterpret_cast<float *>(ring) : part + (size_t)warp * PF;
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    float *row = to + (TOP ? g + 8 * r : 2 * t4 + r) * PAD + (TOP ? 2 * t4 : g);
+#pragma unroll
+                    for (int d = 0; d < NA; d++) {
+                        if (TOP) *reinterpret_cast<float2 *>(row + 8 * d) = make_float2(acc[d][2 * r], acc[d][2 * r + 1]);
+                        else row[16 * d] = acc[d][r], row[16 * d + 8] = acc[d][2 + r];
+                    }
                 }
+#pragma unroll
+                for (int r = 0; r < (TOP ? 2 : 1); r++) {
+                    const float ls = quad_sum(l[r]);
+                    float *ml = to + R * PAD + g + 8 * r;
+                    if (t4 == 0) ml[0] = m[r], ml[R] = ls, ml[2 * R] = N[r];
+                }
+                if (lane == 0) segs[2 * warp + last] = {j.u0, j.nt, j.b, j.h, j.rt};
             }
         }
     }
-    // the ring is drained: every unit issued was waited for, or the wait ran out
-    if (!fine) {
-        for (int s = 0; s < S; s++) {
-            // copies may still be in flight: wait for each stage's last phase, with a limit
-            const int n = (int)(iu - u0);
-            if (s < n) {
-                const int last = (n - 1 - s) / S;
-                bar_wait(smem_u32(&bars[warp][s]), (uint32_t)last & 1, f.status, 91);
-            }
-        }
-        tail = nullptr;
-    }
-    __syncwarp();
-    if (tail) {
-        store_partial(tail);
-        if (lane == 0) seg_job[2 * warp + 1] = j.u0;
-    }
+    if (!fine)   // copies may still be in flight: each stage's last phase, with a limit
+        for (int s = 0; s < S; s++)
+            if (s < iu - u0) bar_wait(smem_u32(&bars[warp][s]), (uint32_t)((iu - u0 - 1 - s) / S) & 1, f.status, 91);
     __syncthreads();
 
     // joining: the CTA's segments in order; those of one job are neighbours
     for (int i = 0; i < 2 * W;) {
-        const long long ju = seg_job[i];
-        if (ju < 0) {
-            i++;
+        const Seg sg = segs[i];
+        int z = i + 1;
+        if (sg.u0 < 0) {
+            i = z;
             continue;
         }
-        int z = i + 1, cnt = 1;
-        for (int x = z; x < 2 * W; x++) {
-            if (seg_job[x] < 0) continue;
-            if (seg_job[x] != ju) break;
-            z = x + 1, cnt++;
-        }
-        Job jj;
-        job_of(pl, a, ju, jj);
-        int row0, n, pos0;
-        kv8_rows(a, jj.b, row0, n, pos0);
-        const int rows = min(kRows, n * f.G - jj.rt * kRows);
-        const bool inside = ju >= c0 && ju + jj.nt <= c1;    // the whole job was this CTA's
-        auto at = [&](int x) { return x & 1 ? reinterpret_cast<const float *>(smem_raw + (size_t)(x >> 1) * S * ST) : part + (size_t)(x >> 1) * PF; };
-        // which CTAs share it, and where their partials are
-        const int fc = inside ? 0 : (int)(((ju + 1) * ctas - 1) / pl.units), ec = inside ? 0 : (int)(((ju + jj.nt) * ctas - 1) / pl.units);
-        float *mine_p = f.parts + ((size_t)blockIdx.x * 2 + (ju >= c0 ? 1 : 0)) * PF;
-        bool finish = inside;
-        int n_parts = cnt;
-        if (!inside) {
-            for (int x = tid; x < rows * (D / 2); x += W * 32) {
-                const int r = x / (D / 2), d = 2 * (x % (D / 2));
-                float mm = -INFINITY, NN = -INFINITY, ll = 0.f;
-                for (int k = i; k < z; k++)
-                    if (seg_job[k] >= 0) mm = fmaxf(mm, at(k)[R * PAD + r]);
-                const float ms = mm == -INFINITY ? 0.f : mm;
-                for (int k = i; k < z; k++)
-                    if (seg_job[k] >= 0) NN = fmaxf(NN, at(k)[R * PAD + r] - ms + at(k)[R * PAD + 2 * R + r]);
-                float2 v = make_float2(0.f, 0.f);
-                for (int k = i; k < z; k++)
-                    if (seg_job[k] >= 0) {
-                        const float *ml = at(k) + R * PAD + r;
-                        const float2 w = *reinterpret_cast<const float2 *>(at(k) + r * PAD + d);
-                        const float c = ml[2 * R] == -INFINITY ? 0.f : ex2(ml[0] - ms + ml[2 * R] - NN);
-                        v.x += c * w.x, v.y += c * w.y;
-                        ll += ml[R] * (ml[0] == -INFINITY ? 1.f : ex2(ml[0] - ms));
-                    }
-                *reinterpret_cast<float2 *>(mine_p + r * PAD + d) = v;
-                if (d == 0) mine_p[R * PAD + r] = mm, mine_p[R * PAD + R + r] = ll, mine_p[R * PAD + 2 * R + r] = NN;
+        if (tid == 0) list[0] = i;
+        int n = 1;
+        for (; z < 2 * W && (segs[z].u0 < 0 || segs[z].u0 == sg.u0); z++)
+            if (segs[z].u0 == sg.u0) {
+                if (tid == 0) list[n] = z;
+                n++;
             }
+        i = z;
+        __syncthreads();
+        int row0, nr, pos0;
+        kv8_rows(a, sg.b, row0, nr, pos0);
+        const int rows = min(kRows, nr * f.G - sg.rt * kRows);
+        auto here = [&](int k) -> const float * {
+            const int x = list[k];
+            return x & 1 ? reinterpret_cast<const float *>(smem_raw + (size_t)(x >> 1) * S * ST) : part + (size_t)(x >> 1) * PF;
+        };
+        join_rows<W>(here, n, rows, R, PAD, cw, mnl);
+        __syncthreads();
+        // the CTAs that share the job, by the even cuts (no cut inside it was moved)
+        const bool inside = sg.u0 >= c0 && sg.u0 + sg.nt <= c1;
+        const int fc = inside ? 0 : (int)(((long long)(sg.u0 + 1) * ctas - 1) / pl.units);
+        const int ec = inside ? 0 : (int)(((long long)(sg.u0 + sg.nt) * ctas - 1) / pl.units);
+        float *mine_p = f.parts + ((size_t)blockIdx.x * 2 + (sg.u0 >= c0 ? 1 : 0)) * PF;
+        auto finish = [&](float2 v, int r, int d) {
+            const int rr = sg.rt * kRows + r, head = sg.h * f.G + rr % f.G;
+            const float k = row_factor(mnl[r], mnl[kRows + r], mnl[2 * kRows + r], a.sinks, head);
+            *reinterpret_cast<__nv_bfloat162 *>(a.out + (long long)(row0 + rr / f.G) * a.o_stride + head * D + d) =
+                __floats2bfloat162_rn(v.x * k, v.y * k);
+        };
+        for (int x = tid; x < rows * (D / 2); x += W * 32) {
+            const int r = x / (D / 2), d = 2 * (x % (D / 2));
+            const float2 v = join_values(here, n, r * PAD + d, cw + r, R);
+            if (inside) finish(v, r, d);
+            else *reinterpret_cast<float2 *>(mine_p + r * PAD + d) = v;
+        }
+        if (!inside) {
+            if (tid < rows)
+                for (int q = 0; q < 3; q++) mine_p[R * PAD + q * R + tid] = mnl[q * kRows + tid];
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const uint32_t seen = atomicAdd(f.tickets + fc, 1);
-                s_last = seen == (uint32_t)(ec - fc);
-                if (s_last) f.tickets[fc] = 0;
+                s_last = atomicAdd(f.tickets + fc, 1) == (uint32_t)(ec - fc);
+                if (s_last) f.tickets[fc] = 0;   // as the next call finds it
                 __threadfence();
             }
             __syncthreads();
-            finish = s_last != 0;
-            n_parts = ec - fc + 1;
-        }
-        if (finish) {
-            for (int x = tid; x < rows * (D / 2); x += W * 32) {
-                const int r = x / (D / 2), d = 2 * (x % (D / 2)), rr = jj.rt * kRows + r;
-                const int head = jj.h * f.G + rr % f.G;
-                float mm = -INFINITY, NN = -INFINITY, ll = 0.f;
-                float2 v = make_float2(0.f, 0.f);
-                auto src = [&](int k) -> const float * {
-                    return inside ? at(k) : f.parts + ((size_t)(fc + k) * 2 + (k == 0 ? 1 : 0)) * PF;
-                };
-                auto get = [&](const float *p) { return inside ? *p : __ldcg(p); };
-                const int k0 = inside ? i : 0, k1 = inside ? z : n_parts;
-                for (int k = k0; k < k1; k++)
-                    if (!inside || seg_job[k] >= 0) mm = fmaxf(mm, get(src(k) + R * PAD + r));
-                const float ms = mm == -INFINITY ? 0.f : mm;
-                for (int k = k0; k < k1; k++)
-                    if (!inside || seg_job[k] >= 0)
-                        NN = fmaxf(NN, get(src(k) + R * PAD + r) - ms + get(src(k) + R * PAD + 2 * R + r));
-                for (int k = k0; k < k1; k++)
-                    if (!inside || seg_job[k] >= 0) {
-                        const float *ml = src(k) + R * PAD + r;
-                        const float pm = get(ml), plv = get(ml + R), pN = get(ml + 2 * R);
-                        const float2 *wp = reinterpret_cast<const float2 *>(src(k) + r * PAD + d);
-                        const float2 w = inside ? *wp : __ldcg(wp);
-                        const float c = pN == -INFINITY ? 0.f : ex2(pm - ms + pN - NN);
-                        v.x += c * w.x, v.y += c * w.y;
-                        ll += plv * (pm == -INFINITY ? 1.f : ex2(pm - ms));
-                    }
-                float den = ll, top = mm;
-                if (a.sinks) {
-                    const float sk = a.sinks[head] * kLog2e;
-                    top = fmaxf(top, sk);
-                    den = top == -INFINITY ? 0.f : (mm == -INFINITY ? ll : ll * ex2(mm - top)) + ex2(sk - top);
+            if (s_last) {
+                auto there = [&](int k) -> const float * { return f.parts + ((size_t)(fc + k) * 2 + (k == 0 ? 1 : 0)) * PF; };
+                join_rows<W>(there, ec - fc + 1, rows, R, PAD, cw, mnl);
+                __syncthreads();
+                for (int x = tid; x < rows * (D / 2); x += W * 32) {
+                    const int r = x / (D / 2), d = 2 * (x % (D / 2));
+                    finish(join_values(there, ec - fc + 1, r * PAD + d, cw + r, R), r, d);
                 }
-                const float k = den == 0.f || NN == -INFINITY ? 0.f : ex2(NN - 15.f + (mm - top)) / den;
-                *reinterpret_cast<__nv_bfloat162 *>(a.out + (long long)(row0 + rr / f.G) * a.o_stride + head * D + d) =
-                    __floats2bfloat162_rn(v.x * k, v.y * k);
             }
         }
-        __syncthreads();   // s_last is written again by the next job
-        i = z;
+        __syncthreads();   // the scratch is the next job's
     }
 }
+
+constexpr size_t kPartOffset = kKv8ClearBytes + (size_t)kKv8MaxSeqs * 12;
 
 template <int D, int P, bool TOP>
 cudaError_t few_launch(FewArgs f, int ctas, cudaStream_t st) {
     constexpr int W = Few<D, TOP>::kWarps;
-    f.rows8 = TOP ? 16 : 8;
-    const size_t fixed = (size_t)W * partial_floats(f.rows8, D) * 4 + (size_t)f.a.n_seqs * 12;
-    f.stages = (int)std::min<size_t>(4, ((size_t)230000 - fixed) / ((size_t)W * Few<D, TOP>::kStage));
-    const size_t smem = fixed + (size_t)f.stages * W * Few<D, TOP>::kStage;
+    if (f.a.n_seqs <= kSmemSeqs) f.seqs = nullptr;
+    const size_t smem = few_smem<D, TOP>() + (f.seqs ? 0 : (size_t)f.a.n_seqs * 12);
     static PerDevice<bool> opted;
     cudaError_t e = smem_optin_once(moe_kv8_few_kernel<D, P, TOP>, opted);
     if (e != cudaSuccess) return e;
@@ -724,7 +808,7 @@ cudaError_t sm_count(int *n) {
 
 }  // namespace
 
-size_t kv8_workspace_bytes(int D) { return kKv8ClearBytes + (size_t)kMaxCtas * 2 * partial_floats(kRows, D) * 4; }
+size_t kv8_workspace_bytes(int D) { return kPartOffset + (size_t)kMaxCtas * 2 * partial_floats(kRows, D) * 4; }
 
 cudaError_t launch_kv8_attend(const Kv8Attend &a, unsigned char *ws, cudaStream_t st) {
     const int G = a.QH / a.c.KVH;
@@ -733,7 +817,8 @@ cudaError_t launch_kv8_attend(const Kv8Attend &a, unsigned char *ws, cudaStream_
         f.a = a, f.G = G;
         f.status = reinterpret_cast<int32_t *>(ws);
         f.tickets = reinterpret_cast<uint32_t *>(ws + 64);
-        f.parts = reinterpret_cast<float *>(ws + kKv8ClearBytes);
+        f.seqs = reinterpret_cast<int *>(ws + kKv8ClearBytes);
+        f.parts = reinterpret_cast<float *>(ws + kPartOffset);
         int ctas = 0;
         const cudaError_t e = sm_count(&ctas);
         if (e != cudaSuccess) return e;
