@@ -129,8 +129,7 @@ __host__ __device__ constexpr int partial_floats(int rows, int D) { return rows 
 
 template <int D, bool TOP>
 __host__ __device__ constexpr int few_smem() {   // without the sequences
-    return Few<D, TOP>::kWarps * (Few<D, TOP>::kStages * Few<D, TOP>::kStage + partial_floats(TOP ? 16 : 8, D) * 4) +
-           kMaxCtas * (TOP ? 16 : 8) * 4;
+    return Few<D, TOP>::kWarps * (Few<D, TOP>::kStages * Few<D, TOP>::kStage + partial_floats(TOP ? 16 : 8, D) * 4);
 }
 
 struct FewArgs {
@@ -197,36 +196,10 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-struct Plan {
-    const int *cum;          // [n_seqs]: units of the sequences before, per kv head
-    const int *lo, *len;     // [n_seqs]: first unit's index in the sequence; tokens of it that can be seen
-    int n_seqs, KVH, units;
-};
-
 struct Job {
     int b, h, rt, nt;  // sequence, kv head, row tile, units
     int u0;            // its first unit
 };
-
-// The job of unit u (0 <= u < units).
-__device__ __noinline__ Job job_of(const Plan &p, int u) {
-    Job j;
-    int lo = 0, hi = p.n_seqs;   // the last sequence with KVH * cum <= u
-    const int uk = u / p.KVH;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cum[mid] <= uk) lo = mid;
-        else hi = mid;
-    }
-    const int per = (lo + 1 < p.n_seqs ? p.cum[lo + 1] : p.units / p.KVH) - p.cum[lo];  // units per kv head
-    j.b = lo;
-    const int off = u - p.cum[lo] * p.KVH;
-    j.h = off / per;
-    j.nt = max(1, (p.len[lo] + kTile - 1) / kTile - p.lo[lo]);
-    j.rt = (off - j.h * per) / j.nt;
-    j.u0 = p.cum[lo] * p.KVH + j.h * per + j.rt * j.nt;
-    return j;
-}
 
 // One of the CTA's pieces of a job: partials that lie side by side in it.
 struct Seg {
@@ -234,56 +207,11 @@ struct Seg {
     int nt, b, h, rt;
 };
 
-// Weights that join n partials of `rows` rows, and their joint m, N and l: a
-// warp a row, a lane a partial.  src(k): partial k.
-template <int W, class F>
-__device__ __forceinline__ void join_rows(F src, int n, int rows, int R, int PAD, float *cw, float *mnl) {
-    const int lane = threadIdx.x & 31;
-    for (int r = threadIdx.x >> 5; r < rows; r += W) {
-        float mm = -INFINITY, NN = -INFINITY, ll = 0.f;
-        for (int k = lane; k < n; k += 32) mm = fmaxf(mm, *(volatile const float *)(src(k) + R * PAD + r));
-#pragma unroll
-        for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-        const float ms = mm == -INFINITY ? 0.f : mm;
-        for (int k = lane; k < n; k += 32) {
-            volatile const float *ml = src(k) + R * PAD + r;
-            const float m = ml[0], l = ml[R], nn = m - ms + ml[2 * R];
-            NN = fmaxf(NN, nn);
-            cw[k * R + r] = nn;
-            ll += l * (m == -INFINITY ? 1.f : ex2(m - ms));   // a NaN score's l has no maximum
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            NN = fmaxf(NN, __shfl_xor_sync(0xffffffffu, NN, d));
-            ll += __shfl_xor_sync(0xffffffffu, ll, d);
-        }
-        for (int k = lane; k < n; k += 32) {
-            const float nn = cw[k * R + r];
-            cw[k * R + r] = nn == -INFINITY ? 0.f : ex2(nn - NN);
-        }
-        if (lane == 0) mnl[r] = mm, mnl[kRows + r] = ll, mnl[2 * kRows + r] = NN;
-    }
-}
-template <class F>
-__device__ __forceinline__ float2 join_values(F src, int n, int at, const float *cw, int R) {
-    float2 v = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < n; k++) {
-        const float c = cw[k * R];
-        volatile const float *p = src(k) + at;
-        v.x = fmaf(c, p[0], v.x), v.y = fmaf(c, p[1], v.y);
-    }
-    return v;
-}
-
-// What turns a row's accumulator into its output.
-__device__ __forceinline__ float row_factor(float m, float l, float N, const float *sinks, int head) {
-    float den = l, top = m;
-    if (sinks) {
-        const float sk = sinks[head] * kLog2e;
-        top = fmaxf(m, sk);
-        den = top == -INFINITY ? 0.f : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sk - top);
-    }
+// What turns a row's accumulator into its output (sink: the head's logit in
+// units of log2, -inf without one).
+__device__ __forceinline__ float row_factor(float m, float l, float N, float sink) {
+    const float top = fmaxf(m, sink);
+    const float den = top == -INFINITY ? l : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sink - top);
     return den == 0.f || N == -INFINITY ? 0.f : ex2(N - 15.f + (m - top)) / den;   // an empty row: 0; NaN stays NaN
 }
 
@@ -296,18 +224,17 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
     extern __shared__ __align__(128) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[W][S];
     __shared__ uint32_t meta[W][S][NP];           // per stage and page: key exponent byte, value's, 1 if it is there
-    __shared__ int scan[W], cuts[2];
+    __shared__ int scan[W];
     __shared__ Seg segs[2 * W];                   // head and tail of each warp
-    __shared__ float mnl[3 * kRows];
-    __shared__ int list[2 * W];
-    __shared__ int s_last;
+    __shared__ int list[2 * W], shared_seg[2], s_last[2];
     const Kv8Attend &a = f.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     unsigned char *ring = smem_raw + (size_t)warp * S * ST;
     float *part = reinterpret_cast<float *>(smem_raw + (size_t)W * S * ST);   // [W] head partials; tails go over the rings
-    float *cw = part + (size_t)W * PF;                                         // [kMaxCtas][R] weights of a join
-    // per sequence; many of them: in the workspace, where every CTA writes the same
-    int *cum = f.seqs ? f.seqs : reinterpret_cast<int *>(cw + kMaxCtas * R), *lo_s = cum + a.n_seqs, *len_s = lo_s + a.n_seqs;
+    // per sequence: units of those before it (a kv head), index of its first unit in it, tokens that can be seen; of
+    // many sequences in the workspace, where every CTA writes the same
+    int *seq_s = reinterpret_cast<int *>(part + (size_t)W * PF);
+    auto seq = [&](int what, int b) { return f.seqs ? f.seqs[what * a.n_seqs + b] : seq_s[what * a.n_seqs + b]; };
     if (lane == 0)
         for (int s = 0; s < S; s++) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&bars[warp][s])));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -339,41 +266,62 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
         if (w < warp) base += scan[w];
         total += scan[w];
     }
-    for (int b = sb0; b < sb1; b++) {   // in the workspace: only these final values are ever written, by every CTA
-        const int cnt = seq_units(b, first, seen_b);
-        cum[b] = base, lo_s[b] = first, len_s[b] = seen_b;
+    int *seq_w = f.seqs ? f.seqs : seq_s;
+    for (int b = sb0; b < sb1; b++) {   // only these final values are ever written
+        const int cnt = per_thr == 1 ? mine : seq_units(b, first, seen_b);
+        seq_w[b] = base, seq_w[a.n_seqs + b] = first, seq_w[2 * a.n_seqs + b] = seen_b;
         base += cnt;
     }
+    if (tid < 2 * W) segs[tid].u0 = -1;
+    if (tid < 2) shared_seg[tid] = -1;
     __syncthreads();
-    const Plan pl{cum, lo_s, len_s, a.n_seqs, a.c.KVH, total * a.c.KVH};
-    const int ctas = min((int)gridDim.x, (pl.units + 3) / 4);
+    const int units = total * a.c.KVH, ctas = min((int)gridDim.x, (units + 3) / 4);
     if ((int)blockIdx.x >= ctas) return;
+    // the job of unit u (0 <= u < units)
+    auto job_of = [&](int u) {
+        Job j;
+        int lo = 0, hi = a.n_seqs;   // the last sequence with KVH * units before it <= u
+        const int uk = (unsigned)u / (unsigned)a.c.KVH;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (seq(0, mid) <= uk) lo = mid;
+            else hi = mid;
+        }
+        const int before = seq(0, lo) * a.c.KVH;
+        j.b = lo;
+        j.nt = max(1, (seq(2, lo) + kTile - 1) / kTile - seq(1, lo));
+        const unsigned tile = (unsigned)(u - before) / (unsigned)j.nt;
+        if (TOP) {
+            const unsigned n_rt = ((lo + 1 < a.n_seqs ? seq(0, lo + 1) : total) - seq(0, lo)) / j.nt;
+            j.h = tile / n_rt;
+            j.rt = tile % n_rt;
+        } else {
+            j.h = tile, j.rt = 0;    // one row tile: at most 8 rows
+        }
+        j.u0 = before + tile * j.nt;
+        return j;
+    };
     // The CTA's share: the even cuts, each moved down to its job's first unit
     // where the job is at most 8 units long (a job that one CTA can take at
     // once is not worth joining across two).
-    if (tid < 2) {
-        int u = (int)((long long)pl.units * (blockIdx.x + tid) / ctas);
-        if (u > 0 && u < pl.units) {
-            const Job j = job_of(pl, u);
-            if (j.nt <= 8) u = j.u0;
-        }
-        cuts[tid] = u;
+    int cut = (int)((long long)units * (blockIdx.x + (lane & 1)) / ctas);
+    if (cut > 0 && cut < units) {
+        const Job j = job_of(cut);
+        if (j.nt <= 8) cut = j.u0;
     }
-    if (tid < 2 * W) segs[tid].u0 = -1;
-    __syncthreads();
-    const int c0 = cuts[0], c1 = cuts[1];
+    const int c0 = __shfl_sync(0xffffffffu, cut, 0), c1 = __shfl_sync(0xffffffffu, cut, 1);
     const int u0 = c0 + (c1 - c0) * warp / W, u1 = c0 + (c1 - c0) * (warp + 1) / W;   // c1 - c0 < 2^31 / 16 (host)
 
     // the issuing side: place of the next unit to copy, its pages read one unit ahead
-    Job ij = {0, 0, 0, 1, 0};
+    Job ij = {0, 0, 0, 1, 0}, ji = ij;   // of unit iu, and of the one issued last
     int iu = u0;
     int pg = -1;
     auto fetch_page = [&]() {   // lane p < NP: page of the unit iu
         pg = -1;
         if (iu < u1 && lane < NP) {
-            const int tile = lo_s[ij.b] + iu - ij.u0;
+            const int tile = seq(1, ij.b) + iu - ij.u0;
             const int t0 = tile * kTile + lane * P;
-            if (t0 < len_s[ij.b]) pg = __ldg(a.table + (size_t)ij.b * a.width + t0 / P);
+            if (t0 < seq(2, ij.b)) pg = __ldg(a.table + (size_t)ij.b * a.width + t0 / P);
         }
     };
     uint32_t pend = 0;
@@ -400,17 +348,20 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
             pend = (uint32_t)__ldg(a.c.ks + ph) | (uint32_t)__ldg(a.c.vs + ph) << 8 | 1u << 16;
         }
         pend_stage = stage;
+        ji = ij;
         iu++;
-        if (iu < u1 && iu == ij.u0 + ij.nt) ij = job_of(pl, iu);
+        if (iu < u1 && iu == ij.u0 + ij.nt) ij = job_of(iu);
         fetch_page();
     };
     if (u0 < u1) {
-        ij = job_of(pl, u0);
+        ij = job_of(u0);
         fetch_page();
     }
+    auto fill = [&](int u) {
+#pragma unroll 1
+        while (iu < u1 && iu < u + S) issue((iu - u0) % S);
+    };
     bool fine = true;
-    int filled = 0;
-    for (; filled < S && u0 + filled < u1; filled++) issue(filled);
 
     // the computing side
     // values: up to 8 rows transposed (16 dims x 8 rows a tile: dims g, g + 8 of rows 2 t4, 2 t4 + 1), else 16
@@ -420,44 +371,56 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
     const float sc = a.scale * kLog2e;
     int up[2] = {0, 0};   // the rows' queries carry 2^up
     uint32_t qf[NC][4];
-    Job j = ij;               // of the unit at hand (the issuing side is at it or ahead)
+    float sink[2] = {-INFINITY, -INFINITY};
+    Job j = ij;
     bool begun = false;
     int pos[2] = {0, 0}, pmin = 0, pmax = 0;
     int seg0 = u0;           // first unit of the running segment
+    static_assert(S <= 2, "the job of a unit that is issued and not begun is ji");
     for (int u = u0; u < u1 && fine; u++) {
         const int i = u - u0, stage = i % S;
-        if (!begun) {
-            // a new job: its rows' queries, scaled per row into fp16
-            j = iu > u && ij.u0 <= u ? ij : job_of(pl, u);
+        // a new job: its rows' queries, on their way while the unit's pages are
+        // (with dims of 128 after the pages: registers)
+        const bool fresh = !begun;
+        uint2 w[TOP ? 2 : 1][NC];
+        if (fresh) j = iu > u ? ji : ij;
+        if (D == 128) fill(u);
+        if (fresh) {
             begun = true, seg0 = u;
             int row0, n, pos0;
             kv8_rows(a, j.b, row0, n, pos0);
             pmin = pos0 + j.rt * kRows / f.G;
             pmax = pos0 + min(n * f.G - 1, j.rt * kRows + kRows - 1) / f.G;
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const int rr = j.rt * kRows + g + 8 * r;
-                const bool on = (TOP || r == 0) && rr < n * f.G;
-                pos[r] = on ? pos0 + rr / f.G : -1;
-                const uint16_t *q = a.q + (long long)(row0 + rr / f.G) * a.q_stride + (j.h * f.G + rr % f.G) * D + 4 * t4;
-                uint2 w[NC];
+            for (int r = 0; r < (TOP ? 2 : 1); r++) {
+                const int rr = j.rt * kRows + g + 8 * r, i2 = rr / f.G, head = j.h * f.G + rr - i2 * f.G;
+                const bool on = rr < n * f.G;
+                pos[r] = on ? pos0 + i2 : -1;
+                const uint16_t *q = a.q + (long long)(row0 + i2) * a.q_stride + head * D + 4 * t4;
+#pragma unroll
+                for (int c = 0; c < NC; c++) w[r][c] = on ? __ldg(reinterpret_cast<const uint2 *>(q + 16 * c)) : make_uint2(0, 0);
+                sink[r] = on && a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
+            }
+        }
+        if (D == 64) fill(u);
+        if (fresh) {
+            // each row scaled: its largest magnitude to [2^14, 2^15) (exponent field e means 2^(e - 127))
+#pragma unroll
+            for (int r = 0; r < (TOP ? 2 : 1); r++) {
                 uint32_t am = 0;
 #pragma unroll
-                for (int c = 0; c < NC; c++) {
-                    w[c] = on ? __ldg(reinterpret_cast<const uint2 *>(q + 16 * c)) : make_uint2(0, 0);
-                    am = max(am, max(max(w[c].x & 0x7FFFu, (w[c].x >> 16) & 0x7FFFu), max(w[c].y & 0x7FFFu, (w[c].y >> 16) & 0x7FFFu)));
-                }
+                for (int c = 0; c < NC; c++)
+                    am = max(am, max(max(w[r][c].x & 0x7FFFu, (w[r][c].x >> 16) & 0x7FFFu), max(w[r][c].y & 0x7FFFu, (w[r][c].y >> 16) & 0x7FFFu)));
                 am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
                 am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-                // largest magnitude to [2^14, 2^15): exponent field e means 2^(e - 127)
-                const int e = (int)(am >> 7);
-                up[r] = min(141 - e, 127);
+                up[r] = min(141 - (int)(am >> 7), 127);
                 const float mul = pow2i(up[r]);
                 m[r] = -INFINITY, l[r] = 0.f, N[r] = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < NC; c++) {
-                    qf[c][r] = pack_f16(__uint_as_float(w[c].x << 16) * mul, __uint_as_float(w[c].x & 0xFFFF0000u) * mul);
-                    qf[c][2 + r] = pack_f16(__uint_as_float(w[c].y << 16) * mul, __uint_as_float(w[c].y & 0xFFFF0000u) * mul);
+                    qf[c][r] = pack_f16(__uint_as_float(w[r][c].x << 16) * mul, __uint_as_float(w[r][c].x & 0xFFFF0000u) * mul);
+                    qf[c][2 + r] = pack_f16(__uint_as_float(w[r][c].y << 16) * mul, __uint_as_float(w[r][c].y & 0xFFFF0000u) * mul);
+                    if (!TOP) qf[c][1] = qf[c][3] = 0u;
                 }
             }
 #pragma unroll
@@ -468,11 +431,11 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
         fine = bar_wait(smem_u32(&bars[warp][stage]), (uint32_t)(i / S) & 1, f.status, 90);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
-        const int seen = len_s[j.b];
+        const int seen = seq(2, j.b), u_at = (seq(1, j.b) + u - j.u0) * kTile;
         // 32 tokens at a time
 #pragma unroll 1
         for (int hf = 0; hf < 2; hf++) {
-            const int t0 = (lo_s[j.b] + u - j.u0) * kTile + 32 * hf;
+            const int t0 = u_at + 32 * hf;
             uint32_t mt[HP];
             bool whole = t0 + 32 <= seen && t0 + 31 <= pmin && (a.window == 0 || t0 > pmax - a.window);
 #pragma unroll
@@ -645,8 +608,7 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                 }
             }
         }
-        __syncwarp();
-        if (u + S < u1) issue(stage);
+        __syncwarp();   // the stage is read: the next iteration fills it
         if (u + 1 == j.u0 + j.nt || u + 1 == u1) {
             begun = false;
             const bool begins = seg0 == j.u0, ends = u + 1 == j.u0 + j.nt;
@@ -657,7 +619,7 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                 float k[2];
 #pragma unroll
                 for (int r = 0; r < (TOP ? 2 : 1); r++)
-                    k[r] = row_factor(m[r], quad_sum(l[r]), N[r], a.sinks, j.h * f.G + (j.rt * kRows + g + 8 * r) % f.G);
+                    k[r] = row_factor(m[r], quad_sum(l[r]), N[r], sink[r]);
                 if (!TOP) {
                     k[1] = __shfl_sync(0xffffffffu, k[0], 8 * t4 + 4);
                     k[0] = __shfl_sync(0xffffffffu, k[0], 8 * t4);
@@ -707,71 +669,101 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
             if (s < iu - u0) bar_wait(smem_u32(&bars[warp][s]), (uint32_t)((iu - u0 - 1 - s) / S) & 1, f.status, 91);
     __syncthreads();
 
-    // joining: the CTA's segments in order; those of one job are neighbours
-    for (int i = 0; i < 2 * W;) {
-        const Seg sg = segs[i];
-        int z = i + 1;
-        if (sg.u0 < 0) {
-            i = z;
-            continue;
-        }
-        if (tid == 0) list[0] = i;
-        int n = 1;
-        for (; z < 2 * W && (segs[z].u0 < 0 || segs[z].u0 == sg.u0); z++)
-            if (segs[z].u0 == sg.u0) {
-                if (tid == 0) list[n] = z;
-                n++;
+    // Joining: the CTA's segments in order (those of one job are neighbours),
+    // then, of the jobs that other CTAs share (at most the first and the last),
+    // those whose other partials are all there.  A join: the partials' m, l and
+    // N side by side in shared memory, then a thread for each row and pair of
+    // dims.
+    const int my_seg = lane < 2 * W ? segs[lane].u0 : -1;
+    unsigned todo = __ballot_sync(0xffffffffu, my_seg >= 0);
+    auto scal = [&](int k) {   // 3 R floats, behind the tails in the rings
+        return reinterpret_cast<float *>(smem_raw + (size_t)(k % W) * S * ST) + PF + k / W * (3 * R);
+    };
+    static_assert((PF + (kMaxCtas + W - 1) / W * 3 * R) * 4 <= S * ST, "room for the scalars of a join");
+    for (int across = 0;;) {
+        Seg sg;
+        int n, fc = 0;
+        if (todo) {
+            const int first_seg = __ffs(todo) - 1;
+            sg = segs[first_seg];
+            const unsigned members = __ballot_sync(0xffffffffu, my_seg == sg.u0);
+            todo &= ~members;
+            n = __popc(members);
+            if (members >> lane & 1) list[__popc(members & ((1u << lane) - 1))] = lane;   // every warp the same
+            if (tid == 0 && !(sg.u0 >= c0 && sg.u0 + sg.nt <= c1)) shared_seg[sg.u0 >= c0 ? 1 : 0] = first_seg;
+        } else {
+            if (across == 0) {
+                __threadfence();
+                __syncthreads();
+                if (tid < 2) {
+                    s_last[tid] = 0;
+                    if (shared_seg[tid] >= 0) {
+                        // the CTAs that share the job, by the even cuts (no cut inside it was moved)
+                        const Seg x = segs[shared_seg[tid]];
+                        const int c_first = (int)(((long long)(x.u0 + 1) * ctas - 1) / units), c_last = (int)(((long long)(x.u0 + x.nt) * ctas - 1) / units);
+                        if (atomicAdd(f.tickets + c_first, 1) == (uint32_t)(c_last - c_first)) {
+                            f.tickets[c_first] = 0;   // as the next call finds it
+                            s_last[tid] = 1 + c_first;
+                            list[tid] = c_last - c_first + 1;
+                        }
+                    }
+                    __threadfence();
+                }
+                __syncthreads();
             }
-        i = z;
+            if (across < 2 && !s_last[across]) across++;
+            if (across < 2 && !s_last[across]) across++;
+            if (across >= 2) break;
+            sg = segs[shared_seg[across]];
+            fc = s_last[across] - 1, n = list[across];
+            across++;
+        }
+        const bool here = !across;
+        auto src = [&](int k) -> const float * {
+            if (!here) return f.parts + ((size_t)(fc + k) * 2 + (k == 0 ? 1 : 0)) * PF;
+            const int x = list[k];
+            return x & 1 ? reinterpret_cast<const float *>(smem_raw + (size_t)(x >> 1) * S * ST) : part + (size_t)(x >> 1) * PF;
+        };
+        if (here) __syncthreads();   // list
+        for (int x = tid; x < n * 3 * R; x += W * 32) {
+            const int k = x / (3 * R), y = x % (3 * R);
+            scal(k)[y] = *(volatile const float *)(src(k) + R * PAD + y);
+        }
         __syncthreads();
         int row0, nr, pos0;
         kv8_rows(a, sg.b, row0, nr, pos0);
         const int rows = min(kRows, nr * f.G - sg.rt * kRows);
-        auto here = [&](int k) -> const float * {
-            const int x = list[k];
-            return x & 1 ? reinterpret_cast<const float *>(smem_raw + (size_t)(x >> 1) * S * ST) : part + (size_t)(x >> 1) * PF;
-        };
-        join_rows<W>(here, n, rows, R, PAD, cw, mnl);
-        __syncthreads();
-        // the CTAs that share the job, by the even cuts (no cut inside it was moved)
-        const bool inside = sg.u0 >= c0 && sg.u0 + sg.nt <= c1;
-        const int fc = inside ? 0 : (int)(((long long)(sg.u0 + 1) * ctas - 1) / pl.units);
-        const int ec = inside ? 0 : (int)(((long long)(sg.u0 + sg.nt) * ctas - 1) / pl.units);
+        const bool done = !here || (sg.u0 >= c0 && sg.u0 + sg.nt <= c1);
         float *mine_p = f.parts + ((size_t)blockIdx.x * 2 + (sg.u0 >= c0 ? 1 : 0)) * PF;
-        auto finish = [&](float2 v, int r, int d) {
-            const int rr = sg.rt * kRows + r, head = sg.h * f.G + rr % f.G;
-            const float k = row_factor(mnl[r], mnl[kRows + r], mnl[2 * kRows + r], a.sinks, head);
-            *reinterpret_cast<__nv_bfloat162 *>(a.out + (long long)(row0 + rr / f.G) * a.o_stride + head * D + d) =
-                __floats2bfloat162_rn(v.x * k, v.y * k);
-        };
         for (int x = tid; x < rows * (D / 2); x += W * 32) {
             const int r = x / (D / 2), d = 2 * (x % (D / 2));
-            const float2 v = join_values(here, n, r * PAD + d, cw + r, R);
-            if (inside) finish(v, r, d);
-            else *reinterpret_cast<float2 *>(mine_p + r * PAD + d) = v;
-        }
-        if (!inside) {
-            if (tid < rows)
-                for (int q = 0; q < 3; q++) mine_p[R * PAD + q * R + tid] = mnl[q * kRows + tid];
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                s_last = atomicAdd(f.tickets + fc, 1) == (uint32_t)(ec - fc);
-                if (s_last) f.tickets[fc] = 0;   // as the next call finds it
-                __threadfence();
+            float mm = -INFINITY, NN = -INFINITY, ll = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < n; k++) mm = fmaxf(mm, scal(k)[r]);
+            const float ms = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
+            for (int k = 0; k < n; k++) NN = fmaxf(NN, scal(k)[r] - ms + scal(k)[2 * R + r]);
+            const float Ns = NN == -INFINITY ? 0.f : NN;
+            float2 v = make_float2(0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < n; k++) {
+                const float km = scal(k)[r], kl = scal(k)[R + r], kn = scal(k)[2 * R + r];
+                const float c = ex2(km - ms + kn - Ns);   // no tokens: 2^-inf
+                volatile const float *p = src(k) + r * PAD + d;
+                v.x = fmaf(c, p[0], v.x), v.y = fmaf(c, p[1], v.y);
+                ll += kl * (km == -INFINITY ? 1.f : ex2(km - ms));   // the l of NaN scores has no maximum
             }
-            __syncthreads();
-            if (s_last) {
-                auto there = [&](int k) -> const float * { return f.parts + ((size_t)(fc + k) * 2 + (k == 0 ? 1 : 0)) * PF; };
-                join_rows<W>(there, ec - fc + 1, rows, R, PAD, cw, mnl);
-                __syncthreads();
-                for (int x = tid; x < rows * (D / 2); x += W * 32) {
-                    const int r = x / (D / 2), d = 2 * (x % (D / 2));
-                    finish(join_values(there, ec - fc + 1, r * PAD + d, cw + r, R), r, d);
-                }
+            if (done) {
+                const int rr = sg.rt * kRows + r, i2 = rr / f.G, head = sg.h * f.G + rr - i2 * f.G;
+                const float k = row_factor(mm, ll, NN, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+                *reinterpret_cast<__nv_bfloat162 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D + d) =
+                    __floats2bfloat162_rn(v.x * k, v.y * k);
+            } else {
+                *reinterpret_cast<float2 *>(mine_p + r * PAD + d) = v;
+                if (d == 0) mine_p[R * PAD + r] = mm, mine_p[R * PAD + R + r] = ll, mine_p[R * PAD + 2 * R + r] = NN;
             }
         }
-        __syncthreads();   // the scratch is the next job's
+        __syncthreads();   // the scratch is the next join's
     }
 }
 
