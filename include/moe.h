@@ -592,7 +592,8 @@ int moe_kv8_get_device_status(moe_kv8 *plan, int *status, void *stream);
 void moe_kv8_destroy(moe_kv8 *plan);
 
 /* The next token of each row of logits (fp32, or bf16 with is_bf16 = 1;
- * [n_rows] rows of vocab values (1..2^24), row_stride elements apart), from
+ * [n_rows] rows of vocab values (1..2^22), row_stride elements apart; at
+ * most 2^24 rows), from
  * given uniform numbers u[n_rows] in [0, 1).  Per row, with M its largest logit
  * and t its temperature, a token's weight is w = e^((l - M) / t), 1 for l = M;
  * NaN and -inf are never chosen.

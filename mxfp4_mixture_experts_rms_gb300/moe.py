@@ -470,26 +470,41 @@ class AttnPlan:
             pass
 
 
-def _arg(t, itemsize: int, shape=None, what="tensor", none=False):
+def _arg(t, itemsize: int, count=None, what="tensor", none=False):
     """Device address of a dense CUDA tensor of `itemsize` bytes an element and
-    (where given) `shape`; None passes where `none` allows it."""
+    (where given) `count` elements; None passes where `none` allows it."""
     if t is None and none:
         return None
     if t is None or not t.is_cuda or t.element_size() != itemsize or not t.is_contiguous() or \
-            (shape is not None and tuple(t.shape) != shape):
+            (count is not None and t.numel() != count):
         raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {itemsize}-byte elements"
-                                   + (f" and shape {list(shape)}" if shape is not None else "") + " is needed")
+                                   + (f" ({count} of them)" if count is not None else "") + " is needed")
     return t.data_ptr()
+
+
+_raw_stream = None
+
+
+def _stream(stream):
+    """cudaStream_t of `stream`, or of the current device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    return _raw_stream[0](_raw_stream[1]())
 
 
 def _head_rows(t, heads: int, dim: int, what: str):
     """(address, row stride) of bf16 rows [n][heads][dim], dense but for the stride from row to row."""
-    if not t.is_cuda or t.element_size() != 2 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+    shape = t.shape
+    if not t.is_cuda or t.element_size() != 2 or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][{heads}][{dim}] is needed")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != dim and heads > 1):
         raise MoeError(MOE_EINVAL, f"{what}: the heads of a row must lie side by side")
-    return t.data_ptr(), s0 if t.shape[0] > 1 else max(s0, heads * dim)
+    return t.data_ptr(), s0 if shape[0] > 1 else heads * dim
 
 
 def pages_assign(page_size: int, cached, fresh, free_pages, counts, counts_out, table, starts, lens, slots, positions=None,
@@ -499,11 +514,13 @@ def pages_assign(page_size: int, cached, fresh, free_pages, counts, counts_out, 
     starts [n + 1], lens [n], slots [max_tokens], positions [max_tokens] or None."""
     n, width = table.shape
     tokens = slots.numel()
-    _check(load().moe_pages_assign(
-        int(page_size), n, _arg(cached, 4, (n,), "cached"), _arg(fresh, 4, (n,), "fresh"), _arg(free_pages, 4, None, "free_pages"),
-        free_pages.numel(), _arg(counts, 4, None, "counts"), _arg(counts_out, 4, (2,), "counts_out"), _arg(table, 4, None, "table"),
-        width, _arg(starts, 4, (n + 1,), "starts"), _arg(lens, 4, (n,), "lens"), _arg(slots, 4, None, "slots"),
-        _arg(positions, 4, (tokens,), "positions", none=True), tokens, _stream_ptr(stream)))
+    rc = (_lib or load()).moe_pages_assign(
+        int(page_size), n, _arg(cached, 4, n, "cached"), _arg(fresh, 4, n, "fresh"), _arg(free_pages, 4, None, "free_pages"),
+        free_pages.numel(), _arg(counts, 4, None, "counts"), _arg(counts_out, 4, 2, "counts_out"), _arg(table, 4, None, "table"),
+        width, _arg(starts, 4, n + 1, "starts"), _arg(lens, 4, n, "lens"), _arg(slots, 4, None, "slots"),
+        _arg(positions, 4, tokens, "positions", none=True), tokens, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 class Kv8:
@@ -525,13 +542,14 @@ class Kv8:
         if softmax_scale is not None:
             _check(self.L.moe_kv8_set_f(self.h, b"softmax_scale", float(softmax_scale)))
         codes, scales = (n_pages, kv_heads, page_size * head_dim), (n_pages, kv_heads)
+        n_scales, n_codes = n_pages * kv_heads, n_pages * kv_heads * page_size * head_dim
         if cache is None:
             cache = [torch.zeros(s, dtype=torch.uint8, device=device) for s in (codes, codes, scales, scales)]
         self.k, self.v, self.k_scale, self.v_scale = cache
-        _check(self.L.moe_kv8_set_cache(self.h, _arg(self.k, 1, codes, "k"), _arg(self.v, 1, codes, "v"),
-                                        _arg(self.k_scale, 1, scales, "k_scale"), _arg(self.v_scale, 1, scales, "v_scale")))
+        _check(self.L.moe_kv8_set_cache(self.h, _arg(self.k, 1, n_codes, "k"), _arg(self.v, 1, n_codes, "v"),
+                                        _arg(self.k_scale, 1, n_scales, "k_scale"), _arg(self.v_scale, 1, n_scales, "v_scale")))
         self.sinks = sinks
-        _check(self.L.moe_kv8_set_sinks(self.h, _arg(sinks, 4, (q_heads,), "sinks", none=True)))
+        _check(self.L.moe_kv8_set_sinks(self.h, _arg(sinks, 4, q_heads, "sinks", none=True)))
         n = int(self.L.moe_kv8_workspace_bytes(self.h))
         self.ws = torch.empty(n + 256, dtype=torch.uint8, device=device) if workspace is None else workspace.ws
         if self.ws.numel() < n + 256:
@@ -545,7 +563,9 @@ class Kv8:
         n = k.shape[0]
         if v.shape[0] != n:
             raise MoeError(MOE_EINVAL, "k and v must have the same number of rows")
-        _check(self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, 4, (n,), "slots"), n, _stream_ptr(stream)))
+        rc = self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, 4, n, "slots"), n, _stream(stream))
+        if rc:
+            _check(rc)
 
     def attend(self, q, lens, table, out, starts=None, max_new: int = 1, stream=None):
         """q, out: bf16 [n_rows][q_heads][head_dim] (rows may be strided); lens int32 [n_seqs]; table int32
@@ -555,13 +575,14 @@ class Kv8:
         n, width = table.shape
         if out.shape[0] != q.shape[0]:
             raise MoeError(MOE_EINVAL, "q and out must have the same number of rows")
-        _check(self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, 4, (n + 1,), "starts", none=True), _arg(lens, 4, (n,), "lens"),
-                                     _arg(table, 4, None, "table"), width, n, int(max_new), q.shape[0], op, os_,
-                                     _stream_ptr(stream)))
+        rc = self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, 4, n + 1, "starts", none=True), _arg(lens, 4, n, "lens"),
+                                   _arg(table, 4, None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream))
+        if rc:
+            _check(rc)
 
     def device_status(self, stream=None) -> int:
         s = C.c_int(0)
-        rc = self.L.moe_kv8_get_device_status(self.h, C.byref(s), _stream_ptr(stream))
+        rc = self.L.moe_kv8_get_device_status(self.h, C.byref(s), _stream(stream))
         if rc not in (MOE_OK, MOE_EDEVICE):
             _check(rc)
         return s.value
@@ -581,13 +602,15 @@ class Kv8:
 def sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
     """Next tokens (moe_sample): logits [n][vocab] fp32 or bf16 (rows may be strided), u float32 [n] in [0, 1), ids
     int32 [n]; temperature, top_p, min_p float32 [n] and top_k int32 [n], each may be None."""
-    import torch
-    if not logits.is_cuda or logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or \
-            (logits.stride(1) != 1 and logits.shape[1] > 1):
+    shape, size = logits.shape, logits.element_size()
+    if not logits.is_cuda or len(shape) != 2 or size not in (2, 4) or not logits.is_floating_point() or \
+            (logits.stride(1) != 1 and shape[1] > 1) or (size == 2 and str(logits.dtype) != "torch.bfloat16"):
         raise MoeError(MOE_EINVAL, "logits: a CUDA tensor of fp32 or bf16 rows is needed")
-    n, vocab = logits.shape
-    _check(load().moe_sample(logits.data_ptr(), int(logits.dtype == torch.bfloat16), n, vocab,
-                             logits.stride(0) if n > 1 else vocab, _arg(temperature, 4, (n,), "temperature", none=True),
-                             _arg(top_k, 4, (n,), "top_k", none=True), _arg(top_p, 4, (n,), "top_p", none=True),
-                             _arg(min_p, 4, (n,), "min_p", none=True), _arg(u, 4, (n,), "u"), _arg(ids, 4, (n,), "ids"),
-                             _stream_ptr(stream)))
+    n, vocab = shape
+    rc = (_lib or load()).moe_sample(
+        logits.data_ptr(), size == 2, n, vocab, logits.stride(0) if n > 1 else vocab,
+        _arg(temperature, 4, n, "temperature", none=True), _arg(top_k, 4, n, "top_k", none=True),
+        _arg(top_p, 4, n, "top_p", none=True), _arg(min_p, 4, n, "min_p", none=True), _arg(u, 4, n, "u"),
+        _arg(ids, 4, n, "ids"), _stream(stream))
+    if rc:
+        _check(rc)

@@ -3,7 +3,7 @@ cache's append, the attention over it, sampling, and a run of them together.
 
 Tolerances.  Page tables and codes are whole numbers: equal.  Attention: oracle.serving.attend gives with each
 output how far it may be off, from the roundings' sizes.  Sampling: a weight e^z, z <= 0, is off by at most
-(2^-22 + |z| 2^-23) of itself, and |z| e^z <= 0.37, so running sums are within 2^-20 of the total; the token
+(2^-22 + |z| 2^-22) of itself, and |z| e^z <= 0.37, so running sums are within 2^-20 of the total; the token
 must be one whose interval of the running sum, widened by 2^-18 of the total, holds u times the total."""
 import numpy as np
 import pytest
@@ -450,6 +450,26 @@ def test_sample_equal_and_odd_logits():
     y = rng.normal(0, 1, (16, V)) + 1e4                            # far from zero; close together
     check_sample(y, u, t=rng.choice([1e-6, 0.01, 1.0, 100.0], 16), p=0.95)
     check_sample(rng.normal(0, 30, (16, V)), u, k=500, p=0.999999, mp=1e-9)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_sample_where_the_threshold_is_hard_to_find(dtype):
+    """Many logits within one step of the first histogram, far below its range, or at its bins' edges."""
+    rng = np.random.default_rng(9)
+    V, n = 60000, 8
+    u = rng.random(n)
+    p = np.array([0.01, 0.3, 0.5, 0.9, 0.99, 0.9999, 0.7, 0.2])
+    k = np.array([1, 7, 100, 3000, 30000, 59999, 50, 2])
+    near = rng.normal(0, 1e-3, (n, V))
+    far = rng.normal(0, 1, (n, V)) - 40
+    far[:, 777] = 9.0
+    edges = np.repeat(rng.normal(0, 4, (n, 60)), 1000, 1)
+    for x in (near, far, edges, np.zeros((n, V)), rng.normal(0, 3, (n, V))):
+        check_sample(x, u, p=p, dtype=dtype)
+        check_sample(x, u, k=k, dtype=dtype)
+        check_sample(x, u, k=k, p=p, t=0.9, dtype=dtype)
+    check_sample(rng.normal(0, 1, (2, 1200000)), u[:2], p=0.9, dtype=dtype)       # more than shared memory holds
+    check_sample(rng.normal(0, 1, (2, 1200000)), u[:2], k=70000, p=0.9, dtype=dtype)
 
 
 def test_sample_the_ends_of_u():
