@@ -86,4 +86,5 @@ __device__ __forceinline__ void kv8_rows(const Kv8Attend &a, int b, int &row0, i
 cudaError_t launch_kv8_append(const Kv8Cache &c, const uint16_t *k, const uint16_t *v, long long k_stride,
                               long long v_stride, const int32_t *slots, int n, cudaStream_t st);
 cudaError_t launch_kv8_attend(const Kv8Attend &a, unsigned char *ws, cudaStream_t st);
+cudaError_t launch_kv8_prompt(const Kv8Attend &a, int32_t *status, cudaStream_t st);
 size_t kv8_workspace_bytes(int head_dim);

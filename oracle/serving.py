@@ -134,18 +134,21 @@ def append(k, v, ks, vs, P, xk, xv, slots):
     return (*pack(kk, vv), ks, vs)
 
 
-def attend(k, v, ks, vs, P, q, starts, lens, table, window=0, sinks=None, scale=None):
+def attend(k, v, ks, vs, P, q, starts, lens, table, window=0, sinks=None, scale=None, floor=2.0 ** -39):
     """-> (out, tol): out [rows][heads][D] float64 (NaN rows where no sequence has one), and how far a result may
     be off that holds probabilities in 11 bits or more, scores and sums in 32 bits, and rounds once to bf16:
     with A = sum_t p_t |v_t| and B = max_t scale sum_d |q_d k_td|,
-        2^-8 |out| + A (2^-10 + 2 (D + 8) 2^-24 B) + 2^-39 F.
+        2^-8 |out| + A (2^-10 + 2 (D + 8) 2^-24 B) + floor F + 2^-110 sum_t |v_t|.
     A score is a sum of D products, off by at most (D + 4) 2^-24 B in 32 bits; turning it into a power of two
     and its argument's rounding add at most 4 * 2^-24 B, since |s| <= B.  Each p_t is off by that relative to
     itself, which moves numerator and denominator by at most A times it; 2^-11 A for the rounding of p, and as
     much again for the sums.
     F = max_t (p_t 2^(e_t)) sum_t |code_td|, with e_t the value page's exponent: weights p_t 2^(e_t) held in fp16,
     scaled so that the largest is at most 2^15, are off by up to half of fp16's smallest step, 2^-25, where they
-    are below 2^-14: 2^-40 of the largest (2^-39 where another unit's reference was up to twice as large)."""
+    are below 2^-14: 2^-40 of the largest (2^-39 where another unit's reference was up to twice as large).  The kernel for prompts moves
+    its reference only when passed by 2^8, and scales the reference to 2^7: 2^-25 / 2^7, doubled likewise: 2^-31.
+    The last term: the factor that turns p_t into its fp16 weight, 2^(15 + e_t - N) with 2^N = max_u p_u 2^(e_u), is
+    held to 2^126, so weights with e_t - N > 111 come out too small; for those p_t <= 2^(N - e_t) < 2^-111."""
     D, H, kv = q.shape[2], q.shape[1], k.shape[1]
     kk, vv = unpack(k, v, P, D)
     scale = 1.0 / np.sqrt(D) if scale is None else scale
@@ -174,7 +177,7 @@ def attend(k, v, ks, vs, P, q, starts, lens, table, window=0, sinks=None, scale=
                 B = scale * (np.abs(kt) @ np.abs(np.asarray(q[r, h], np.float64))).max()
                 ve = vs[pages, g].astype(np.float64) - 127
                 F = (w / den * 2.0 ** ve).max() * np.abs(E4M3[vv[pages, at, g]]).sum(0)
-                tol[r, h] = 2.0 ** -39 * F + 2.0 ** -8 * np.abs(out[r, h]) + (w / den) @ np.abs(vt) * (2.0 ** -10 + 2 * (D + 8) * 2.0 ** -24 * B)
+                tol[r, h] = floor * F + 2.0 ** -110 * np.abs(vt).sum(0) + 2.0 ** -8 * np.abs(out[r, h]) + (w / den) @ np.abs(vt) * (2.0 ** -10 + 2 * (D + 8) * 2.0 ** -24 * B)
     return out, tol + 1e-30
 
 

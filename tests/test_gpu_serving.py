@@ -236,7 +236,8 @@ def check_attend(rng, P, D, kv, H, lens, rows, window=0, sinks=True, width=None,
         out.fill_(7.5)
         plan.attend(qd, dev(np.array(lens, np.int32)), dev(table), out, starts=dev(starts) if use else None, max_new=most)
         got = out.double().cpu().numpy()
-        ref, tol = S.attend(*c, P, q, starts, lens, table, window, s, scale)
+        # more than 64 rows (new tokens x query heads of a kv head) a sequence: the kernel for prompts
+        ref, tol = S.attend(*c, P, q, starts, lens, table, window, s, scale, 2.0 ** -31 if most * (H // kv) > 64 else 2.0 ** -39)
         for b in range(len(lens)):
             a, z = starts[b], min(starts[b] + most, starts[b + 1])
             far = np.abs(got[a:z] - ref[a:z]) / tol[a:z]
@@ -569,7 +570,7 @@ def test_a_serving_run_of_all_operators_and_its_graph():
         got = calls[s]
         for g, w in zip(got[:9], (table, r["starts"], r["lens"], r["slots"], r["counts"], *cache)):
             assert np.array_equal(g, w), s
-        ref, tol = S.attend(*cache, P, x[:, :H], r["starts"], r["lens"], table, 50, sinks)
+        ref, tol = S.attend(*cache, P, x[:, :H], r["starts"], r["lens"], table, 50, sinks, floor=2.0 ** -31)
         a = slice(0, int(r["starts"][-1]))
         assert (np.abs(got[10][a] - ref[a]) / tol[a]).max() <= 1, s
         assert np.all(got[10][a.stop:] == 0)
