@@ -252,10 +252,10 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
             if (t0 < seq(2, ij.b)) pg = __ldg(a.table + (size_t)ij.b * a.width + t0 / P);
         }
     };
-    uint32_t pend = 0;
+    uint32_t pend_k = 0, pend_v = 0, pend_there = 0;   // put together only when they are stored: nothing waits for them here
     int pend_stage = -1;
     auto flush = [&]() {
-        if (pend_stage >= 0 && lane < NP) meta[warp][pend_stage][lane] = pend;
+        if (pend_stage >= 0 && lane < NP) meta[warp][pend_stage][lane] = pend_k | pend_v << 8 | pend_there;
         pend_stage = -1;
     };
     auto issue = [&](int stage) {
@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
             asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(bar),
                          "r"((uint32_t)(__popc(okm) * 2 * P * D)) : "memory");
         __syncwarp();
-        pend = 0;
+        pend_k = pend_v = pend_there = 0;
         if (ok) {
             const size_t ph = (size_t)pg * a.c.KVH + ij.h;
             const uint32_t dst = smem_u32(ring + stage * ST) + lane * (P * D);
             bulk_copy(dst, a.c.k + ph * (P * D), P * D, bar);
             bulk_copy(dst + kTile * D, a.c.v + ph * (P * D), P * D, bar);
-            pend = (uint32_t)__ldg(a.c.ks + ph) | (uint32_t)__ldg(a.c.vs + ph) << 8 | 1u << 16;
+            pend_k = __ldg(a.c.ks + ph), pend_v = __ldg(a.c.vs + ph), pend_there = 1u << 16;
         }
         pend_stage = stage;
         ji = ij;

@@ -2,22 +2,24 @@
 // tokens a sequence (prompts, or pieces of them): tensor-core products on
 // tcgen05 with accumulators in tensor memory.
 //
-// One CTA per (sequence, kv head, 128 rows), a row being a new token and one of
+// One CTA per (sequence, kv head, 256 rows), a row being a new token and one of
 // the kv head's query heads; 64 cached tokens a step.  Its warps:
-//  * 4..7 read the step's pages (16-byte loads, the next step's on their way),
+//  * 8..10 have the pages copied into shared memory steps ahead (bulk copies),
 //    turn E4M3 codes into fp16 (exact) and write them as the K-major,
-//    128-byte-swizzled operand tiles K [64 tokens][D] and V^T [D][64 tokens],
-//    two stages;
-//  * 8 (one lane) issues S = Q K^T (M 128, N 64) into one of two score buffers
-//    one step ahead, and O += P V (N = D), fp32 in tensor memory;
-//  * 0..3 are the softmax, a thread a row: scores by tcgen05.ld, no shuffles,
-//    weights as fp16 into the P tile.
-// Softmax references as in the kernel for a few tokens (m of the scores, N + m
-// of score + value exponent), but moved only when a score passes one by more
+//    128-byte-swizzled operand tiles K [64 tokens][D] and V^T [D][64 tokens];
+//  * 11 (one lane) issues, for each half of the rows, S = Q K^T (M 128, N 64)
+//    into one of two score buffers one step ahead, and O += P V (N = D), fp32
+//    in tensor memory;
+//  * 0..3 and 4..7 are the halves' softmax, a thread a row: scores by
+//    tcgen05.ld, no shuffles, weights as fp16 into the half's P tile.
+// Softmax references as in the kernel for a few tokens (m of the scores, m + N
+// of score + value exponent e), but moved only when a score passes one by more
 // than 2^8, so that the accumulator in tensor memory is rarely rescaled:
-// weights are 2^(7 + s + e - M) <= 2^15.  Two CTAs share an SM, one's softmax
-// beside the other's products.  Bound by the softmax's instructions (about
-// five a score) at head dims of 64.
+// weights are w = 2^(7 + s - m + e - N) <= 2^15, and a page's share of the sum
+// l is its weights' sum times 2^(N - e - 7).  There e - N is taken as at least
+// -80: a page that small adds nothing to the values, but its weights count.
+// Bound by the softmax's instructions: about three a score with packed fp32
+// arithmetic and three-input maxima.
 //
 // A NaN value that only some of a tile's rows see would reach the others as
 // 0 * NaN: where the pages hold one in a step that not all rows see, the CTA's
@@ -28,20 +30,23 @@
 
 namespace {
 
-constexpr int kM = 128;         // rows of a CTA
+constexpr int kM = 128;         // rows of a half
 constexpr int kT = 64;          // tokens of a step
-constexpr int kStages = 2;
-constexpr int kThreads = 9 * 32;
+constexpr int kLoaders = 96;    // threads that read pages
+constexpr int kThreads = 12 * 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Smem {   // offsets from a 1024-byte boundary
+    static constexpr int kStages = D == 64 ? 3 : 2, kRaw = D == 64 ? 4 : 3;   // operand tiles; steps of copied pages
     static constexpr int kQ = 0;
-    static constexpr int kP = kM * D * 2;
-    static constexpr int kK = kP + kM * kT * 2;             // kStages x [64][D]
+    static constexpr int kQ1 = kM * D * 2;                  // of a half: Q [128][D], P [128][64]
+    static constexpr int kP = 2 * kQ1, kP1 = kM * kT * 2;
+    static constexpr int kK = kP + 2 * kP1;                 // kStages x [64][D]
     static constexpr int kV = kK + kStages * kT * D * 2;    // kStages x [D][64]
-    static constexpr int kBytes = kV + kStages * kT * D * 2;
+    static constexpr int kCodes = kV + kStages * kT * D * 2; // kRaw x keys, values as they lie in the pages
+    static constexpr int kBytes = kCodes + kRaw * kT * D * 2;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -58,8 +63,7 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
 }
 // Bounded wait: false (and the status word set) after about 2 s, or when a
 // failure was reported elsewhere first; drain: only the time limit ends it.
-__device__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *status, int where, bool drain = false) {
-    if (bar_try(b, parity)) return true;
+__device__ __noinline__ bool bar_wait_long(uint64_t *b, uint32_t parity, int32_t *status, int where, bool drain) {
     const uint64_t t0 = now_ns();
     for (uint32_t i = 1;; i++) {
         if (bar_try(b, parity)) return true;
@@ -72,11 +76,23 @@ __device__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *status, int wher
         }
     }
 }
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *status, int where, bool drain = false) {
+#pragma unroll 1
+    for (int i = 0; i < 16; i++)
+        if (bar_try(b, parity)) return true;
+    return bar_wait_long(b, parity, status, where, drain);
+}
 __device__ __forceinline__ void bar_init(uint64_t *b, uint32_t n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n));
 }
 __device__ __forceinline__ void bar_arrive(uint64_t *b) {
     asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_u32(b)) : "memory");
+}
+// One arrival a warp: 32 of one warp on a barrier are taken one after another
+// (several hundred cycles).
+__device__ __forceinline__ void bar_arrive_warp(uint64_t *b) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(b);
 }
 __device__ __forceinline__ void commit(uint64_t *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
@@ -84,6 +100,11 @@ __device__ __forceinline__ void commit(uint64_t *b) {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 // Operand tile: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
 __device__ __forceinline__ uint64_t tile_desc(uint32_t at) {
     return (uint64_t)((at >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
@@ -91,12 +112,18 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t at) {
 __device__ __forceinline__ uint32_t swizzled(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
 // fp16 operands, fp32 accumulator, M = 128.
 constexpr uint32_t inst_desc(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kM >> 4) << 24); }
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <bool ACC>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc));
+                 "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
 }
-// 32 consecutive columns of the thread's TMEM lane; wait_ld before their use.
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+// 32 consecutive columns of the thread's TMEM lane; tmem_wait before their use.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
         "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -105,7 +132,28 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
           "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
           "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(at));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// The wait takes the registers in and out, so that no use of them moves above it.
+__device__ __forceinline__ void tmem_wait(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+          "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+          "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+          "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
+// Packed fp32: (x0, x1) * k + c, and sums.
+__device__ __forceinline__ void fma2(float &y0, float &y1, float x0, float x1, float k, float c) {
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 d, {%5, %5}; fma.rn.f32x2 a, a, b, d; mov.b64 {%0, %1}, a; }"
+        : "=f"(y0), "=f"(y1) : "f"(x0), "f"(x1), "f"(k), "f"(c));
+}
+__device__ __forceinline__ void add2(float &s0, float &s1, float x0, float x1) {
+    asm("{ .reg .b64 a, b; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+        : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32]) {
     asm volatile(
@@ -211,36 +259,41 @@ __device__ void slow_row(const Kv8Attend &a, int b, int kvh, int head, int row, 
 }
 
 template <int D, int P>
-__global__ void __launch_bounds__(kThreads, 2) moe_kv8_prompt_kernel(const __grid_constant__ PromptArgs f) {
-    constexpr int NP = kT / P, KU = kT * (D / 16) / 128;   // pages of a step; 16-byte units of keys (and of values) a thread
+__global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __grid_constant__ PromptArgs f) {
+    constexpr int NP = kT / P, NU = kT * (D / 16), KU = (NU + kLoaders - 1) / kLoaders;   // pages; 16-byte units of keys (and of values): all, a thread's
+    constexpr int kUnroll = D == 64 ? KU : 2;
     typedef Smem<D> L;
+    constexpr int kStages = L::kStages, kRaw = L::kRaw;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], s_full[2], q_full, p_full, o_done, drain;
-    __shared__ uint32_t meta[kStages][NP];   // key exponent byte, value's, 1 if the page is there
+    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2], drain;
+    __shared__ uint32_t rmeta[kRaw][NP], meta[kStages][NP];   // key exponent byte, value's, 1 if the page is there
     __shared__ uint32_t tmem_slot;
     __shared__ int job[2], odd;
     const Kv8Attend &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.y;
     if (tid == 0) {
-        for (int s = 0; s < kStages; s++) bar_init(&full[s], 128), bar_init(&empty[s], 1), bar_init(&s_full[s], 1);
-        bar_init(&q_full, 128), bar_init(&p_full, 128), bar_init(&o_done, 1), bar_init(&drain, 1);
+        for (int s = 0; s < kStages; s++) bar_init(&full[s], kLoaders / 32), bar_init(&empty[s], 1);
+        for (int s = 0; s < kRaw; s++) bar_init(&raw[s], 2), bar_init(&raw_empty[s], kLoaders / 32);
+        for (int h = 0; h < 2; h++)
+            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], 4), bar_init(&p_full[h], 4), bar_init(&o_done[h], 1);
+        bar_init(&drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         odd = 0;
     }
-    if (warp == 8) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(&tmem_slot)));
+    if (warp == 11) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
-        // the blockIdx.x-th row tile: sequences in order, a sequence's last
-        // (longest) tile first
+        // the blockIdx.x-th tile of 256 rows: sequences in order, a sequence's
+        // last (longest) tile first
         int x = blockIdx.x, found = -1, rt = 0;
         for (int b0 = 0; b0 < a.n_seqs && found < 0; b0 += 32) {
             int row0, n = 0, pos0;
             if (b0 + lane < a.n_seqs) kv8_rows(a, b0 + lane, row0, n, pos0);
-            const int mine = (n * f.G + kM - 1) / kM;
+            const int mine = (n * f.G + 2 * kM - 1) / (2 * kM);
             int inc = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -251,8 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kv8_prompt_kernel(const __gri
             if (hit) {
                 const int at = __ffs(hit) - 1;
                 found = b0 + at;
-                const int last = __shfl_sync(0xffffffffu, inc, at), cnt = __shfl_sync(0xffffffffu, mine, at);
-                rt = cnt - 1 - (x - (last - cnt));
+                rt = __shfl_sync(0xffffffffu, inc, at) - 1 - x;
             } else {
                 x -= __shfl_sync(0xffffffffu, inc, 31);
             }
@@ -270,269 +322,344 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kv8_prompt_kernel(const __gri
     if (b >= 0) {
         int row0, n, pos0;
         kv8_rows(a, b, row0, n, pos0);
-        const int r0 = job[1] * kM, rows = min(kM, n * f.G - r0);
+        const int r0 = job[1] * 2 * kM, rows = min(2 * kM, n * f.G - r0), halves = rows > kM ? 2 : 1;
         const int p_first = pos0 + r0 / f.G, p_last = pos0 + (r0 + rows - 1) / f.G;
         // tokens that any row sees, and the steps over them (aligned to 64)
         const int seen = (int)max(0ll, min((long long)p_last + 1, (long long)a.width * P));
         const int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
         const int step0 = lo / kT, steps = max(1, (seen + kT - 1) / kT - step0);
         int32_t *status = f.status;
-        // does every row see all of the step's tokens (where their pages are)?
-        auto whole = [&](int t0) { return t0 + kT <= seen && t0 + kT - 1 <= p_first && (a.window == 0 || t0 > p_last - a.window); };
+        // do the rows at positions first .. last all see all of the step's tokens (where their pages are)?
+        auto whole = [&](int t0, int first, int last) { return t0 + kT <= seen && t0 + kT - 1 <= first && (a.window == 0 || t0 > last - a.window); };
 
-        if (warp < 4) {
+        if (warp < 8) {
             // ---- the softmax ----
-            const int r = tid, rr = r0 + r, i2 = rr / f.G, head = kvh * f.G + rr - i2 * f.G;
-            const bool on = r < rows;
-            const int pos = on ? pos0 + i2 : -1;
-            int up;
-            {
-                // the row's queries, scaled by a power of two: largest magnitude in [2^14, 2^15)
-                const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (long long)(row0 + i2) * a.q_stride + head * D);
-                uint32_t am = 0;
+            const int h = warp >> 2;
+            if (h < halves) {
+                const int r = tid & (kM - 1), rr = r0 + h * kM + r, i2 = rr / f.G, head = kvh * f.G + rr - i2 * f.G;
+                const bool on = h * kM + r < rows;
+                const int pos = on ? pos0 + i2 : -1;
+                const int h_first = pos0 + (r0 + h * kM) / f.G, h_last = pos0 + (r0 + min(rows, (h + 1) * kM) - 1) / f.G;
+                int up;
+                {
+                    // the row's queries, scaled by a power of two: largest magnitude in [2^14, 2^15)
+                    const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (long long)(row0 + i2) * a.q_stride + head * D);
+                    uint4 w[D / 8];
+                    uint32_t am = 0;
 #pragma unroll
-                for (int c = 0; c < D / 8; c++) {
-                    const uint4 w = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    for (int c = 0; c < D / 8; c++) {
+                        w[c] = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-                    for (int e = 0; e < 4; e++) am = max(am, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+                        for (int e = 0; e < 4; e++) am = max(am, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+                    }
+                    up = min(141 - (int)(am >> 7), 127);
+                    const float mul = pow2i(up);
+#pragma unroll
+                    for (int c = 0; c < D / 8; c++) {
+                        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) y[e] = pack_f16(__uint_as_float(x[e] << 16) * mul, __uint_as_float(x[e] & 0xFFFF0000u) * mul);
+                        *reinterpret_cast<uint4 *>(smem + L::kQ + h * L::kQ1 + (c / 8) * (kM * 128) + swizzled(r, c % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                    fence_async();
+                    bar_arrive_warp(&q_full[h]);
                 }
-                up = min(141 - (int)(am >> 7), 127);
-                const float mul = pow2i(up);
-#pragma unroll
-                for (int c = 0; c < D / 8; c++) {
-                    const uint4 w = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t y[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) y[e] = pack_f16(__uint_as_float(x[e] << 16) * mul, __uint_as_float(x[e] & 0xFFFF0000u) * mul);
-                    *reinterpret_cast<uint4 *>(smem + L::kQ + (c / 8) * (kM * 128) + swizzled(r, c % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-                fence_async();
-                bar_arrive(&q_full);
-            }
-            const float sc = a.scale * kLog2e;
-            float m = -INFINITY, N = -INFINITY, l = 0.f;
-            const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-            bool ok = true;
-            for (int j = 0; j < steps; j++) {
-                const int st = j % kStages, t0 = (step0 + j) * kT;
-                ok = bar_wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1, status, 100);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                fence_after();
-                uint32_t mt[NP];
-                bool all = whole(t0);
-#pragma unroll
-                for (int p = 0; p < NP; p++) mt[p] = meta[st][p], all = all && (mt[p] >> 16);
-                // 32 scores at a time, read twice: for the largest, and for the weights
-                auto scores = [&](int hf, float (&s)[32]) {
-                    tmem_ld32(lanes + (j & 1) * kT + 32 * hf, s);
-                    if (!all)
-#pragma unroll
-                        for (int c = 0; c < 32; c++) {
-                            const int t = t0 + 32 * hf + c;
-                            if (!(t < seen && t <= pos && (a.window == 0 || t > pos - a.window) && (mt[(32 * hf + c) / P] >> 16))) s[c] = -INFINITY;
-                        }
-                };
-                auto key_scale = [&](int p) { return fmaxf(pow2i((int)(mt[p] & 255u) - 127 - up) * sc, 1e-37f); };   // > 0: -inf stays
-                float pm[NP], mx = -INFINITY, mv = -INFINITY;
-#pragma unroll
-                for (int p = 0; p < NP; p++) pm[p] = -INFINITY;
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    float s[32];
-                    scores(hf, s);
-#pragma unroll
-                    for (int c = 0; c < 32; c++) pm[(32 * hf + c) / P] = fmaxf(pm[(32 * hf + c) / P], s[c]);
-                }
-                const float ms0 = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                for (int p = 0; p < NP; p++) {
-                    pm[p] *= key_scale(p);
-                    mx = fmaxf(mx, pm[p]), mv = fmaxf(mv, pm[p] - ms0 + (float)((int)((mt[p] >> 8) & 255u) - 127));
-                }
-                // the references follow when passed by more than 2^8
-                float corr = 1.f;
-                const bool move = mx > m + 8.f || mv > N + 8.f;
-                if (move) {
-                    const float mn = fmaxf(m, mx), was = N + (m - mn);
-                    float nn = was;
-#pragma unroll
-                    for (int p = 0; p < NP; p++) nn = fmaxf(nn, pm[p] - mn + (float)((int)((mt[p] >> 8) & 255u) - 127));
-                    l *= ex2(m - mn);
-                    corr = ex2(was - nn);
-                    m = mn, N = nn;
-                }
-                const float ms = m == -INFINITY ? 0.f : m, Ns = N == -INFINITY ? 0.f : N;
-                // weights; the products of the step before have read the P tile
-                if (j > 0) {
-                    ok = bar_wait(&o_done, (uint32_t)(j - 1) & 1, status, 101);
+                const float sc = a.scale * kLog2e;
+                float m = -INFINITY, N = -INFINITY, l = 0.f;
+                const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * h;
+                unsigned char *pt = smem + L::kP + h * L::kP1;
+                bool ok = true;
+                for (int j = 0; j < steps; j++) {
+                    const int st = j % kStages, t0 = (step0 + j) * kT;
+                    ok = bar_wait(&s_full[h][j & 1], (uint32_t)(j >> 1) & 1, status, 100);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     fence_after();
-                    if (__any_sync(0xffffffffu, move)) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(lanes + 2 * kT + c, o);
+                    float s[kT];
+                    tmem_ld32(lanes + (j & 1) * kT, s);
+                    tmem_ld32(lanes + (j & 1) * kT + 32, s + 32);
+                    uint32_t mt[NP];
+                    bool all = whole(t0, h_first, h_last);
 #pragma unroll
-                            for (int e = 0; e < 32; e++) o[e] *= corr;
-                            tmem_st32(lanes + 2 * kT + c, o);
+                    for (int p = 0; p < NP; p++) mt[p] = meta[st][p], all = all && (mt[p] >> 16);
+                    tmem_wait(s);
+                    tmem_wait(s + 32);
+                    if (!all) {
+#pragma unroll
+                        for (int c = 0; c < kT; c++) {
+                            const int t = t0 + c;
+                            if (!(t < seen && t <= pos && (a.window == 0 || t > pos - a.window) && (mt[c / P] >> 16))) s[c] = -INFINITY;
                         }
                     }
-                }
-                float sum = 0.f;
+                    auto key_scale = [&](int p) { return fmaxf(pow2i((int)(mt[p] & 255u) - 127 - up) * sc, 1e-37f); };   // > 0: -inf stays
+                    float pm[NP], mx = -INFINITY, mv = -INFINITY;
+                    const float ms0 = m == -INFINITY ? 0.f : m;
 #pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    float s[32];
-                    scores(hf, s);
+                    for (int p = 0; p < NP; p++) {
+                        float x[4];   // four chains
 #pragma unroll
-                    for (int c8 = 0; c8 < 4; c8++) {
-                        const int p = (32 * hf + 8 * c8) / P;
-                        const float fac = ex2(fminf((float)((int)((mt[p] >> 8) & 255u) - 120) - Ns, 126.f)), ks = key_scale(p);
-                        uint32_t y[4];
+                        for (int c = 0; c < 4; c++) x[c] = max3(s[p * P + c], s[p * P + 4 + c], s[p * P + 8 + c]);
 #pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const float w0 = ex2(fmaf(s[8 * c8 + 2 * e], ks, -ms)), w1 = ex2(fmaf(s[8 * c8 + 2 * e + 1], ks, -ms));
-                            sum += w0 + w1;
-                            y[e] = pack_f16(w0 * fac, w1 * fac);
+                        for (int c = 12; c < P; c++) {
+                            if (c + 4 < P && (c / 4) % 2 == 1) x[c % 4] = max3(x[c % 4], s[p * P + c], s[p * P + c + 4]);
+                            else if (c + 4 >= P && (c / 4) % 2 == 1) x[c % 4] = fmaxf(x[c % 4], s[p * P + c]);
                         }
-                        *reinterpret_cast<uint4 *>(smem + L::kP + swizzled(r, 4 * hf + c8)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        pm[p] = fmaxf(max3(x[0], x[1], x[2]), x[3]) * key_scale(p);
+                        mx = fmaxf(mx, pm[p]), mv = fmaxf(mv, pm[p] - ms0 + (float)((int)((mt[p] >> 8) & 255u) - 127));
+                    }
+                    // the references follow when passed by more than 2^8
+                    float corr = 1.f;
+                    const bool move = mx > m + 8.f || mv > N + 8.f;
+                    if (move) {
+                        const float mn = fmaxf(m, mx), was = N + (m - mn);
+                        float nn = was;
+#pragma unroll
+                        for (int p = 0; p < NP; p++) nn = fmaxf(nn, pm[p] - mn + (float)((int)((mt[p] >> 8) & 255u) - 127));
+                        l *= ex2(m - mn);
+                        corr = ex2(was - nn);
+                        m = mn, N = nn;
+                    }
+                    const float ms = m == -INFINITY ? 0.f : m, Ns = N == -INFINITY ? 0.f : N;
+                    // the products of the step before have read the P tile
+                    if (j > 0) {
+                        ok = bar_wait(&o_done[h], (uint32_t)(j - 1) & 1, status, 101);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        fence_after();
+                        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                tmem_ld32(lanes + 2 * kT + c, o);
+                                tmem_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 32; e++) o[e] *= corr;
+                                tmem_st32(lanes + 2 * kT + c, o);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int p = 0; p < NP; p++) {
+                        const float fe = fmaxf((float)((int)((mt[p] >> 8) & 255u) - 127) - Ns, -80.f) + 7.f, bias = fe - ms, ks = key_scale(p);
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int c = p * P; c < (p + 1) * P; c += 8) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                float w0, w1;
+                                fma2(w0, w1, s[c + 2 * e], s[c + 2 * e + 1], ks, bias);
+                                w0 = ex2(w0), w1 = ex2(w1);
+                                add2(s0, s1, w0, w1);
+                                y[e] = pack_f16(w0, w1);
+                            }
+                            *reinterpret_cast<uint4 *>(pt + swizzled(r, c / 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                        l = fmaf(s0 + s1, ex2(-fe), l);
+                    }
+                    fence_async();
+                    fence_before();
+                    bar_arrive_warp(&p_full[h]);
+                }
+                if (ok) ok = __all_sync(0xffffffffu, bar_wait(&o_done[h], (uint32_t)(steps - 1) & 1, status, 102));
+                if (ok) {
+                    fence_after();
+                    const float sink = on && a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
+                    const float top = fmaxf(m, sink);
+                    const float den = top == -INFINITY ? l : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sink - top);
+                    const float k = den == 0.f || N == -INFINITY ? 0.f : ex2(N - 7.f + (m - top)) / den;
+                    uint4 *o = reinterpret_cast<uint4 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float v[32];
+                        tmem_ld32(lanes + 2 * kT + c, v);
+                        tmem_wait(v);
+                        if (!on) continue;
+#pragma unroll
+                        for (int x = 0; x < 4; x++)
+                            o[c / 8 + x] = make_uint4(bits_of(__floats2bfloat162_rn(v[8 * x] * k, v[8 * x + 1] * k)),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 2] * k, v[8 * x + 3] * k)),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 4] * k, v[8 * x + 5] * k)),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 6] * k, v[8 * x + 7] * k)));
                     }
                 }
-                l += sum;
-                fence_async();
-                fence_before();
-                bar_arrive(&p_full);
             }
-            if (ok) ok = __all_sync(0xffffffffu, bar_wait(&o_done, (uint32_t)(steps - 1) & 1, status, 102));
-            if (ok) {
-                fence_after();
-                const float sink = on && a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
-                const float top = fmaxf(m, sink);
-                const float den = top == -INFINITY ? l : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sink - top);
-                const float k = den == 0.f || N == -INFINITY ? 0.f : ex2(N - 7.f + (m - top)) / den;
-                uint4 *o = reinterpret_cast<uint4 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D);
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float v[32];
-                    tmem_ld32(lanes + 2 * kT + c, v);
-                    if (!on) continue;
-#pragma unroll
-                    for (int x = 0; x < 4; x++)
-                        o[c / 8 + x] = make_uint4(bits_of(__floats2bfloat162_rn(v[8 * x] * k, v[8 * x + 1] * k)),
-                                                  bits_of(__floats2bfloat162_rn(v[8 * x + 2] * k, v[8 * x + 3] * k)),
-                                                  bits_of(__floats2bfloat162_rn(v[8 * x + 4] * k, v[8 * x + 5] * k)),
-                                                  bits_of(__floats2bfloat162_rn(v[8 * x + 6] * k, v[8 * x + 7] * k)));
-                }
-            }
-        } else if (warp < 8) {
+        } else if (warp < 11) {
             // ---- pages to operand tiles ----
-            const int x = tid - 128;
+            const int x = tid - 256;
             const int32_t *tab = a.table + (size_t)b * a.width;
             auto page_at = [&](int t) {   // of token t, -1 where there is none
                 const int pg = t < seen ? __ldg(tab + t / P) : -1;
                 return pg >= 0 && pg < a.c.n_pages ? pg : -1;
             };
-            uint4 kw[KU], vw[KU];
-            uint32_t mw = 0;
-            // unit i of a thread: keys of token x % 64, dims 16 (x / 64 + 2 i) ..; values of dim u % D, tokens 16 (u / D) ..
-            auto load = [&](int j) {
-                const int t0 = (step0 + j) * kT;
-                const int kp = page_at(t0 + x % kT), at = (t0 + x % kT) % P;
-#pragma unroll
-                for (int i = 0; i < KU; i++)
-                    kw[i] = kp >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.c.k + ((size_t)kp * a.c.KVH + kvh) * (P * D) + (x / kT + 2 * i) * (P * 16) + at * 16))
-                                    : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < KU; i++) {
-                    const int u = x + 128 * i, dim = u % D, blk = u / D, t = t0 + 16 * blk, vp = page_at(t);
-                    vw[i] = vp >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.c.v + ((size_t)vp * a.c.KVH + kvh) * (P * D) + (t % P) * D + dim * 16))
-                                    : make_uint4(0, 0, 0, 0);
-                }
-                if (x < NP) {
-                    const int pg = page_at(t0 + x * P);
-                    const size_t ph = (size_t)max(pg, 0) * a.c.KVH + kvh;
-                    mw = pg >= 0 ? (uint32_t)__ldg(a.c.ks + ph) | (uint32_t)__ldg(a.c.vs + ph) << 8 | 1u << 16 : 0u;
-                }
+            // warp 8, lane p < NP: page p of the step to copy next, read one step ahead
+            int pg = -1, issued = 0, pend_slot = -1;
+            uint32_t pend_k = 0, pend_v = 0, pend_there = 0;   // put together only when they are stored: nothing waits for them here
+            auto fetch = [&]() { pg = warp == 8 && lane < NP && issued < steps ? page_at((step0 + issued) * kT + lane * P) : -1; };
+            auto flush = [&]() {   // the scales, read since the copies went out: the slot's second arrival
+                if (pend_slot < 0) return;
+                if (lane < NP) rmeta[pend_slot][lane] = pend_k | pend_v << 8 | pend_there;
+                __syncwarp();
+                if (lane == 0) bar_arrive(&raw[pend_slot]);
+                pend_slot = -1;
             };
-            load(0);
+            auto issue = [&]() {   // warp 8
+                flush();
+                const int slot = issued % kRaw;
+                const unsigned there = __ballot_sync(0xffffffffu, pg >= 0);
+                if (lane == 0)
+                    asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(smem_u32(&raw[slot])),
+                                 "r"((uint32_t)(__popc(there) * 2 * P * D)) : "memory");
+                __syncwarp();
+                pend_k = pend_v = pend_there = 0;
+                if (pg >= 0) {
+                    const size_t ph = (size_t)pg * a.c.KVH + kvh;
+                    const uint32_t dst = smem_u32(smem + L::kCodes + slot * (2 * kT * D)) + lane * (P * D), bar = smem_u32(&raw[slot]);
+                    bulk_copy(dst, a.c.k + ph * (P * D), P * D, bar);
+                    bulk_copy(dst + kT * D, a.c.v + ph * (P * D), P * D, bar);
+                    pend_k = __ldg(a.c.ks + ph), pend_v = __ldg(a.c.vs + ph), pend_there = 1u << 16;
+                }
+                pend_slot = slot;
+                issued++;
+                fetch();
+            };
+            if (warp == 8) fetch();
+            bool ok = true;
             for (int j = 0; j < steps; j++) {
-                const int st = j % kStages, t0 = (step0 + j) * kT;
-                if (j >= kStages && !bar_wait(&empty[st], (uint32_t)(j / kStages - 1) & 1, status, 103)) break;
-                unsigned char *K = smem + L::kK + st * (kT * D * 2), *V = smem + L::kV + st * (kT * D * 2);
-                const bool part = !whole(t0);
+                const int st = j % kStages, slot = j % kRaw, t0 = (step0 + j) * kT;
+                if (warp == 8) {
+                    // a slot is filled again once the step in it, before this one, has been read
+#pragma unroll 1
+                    while (ok && issued < steps && issued - kRaw < j) {
+                        if (issued >= kRaw) ok = __all_sync(0xffffffffu, bar_wait(&raw_empty[issued % kRaw], (uint32_t)(issued / kRaw - 1) & 1, status, 110));
+                        if (ok) issue();
+                    }
+                    if (pend_slot == slot) flush();
+                    if (!ok) break;
+                }
+                ok = bar_wait(&raw[slot], (uint32_t)(j / kRaw) & 1, status, 108);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (j >= kStages) {
+                    ok = __all_sync(0xffffffffu, bar_wait(&empty[st], (uint32_t)(j / kStages - 1) & 1, status, 103));
+                    if (!ok) break;
+                }
+                const uint32_t mw = x < NP ? rmeta[slot][x] : 0u;
+                uint32_t there = 0;   // pages of the step that are there
 #pragma unroll
+                for (int p = 0; p < NP; p++) there |= (rmeta[slot][p] >> 16) << p;
+                const bool part = !whole(t0, p_first, p_last) || there != (1u << NP) - 1;
+                // unit u: keys of token u % 64, dims 16 (u / 64) ..; values of dim u % D, tokens 16 (u / D) ..; what no
+                // page brought is what the slot held before, and never seen
+                const unsigned char *codes = smem + L::kCodes + slot * (2 * kT * D);
+                unsigned char *K = smem + L::kK + st * (kT * D * 2), *V = smem + L::kV + st * (kT * D * 2);
+#pragma unroll kUnroll
                 for (int i = 0; i < KU; i++) {
+                    const int u = x + kLoaders * i, tok = u % kT, ch = 2 * (u / kT);   // 16-byte chunk of the row: dims 8 ch ..
+                    if (u >= NU) break;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(codes + (tok / P) * (P * D) + (u / kT) * (P * 16) + (tok % P) * 16);
                     uint4 c0, c1;
-                    decode16(kw[i], true, c0, c1);
-                    const int tok = x % kT, ch = 2 * (x / kT + 2 * i);   // 16-byte chunk of the row: dims 8 ch ..
+                    decode16(w, true, c0, c1);
                     unsigned char *to = K + (ch / 8) * (kT * 128);
                     *reinterpret_cast<uint4 *>(to + swizzled(tok, ch % 8)) = c0;
                     *reinterpret_cast<uint4 *>(to + swizzled(tok, ch % 8 + 1)) = c1;
                 }
-#pragma unroll
+#pragma unroll kUnroll
                 for (int i = 0; i < KU; i++) {
-                    const int u = x + 128 * i, dim = u % D, blk = u / D;
+                    const int u = x + kLoaders * i, dim = u % D, blk = u / D;
+                    if (u >= NU) break;
+                    uint4 v = *reinterpret_cast<const uint4 *>(codes + kT * D + u * 16);
                     if (part) {
                         // tokens that no row sees to zero; a NaN among the others: not all rows see it
-                        uint32_t w[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w}, nan = 0;
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w}, nan = 0;
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const int t = t0 + 16 * blk + 2 * q + (e & 1) + 8 * (e >> 1);
-                                if (t >= seen || t < lo) w[q] &= ~(0xFFu << (8 * e));
+                                if (t >= seen || t < lo || !(there >> (16 * blk / P) & 1)) w[q] &= ~(0xFFu << (8 * e));
                             }
                             nan |= ((w[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                         }
                         if (nan) odd = 1;
-                        vw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        v = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     uint4 c0, c1;
-                    decode16(vw[i], false, c0, c1);
+                    decode16(v, false, c0, c1);
                     *reinterpret_cast<uint4 *>(V + swizzled(dim, 2 * blk)) = c0;
                     *reinterpret_cast<uint4 *>(V + swizzled(dim, 2 * blk + 1)) = c1;
                 }
+                bar_arrive_warp(&raw_empty[slot]);
                 if (x < NP) meta[st][x] = mw;
                 fence_async();
-                bar_arrive(&full[st]);
-                if (j + 1 < steps) load(j + 1);
+                bar_arrive_warp(&full[st]);
             }
-        } else if (lane == 0) {
-            // ---- the products ----
-            const uint32_t Q = smem_u32(smem + L::kQ), Pt = smem_u32(smem + L::kP);
-            bool ok = bar_wait(&q_full, 0, status, 104);
-            auto scores = [&](int j) {   // into score buffer j & 1
-                const int st = j % kStages;
-                if (!bar_wait(&full[st], (uint32_t)(j / kStages) & 1, status, 105)) return false;
+            // copies still in flight land before the shared memory goes
+            flush();
+            if (warp == 8)
+                for (int j = max(0, issued - kRaw); j < issued; j++) bar_wait(&raw[j % kRaw], (uint32_t)(j / kRaw) & 1, status, 109, true);
+        } else {
+            // ---- the products: the warp together, so that descriptors stay in uniform registers; one lane issues ----
+            const uint64_t Q = tile_desc(smem_u32(smem + L::kQ)), Pt = tile_desc(smem_u32(smem + L::kP));
+            const uint64_t K0 = tile_desc(smem_u32(smem + L::kK)), V0 = tile_desc(smem_u32(smem + L::kV));
+            constexpr uint64_t kTile16 = kT * D * 2 / 16;   // descriptors count 16 bytes
+            bool ok = true;
+            for (int h = 0; h < halves && ok; h++) ok = __all_sync(0xffffffffu, bar_wait(&q_full[h], 0, status, 104));
+            auto scores = [&](int j, int st, uint32_t parity) {   // into score buffers j & 1
+                if (!__all_sync(0xffffffffu, bar_wait(&full[st], parity, status, 105))) return false;
                 fence_after();
-                const uint32_t K = smem_u32(smem + L::kK + st * (kT * D * 2));
+                const uint64_t K = K0 + st * kTile16;
+                const uint32_t to = tmem + (j & 1) * kT;
+                if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < D / 16; c++)
-                    mma(tmem + (j & 1) * kT, tile_desc(Q + (c / 4) * (kM * 128) + (c % 4) * 32), tile_desc(K + (c / 4) * (kT * 128) + (c % 4) * 32),
-                        inst_desc(kT), c != 0);
-                commit(&s_full[j & 1]);
+                    for (int c = 0; c < D / 16; c++) {
+                        const uint64_t q = Q + (c / 4) * (kM * 8) + (c % 4) * 2, k = K + (c / 4) * (kT * 8) + (c % 4) * 2;
+                        if (c == 0) mma<false>(to, q, k, inst_desc(kT));
+                        else mma<true>(to, q, k, inst_desc(kT));
+                    }
+                    commit(&s_full[0][j & 1]);
+                    if (halves > 1) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; c++) {
+                            const uint64_t q = Q + L::kQ1 / 16 + (c / 4) * (kM * 8) + (c % 4) * 2, k = K + (c / 4) * (kT * 8) + (c % 4) * 2;
+                            if (c == 0) mma<false>(to + 256, q, k, inst_desc(kT));
+                            else mma<true>(to + 256, q, k, inst_desc(kT));
+                        }
+                        commit(&s_full[1][j & 1]);
+                    }
+                }
+                __syncwarp();
                 return true;
             };
-            if (ok) ok = scores(0);
-            for (int j = 0; j < steps && ok; j++) {
-                // the next scores go ahead of this step's values: their buffer was read before step j - 1's weights were
-                if (j + 1 < steps) ok = scores(j + 1);
-                if (ok) ok = bar_wait(&p_full, (uint32_t)j & 1, status, 106);
-                if (!ok) break;
-                fence_after();
-                const int st = j % kStages;
-                const uint32_t V = smem_u32(smem + L::kV + st * (kT * D * 2));
+            int st = 0, st1 = 0;          // stages of steps j and j + 1
+            uint32_t par1 = 0;
+            if (ok) ok = scores(0, 0, 0);
+            for (int j = 0; j < steps && ok; j++, st = st1) {
+                if (++st1 == kStages) st1 = 0, par1 ^= 1;
+                // the next scores go ahead of this step's values: their buffers were read before step j - 1's weights were
+                if (j + 1 < steps) ok = scores(j + 1, st1, par1);
+                const uint64_t V = V0 + st * kTile16;
+                for (int h = 0; h < halves && ok; h++) {
+                    ok = __all_sync(0xffffffffu, bar_wait(&p_full[h], (uint32_t)j & 1, status, 106));
+                    if (!ok) break;
+                    fence_after();
+                    const uint64_t w = Pt + h * (L::kP1 / 16);
+                    const uint32_t to = tmem + 256 * h + 2 * kT;
+                    if (elect_one()) {
+                        if (j == 0) mma<false>(to, w, V, inst_desc(D));
+                        else mma<true>(to, w, V, inst_desc(D));
 #pragma unroll
-                for (int c = 0; c < kT / 16; c++)
-                    mma(tmem + 2 * kT, tile_desc(Pt + c * 32), tile_desc(V + c * 32), inst_desc(D), j > 0 || c > 0);
-                commit(&empty[st]);
-                commit(&o_done);
+                        for (int c = 1; c < kT / 16; c++) mma<true>(to, w + c * 2, V + c * 2, inst_desc(D));
+                        commit(&o_done[h]);
+                        if (h + 1 == halves) commit(&empty[st]);
+                    }
+                    __syncwarp();
+                }
             }
             if (!ok) {   // the products already issued finish before tensor memory is released
-                commit(&drain);
+                if (elect_one()) commit(&drain);
                 bar_wait(&drain, 0, status, 107, true);
             }
         }
@@ -546,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kv8_prompt_kernel(const __gri
     }
     fence_before();
     __syncthreads();
-    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
+    if (warp == 11) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 template <int D, int P>
@@ -566,8 +693,8 @@ cudaError_t prompt_page(const PromptArgs &f, dim3 grid, cudaStream_t st) {
 cudaError_t launch_kv8_prompt(const Kv8Attend &a, int32_t *status, cudaStream_t st) {
     PromptArgs f{a, a.QH / a.c.KVH, status};
     // row tiles: a sequence's last may be partly filled
-    const long long tiles = (long long)a.n_rows * f.G / kM + a.n_seqs;
-    const long long most = (long long)a.n_seqs * (((long long)a.max_new * f.G + kM - 1) / kM);
+    const long long tiles = (long long)a.n_rows * f.G / (2 * kM) + a.n_seqs;
+    const long long most = (long long)a.n_seqs * (((long long)a.max_new * f.G + 2 * kM - 1) / (2 * kM));
     const dim3 grid((unsigned)std::min(tiles, most), a.c.KVH);
     return a.c.D == 64 ? prompt_page<64>(f, grid, st) : prompt_page<128>(f, grid, st);
 }
