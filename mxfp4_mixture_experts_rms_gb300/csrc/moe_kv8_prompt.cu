@@ -344,20 +344,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                 {
                     // the row's queries, scaled by a power of two: largest magnitude in [2^14, 2^15)
                     const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (long long)(row0 + i2) * a.q_stride + head * D);
-                    uint4 w[D / 8];
                     uint32_t am = 0;
-#pragma unroll
+#pragma unroll 8
                     for (int c = 0; c < D / 8; c++) {
-                        w[c] = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
-                        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                        const uint4 w = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int e = 0; e < 4; e++) am = max(am, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
                     }
                     up = min(141 - (int)(am >> 7), 127);
                     const float mul = pow2i(up);
-#pragma unroll
+#pragma unroll 8
                     for (int c = 0; c < D / 8; c++) {
-                        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                        const uint4 w = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
                         uint32_t y[4];
 #pragma unroll
                         for (int e = 0; e < 4; e++) y[e] = pack_f16(__uint_as_float(x[e] << 16) * mul, __uint_as_float(x[e] & 0xFFFF0000u) * mul);
