@@ -19,20 +19,43 @@ namespace {
 // magnitude, the page's new exponent, the earlier tokens' codes re-rounded if
 // the exponent rose, the new codes.  With amax = m * 2^e (m in [1, 2)) the
 // exponent ceil(log2(amax / 448)) is e - 8 + (m > 1.75): no division.
+//
+// A run that fills its page (all but the ends of a prompt) is read once, into
+// registers, 16 bytes a load; values' codes are turned through shared memory.
+// Other runs are read twice and keep the bytes around them.
+// Bound by HBM for prompts (4 bytes read, 2 written a value pair); a decode
+// step is a chain of four dependent loads.
 __device__ __forceinline__ int kv8_exponent(float amax) {
     const uint32_t b = min(max(__float_as_uint(amax), 0x04E00000u), 0x7F7FFFFFu);  // at least 448 * 2^-126, finite
     return (int)(b >> 23) - 135 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
 }
-
-__device__ __forceinline__ void bf16x8(const uint4 v, float (&f)[8]) {
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// The larger of am and the magnitudes of four bf16 pairs (NaN passes over).
+__device__ __forceinline__ float amax8(float am, const uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; i++) am = fmaxf(am, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+    return am;
 }
-
+// The same on the bits, as two 16-bit lanes; a NaN shows as more than 0x7F80.
+__device__ __forceinline__ uint32_t bits8(uint32_t m, const uint4 v) {
+    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+    return __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+    return v;
+}
+// Four bf16 pairs times a power of two -> eight codes.
+__device__ __forceinline__ uint2 encode8(const uint4 v, float inv) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) c[i] = f32x2_to_e4m3(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
 // Four codes times f (a power of two at most 1), rounded again.
 __device__ __forceinline__ uint32_t requant4(uint32_t w, float f) {
     const float2 a = e4m3x2_to_f32(w), b = e4m3x2_to_f32(w >> 16);
@@ -40,17 +63,137 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float f) {
 }
 
 constexpr int kAppendWarps = 4;
-constexpr int kMaxWindow = 128;  // tokens of one CTA
+constexpr int kMaxWindow = 64;  // tokens of one CTA
 
-template <int D>
-__global__ void __launch_bounds__(kAppendWarps * 32, 6) moe_kv8_append_kernel(Kv8Cache c, const uint16_t *k, const uint16_t *v,
-                                                                   long long k_stride, long long v_stride,
-                                                                   const int32_t *slots, int n, int window) {
+// A page's run; x: its first row, at this kv head; base: the page's codes;
+// turn: P * D bytes of the warp's own; returns the scale byte.
+template <int D, int P>
+__device__ __forceinline__ int append_page(bool keys, const uint16_t *x, long long stride, uint8_t *base, uint8_t *turn, int lane) {
+    // a warp reads kTok tokens at a time, 16 bytes (8 dims) a lane; up to 16
+    // loads held, the others read again
+    constexpr int kTok = 256 / D, N = P / kTok, HELD = N < 16 ? N : 16;
+    const int tok = lane / (D / 8), ch = lane % (D / 8);
+    const uint16_t *p = x + (long long)tok * stride + 8 * ch;
+    const long long step = kTok * stride;
+    uint4 v[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; i++) v[i] = __ldg(reinterpret_cast<const uint4 *>(p + i * step));
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int i = HELD; i < N; i++) m = bits8(m, __ldg(reinterpret_cast<const uint4 *>(p + i * step)));
+#pragma unroll
+    for (int i = 0; i < HELD; i++) m = bits8(m, v[i]);
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    float am = __uint_as_float(m << 16);
+    if (m > 0x7F80u) {
+        am = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < N; i++) am = amax8(am, __ldg(reinterpret_cast<const uint4 *>(p + i * step)));
+        am = warp_max(am);
+    }
+    const int byte = kv8_exponent(am) + 127;
+    const float inv = pow2i(127 - byte);
+    uint8_t *to = keys ? base + (ch / 2) * (P * 16) + tok * 16 + (ch % 2) * 8 : turn + tok * D + ch * 8;
+    const int next = keys ? kTok * 16 : kTok * D;
+#pragma unroll
+    for (int i = 0; i < HELD; i++, to += next) *reinterpret_cast<uint2 *>(to) = encode8(v[i], inv);
+#pragma unroll 4
+    for (int i = HELD; i < N; i++, to += next) *reinterpret_cast<uint2 *>(to) = encode8(__ldg(reinterpret_cast<const uint4 *>(p + i * step)), inv);
+    if (!keys) {
+        // values lie [token][dim]: 4 dims and 16 tokens a lane, turned by words
+        __syncwarp();
+#pragma unroll 1
+        for (int w = lane; w < P / 16 * (D / 4); w += 32) {
+            const int g = w / (D / 4), d = 4 * (w % (D / 4));
+            uint32_t in[16];
+#pragma unroll
+            for (int t = 0; t < 16; t++) in[t] = *reinterpret_cast<const uint32_t *>(turn + (16 * g + t) * D + d);
+            uint32_t out[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; q++) {   // tokens 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q
+                const uint32_t a0 = __byte_perm(in[2 * q], in[2 * q + 1], 0x5140), a1 = __byte_perm(in[2 * q], in[2 * q + 1], 0x7362);
+                const uint32_t b0 = __byte_perm(in[8 + 2 * q], in[9 + 2 * q], 0x5140), b1 = __byte_perm(in[8 + 2 * q], in[9 + 2 * q], 0x7362);
+                out[0][q] = __byte_perm(a0, b0, 0x5410), out[1][q] = __byte_perm(a0, b0, 0x7632);
+                out[2][q] = __byte_perm(a1, b1, 0x5410), out[3][q] = __byte_perm(a1, b1, 0x7632);
+            }
+            uint4 *o = reinterpret_cast<uint4 *>(base + g * (D * 16) + d * 16);
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[e] = make_uint4(out[e][0], out[e][1], out[e][2], out[e][3]);
+        }
+        __syncwarp();   // the buffer is the next run's
+    }
+    return byte;
+}
+
+// A run of len tokens from place o0 on; old: the page's scale byte (0: it starts here).
+template <int D, int P>
+__device__ __forceinline__ int append_run(bool keys, const uint16_t *x, long long stride, uint8_t *base, int o0, int len, int old, int lane) {
+    float am = 0.f;
+    for (int u = lane; u < len * (D / 8); u += 32)
+        am = amax8(am, __ldg(reinterpret_cast<const uint4 *>(x + (long long)(u / (D / 8)) * stride) + u % (D / 8)));
+    const int now = max(kv8_exponent(warp_max(am)) + 127, old);
+    const float inv = pow2i(127 - now), shrink = pow2i(old - now);
+    const bool again = o0 > 0 && now > old;
+    if (keys) {
+        if (again)
+            for (int u = lane; u < o0 * (D / 16); u += 32) {
+                uint4 *p = reinterpret_cast<uint4 *>(base + (size_t)(u % (D / 16)) * P * 16 + u / (D / 16) * 16);
+                uint4 w = *p;
+                w.x = requant4(w.x, shrink), w.y = requant4(w.y, shrink);
+                w.z = requant4(w.z, shrink), w.w = requant4(w.w, shrink);
+                *p = w;
+            }
+        for (int u = lane; u < len * (D / 8); u += 32) {
+            const int j = u / (D / 8), ch = u % (D / 8);
+            *reinterpret_cast<uint2 *>(base + (ch / 2) * (P * 16) + (o0 + j) * 16 + (ch % 2) * 8) =
+                encode8(__ldg(reinterpret_cast<const uint4 *>(x + (long long)j * stride) + ch), inv);
+        }
+        return now;
+    }
+    // (16 tokens, 2 dims) at a time: bytes of tokens outside the run keep
+    // their codes (re-rounded if the exponent rose)
+    const int g0 = again ? 0 : o0 / 16, g1 = (o0 + len + 15) / 16;
+    for (int u = lane; u < (g1 - g0) * (D / 2); u += 32) {
+        const int gr = g0 + u / (D / 2), d = 2 * (u % (D / 2));
+        uint4 *p = reinterpret_cast<uint4 *>(base + (size_t)gr * D * 16 + d * 16);
+        const uint4 a = p[0], b = p[1];
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            // tokens 2q, 2q + 1, 8 + 2q, 9 + 2q of the group in byte order
+            uint32_t n0 = w[q], n1 = w[4 + q];
+            const uint32_t r0 = again ? requant4(n0, shrink) : n0, r1 = again ? requant4(n1, shrink) : n1;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int tok = gr * 16 + 2 * q + (e & 1) + 8 * (e >> 1), sh = 8 * e;
+                const uint32_t mask = 0xFFu << sh;
+                if (tok >= o0 && tok < o0 + len) {
+                    const uint32_t pr = __ldg(reinterpret_cast<const uint32_t *>(x + (long long)(tok - o0) * stride + d));
+                    const uint32_t cd = f32x2_to_e4m3(bf16_lo(pr) * inv, bf16_hi(pr) * inv);
+                    n0 = (n0 & ~mask) | ((cd & 0xFFu) << sh);
+                    n1 = (n1 & ~mask) | ((cd >> 8) << sh);
+                } else if (tok < o0) {
+                    n0 = (n0 & ~mask) | (r0 & mask);
+                    n1 = (n1 & ~mask) | (r1 & mask);
+                }
+            }
+            w[q] = n0, w[4 + q] = n1;
+        }
+        p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return now;
+}
+
+// Window of tokens blockIdx.x; warps over (kv head, side) pairs.
+template <int D, int P>
+__global__ void __launch_bounds__(kAppendWarps * 32, 5) moe_kv8_append_kernel(Kv8Cache c, const uint16_t *k, const uint16_t *v,
+                                                                           long long k_stride, long long v_stride,
+                                                                           const int32_t *slots, int n, int window) {
+    __shared__ __align__(16) uint8_t turn[kAppendWarps][P * D];
     __shared__ int s[kMaxWindow + 1 + 64];  // slot of the token before, the window's, those a run can reach into
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t0 = blockIdx.x * window, h = blockIdx.y;
-    const bool keys = blockIdx.z == 0;
-    const int total = c.n_pages * c.P;
+    const int tid = threadIdx.x, lane = tid & 31, pair = blockIdx.y * kAppendWarps + (tid >> 5);
+    const int t0 = blockIdx.x * window, total = c.n_pages * P;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = tid; i < window + 65; i += kAppendWarps * 32) {
@@ -59,107 +202,50 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) moe_kv8_append_kernel(Kv
         s[i] = x >= 0 && x < total ? x : -1;
     }
     __syncthreads();
-    const uint16_t *x = keys ? k : v;
+    if (pair >= 2 * c.KVH) return;
+    const int h = pair >> 1;
+    const bool keys = (pair & 1) == 0;
+    const uint16_t *x = (keys ? k : v) + h * D;
     const long long stride = keys ? k_stride : v_stride;
     uint8_t *codes = keys ? c.k : c.v, *scales = keys ? c.ks : c.vs;
     // does token i of the window (i >= 0) continue the run of the one before?
-    auto cont = [&](int i) { return s[i + 1] > 0 && s[i] + 1 == s[i + 1] && s[i + 1] % c.P != 0; };
-    int rank = 0;
+    auto cont = [&](int i) { return s[i + 1] > 0 && s[i] + 1 == s[i + 1] && s[i + 1] % P != 0; };
     for (int w0 = 0; w0 < window; w0 += 32) {
         const int i = w0 + lane;
         unsigned lead = __ballot_sync(0xffffffffu, i < window && s[i + 1] >= 0 && !cont(i));
-        while (lead) {
+        for (; lead; lead &= lead - 1) {
             const int at = w0 + __ffs(lead) - 1;
-            lead &= lead - 1;
-            if (rank++ % kAppendWarps != warp) continue;
             // the run's length: continuations that follow, at most P - 1
             const unsigned c0 = __ballot_sync(0xffffffffu, !(at + 1 + lane < window + 64 && cont(at + 1 + lane)));
             const unsigned c1 = __ballot_sync(0xffffffffu, !(at + 33 + lane < window + 64 && cont(at + 33 + lane)));
             const int len = 1 + (c0 ? __ffs(c0) - 1 : 32 + (c1 ? __ffs(c1) - 1 : 32));
-            const int slot = s[at + 1], page = slot / c.P, o0 = slot % c.P;
-            const uint16_t *x0 = x + (long long)(t0 + at) * stride + h * D;
-            // largest magnitude of the run (NaN passes over)
-            float am = 0.f;
-            for (int u = lane; u < len * (D / 8); u += 32) {
-                float f[8];
-                bf16x8(__ldg(reinterpret_cast<const uint4 *>(x0 + (long long)(u / (D / 8)) * stride) + u % (D / 8)), f);
-#pragma unroll
-                for (int i2 = 0; i2 < 8; i2++) am = fmaxf(am, fabsf(f[i2]));
-            }
-#pragma unroll
-            for (int m = 16; m; m >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, m));
+            const int slot = s[at + 1], page = slot / P, o0 = slot % P;
             const size_t ph = (size_t)page * c.KVH + h;
-            const int need = kv8_exponent(am) + 127, old = o0 ? scales[ph] : 0;
-            const int now = max(need, old);
+            const uint16_t *row = x + (long long)(t0 + at) * stride;
+            uint8_t *base = codes + ph * (size_t)(P * D);
+            const int byte = len == P ? append_page<D, P>(keys, row, stride, base, turn[tid >> 5], lane)
+                                      : append_run<D, P>(keys, row, stride, base, o0, len, o0 ? scales[ph] : 0, lane);
             __syncwarp();
-            if (lane == 0) scales[ph] = (uint8_t)now;
-            const float inv = pow2i(127 - now), shrink = pow2i(old - now);
-            const bool again = o0 > 0 && now > old;
-            uint8_t *base = codes + ph * (size_t)(c.P * D);
-            if (keys) {
-                if (again)
-                    for (int u = lane; u < o0 * (D / 16); u += 32) {
-                        uint4 *p = reinterpret_cast<uint4 *>(base + (size_t)(u % (D / 16)) * c.P * 16 + u / (D / 16) * 16);
-                        uint4 w = *p;
-                        w.x = requant4(w.x, shrink), w.y = requant4(w.y, shrink);
-                        w.z = requant4(w.z, shrink), w.w = requant4(w.w, shrink);
-                        *p = w;
-                    }
-                for (int u = lane; u < len * (D / 16); u += 32) {
-                    const int j = u / (D / 16), ch = u % (D / 16);
-                    const uint4 *src = reinterpret_cast<const uint4 *>(x0 + (long long)j * stride) + 2 * ch;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int hf = 0; hf < 2; hf++) {
-                        float f[8];
-                        bf16x8(__ldg(src + hf), f);
-#pragma unroll
-                        for (int q = 0; q < 2; q++)
-                            w[2 * hf + q] = f32x2_to_e4m3(f[4 * q] * inv, f[4 * q + 1] * inv) |
-                                            (f32x2_to_e4m3(f[4 * q + 2] * inv, f[4 * q + 3] * inv) << 16);
-                    }
-                    *reinterpret_cast<uint4 *>(base + (size_t)ch * c.P * 16 + (o0 + j) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            } else {
-                // (16 tokens, 2 dims) at a time: bytes of tokens outside the
-                // run keep their codes (re-rounded if the exponent rose)
-                const int g0 = again ? 0 : o0 / 16, g1 = (o0 + len + 15) / 16;
-                for (int u = lane; u < (g1 - g0) * (D / 2); u += 32) {
-                    const int gr = g0 + u / (D / 2), d = 2 * (u % (D / 2));
-                    uint4 *p = reinterpret_cast<uint4 *>(base + (size_t)gr * D * 16 + d * 16);
-                    uint32_t w[8];
-                    const bool whole = gr * 16 >= o0 && gr * 16 + 16 <= o0 + len;
-                    if (!whole) {
-                        const uint4 a = p[0], b = p[1];
-                        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-                        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        // tokens 2q, 2q + 1, 8 + 2q, 9 + 2q of the group in byte order
-                        uint32_t n0 = whole ? 0 : w[q], n1 = whole ? 0 : w[4 + q];
-                        const uint32_t r0 = again ? requant4(n0, shrink) : n0, r1 = again ? requant4(n1, shrink) : n1;
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const int tok = gr * 16 + 2 * q + (e & 1) + 8 * (e >> 1), sh = 8 * e;
-                            if (tok >= o0 && tok < o0 + len) {
-                                const uint32_t pr = __ldg(reinterpret_cast<const uint32_t *>(x0 + (long long)(tok - o0) * stride + d));
-                                const uint32_t cd = f32x2_to_e4m3(__uint_as_float(pr << 16) * inv, __uint_as_float(pr & 0xFFFF0000u) * inv);
-                                n0 = (n0 & ~(0xFFu << sh)) | ((cd & 0xFFu) << sh);
-                                n1 = (n1 & ~(0xFFu << sh)) | ((cd >> 8) << sh);
-                            } else if (again && tok < o0) {
-                                n0 = (n0 & ~(0xFFu << sh)) | (r0 & (0xFFu << sh));
-                                n1 = (n1 & ~(0xFFu << sh)) | (r1 & (0xFFu << sh));
-                            }
-                        }
-                        w[q] = n0, w[4 + q] = n1;
-                    }
-                    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-            }
+            if (lane == 0) scales[ph] = (uint8_t)byte;
         }
     }
+}
+
+template <int D, int P>
+cudaError_t append_launch(const Kv8Cache &c, const uint16_t *k, const uint16_t *v, long long k_stride, long long v_stride,
+                          const int32_t *slots, int n, cudaStream_t st) {
+    // Prompts: a page of tokens a CTA, as a rule one run.  Few tokens: each its
+    // own run as a rule, two a warp keep a decode step's launch to one wave.
+    const int window = n <= 1024 ? 2 : P;
+    const dim3 grid((n + window - 1) / window, (2 * c.KVH + kAppendWarps - 1) / kAppendWarps), block(kAppendWarps * 32);
+    return launch_pdl(moe_kv8_append_kernel<D, P>, grid, block, 0, st, c, k, v, k_stride, v_stride, slots, n, window);
+}
+template <int D>
+cudaError_t append_size(const Kv8Cache &c, const uint16_t *k, const uint16_t *v, long long k_stride, long long v_stride,
+                        const int32_t *slots, int n, cudaStream_t st) {
+    return c.P == 16   ? append_launch<D, 16>(c, k, v, k_stride, v_stride, slots, n, st)
+           : c.P == 32 ? append_launch<D, 32>(c, k, v, k_stride, v_stride, slots, n, st)
+                       : append_launch<D, 64>(c, k, v, k_stride, v_stride, slots, n, st);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -168,11 +254,7 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 cudaError_t launch_kv8_append(const Kv8Cache &c, const uint16_t *k, const uint16_t *v, long long k_stride,
                               long long v_stride, const int32_t *slots, int n, cudaStream_t st) {
-    const int window = 8;
-    const dim3 grid((n + window - 1) / window, c.KVH, 2), block(kAppendWarps * 32);
-    if (c.D == 64)
-        return launch_pdl(moe_kv8_append_kernel<64>, grid, block, 0, st, c, k, v, k_stride, v_stride, slots, n, window);
-    return launch_pdl(moe_kv8_append_kernel<128>, grid, block, 0, st, c, k, v, k_stride, v_stride, slots, n, window);
+    return c.D == 64 ? append_size<64>(c, k, v, k_stride, v_stride, slots, n, st) : append_size<128>(c, k, v, k_stride, v_stride, slots, n, st);
 }
 
 struct moe_kv8 {

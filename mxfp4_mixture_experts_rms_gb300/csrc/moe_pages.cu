@@ -2,154 +2,281 @@
 // GPU from request lengths: finished requests' pages go back to the free
 // list, the others take what their new tokens need, and every new token gets
 // its slot and position.
+//
+// Three prefix sums over the requests (entries that finished ones give back,
+// pages that the others take, new tokens) make everything flat: entry e,
+// page p and token t each find their request by binary search, and the page
+// of a token is either in the table or at a known place of the free list, so
+// that tables and slots are written side by side.  What remains in order is
+// the free list: entries are compacted (those below 0 are none) and pushed
+// before any is popped.
+//
+// A small step is one kernel of one CTA, bound by its chain of dependent
+// loads; a large one is a cluster that pushes, then a grid that writes tables
+// and slots, whose CTAs each repeat the prefix sums (two loads a request from
+// L2) rather than wait for them through memory.
 #include "moe_common.cuh"
 #include "../../include/moe.h"
 
+#include <cooperative_groups.h>
+
+#include <algorithm>
 #include <climits>
+
+namespace cg = cooperative_groups;
 
 namespace {
 
 constexpr int kMaxSeqs = 4096;
-constexpr int kThreads = 1024;
-constexpr int kPer = kMaxSeqs / kThreads;  // requests a thread scans
+constexpr int kPushThreads = 512, kSmallThreads = 256;
+constexpr int kFillThreads = 256;
+constexpr int kCluster = 8;
+// One CTA does it all up to so many requests, tokens and table entries; above,
+// the second kernel's parallel writes gain more than its launch costs.
+constexpr int kSmallSeqs = 1024, kSmallTokens = 8192, kSmallTable = 65536;
 
 struct PagesArgs {
-    int P, n, width, cap, max_tokens;
+    int P, shift, n, width, cap, max_tokens;   // shift: log2 P where P is a power of two, else -1
     const int32_t *cached, *fresh;
     int32_t *table, *free_pages;
     const int32_t *counts;
     int32_t *counts_out, *starts, *lens, *slots, *positions;
 };
 
-// Exclusive block scan of three values a thread, and their sums.
-struct Sum3 {
+// Exclusive sums over requests: entries given back (those below 0 among them),
+// pages wanted, new tokens.
+struct Sums {
     int back, want;
     long long tok;
 };
-__device__ __forceinline__ Sum3 operator+(Sum3 a, Sum3 b) { return {a.back + b.back, a.want + b.want, a.tok + b.tok}; }
-__device__ __forceinline__ Sum3 shfl_up(Sum3 v, int d) {
-    return {__shfl_up_sync(0xffffffffu, v.back, d), __shfl_up_sync(0xffffffffu, v.want, d),
-            __shfl_up_sync(0xffffffffu, v.tok, d)};
-}
-__device__ Sum3 block_scan(Sum3 v, Sum3 *part, Sum3 &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sum3 inc = v;
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.back + b.back, a.want + b.want, a.tok + b.tok}; }
+__device__ __forceinline__ Sums operator-(Sums a, Sums b) { return {a.back - b.back, a.want - b.want, a.tok - b.tok}; }
+__device__ __forceinline__ Sums warp_inclusive(Sums v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const Sum3 o = shfl_up(inc, d);
-        if (lane >= d) inc = inc + o;
+        const Sums o = {__shfl_up_sync(0xffffffffu, v.back, d), __shfl_up_sync(0xffffffffu, v.want, d), __shfl_up_sync(0xffffffffu, v.tok, d)};
+        if (lane >= d) v = v + o;
     }
-    if (lane == 31) part[warp] = inc;
-    __syncthreads();
-    if (warp == 0) {
-        Sum3 w = part[lane], own = w;
-        for (int d = 1; d < 32; d <<= 1) {
-            const Sum3 o = shfl_up(w, d);
-            if (lane >= d) w = w + o;
-        }
-        part[lane] = {w.back - own.back, w.want - own.want, w.tok - own.tok};
-        if (lane == 31) part[32] = w;
-    }
-    __syncthreads();
-    total = part[32];
-    const Sum3 base = part[warp];
-    return {base.back + inc.back - v.back, base.want + inc.want - v.want, base.tok + inc.tok - v.tok};
+    return v;
 }
 
-__device__ __forceinline__ int pages_of(long long tokens, const PagesArgs &a) {
-    return (int)min((tokens + a.P - 1) / a.P, (long long)a.width);
+// x / P for x below 2^32: lengths and their sums are
+__device__ __forceinline__ unsigned page_of(unsigned x, const PagesArgs &a) { return a.shift >= 0 ? x >> a.shift : x / (unsigned)a.P; }
+// pages of so many tokens, at most a row of the table
+__device__ __forceinline__ int pages_of(unsigned tokens, const PagesArgs &a) {
+    return tokens ? (int)min(page_of(tokens - 1, a) + 1, (unsigned)a.width) : 0;
 }
 __device__ __forceinline__ int clamp_int(long long v) { return (int)min(v, (long long)INT_MAX); }
 
-__global__ void __launch_bounds__(kThreads) moe_pages_kernel(const PagesArgs a) {
-    __shared__ Sum3 part[33];
-    // off: a finished request's page count, then the index of its first page
-    // among those given back; of another request, among those taken
-    __shared__ int off[kMaxSeqs];
-    __shared__ int start[kMaxSeqs + 1];
+// Shared memory: [n] each, exclusive sums over the requests before.
+struct Requests {
+    int *have, *fresh, *back, *want, *start;
+    __device__ Requests(int *s, int n) : have(s), fresh(s + n), back(s + 2 * n), want(s + 3 * n), start(s + 4 * n) {}
+};
+
+template <int T>
+__device__ Sums scan_requests(const PagesArgs &a, const Requests &q, Sums *part) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n_free = min(max(a.counts[0], 0), a.cap);
-    // pages that finished requests give back (a warp a request; entries < 0 are none)
-    for (int b = warp; b < a.n; b += kThreads / 32) {
-        int c = 0;
-        if (a.fresh[b] < 0) {
-            const int held = pages_of(max(a.cached[b], 0), a);
-            for (int j0 = 0; j0 < held; j0 += 32)
-                c += __popc(__ballot_sync(0xffffffffu, j0 + lane < held && a.table[(size_t)b * a.width + j0 + lane] >= 0));
-        }
-        if (lane == 0) off[b] = c;
-    }
+    for (int b = tid; b < a.n; b += T) q.have[b] = max(a.cached[b], 0), q.fresh[b] = a.fresh[b];
     __syncthreads();
-    auto counts_of = [&](int b) {
-        const int have = max(a.cached[b], 0), f = a.fresh[b];
-        Sum3 v = {0, 0, 0};
-        if (f < 0) v.back = off[b];
-        else v.want = pages_of((long long)have + f, a) - pages_of(have, a), v.tok = f;
-        return v;
+    const int per = (a.n + T - 1) / T, b0 = min(tid * per, a.n), b1 = min(b0 + per, a.n);
+    auto of = [&](int b) {
+        const int f = q.fresh[b], held = pages_of(q.have[b], a);
+        return f < 0 ? Sums{held, 0, 0} : Sums{0, pages_of((unsigned)q.have[b] + (unsigned)f, a) - held, f};
     };
-    Sum3 sum = {0, 0, 0};
-    const int b0 = tid * kPer, b1 = min(b0 + kPer, a.n);
-    for (int b = b0; b < b1; b++) sum = sum + counts_of(b);
-    Sum3 total, at = block_scan(sum, part, total);
+    Sums v = {0, 0, 0};
+    for (int b = b0; b < b1; b++) v = v + of(b);
+    const Sums inc = warp_inclusive(v);
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    const Sums mine = lane < T / 32 ? part[lane] : Sums{0, 0, 0}, upto = warp_inclusive(mine), before = upto - mine;
+    const Sums total = {__shfl_sync(0xffffffffu, upto.back, 31), __shfl_sync(0xffffffffu, upto.want, 31), __shfl_sync(0xffffffffu, upto.tok, 31)};
+    Sums at = inc - v;
+    at = at + Sums{__shfl_sync(0xffffffffu, before.back, warp), __shfl_sync(0xffffffffu, before.want, warp), __shfl_sync(0xffffffffu, before.tok, warp)};
     for (int b = b0; b < b1; b++) {
-        const Sum3 v = counts_of(b);
-        const int f = a.fresh[b];
-        off[b] = f < 0 ? at.back : at.want, start[b] = clamp_int(at.tok);
-        a.starts[b] = start[b];
-        a.lens[b] = f < 0 ? 0 : clamp_int((long long)max(a.cached[b], 0) + f);
-        at = at + v;
-    }
-    if (tid == 0) start[a.n] = a.starts[a.n] = clamp_int(total.tok);
-    __syncthreads();
-    for (int b = warp; b < a.n; b += kThreads / 32) {
-        if (a.fresh[b] >= 0) continue;
-        const int held = pages_of(max(a.cached[b], 0), a);
-        int to = n_free + off[b];
-        for (int j0 = 0; j0 < held; j0 += 32) {
-            const int id = j0 + lane < held ? a.table[(size_t)b * a.width + j0 + lane] : -1;
-            const unsigned m = __ballot_sync(0xffffffffu, id >= 0);
-            const int k = to + __popc(m & ((1u << lane) - 1));
-            if (id >= 0 && k < a.cap) a.free_pages[k] = id;
-            to += __popc(m);
-        }
+        q.back[b] = at.back, q.want[b] = at.want, q.start[b] = clamp_int(at.tok);
+        at = at + of(b);
     }
     __syncthreads();
-    const int n1 = min(n_free + total.back, a.cap);
-    for (int b = warp; b < a.n; b += kThreads / 32) {
-        const int f = a.fresh[b], have = max(a.cached[b], 0);
-        if (f <= 0) continue;
-        const int held = pages_of(have, a), w = pages_of((long long)have + f, a) - held;
-        for (int j = lane; j < w; j += 32) {
-            const int src = n1 - 1 - (off[b] + j);
-            a.table[(size_t)b * a.width + held + j] = src >= 0 ? a.free_pages[src] : -1;
-        }
+    return total;
+}
+
+// The last request whose sum is at most x (the one that x lies in).
+__device__ __forceinline__ int request_of(const int *sum, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sum[mid] <= x) lo = mid;
+        else hi = mid;
     }
-    __syncthreads();
-    if (tid == 0) {
-        const int left = n1 - total.want;
-        a.counts_out[0] = max(left, 0);
-        a.counts_out[1] = max(-left, 0);
+    return lo;
+}
+
+// Tables of wanted pages first, first + step, .. and slots and positions of
+// tokens likewise, four neighbours at a time.  n1: free pages before the pops.
+__device__ __forceinline__ void fill(const PagesArgs &a, const Requests &q, const Sums &total, int n1, int first, int step) {
+    for (int p = first; p < total.want; p += step) {
+        const int b = request_of(q.want, a.n, p), src = n1 - 1 - p;
+        a.table[(size_t)b * a.width + pages_of(q.have[b], a) + (p - q.want[b])] = src >= 0 ? a.free_pages[src] : -1;
     }
-    for (int t = tid; t < a.max_tokens; t += kThreads) {
-        int slot = -1, pos = -1;
-        if (t < start[a.n]) {
-            int lo = 0, hi = a.n;  // the last request that starts at or before t
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (start[mid] <= t) lo = mid;
-                else hi = mid;
+    const int tokens = clamp_int(total.tok), most = INT_MAX / a.P;   // pages whose slots are 32-bit
+    const bool wide = (((uintptr_t)a.slots | (uintptr_t)a.positions) & 15u) == 0;
+    for (long long t0 = 4ll * first; t0 < a.max_tokens; t0 += 4ll * step) {
+        int slot[4], pos[4], b = t0 < tokens ? request_of(q.start, a.n, (int)t0) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int t = (int)min(t0 + e, (long long)INT_MAX);
+            slot[e] = pos[e] = -1;
+            if (t >= tokens || t >= a.max_tokens) continue;
+            while (b + 1 < a.n && q.start[b + 1] <= t) b++;
+            const unsigned x = (unsigned)q.have[b] + (unsigned)(t - q.start[b]), j = page_of(x, a);
+            pos[e] = (int)min(x, (unsigned)INT_MAX);
+            if (j >= (unsigned)a.width) continue;
+            const int held = pages_of(q.have[b], a);
+            int page = -1;
+            if ((int)j < held) {
+                page = a.table[(size_t)b * a.width + j];
+            } else {
+                const int src = n1 - 1 - (q.want[b] + (int)j - held);
+                if (src >= 0) page = a.free_pages[src];
             }
-            const long long p = (long long)max(a.cached[lo], 0) + (t - start[lo]);
-            pos = clamp_int(p);
-            if (p / a.P < a.width) {
-                const int page = a.table[(size_t)lo * a.width + p / a.P];
-                if (page >= 0 && page < INT_MAX / a.P) slot = page * a.P + (int)(p % a.P);
+            if (page >= 0 && page < most) slot[e] = page * a.P + (int)(x - j * a.P);
+        }
+        if (wide && t0 + 4 <= a.max_tokens) {
+            *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            if (a.positions) *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+            for (int e = 0; e < 4 && t0 + e < a.max_tokens; e++) {
+                a.slots[t0 + e] = slot[e];
+                if (a.positions) a.positions[t0 + e] = pos[e];
             }
         }
-        a.slots[t] = slot;
-        if (a.positions) a.positions[t] = pos;
     }
+}
+
+// The pushes, and what there is one of; SMALL (one CTA): all of it.
+template <bool SMALL, int T>
+__global__ void __launch_bounds__(T) moe_pages_push_kernel(const PagesArgs a) {
+    extern __shared__ int smem[];
+    __shared__ Sums part[T / 32];
+    __shared__ int wsum[T / 32], told[kCluster], s_base;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int rank = 0, C = 1;
+    if (!SMALL) rank = (int)cg::this_cluster().block_rank(), C = (int)cg::this_cluster().num_blocks();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (after the wait: the second kernel reads the request lengths before its own)
+    asm volatile("griddepcontrol.launch_dependents;");
+    const Requests q(smem, a.n);
+    const int n_free = min(max(a.counts[0], 0), a.cap);
+    const Sums total = scan_requests<T>(a, q, part);
+    // this CTA's entries, in order; kPer neighbours a thread at a time
+    constexpr int kPer = 4;
+    const int e0 = (int)((long long)total.back * rank / C), e1 = (int)((long long)total.back * (rank + 1) / C);
+    auto load = [&](int x0, int (&id)[kPer]) {   // and how many are there
+        int c = 0, b = x0 < e1 ? request_of(q.back, a.n, x0) : 0;
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            id[i] = -1;
+            if (x0 + i >= e1) continue;
+            while (b + 1 < a.n && q.back[b + 1] <= x0 + i) b++;
+            id[i] = a.table[(size_t)b * a.width + (x0 + i - q.back[b])];
+            c += id[i] >= 0;
+        }
+        return c;
+    };
+    int base = n_free, all = 0;
+    if (C > 1) {
+        // entries that are there in each CTA's share
+        int c = 0, id[kPer];
+        for (int x = e0 + kPer * tid; x < e1; x += kPer * T) c += load(x, id);
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) wsum[warp] = c;
+        __syncthreads();
+        c = __reduce_add_sync(0xffffffffu, lane < T / 32 ? wsum[lane] : 0);
+        if (tid < C) cg::this_cluster().map_shared_rank(told, tid)[rank] = c;
+        cg::this_cluster().sync();
+        for (int x = 0; x < C; x++) {
+            if (x < rank) base += told[x];
+            all += told[x];
+        }
+    }
+    if (tid == 0) s_base = base;
+    __syncthreads();
+    for (int x = e0; x < e1; x += kPer * T) {
+        int id[kPer], c = load(x + kPer * tid, id), inc = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        const int ws = lane < T / 32 ? wsum[lane] : 0;
+        const int sum = __reduce_add_sync(0xffffffffu, ws);
+        int at = s_base + inc - c + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (id[i] >= 0) {
+                if (at < a.cap) a.free_pages[at] = id[i];
+                at++;
+            }
+        __syncthreads();
+        if (tid == 0) s_base += sum;
+        __syncthreads();
+    }
+    const int n1 = min(C > 1 ? n_free + all : s_base, a.cap);
+    if (rank == 0) {
+        for (int b = tid; b < a.n; b += T) {
+            a.starts[b] = q.start[b];
+            a.lens[b] = q.fresh[b] < 0 ? 0 : clamp_int((long long)q.have[b] + q.fresh[b]);
+        }
+        if (tid == 0) {
+            a.starts[a.n] = clamp_int(total.tok);
+            const int left = n1 - total.want;
+            a.counts_out[0] = max(left, 0);
+            a.counts_out[1] = max(-left, 0);
+        }
+    }
+    if (SMALL) fill(a, q, total, n1, tid, T);
+}
+
+__global__ void __launch_bounds__(kFillThreads) moe_pages_fill_kernel(const PagesArgs a) {
+    extern __shared__ int smem[];
+    __shared__ Sums part[kFillThreads / 32];
+    const Requests q(smem, a.n);
+    const Sums total = scan_requests<kFillThreads>(a, q, part);   // (the first kernel has waited for what this reads)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    // the first kernel left counts_out = (free pages left, or 0; pages missing, or 0)
+    const int n1 = a.counts_out[0] - a.counts_out[1] + total.want;
+    fill(a, q, total, n1, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads);
+}
+
+cudaError_t pages_launch(const PagesArgs &a, cudaStream_t st) {
+    const size_t smem = (size_t)a.n * 20;
+    if (a.n <= kSmallSeqs && a.max_tokens <= kSmallTokens && (long long)a.n * a.width <= kSmallTable)
+        return launch_pdl(moe_pages_push_kernel<true, kSmallThreads>, dim3(1), dim3(kSmallThreads), smem, st, a);
+    static PerDevice<bool> push_opted, fill_opted;
+    MOE_CUDA_TRY(smem_optin_once(moe_pages_push_kernel<false, kPushThreads>, push_opted));
+    MOE_CUDA_TRY(smem_optin_once(moe_pages_fill_kernel, fill_opted));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kPushThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, moe_pages_push_kernel<false, kPushThreads>, a));
+    // four tokens a thread, at most four CTAs an SM of a 152-SM GPU
+    const long long want = (a.max_tokens + 4ll * kFillThreads - 1) / (4ll * kFillThreads);
+    const int grid = (int)std::min(std::max(want, 32ll), 608ll);
+    return launch_pdl(moe_pages_fill_kernel, dim3(grid), dim3(kFillThreads), smem, st, a);
 }
 
 }  // namespace
@@ -172,8 +299,12 @@ extern "C" int moe_pages_assign(int page_size, int n_seqs, const int32_t *cached
         return moe_fail_status(MOE_EINVAL, "pointers must be 4-byte aligned");
     if (n_seqs && cached < lens + n_seqs && lens < cached + n_seqs)
         return moe_fail_status(MOE_EINVAL, "lens must not overlap cached");
-    PagesArgs a{page_size, n_seqs, table_width, capacity, max_tokens, cached, fresh, table, free_pages, counts, counts_out,
+    int shift = -1;
+    if ((page_size & (page_size - 1)) == 0)
+        for (shift = 0; (1 << shift) < page_size; shift++) {
+        }
+    PagesArgs a{page_size, shift, n_seqs, table_width, capacity, max_tokens, cached, fresh, table, free_pages, counts, counts_out,
                 starts, lens, slots, positions};
-    const cudaError_t e = launch_pdl(moe_pages_kernel, dim3(1), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = pages_launch(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : moe_fail_status(MOE_ECUDA, "moe_pages_assign: %s", cudaGetErrorString(e));
 }
