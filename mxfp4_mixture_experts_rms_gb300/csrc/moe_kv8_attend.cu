@@ -40,15 +40,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Warps, and units in each one's ring.  What bounds the kernel is latency at
 // the instructions of a unit, so as many warps as registers and the 227 KB of
 // shared memory allow come before a deeper ring: a warp's own copies are in
-// flight while the others compute.
+// flight while the others compute (8 rows of D = 64, 16 x 1024 tokens: 16
+// warps with one unit each 17.3 us, 11 with two 23.4; 32 x 16384 tokens, the
+// only side where the ring gained: 101 and 96).
 template <int D, bool TOP>
 struct Few {
-#ifndef FW
-#define FW 16
-#define FS 1
-#endif
-    static constexpr int kWarps = D == 64 ? (TOP ? 10 : FW) : (TOP ? 8 : 10);
-    static constexpr int kStages = D == 64 ? (TOP ? 2 : FS) : 1;
+    static constexpr int kWarps = D == 64 ? (TOP ? 10 : 16) : (TOP ? 8 : 10);
+    static constexpr int kStages = D == 64 ? (TOP ? 2 : 1) : 1;
     static constexpr int kStage = 2 * kTile * D;   // bytes of one unit: keys, values
     static constexpr int kPad = D + 8;             // floats of a partial's row: 64-bit stores on distinct banks
 };

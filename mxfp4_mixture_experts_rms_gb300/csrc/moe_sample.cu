@@ -8,22 +8,28 @@
 // of theirs, min-p of those the ones with w >= min_p.  Nothing is sorted: the
 // kept set is "logit above T, and the first r tokens with logit T", so T and r
 // are looked for, by count for top-k and by weight for top-p:
-//  1. a histogram of 512 bins of equal width in log2 w (24 powers of two; what
-//     is below is not counted) finds the bin that holds T; counts are exact,
-//     weights here 32-bit fixed point relative to the bin's upper edge;
-//  2. one more pass sums what lies above that bin exactly and lists the bin's
-//     logits;
+//  1. a histogram over the weights' leading bits (16 bins an octave, 32
+//     octaves; what is below is not counted) finds the bin that holds T; a
+//     weight adds its mantissa, so bins hold their weights in units of their
+//     octave;
+//  2. one more pass sums what lies above that bin and lists the bin's logits;
 //  3. the list is cut by histograms over the logits' order-preserving 32-bit
 //     keys until one key is left.
-// Where a bin's list does not fit, where T lies below the 24 powers of two, or
-// where step 1's rounding named a neighbour of T's bin, step 3 runs over the
-// row instead.  Weights are summed as whole multiples of 2^-40, so sums do not
-// depend on their order.
+// A top-k of few tokens lists all of them in step 2 instead, and a CTA ranks
+// the list by comparing each with each: top-k, top-p and the choice itself
+// need nothing more of the row.  Where a bin's list does not fit, step 3 counts
+// the bin's keys in the row, taking a sub-bin's weight as its count times one
+// of its weights; then, and where step 1's rounding named a neighbour of T's
+// bin, T moves by single keys until the exact sums hold.  A T below the 32
+// octaves is looked for by exact weights over the row.  Sums are fp32 over a
+// lane's logits and whole multiples of 2^-40 above that, so they do not depend
+// on their order.
 //
 // A row is a cluster's: each CTA keeps its part in shared memory (read from
 // memory once) where it fits, and meets the others through distributed shared
-// memory.  Bound by HBM for large batches in principle (2 or 4 bytes a
-// logit); what it spends its time on is the instructions of the passes.
+// memory.  Large batches are bound by the passes' instructions (about eleven a
+// logit in step 1, three where a pass skips it), single rows by the cluster's
+// meetings, about half a microsecond each.
 #include "moe_common.cuh"
 #include "../../include/moe.h"
 
@@ -37,10 +43,28 @@ namespace cg = cooperative_groups;
 namespace {
 
 typedef unsigned long long u64;
+// Another CTA's shared memory, by 32-bit addresses.
+__device__ __forceinline__ uint32_t remote(const void *p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t remote_u32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ u64 remote_u64(uint32_t at) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
 constexpr int kBins = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 2048;           // keys listed by a CTA
-constexpr float kSpan = 24.f;         // powers of two that the first histogram covers
+constexpr int kKeys = 2048;           // listed keys of a row that a CTA has room for
+constexpr int kRank = 512;            // tokens that are ranked by comparing each with each
+constexpr int kBinShift = 19;         // a weight's bits above: exponent and four bits of mantissa
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct SampleArgs {
@@ -52,7 +76,7 @@ struct SampleArgs {
     const float *top_p, *min_p, *u;
     int32_t *ids;
     int seg;         // 16-byte vectors of a row's part
-    float bin_unit;  // weight units of the first histogram: 2^30 / (the power of two <= V)
+    int drop;        // mantissa bits that a sum of V weights in 32 bits has no room for
 };
 
 // Larger logit, larger key; NaN and -inf (never chosen): 0.
@@ -116,12 +140,19 @@ struct Row {
         }
     }
     __device__ __forceinline__ uint4 vec(int v) const { return RES ? s[v - c0] : fetch(v); }
-    // f(logits, first one's index) for the warp's vectors, a lane a vector; in order of index
+    // f(logits, first one's index) for the warp's vectors, a lane a vector; in
+    // order of index; the next vector is read ahead
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32) {
+        int v = v0 + (threadIdx.x & 31);
+        if (v >= v1) return;
+        uint4 next = vec(v);
+#pragma unroll 1
+        for (; v < v1; v += 32) {
+            const uint4 w = next;
+            if (v + 32 < v1) next = vec(v + 32);
             float x[VE];
-            values(vec(v), x);
+            values(w, x);
             f(x, v * VE - off);
         }
     }
@@ -132,9 +163,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     typedef Row<BF16, RES, NT> R;
     constexpr int VE = R::VE, NW = NT / 32;
     extern __shared__ __align__(16) uint4 data[];
-    __shared__ u64 hist[kBins];
+    __shared__ u64 hist[kBins];         // (also: weights of the ranked tokens)
     __shared__ uint32_t hist32[kBins];
-    __shared__ uint32_t list[kList];
+    __shared__ uint2 list[kList];       // key, index
+    __shared__ uint32_t keys[kKeys];    // all CTAs' listed keys (or the ranked tokens' keys and indices)
+    uint2 *const all = reinterpret_cast<uint2 *>(keys);
+    __shared__ int ranks[kRank];
     __shared__ Told told[2][kMaxCluster];
     __shared__ u64 part[NW], s_above, wmass[NW];
     __shared__ uint32_t red[NW], s_lo, s_hi;
@@ -152,9 +186,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         d.off = (int)(at & 15) / (BF16 ? 2 : 4);
         d.V = a.V;
         d.s = data;
-        const int all = (d.off + a.V + VE - 1) / VE;
-        d.c0 = min(rank * a.seg, all);
-        const int c1 = min(d.c0 + a.seg, all), per = (c1 - d.c0 + NW - 1) / NW;
+        const int vecs = (d.off + a.V + VE - 1) / VE;
+        d.c0 = min(rank * a.seg, vecs);
+        const int c1 = min(d.c0 + a.seg, vecs), per = (c1 - d.c0 + NW - 1) / NW;
         d.v0 = min(d.c0 + warp * per, c1), d.v1 = min(d.v0 + per, c1);
     }
     const float t = a.temperature ? fminf(a.temperature[row], 3.402823466e38f) : 1.f;
@@ -171,21 +205,24 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
 
     // the row's largest logit, while its part comes in
     uint32_t km = 0;
-    for (int v = d.v0 + lane; v < d.v1; v += 128) {   // four vectors a lane on their way
-        uint4 w[4];
+    {
+        float m = -INFINITY;
+        for (int v = d.v0 + lane; v < d.v1; v += 128) {   // four vectors a lane on their way
+            uint4 w[4];
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-            if (v + 32 * q < d.v1) w[q] = d.fetch(v + 32 * q);
+            for (int q = 0; q < 4; q++)
+                if (v + 32 * q < d.v1) w[q] = d.fetch(v + 32 * q);
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-            if (v + 32 * q < d.v1) {
-                if (RES) data[v + 32 * q - d.c0] = w[q];
-                float x[VE], m = -INFINITY;
-                R::values(w[q], x);
+            for (int q = 0; q < 4; q++)
+                if (v + 32 * q < d.v1) {
+                    if (RES) data[v + 32 * q - d.c0] = w[q];
+                    float x[VE];
+                    R::values(w[q], x);
 #pragma unroll
-                for (int e = 0; e < VE; e++) m = fmaxf(m, x[e]);   // NaN passes over
-                km = max(km, order_key(m));
-            }
+                    for (int e = 0; e < VE; e++) m = fmaxf(m, x[e]);   // NaN passes over
+                }
+        }
+        km = order_key(m);
     }
     km = __reduce_max_sync(0xffffffffu, km);
     if (lane == 0) red[warp] = km;
@@ -197,228 +234,385 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         if (rank == 0 && tid == 0) a.ids[row] = -1;
         return;
     }
-    const float top = key_logit(km), scale = kLog2e / t;
+    const float top = key_logit(km), scale = t > 0.f ? fminf(kLog2e / t, 1e30f) : 0.f;
+    // An infinite largest logit: then only infinite ones weigh anything.  A
+    // row of steep scale: differences first, so that 0 stays 0.  Else the
+    // weights are 2^(x scale - top scale), the constant rounded: one factor,
+    // within 2^-14 of 1, on all of them.
+    const bool endless = top == INFINITY, steep = !(fabsf(top * scale) < 1000.f);
+    const float shift_w = endless || steep ? 0.f : -top * scale;
+    auto weight = [&](float x) {
+        float w;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(steep ? (x - top) * scale : fmaf(x, scale, shift_w)));
+        return endless ? (x == top ? 1.f : 0.f) : w;
+    };
+    auto weights = [&](const float (&x)[VE], float (&w)[VE]) {
+        if (endless || steep) {
+#pragma unroll
+            for (int e = 0; e < VE; e++) w[e] = weight(x[e]);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < VE; e += 2) {
+            asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5}; fma.rn.f32x2 a, a, b, c; "
+                "mov.b64 {%0, %1}, a; }" : "=f"(w[e]), "=f"(w[e + 1]) : "f"(x[e]), "f"(x[e + 1]), "f"(scale), "f"(shift_w));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(w[e]));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(w[e + 1]));
+        }
+    };
+    const float least = mp * weight(top);   // min-p is relative to the largest weight
+    // 0 - the bin of weight 1 - downwards; NaN is never asked for
+    auto bin_of = [](float w) { return max((0x3F800000 >> kBinShift) - (int)(__float_as_uint(w) >> kBinShift), 0); };
+    auto fixed_sum = [](float sum) { return (u64)(sum * 0x1p40f); };
+    // block-wide sum
+    auto total = [&](u64 v) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        __syncthreads();
+        if (lane == 0) part[warp] = v;
+        __syncthreads();
+        v = lane < NW ? part[lane] : 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    // block-wide: the first bin whose inclusive sum of h (one a thread, kBins of them) reaches goal
+    auto find = [&](u64 h, u64 goal) {
+        u64 inc = h;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31 && warp < kBins / 32) part[warp] = inc;
+        if (tid == 0) s_bin = -1;
+        __syncthreads();
+        if (tid < kBins) {
+            u64 w = lane < warp ? part[lane] : 0;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            inc += w;
+            if (inc >= goal && inc - h < goal) s_bin = tid, s_above = inc - h;
+        }
+        __syncthreads();
+        return s_bin;
+    };
     // kept: keys above T, and the first r tokens whose key is T
     uint32_t T = 0;
     u64 r = 0;
-    if (!(t > 0.f)) {
-        T = km, r = 1;
-    } else {
-        auto log2w = [&](float x) { return x == top ? 0.f : (x - top) * scale; };
-        auto weight = [&](float x) {
-            float w;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(log2w(x)));
-            return w;
-        };
-        constexpr float kPerBin = kSpan / kBins;
-        auto bin_of = [&](float x) { return log2w(x) * (-1.f / kPerBin); };   // truncated: 0 holds the largest
-        // block-wide: the first bin whose inclusive sum of h (one a thread, kBins of them) reaches goal
-        auto find = [&](u64 h, u64 goal) {
-            u64 inc = h;
+    if (!(t > 0.f)) T = km, r = 1;
+    for (int stage = 0; stage < 2 && t > 0.f; stage++) {
+        const bool by_weight = stage == 1;
+        if (by_weight ? !(p < 1.f) : !(k > 0 && k < a.V)) continue;
+        const float over = T ? key_logit(T) : -INFINITY;   // what top-k left lies above, and r tokens at it
+        // 1. the histogram, and the weight of all
+        __syncthreads();
+        for (int b = tid; b < kBins; b += NT) hist32[b] = 0;
+        __syncthreads();
+        float sum = 0.f;
+        const uint32_t half = (1u << a.drop) >> 1;
+        d.each([&](float (&x)[VE], int) {
+            float w[VE];
+            weights(x, w);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
+            for (int e = 0; e < VE; e++) {
+                const bool in = x[e] > over;
+                const int b = bin_of(w[e]);
+                sum += in ? w[e] : 0.f;
+                if (in && b < kBins) atomicAdd(&hist32[b], by_weight ? (((__float_as_uint(w[e]) & 0x7FFFFFu) | 0x800000u) + half) >> a.drop : 1u);
             }
-            if (lane == 31 && warp < kBins / 32) part[warp] = inc;
-            if (tid == 0) s_bin = -1;
-            __syncthreads();
-            if (tid < kBins) {
-                for (int w = 0; w < warp; w++) inc += part[w];
-                if (inc >= goal && inc - h < goal) s_bin = tid, s_above = inc - h;
+        });
+        u64 goal = (u64)k, everything = 0;
+        tell({0, 0, 0, by_weight ? total(fixed_sum(sum)) : 0});   // and the histograms are there
+        if (by_weight) {
+            const u64 at_T = T ? fixed40(weight(key_logit(T))) : 0;
+            for (int c = 0; c < C; c++) everything += told[turn][c].sum;
+            goal = max((u64)ceil((double)fmaxf(p, 0.f) * (double)(everything + r * at_T)), (u64)1);
+            if (goal > everything && T) {   // among the tokens at T
+                if (at_T) r = min(r, (goal - everything + at_T - 1) / at_T);
+                cl.sync();                  // the histograms are read no more
+                continue;
             }
-            __syncthreads();
-            return s_bin;
-        };
-        // block-wide sum
-        auto total = [&](u64 v) {
+        }
+        u64 h = 0;
+        if (tid < kBins) {
 #pragma unroll
-            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            for (int c = 0; c < kMaxCluster; c++)
+                if (c < C) h += remote_u32(remote(hist32 + tid, c));
+            // mantissas of bins in one octave have one unit: 2^(drop - 23 - octave), here of 2^-40
+            const int shift = 40 - 23 + a.drop + (int)(((0x3F800000u >> kBinShift) - (unsigned)tid) >> (23 - kBinShift)) - 127;
+            if (by_weight) h = shift >= 0 ? h << shift : h >> -shift;
+        }
+        int bin = find(h, goal);
+        // 2. what lies above the bin, and the bin's keys; few tokens: all of them
+        u64 above = 0;
+        uint32_t lo = 1, hi = km;   // T is among these keys
+        if (bin >= 0) {
+            if (tid == bin) s_n = (int)min(s_above + h, (u64)INT_MAX);   // by count: tokens up to the bin
             __syncthreads();
-            if (lane == 0) part[warp] = v;
+            const bool few = !by_weight && s_n <= kRank;
             __syncthreads();
-            v = 0;
-            for (int w = 0; w < NW; w++) v += part[w];
-            return v;
-        };
-        for (int stage = 0; stage < 2; stage++) {
-            const bool by_weight = stage == 1;
-            if (by_weight ? !(p < 1.f) : !(k > 0 && k < a.V)) continue;
-            const float over = T ? key_logit(T) : -INFINITY;   // what top-k left lies above, and r tokens at it
-            // 1. the histogram, and the weight of all
+            if (tid == 0) s_n = 0, s_lo = 0xFFFFFFFFu, s_hi = 0;
             __syncthreads();
-            for (int b = tid; b < kBins; b += NT) hist32[b] = 0;
-            __syncthreads();
-            float sum = 0.f;
-            d.each([&](float (&x)[VE], int) {
+            float before = 0.f;
+            int count = 0;
+            d.each([&](float (&x)[VE], int i) {
+                float w[VE];
+                weights(x, w);
+                uint32_t take = 0;
 #pragma unroll
                 for (int e = 0; e < VE; e++) {
-                    if (!(x[e] > over)) continue;
-                    const float f = bin_of(x[e]);
-                    float w = 1.f;
-                    if (by_weight) {
-                        w = weight(x[e]);
-                        sum += w;
-                    }
-                    if (f < (float)(kBins - 1)) {
-                        const int b = (int)f;
-                        uint32_t add = 1;
-                        if (by_weight) {
-                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf((float)b, kPerBin, log2w(x[e]))));
-                            add = (uint32_t)fmaf(w, a.bin_unit, 0.5f);
-                        }
-                        atomicAdd(&hist32[b], add);
-                    }
+                    const int b = x[e] > over ? bin_of(w[e]) : kBins;
+                    before += b < bin ? w[e] : 0.f;
+                    count += b < bin;
+                    take |= (uint32_t)(few ? b <= bin : b == bin) << e;
+                }
+                while (take) {
+                    const int e = __ffs(take) - 1, at = atomicAdd(&s_n, 1);
+                    take &= take - 1;
+                    float v = x[0];
+#pragma unroll
+                    for (int q = 1; q < VE; q++) v = e == q ? x[q] : v;
+                    if (at < kList) list[at] = make_uint2(order_key(v), i + e);
                 }
             });
-            u64 goal = (u64)k, all = 0;
-            u64 mine = 0;
-            if (by_weight) {
-                // fp32 over a lane's logits, then whole multiples of 2^-40
-                mine = total((u64)(sum * 0x1p40f));
+            const u64 mine = total(by_weight ? fixed_sum(before) : few ? 0 : (u64)count);
+            tell({0, s_n, 0, mine});
+            bool listed = true;
+            int n = 0, base = 0;
+            for (int c = 0; c < C; c++) {
+                above += told[turn][c].sum, listed = listed && told[turn][c].n <= kList;
+                if (c < rank) base += told[turn][c].n;
+                n += told[turn][c].n;
             }
-            tell({0, 0, 0, mine});   // and the histograms are there
-            const u64 at_T = T ? fixed40(weight(key_logit(T))) : 0;
-            if (by_weight) {
-                for (int c = 0; c < C; c++) all += told[turn][c].sum;
-                goal = max((u64)ceil((double)fmaxf(p, 0.f) * (double)(all + r * at_T)), (u64)1);
-                if (goal > all && T) {   // among the tokens at T
-                    if (at_T) r = min(r, (goal - all + at_T - 1) / at_T);
-                    cl.sync();           // the histograms are read no more
-                    continue;
-                }
-            }
-            u64 h = 0;
-            if (tid < kBins) {
-                for (int c = 0; c < C; c++) h += cl.map_shared_rank(hist32, c)[tid];
-                if (by_weight) {
-                    float w;
-                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(-(float)tid * kPerBin));
-                    h = (u64)((float)h / a.bin_unit * w * 0x1p40f);
-                }
-            }
-            int bin = find(h, goal);
-            // 2. what lies above the bin, exactly, and the bin's keys
-            u64 above = 0;
-            uint32_t lo = 1, hi = km;   // T is among these keys
-            bool listed = false;
-            if (bin >= 0) {
-                if (tid == 0) s_n = 0;
-                __syncthreads();
-                u64 before = 0;
-                d.each([&](float (&x)[VE], int) {
-#pragma unroll
-                    for (int e = 0; e < VE; e++) {
-                        const float f = bin_of(x[e]);
-                        if (!(x[e] > over) || !(f < (float)(bin + 1))) continue;
-                        if (f < (float)bin) {
-                            before += by_weight ? fixed40(weight(x[e])) : 1;
-                        } else {
-                            const int at = atomicAdd(&s_n, 1);
-                            if (at < kList) list[at] = order_key(x[e]);
-                        }
+            if (few && n <= kRank) {
+                // all that top-k can keep, in the first CTA: each token against each
+                uint2 *to = cl.map_shared_rank(all, 0);
+                for (int i = tid; i < s_n; i += NT) to[base + i] = list[i];
+                cl.sync();
+                if (rank != 0) return;
+                uint2 me = make_uint2(0, 0);
+                u64 w = 0;
+                int mine = 0;
+                if (tid < n) {
+                    me = all[tid];
+#pragma unroll 4
+                    for (int j = 0; j < n; j++) {
+                        const uint2 o = all[j];
+                        mine += o.x > me.x || (o.x == me.x && o.y < me.y);
                     }
-                });
-                before = total(before);
-                tell({0, s_n, 0, before});
-                listed = true;
-                for (int c = 0; c < C; c++) above += told[turn][c].sum, listed = listed && told[turn][c].n <= kList;
-                listed = listed && above < goal;
-                if (!listed) above = 0;   // the whole row decides, from its first key on
-            } else {
-                cl.sync();   // the histograms are read no more
-            }
-            // 3. by keys: of the lists (all of them read by every CTA), else of the row
-            if (listed) {
-                if (tid == 0) s_lo = 0xFFFFFFFFu, s_hi = 0;
+                    if (mine < k) w = fixed40(weight(key_logit(me.x)));
+                    ranks[tid] = mine, hist[tid] = w;
+                }
+                const u64 kept = total(w);
+                bool keep = tid < n && mine < k;
+                if (p < 1.f) {
+                    const u64 g = max((u64)ceil((double)fmaxf(p, 0.f) * (double)kept), (u64)1);
+                    u64 ahead = 0;
+                    if (keep)
+#pragma unroll 4
+                        for (int j = 0; j < n; j++) ahead += ranks[j] < mine ? hist[j] : 0;
+                    keep = keep && ahead < g;
+                }
+                keep = keep && weight(key_logit(me.x)) >= least;
                 __syncthreads();
+                w = keep ? w : 0;
+                if (tid < n) hist[tid] = w;
+                const u64 all_kept = total(w);
+                u64 target = (u64)((double)u * (double)all_kept);
+                if (target >= all_kept) target = all_kept - 1;
+                u64 run = 0;
+                if (w)
+#pragma unroll 4
+                    for (int j = 0; j < n; j++) run += all[j].y < me.y ? hist[j] : 0;
+                if (w && target >= run && target < run + w) a.ids[row] = (int)me.y;
+                return;
+            }
+            listed = listed && above < goal && n <= kKeys;
+            bool step = by_weight;   // does T still have to be moved by exact sums?
+            // 3. by keys: of the lists (every CTA all of them), else of the row
+            if (listed) {
+                // into this CTA's own copy, a warp a list at a time
                 uint32_t l = 0xFFFFFFFFu, m = 0;
+                int at = 0;
                 for (int c = 0; c < C; c++) {
-                    const uint32_t *q = cl.map_shared_rank(list, c);
-                    for (int i = tid; i < told[turn][c].n; i += NT) l = min(l, q[i]), m = max(m, q[i]);
+                    const uint32_t q = remote(list, c);
+                    const int nc = told[turn][c].n;
+                    if (warp % C == c)
+                        for (int i = warp / C * 32 + lane; i < nc; i += (NW + C - 1 - c) / C * 32) {
+                            const uint32_t key = remote_u32(q + 8 * i);
+                            keys[at + i] = key;
+                            l = min(l, key), m = max(m, key);
+                        }
+                    at += nc;
                 }
                 l = __reduce_min_sync(0xffffffffu, l), m = __reduce_max_sync(0xffffffffu, m);
                 if (lane == 0) atomicMin(&s_lo, l), atomicMax(&s_hi, m);
                 __syncthreads();
                 lo = s_lo, hi = s_hi;
-            }
-            const int listed_turn = turn;
-            for (bool again = true; again;) {
-                u64 base = above;
-                again = false;
-                for (;;) {
-                    const int shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
-                    __syncthreads();
-                    for (int b = tid; b < kBins; b += NT) hist[b] = 0;
-                    __syncthreads();
-                    auto count = [&](uint32_t key) {
-                        if (key >= lo && key <= hi)
-                            atomicAdd(&hist[(hi - key) >> shift], by_weight ? fixed40(weight(key_logit(key))) : 1ull);
-                    };
-                    if (listed) {
-                        for (int c = 0; c < C; c++) {
-                            const uint32_t *q = cl.map_shared_rank(list, c);
-                            for (int i = tid; i < told[listed_turn][c].n; i += NT) count(q[i]);
-                        }
-                        __syncthreads();
-                        h = tid < kBins ? hist[tid] : 0;
-                    } else {
-                        d.each([&](float (&x)[VE], int) {
+            } else {
+                // too many to list, or a neighbour's bin: its keys' range
+                uint32_t l = 0xFFFFFFFFu, m = 0;
+                d.each([&](float (&x)[VE], int) {
 #pragma unroll
-                            for (int e = 0; e < VE; e++)
-                                if (x[e] > over) count(order_key(x[e]));
-                        });
-                        cl.sync();
-                        h = 0;
-                        if (tid < kBins)
-                            for (int c = 0; c < C; c++) h += cl.map_shared_rank(hist, c)[tid];
-                    }
-                    bin = find(h, goal - base);
-                    if (!listed) cl.sync();
-                    if (bin < 0) break;
-                    base += s_above;
-                    const uint32_t width = (1u << shift) - 1, top_key = hi - ((uint32_t)bin << shift);
-                    lo = max(lo, top_key - min(width, top_key)), hi = top_key;
-                    if (shift == 0) break;
-                }
-                if (bin >= 0) {
-                    T = hi;
-                    const u64 w = by_weight ? fixed40(weight(key_logit(T))) : 1;
-                    r = w ? (goal - base + w - 1) / w : 1;
-                } else if (listed) {   // the bin falls short: a neighbour of it was named; the whole row decides
-                    listed = false, again = true, above = 0, lo = 1, hi = km;
-                    cl.sync();
-                } else {
-                    if (!by_weight) T = 0, r = 0;   // fewer than k tokens; or a goal beyond the rounding of the sum: all
-                }
+                    for (int e = 0; e < VE; e++)
+                        if (x[e] > over && bin_of(weight(x[e])) == bin) l = min(l, order_key(x[e])), m = max(m, order_key(x[e]));
+                });
+                l = __reduce_min_sync(0xffffffffu, l), m = __reduce_max_sync(0xffffffffu, m);
+                if (lane == 0) atomicMin(&s_lo, l), atomicMax(&s_hi, m);
+                __syncthreads();
+                tell({s_lo, (int)s_hi, 0, 0});
+                lo = 0xFFFFFFFFu, hi = 0;
+                for (int c = 0; c < C; c++) lo = min(lo, told[turn][c].key), hi = max(hi, (uint32_t)told[turn][c].n);
             }
-            cl.sync();   // lists and histograms are read no more
+            u64 at = above;
+            for (int shift = 1; shift && above < goal;) {
+                shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
+                __syncthreads();
+                for (int b = tid; b < kBins; b += NT) hist[b] = 0;
+                __syncthreads();
+                uint32_t *const limbs = reinterpret_cast<uint32_t *>(hist);
+                h = 0;
+                if (listed) {
+                    // exact weights in two limbs of 20 bits, at most 2^31 of 2^11 keys: 32-bit additions are the fast
+                    // ones where many keys are equal
+                    for (int i = tid; i < n; i += NT) {
+                        const uint32_t key = keys[i];
+                        if (key < lo || key > hi) continue;
+                        const u64 w = by_weight ? fixed40(weight(key_logit(key))) : 1;
+                        const int b = (int)((hi - key) >> shift);
+                        atomicAdd(&limbs[2 * b], (uint32_t)(w & 0xFFFFFu));
+                        if (w >> 20) atomicAdd(&limbs[2 * b + 1], (uint32_t)(w >> 20));
+                    }
+                    __syncthreads();
+                    if (tid < kBins) h = limbs[2 * tid] + ((u64)limbs[2 * tid + 1] << 20);
+                } else {
+                    // counts, times the weight of the sub-bin's largest key
+                    d.each([&](float (&x)[VE], int) {
+#pragma unroll
+                        for (int e = 0; e < VE; e++) {
+                            const uint32_t key = order_key(x[e]);
+                            if (key >= lo && key <= hi) atomicAdd(&limbs[2 * ((hi - key) >> shift)], 1u);
+                        }
+                    });
+                    cl.sync();
+                    if (tid < kBins) {
+#pragma unroll
+                        for (int c = 0; c < kMaxCluster; c++)
+                            if (c < C) h += remote_u32(remote(limbs + 2 * tid, c));
+                        if (by_weight && h) h *= fixed40(weight(key_logit(hi - min((uint32_t)tid << shift, hi - 1))));
+                    }
+                }
+                bin = find(h, goal - at);
+                if (!listed) cl.sync();
+                if (bin < 0) break;
+                at += s_above;
+                const uint32_t width = (1u << shift) - 1, top_key = hi - ((uint32_t)bin << shift);
+                lo = max(lo, top_key - min(width, top_key)), hi = top_key;
+            }
+            T = above < goal && bin < 0 ? lo : hi, r = above < goal && goal > at ? goal - at : 1;
+            if (by_weight) {
+                const u64 w = fixed40(weight(key_logit(T)));
+                r = w ? (r + w - 1) / w : 1;
+                step = !listed || bin < 0;
+            }
+            // to the key whose tokens reach the goal
+#pragma unroll 1
+            for (int tries = 0; step && tries < 16; tries++) {
+                const float xT = key_logit(T);
+                float sums = 0.f;
+                int ties = 0;
+                uint32_t below = 0, next = 0xFFFFFFFFu;
+                d.each([&](float (&x)[VE], int) {
+                    float w[VE];
+                    weights(x, w);
+#pragma unroll
+                    for (int e = 0; e < VE; e++) {
+                        if (!(x[e] > over)) continue;
+                        const uint32_t key = order_key(x[e]);
+                        sums += x[e] > xT ? w[e] : 0.f;
+                        ties += x[e] == xT;
+                        if (key < T) below = max(below, key);
+                        if (key > T) next = min(next, key);
+                    }
+                });
+                const u64 mine_sum = total(fixed_sum(sums));
+                const int mine_ties = (int)total((u64)ties);
+                if (tid == 0) s_lo = 0xFFFFFFFFu, s_hi = 0;
+                __syncthreads();
+                below = __reduce_max_sync(0xffffffffu, below), next = __reduce_min_sync(0xffffffffu, next);
+                if (lane == 0) atomicMin(&s_lo, next), atomicMax(&s_hi, below);
+                __syncthreads();
+                tell({s_hi, (int)s_lo, mine_ties, mine_sum});
+                u64 exact = 0, tied = 0;
+                below = 0, next = 0xFFFFFFFFu;
+                for (int c = 0; c < C; c++) {
+                    exact += told[turn][c].sum, tied += told[turn][c].ties;
+                    below = max(below, told[turn][c].key), next = min(next, (uint32_t)told[turn][c].n);
+                }
+                const u64 w = fixed40(weight(xT));
+                r = w && goal > exact ? (goal - exact + w - 1) / w : 1;
+                if (exact >= goal && next != 0xFFFFFFFFu) T = next;
+                else if (exact + tied * w < goal && below) T = below;
+                else step = false;
+            }
+        } else {
+            // below the histogram's octaves: exact weights (or counts) by keys of the row
+            cl.sync();   // the first histograms are read no more
+            u64 at = 0;
+            for (int shift = 1; shift;) {
+                shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
+                __syncthreads();
+                for (int b = tid; b < kBins; b += NT) hist[b] = 0;
+                __syncthreads();
+                d.each([&](float (&x)[VE], int) {
+#pragma unroll
+                    for (int e = 0; e < VE; e++) {
+                        const uint32_t key = order_key(x[e]);
+                        if (x[e] > over && key >= lo && key <= hi)
+                            atomicAdd(&hist[(hi - key) >> shift], by_weight ? fixed40(weight(x[e])) : 1ull);
+                    }
+                });
+                cl.sync();
+                h = 0;
+                if (tid < kBins)
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; c++)
+                        if (c < C) h += remote_u64(remote(hist + tid, c));
+                bin = find(h, goal - at);
+                cl.sync();
+                if (bin < 0) break;
+                at += s_above;
+                const uint32_t width = (1u << shift) - 1, top_key = hi - ((uint32_t)bin << shift);
+                lo = max(lo, top_key - min(width, top_key)), hi = top_key;
+            }
+            if (bin >= 0) {
+                T = hi;
+                const u64 w = by_weight ? fixed40(weight(key_logit(T))) : 1;
+                r = w ? (goal - at + w - 1) / w : 1;
+            } else if (!by_weight) {
+                T = 0, r = 0;   // fewer than k tokens
+            }                   // (a goal beyond the rounding of the sum: all that top-k left)
         }
+        cl.sync();   // lists, histograms and what was told are read no more
     }
 
     // the kept weight of each warp's part, and its tokens at T
     const float xT = T ? key_logit(T) : -INFINITY;
-    const float sc = t > 0.f ? scale : 0.f;
-    auto weight = [&](float x) {
-        float w;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(x == top ? 0.f : (x - top) * sc));
-        return w;
-    };
     const float wT = T ? weight(xT) : 0.f;
-    const u64 fT = wT >= mp ? fixed40(wT) : 0;
-    u64 mass = 0;
+    const u64 fT = wT >= least ? fixed40(wT) : 0;
+    float sum = 0.f;
     int ties = 0;
     d.each([&](float (&x)[VE], int) {
+        float w[VE];
+        weights(x, w);
 #pragma unroll
         for (int e = 0; e < VE; e++) {
-            if (x[e] > xT) {
-                const float w = weight(x[e]);
-                if (w >= mp) mass += fixed40(w);
-            } else if (T && x[e] == xT) {
-                ties++;
-            }
+            sum += x[e] > xT && w[e] >= least ? w[e] : 0.f;
+            ties += x[e] == xT;   // (-inf where no logit is at T: not counted below, as r is 0)
         }
     });
+    u64 mass = fixed_sum(sum);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
     ties = __reduce_add_sync(0xffffffffu, ties);
@@ -428,15 +622,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     for (int w = 0; w < NW; w++) mass += wmass[w], ties += wties[w];
     tell({0, 0, ties, mass});
     // in order of index: kept weight before each CTA, warp, vector, logit
-    u64 sum = 0, base = 0, tb = 0, tsum = 0, own = 0;
+    u64 kept = 0, base = 0, tb = 0, tsum = 0, own = 0;
     for (int c = 0; c < C; c++) {
         const u64 ct = told[turn][c].ties, keep_t = tsum < r ? min(r - tsum, ct) : 0;
         const u64 m = told[turn][c].sum + keep_t * fT;
-        if (c == rank) base = sum, tb = tsum, own = m;
-        sum += m, tsum += ct;
+        if (c == rank) base = kept, tb = tsum, own = m;
+        kept += m, tsum += ct;
     }
-    u64 target = (u64)((double)u * (double)sum);   // the first token whose running sum exceeds u times the total
-    if (target >= sum) target = sum - 1;           // (u = 1 - 2^-24 rounds up to the total at most)
+    u64 target = (u64)((double)u * (double)kept);   // the first token whose running sum exceeds u times the total
+    if (target >= kept) target = kept - 1;          // (u = 1 - 2^-24 rounds up to the total at most)
     if (target < base || target >= base + own) return;
     for (int w = 0; w < NW; w++) {
         const u64 ct = wties[w], keep_t = tb < r ? min(r - tb, ct) : 0, m = wmass[w] + keep_t * fT;
@@ -446,7 +640,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         }
         base += m, tb += ct;
     }
-    // this warp's: 32 vectors at a time
+    // this warp's: 32 vectors at a time.  Its sum was rounded lane by lane, a
+    // token's weight here is not: where the running sum stays below the
+    // target to the end, the last kept token is the one.
+    int last = -1;
     for (int v = d.v0; v < d.v1; v += 32) {
         float x[VE];
         int mt = 0;
@@ -472,11 +669,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             we[e] = 0;
             if (x[e] > xT) {
                 const float w = weight(x[e]);
-                we[e] = w >= mp ? fixed40(w) : 0;
+                we[e] = w >= least ? fixed40(w) : 0;
             } else if (T && x[e] == xT) {
                 we[e] = rt++ < r ? fT : 0;
             }
             m += we[e];
+            if (we[e]) last = (v + lane) * VE - d.off + e;
         }
         u64 inc = m;
 #pragma unroll
@@ -485,7 +683,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             if (lane >= o) inc += y;
         }
         u64 run = base + inc - m;
-        if (target >= run && target < run + m) {
+        const bool mine = target >= run && target < run + m;
+        if (mine) {
             int id = 0;
 #pragma unroll
             for (int e = 0; e < VE; e++) {
@@ -494,10 +693,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             }
             a.ids[row] = id;
         }
+        if (__any_sync(0xffffffffu, mine)) return;
         base += __shfl_sync(0xffffffffu, inc, 31);
         tb += __shfl_sync(0xffffffffu, it, 31);
-        if (target < base) break;
     }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0) a.ids[row] = last;
 }
 
 template <bool BF16, bool RES, int NT>
@@ -524,18 +725,21 @@ template <bool BF16>
 cudaError_t sample_plan(SampleArgs a, cudaStream_t st) {
     const int VE = BF16 ? 8 : 4;
     const long long vecs = ((long long)a.V + VE - 1) / VE + 1;   // one more where the first is cut
-    // CTAs of a row: as many as give a large GPU two a multiprocessor, each
-    // with at least 256 vectors; more where a part must fit shared memory
+    // CTAs of a row: enough for one an SM, each with at least 256 vectors
+    // (16 x 200 K fp32: 160, 85, 60, 53 us with 1, 2, 4, 8; one row of 32 K:
+    // 19, 15, 11, 10), and where there are more, as many as two an SM need to
+    // keep their parts in shared memory (256 x 128 K bf16, mixed: 143 and 108
+    // us with 1 and 2 that read it from L2 again, 95 with 4, 124 with 8).
     int C = 1;
-    while (C < kMaxCluster && ((long long)a.rows * C < 152 && vecs / C > 256 || vecs * 16 / C > 100000)) C *= 2;
+    while (C < kMaxCluster && ((vecs / C > 256 && (long long)a.rows * C < 152) || vecs * 16 / C > 80000)) C *= 2;
     a.seg = (int)((vecs + C - 1) / C);
     const size_t smem = (size_t)a.seg * 16;
-    float unit = 256.f;   // 2^30 / 2^22
-    for (int b = 1 << 22; b > a.V && b > 2; b >>= 1) unit *= 2.f;
-    a.bin_unit = unit;
-    const bool wide = (long long)a.rows * C <= 152;
-    if (smem > 190000) return sample_launch<BF16, false, 1024>(a, C, 0, st);
-    return wide ? sample_launch<BF16, true, 1024>(a, C, smem, st) : sample_launch<BF16, true, 512>(a, C, smem, st);
+    const bool alone = (long long)a.rows * C <= 152;   // one CTA an SM
+    a.drop = 0;
+    while (((long long)a.V << 24) >> a.drop > 0xFFFFFFFFll - a.V) a.drop++;
+    if (smem > (alone ? 170000u : 80000u)) return sample_launch<BF16, false, 512>(a, C, 0, st);
+    // (alone, with much to do: all its warps)
+    return alone && a.seg >= 2048 ? sample_launch<BF16, true, 1024>(a, C, smem, st) : sample_launch<BF16, true, 512>(a, C, smem, st);
 }
 
 }  // namespace
