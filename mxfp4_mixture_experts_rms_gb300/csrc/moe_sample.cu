@@ -64,6 +64,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kList = 2048;           // keys listed by a CTA
 constexpr int kKeys = 2048;           // listed keys of a row that a CTA has room for
 constexpr int kRank = 512;            // tokens that are ranked by comparing each with each
+constexpr int kAloneBytes = 170000, kSharedBytes = 80000;   // of a row's part in shared memory: one CTA an SM, two
 constexpr int kBinShift = 19;         // a weight's bits above: exponent and four bits of mantissa
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     uint2 *const all = reinterpret_cast<uint2 *>(keys);
     __shared__ int ranks[kRank];
     __shared__ Told told[2][kMaxCluster];
-    __shared__ u64 part[NW], s_above, wmass[NW];
+    __shared__ u64 part[NW], sums[2][NW], s_above, wmass[NW];
     __shared__ uint32_t red[NW], s_lo, s_hi;
     __shared__ int s_bin, s_n, wties[NW];
     cg::cluster_group cl = cg::this_cluster();
@@ -264,34 +265,36 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     // 0 - the bin of weight 1 - downwards; NaN is never asked for
     auto bin_of = [](float w) { return max((0x3F800000 >> kBinShift) - (int)(__float_as_uint(w) >> kBinShift), 0); };
     auto fixed_sum = [](float sum) { return (u64)(sum * 0x1p40f); };
-    // block-wide sum
-    auto total = [&](u64 v) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        __syncthreads();
-        if (lane == 0) part[warp] = v;
-        __syncthreads();
-        v = lane < NW ? part[lane] : 0;
+    auto warp_sum = [](u64 v) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     };
-    // block-wide: the first bin whose inclusive sum of h (one a thread, kBins of them) reaches goal
-    auto find = [&](u64 h, u64 goal) {
-        u64 inc = h;
+    auto scan = [&](u64 v) {   // inclusive, over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+            const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
         }
+        return v;
+    };
+    // block-wide sum; the buffers take turns, so that one barrier does
+    int buffer = 0;
+    auto total = [&](u64 v) {
+        v = warp_sum(v);
+        buffer ^= 1;
+        if (lane == 0) sums[buffer][warp] = v;
+        __syncthreads();
+        return warp_sum(lane < NW ? sums[buffer][lane] : 0);
+    };
+    // block-wide: the first bin whose inclusive sum of h (one a thread, kBins of them) reaches goal
+    auto find = [&](u64 h, u64 goal) {
+        u64 inc = scan(h);
         if (lane == 31 && warp < kBins / 32) part[warp] = inc;
         if (tid == 0) s_bin = -1;
         __syncthreads();
         if (tid < kBins) {
-            u64 w = lane < warp ? part[lane] : 0;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            inc += w;
+            inc += warp_sum(lane < warp ? part[lane] : 0);
             if (inc >= goal && inc - h < goal) s_bin = tid, s_above = inc - h;
         }
         __syncthreads();
@@ -356,16 +359,20 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             __syncthreads();
             float before = 0.f;
             int count = 0;
+            // the bin's weights: from w_in up to w_up; listed: from w_in, up to w_end (NaN nowhere)
+            const float w_in = __uint_as_float((uint32_t)((0x3F800000 >> kBinShift) - bin) << kBinShift);
+            const float w_up = bin ? __uint_as_float((uint32_t)((0x3F800000 >> kBinShift) - bin + 1) << kBinShift) : INFINITY;
+            const float w_end = few ? INFINITY : w_up;
             d.each([&](float (&x)[VE], int i) {
                 float w[VE];
                 weights(x, w);
                 uint32_t take = 0;
 #pragma unroll
                 for (int e = 0; e < VE; e++) {
-                    const int b = x[e] > over ? bin_of(w[e]) : kBins;
-                    before += b < bin ? w[e] : 0.f;
-                    count += b < bin;
-                    take |= (uint32_t)(few ? b <= bin : b == bin) << e;
+                    const bool in = x[e] > over, up = in && w[e] >= w_up;
+                    before += up ? w[e] : 0.f;
+                    count += up;
+                    take |= in && w[e] >= w_in && w[e] < w_end ? 1u << e : 0u;
                 }
                 while (take) {
                     const int e = __ffs(take) - 1, at = atomicAdd(&s_n, 1);
@@ -612,16 +619,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             ties += x[e] == xT;   // (-inf where no logit is at T: not counted below, as r is 0)
         }
     });
-    u64 mass = fixed_sum(sum);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    u64 mass = warp_sum(fixed_sum(sum));
     ties = __reduce_add_sync(0xffffffffu, ties);
     if (lane == 0) wmass[warp] = mass, wties[warp] = ties;
     __syncthreads();
-    mass = 0, ties = 0;
-    for (int w = 0; w < NW; w++) mass += wmass[w], ties += wties[w];
-    tell({0, 0, ties, mass});
-    // in order of index: kept weight before each CTA, warp, vector, logit
+    // (a lane a warp from here on)
+    mass = lane < NW ? wmass[lane] : 0, ties = lane < NW ? wties[lane] : 0;
+    tell({0, 0, (int)__reduce_add_sync(0xffffffffu, ties), warp_sum(mass)});
+    // in order of index: kept weight before each CTA, warp, lane, logit
     u64 kept = 0, base = 0, tb = 0, tsum = 0, own = 0;
     for (int c = 0; c < C; c++) {
         const u64 ct = told[turn][c].ties, keep_t = tsum < r ? min(r - tsum, ct) : 0;
@@ -632,13 +637,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     u64 target = (u64)((double)u * (double)kept);   // the first token whose running sum exceeds u times the total
     if (target >= kept) target = kept - 1;          // (u = 1 - 2^-24 rounds up to the total at most)
     if (target < base || target >= base + own) return;
-    for (int w = 0; w < NW; w++) {
-        const u64 ct = wties[w], keep_t = tb < r ? min(r - tb, ct) : 0, m = wmass[w] + keep_t * fT;
-        if (target < base + m) {
-            if (w != warp) return;
-            break;
-        }
-        base += m, tb += ct;
+    {
+        const u64 t0 = tb + scan((u64)ties) - ties;   // tokens at T before the lane's warp
+        mass += (t0 < r ? min(r - t0, (u64)ties) : 0) * fT;
+        const u64 m0 = base + scan(mass) - mass;
+        const unsigned hit = __ballot_sync(0xffffffffu, target >= m0 && target < m0 + mass);
+        if (warp != __ffs(hit) - 1) return;
+        base = __shfl_sync(0xffffffffu, m0, warp), tb = __shfl_sync(0xffffffffu, t0, warp);
     }
     // this warp's: 32 vectors at a time.  Its sum was rounded lane by lane, a
     // token's weight here is not: where the running sum stays below the
@@ -646,59 +651,85 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     int last = -1;
     for (int v = d.v0; v < d.v1; v += 32) {
         float x[VE];
-        int mt = 0;
-        u64 m = 0;
         if (v + lane < d.v1) {
             R::values(d.vec(v + lane), x);
         } else {
 #pragma unroll
             for (int e = 0; e < VE; e++) x[e] = -INFINITY;
         }
+        int mt = 0;
 #pragma unroll
         for (int e = 0; e < VE; e++) mt += T && x[e] == xT;
-        int it = mt;
+        u64 rt = tb;   // tokens at T before this lane's
+        if (__any_sync(0xffffffffu, mt)) {
+            int it = mt;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, it, o);
-            if (lane >= o) it += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, it, o);
+                if (lane >= o) it += y;
+            }
+            rt += it - mt;
+            tb += __shfl_sync(0xffffffffu, it, 31);
         }
-        u64 rt = tb + it - mt;   // tokens at T before this lane's
-        u64 we[VE];
+        u64 we[VE], m = 0;
 #pragma unroll
         for (int e = 0; e < VE; e++) {
-            we[e] = 0;
-            if (x[e] > xT) {
-                const float w = weight(x[e]);
-                we[e] = w >= least ? fixed40(w) : 0;
-            } else if (T && x[e] == xT) {
-                we[e] = rt++ < r ? fT : 0;
-            }
+            const float w = weight(x[e]);
+            we[e] = x[e] > xT && w >= least ? fixed40(w) : 0;
+            if (mt && x[e] == xT) we[e] = rt++ < r ? fT : 0;
             m += we[e];
             if (we[e]) last = (v + lane) * VE - d.off + e;
         }
-        u64 inc = m;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+        const u64 here = warp_sum(m);
+        if (target >= base + here) {
+            base += here;
+            continue;
         }
-        u64 run = base + inc - m;
-        const bool mine = target >= run && target < run + m;
-        if (mine) {
+        u64 at = base + scan(m) - m;
+        if (target >= at && target < at + m) {
             int id = 0;
 #pragma unroll
             for (int e = 0; e < VE; e++) {
-                if (target >= run && target < run + we[e]) id = (v + lane) * VE - d.off + e;
-                run += we[e];
+                if (target >= at && target < at + we[e]) id = (v + lane) * VE - d.off + e;
+                at += we[e];
             }
             a.ids[row] = id;
         }
-        if (__any_sync(0xffffffffu, mine)) return;
-        base += __shfl_sync(0xffffffffu, inc, 31);
-        tb += __shfl_sync(0xffffffffu, it, 31);
+        return;
     }
     last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) a.ids[row] = last;
+}
+
+// Clusters of C CTAs, 1 .. kMaxCluster, that the device runs at once with one
+// CTA an SM: sizes of clusters and of the device's partitions need not go into
+// one another.
+struct Fits {
+    int n[kMaxCluster + 1];
+    bool known;
+};
+template <bool BF16>
+cudaError_t sample_fits(const Fits *&out) {
+    static PerDevice<Fits> fits;
+    static PerDevice<bool> opted;
+    int dev = 0;
+    cudaError_t e = current_device_slot(&dev);
+    if (e != cudaSuccess) return e;
+    Fits &f = fits.v[dev];
+    out = &f;
+    if (f.known) return cudaSuccess;
+    e = smem_optin_once(moe_sample_kernel<BF16, true, 1024>, opted);
+    for (int C = 1; C <= kMaxCluster && e == cudaSuccess; C++) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(C), cfg.blockDim = dim3(1024), cfg.dynamicSmemBytes = kAloneBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = C, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr, cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&f.n[C], moe_sample_kernel<BF16, true, 1024>, &cfg);
+    }
+    f.known = e == cudaSuccess;
+    return e;
 }
 
 template <bool BF16, bool RES, int NT>
@@ -725,19 +756,26 @@ template <bool BF16>
 cudaError_t sample_plan(SampleArgs a, cudaStream_t st) {
     const int VE = BF16 ? 8 : 4;
     const long long vecs = ((long long)a.V + VE - 1) / VE + 1;   // one more where the first is cut
-    // CTAs of a row: enough for one an SM, each with at least 256 vectors
-    // (16 x 200 K fp32: 160, 85, 60, 53 us with 1, 2, 4, 8; one row of 32 K:
-    // 19, 15, 11, 10), and where there are more, as many as two an SM need to
-    // keep their parts in shared memory (256 x 128 K bf16, mixed: 143 and 108
-    // us with 1 and 2 that read it from L2 again, 95 with 4, 124 with 8).
-    int C = 1;
-    while (C < kMaxCluster && ((vecs / C > 256 && (long long)a.rows * C < 152) || vecs * 16 / C > 80000)) C *= 2;
+    // CTAs of a row: as many as run at once with one an SM, each with at least
+    // 128 vectors (one row of 32 K fp32: 19, 15, 11, 10 us with 1, 2, 4, 8; 16 x
+    // 200 K: 52 with 8, where the 16th cluster had to wait for another's SMs, 29
+    // with the most that all fit),
+    // and where there are more rows, as many as two an SM need to keep their
+    // parts in shared memory (256 x 128 K bf16, mixed: 143 and 108 us with 1 and
+    // 2 that read it from L2 again, 95 with 4, 124 with 8, before the other
+    // steps to 87).
+    const Fits *fits;
+    const cudaError_t e = sample_fits<BF16>(fits);
+    if (e != cudaSuccess) return e;
+    int C = kMaxCluster;
+    while (C > 1 && (a.rows > fits->n[C] || vecs / C < 128)) C--;
+    const bool alone = a.rows <= fits->n[C];   // one CTA an SM
+    while (!alone && C < kMaxCluster && vecs * 16 / C > kSharedBytes) C++;
     a.seg = (int)((vecs + C - 1) / C);
     const size_t smem = (size_t)a.seg * 16;
-    const bool alone = (long long)a.rows * C <= 152;   // one CTA an SM
     a.drop = 0;
     while (((long long)a.V << 24) >> a.drop > 0xFFFFFFFFll - a.V) a.drop++;
-    if (smem > (alone ? 170000u : 80000u)) return sample_launch<BF16, false, 512>(a, C, 0, st);
+    if (smem > (alone ? kAloneBytes : kSharedBytes)) return sample_launch<BF16, false, 512>(a, C, 0, st);
     // (alone, with much to do: all its warps)
     return alone && a.seg >= 2048 ? sample_launch<BF16, true, 1024>(a, C, smem, st) : sample_launch<BF16, true, 512>(a, C, smem, st);
 }
