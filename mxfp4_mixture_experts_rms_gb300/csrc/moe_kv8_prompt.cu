@@ -4,22 +4,27 @@
 //
 // One CTA per (sequence, kv head, 256 rows), a row being a new token and one of
 // the kv head's query heads; 64 cached tokens a step.  Its warps:
-//  * 8..10 have the pages copied into shared memory steps ahead (bulk copies),
-//    turn E4M3 codes into fp16 (exact) and write them as the K-major,
-//    128-byte-swizzled operand tiles K [64 tokens][D] and V^T [D][64 tokens];
-//  * 11 (one lane) issues, for each half of the rows, S = Q K^T (M 128, N 64)
-//    into one of two score buffers one step ahead, and O += P V (N = D), fp32
-//    in tensor memory;
 //  * 0..3 and 4..7 are the halves' softmax, a thread a row: scores by
-//    tcgen05.ld, no shuffles, weights as fp16 into the half's P tile.
+//    tcgen05.ld, no shuffles, weights as fp16 into the half's P tile;
+//  * 8..11 turn E4M3 codes into fp16 (exact) and write them as the K-major,
+//    128-byte-swizzled operand tiles K [64 tokens][D] and V^T [D][64 tokens];
+//  * 12 has the pages copied into shared memory steps ahead (bulk copies);
+//  * 13 and 14 (one lane each) issue a half's products, S = Q K^T (M 128, N 64)
+//    into one of two score buffers one step ahead, and O += P V (N = D), fp32
+//    in tensor memory.
 // Softmax references as in the kernel for a few tokens (m of the scores, m + N
 // of score + value exponent e), but moved only when a score passes one by more
 // than 2^8, so that the accumulator in tensor memory is rarely rescaled:
 // weights are w = 2^(7 + s - m + e - N) <= 2^15, and a page's share of the sum
 // l is its weights' sum times 2^(N - e - 7).  There e - N is taken as at least
 // -80: a page that small adds nothing to the values, but its weights count.
-// Bound by the softmax's instructions: about three a score with packed fp32
-// arithmetic and three-input maxima.
+// Bound by the softmax warps' chains: a step takes them about 2050 cycles (wait
+// for the scores 400, read 200, maxima 250, wait for the products 250, weights
+// 750, hand over 150), the tensor cores about 540 of them and the exponentials
+// 512.  3 x 1024 new tokens at 64 / 8 heads of 64, up to 4096 cached: 163 us
+// (205 with one issuing warp for both halves and page copies by a decoder;
+// 193 with 16 softmax warps of 32 scores a thread, whose fixed work a step is
+// the same for half the scores; 170 before a tile's heads came together).
 //
 // A NaN value that only some of a tile's rows see would reach the others as
 // 0 * NaN: where the pages hold one in a step that not all rows see, the CTA's
@@ -32,8 +37,10 @@ namespace {
 
 constexpr int kM = 128;         // rows of a half
 constexpr int kT = 64;          // tokens of a step
-constexpr int kLoaders = 96;    // threads that read pages
-constexpr int kThreads = 12 * 32;
+constexpr int kSoftmax = 8;     // warps
+constexpr int kLoaders = 128;   // threads that turn pages into operands
+constexpr int kCopier = kSoftmax + kLoaders / 32, kIssuer = kCopier + 1;   // warps
+constexpr int kThreads = (kIssuer + 2) * 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -81,6 +88,9 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *
     for (int i = 0; i < 16; i++)
         if (bar_try(b, parity)) return true;
     return bar_wait_long(b, parity, status, where, drain);
+}
+__device__ __forceinline__ bool bar_wait_warp(uint64_t *b, uint32_t parity, int32_t *status, int where, bool drain = false) {
+    return __all_sync(0xffffffffu, bar_wait(b, parity, status, where, drain));
 }
 __device__ __forceinline__ void bar_init(uint64_t *b, uint32_t n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n));
@@ -155,16 +165,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32]) {
+// 16 columns, to be scaled.
+__device__ __forceinline__ void tmem_scale16(uint32_t at, float k) {
+    float v[16];
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16]; tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(at) : "memory");
+#pragma unroll
+    for (int e = 0; e < 16; e++) v[e] *= k;
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16}; tcgen05.wait::st.sync.aligned;" ::"r"(at),
         "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
-        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
-        "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]),
-        "f"(v[31])
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -260,36 +275,34 @@ __device__ void slow_row(const Kv8Attend &a, int b, int kvh, int head, int row, 
 
 template <int D, int P>
 __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __grid_constant__ PromptArgs f) {
-    constexpr int NP = kT / P, NU = kT * (D / 16), KU = (NU + kLoaders - 1) / kLoaders;   // pages; 16-byte units of keys (and of values): all, a thread's
-    constexpr int kUnroll = D == 64 ? KU : 2;
+    constexpr int NP = kT / P, NU = kT * (D / 16), KU = NU / kLoaders;   // pages; 16-byte units of keys (and of values): all, a thread's
     typedef Smem<D> L;
     constexpr int kStages = L::kStages, kRaw = L::kRaw;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2], drain;
+    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2], drain[2];
     __shared__ uint32_t rmeta[kRaw][NP], meta[kStages][NP];   // key exponent byte, value's, 1 if the page is there
     __shared__ uint32_t tmem_slot;
     __shared__ int job[2], odd;
     const Kv8Attend &a = f.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.x % a.c.KVH;
     if (tid == 0) {
-        for (int s = 0; s < kStages; s++) bar_init(&full[s], kLoaders / 32), bar_init(&empty[s], 1);
+        for (int s = 0; s < kStages; s++) bar_init(&full[s], kLoaders / 32), bar_init(&empty[s], 2);
         for (int s = 0; s < kRaw; s++) bar_init(&raw[s], 2), bar_init(&raw_empty[s], kLoaders / 32);
         for (int h = 0; h < 2; h++)
-            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], 4), bar_init(&p_full[h], 4), bar_init(&o_done[h], 1);
-        bar_init(&drain, 1);
+            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], kSoftmax / 2), bar_init(&p_full[h], kSoftmax / 2), bar_init(&o_done[h], 1), bar_init(&drain[h], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         odd = 0;
     }
-    if (warp == 11) {
+    if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
-        // the blockIdx.x-th tile of 256 rows: sequences in order, a sequence's
-        // last (longest) tile first
-        int x = blockIdx.x, found = -1, rt = 0;
+        // a tile of 256 rows: sequences in order, a sequence's last (longest)
+        // tile first, its heads together, so that the last to start are short
+        int x = blockIdx.x / a.c.KVH, found = -1, rt = 0;
         for (int b0 = 0; b0 < a.n_seqs && found < 0; b0 += 32) {
             int row0, n = 0, pos0;
             if (b0 + lane < a.n_seqs) kv8_rows(a, b0 + lane, row0, n, pos0);
@@ -329,17 +342,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
         const int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
         const int step0 = lo / kT, steps = max(1, (seen + kT - 1) / kT - step0);
         int32_t *status = f.status;
-        // do the rows at positions first .. last all see all of the step's tokens (where their pages are)?
-        auto whole = [&](int t0, int first, int last) { return t0 + kT <= seen && t0 + kT - 1 <= first && (a.window == 0 || t0 > last - a.window); };
 
-        if (warp < 8) {
+        if (warp < kSoftmax) {
             // ---- the softmax ----
             const int h = warp >> 2;
             if (h < halves) {
                 const int r = tid & (kM - 1), rr = r0 + h * kM + r, i2 = rr / f.G, head = kvh * f.G + rr - i2 * f.G;
                 const bool on = h * kM + r < rows;
-                const int pos = on ? pos0 + i2 : -1;
-                const int h_first = pos0 + (r0 + h * kM) / f.G, h_last = pos0 + (r0 + min(rows, (h + 1) * kM) - 1) / f.G;
+                // tokens from .. to that the row sees, and all_from .. all_to that all rows of the half see (where their pages are)
+                const int to = on ? min(seen - 1, pos0 + i2) : -1, from = a.window ? pos0 + i2 - a.window + 1 : 0;
+                const int all_to = min(seen - 1, pos0 + (r0 + h * kM) / f.G);
+                const int all_from = a.window ? pos0 + (r0 + min(rows, (h + 1) * kM) - 1) / f.G - a.window + 1 : 0;
                 int up;
                 {
                     // the row's queries, scaled by a power of two: largest magnitude in [2^14, 2^15)
@@ -373,15 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                 bool ok = true;
                 for (int j = 0; j < steps; j++) {
                     const int st = j % kStages, t0 = (step0 + j) * kT;
+                    // (a wait that gave up is only found out below: what it waited for is then read as it is)
                     ok = bar_wait(&s_full[h][j & 1], (uint32_t)(j >> 1) & 1, status, 100);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    __syncwarp();
                     fence_after();
                     float s[kT];
                     tmem_ld32(lanes + (j & 1) * kT, s);
                     tmem_ld32(lanes + (j & 1) * kT + 32, s + 32);
                     uint32_t mt[NP];
-                    bool all = whole(t0, h_first, h_last);
+                    bool all = t0 >= all_from && t0 + kT - 1 <= all_to;
 #pragma unroll
                     for (int p = 0; p < NP; p++) mt[p] = meta[st][p], all = all && (mt[p] >> 16);
                     tmem_wait(s);
@@ -390,12 +403,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
 #pragma unroll
                         for (int c = 0; c < kT; c++) {
                             const int t = t0 + c;
-                            if (!(t < seen && t <= pos && (a.window == 0 || t > pos - a.window) && (mt[c / P] >> 16))) s[c] = -INFINITY;
+                            if (!(t >= from && t <= to && (mt[c / P] >> 16))) s[c] = -INFINITY;
                         }
                     }
                     auto key_scale = [&](int p) { return fmaxf(pow2i((int)(mt[p] & 255u) - 127 - up) * sc, 1e-37f); };   // > 0: -inf stays
-                    float pm[NP], mx = -INFINITY, mv = -INFINITY;
-                    const float ms0 = m == -INFINITY ? 0.f : m;
+                    auto value_exp = [&](int p) { return (float)((int)((mt[p] >> 8) & 255u) - 127); };
+                    float mx = -INFINITY, mv = -INFINITY;
 #pragma unroll
                     for (int p = 0; p < NP; p++) {
                         float x[4];   // four chains
@@ -406,43 +419,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                             if (c + 4 < P && (c / 4) % 2 == 1) x[c % 4] = max3(x[c % 4], s[p * P + c], s[p * P + c + 4]);
                             else if (c + 4 >= P && (c / 4) % 2 == 1) x[c % 4] = fmaxf(x[c % 4], s[p * P + c]);
                         }
-                        pm[p] = fmaxf(max3(x[0], x[1], x[2]), x[3]) * key_scale(p);
-                        mx = fmaxf(mx, pm[p]), mv = fmaxf(mv, pm[p] - ms0 + (float)((int)((mt[p] >> 8) & 255u) - 127));
+                        const float pm = fmaxf(max3(x[0], x[1], x[2]), x[3]) * key_scale(p);
+                        mx = fmaxf(mx, pm), mv = fmaxf(mv, pm + value_exp(p));
                     }
                     // the references follow when passed by more than 2^8
                     float corr = 1.f;
-                    const bool move = mx > m + 8.f || mv > N + 8.f;
+                    const bool move = mx > m + 8.f || mv > N + 8.f + (m == -INFINITY ? 0.f : m);
                     if (move) {
-                        const float mn = fmaxf(m, mx), was = N + (m - mn);
-                        float nn = was;
-#pragma unroll
-                        for (int p = 0; p < NP; p++) nn = fmaxf(nn, pm[p] - mn + (float)((int)((mt[p] >> 8) & 255u) - 127));
+                        const float mn = fmaxf(m, mx), was = N + (m - mn), nn = fmaxf(was, mv - mn);
                         l *= ex2(m - mn);
                         corr = ex2(was - nn);
                         m = mn, N = nn;
                     }
                     const float ms = m == -INFINITY ? 0.f : m, Ns = N == -INFINITY ? 0.f : N;
                     // the products of the step before have read the P tile
-                    if (j > 0) {
-                        ok = bar_wait(&o_done[h], (uint32_t)(j - 1) & 1, status, 101);
+                    if (j > 0) ok = bar_wait(&o_done[h], (uint32_t)(j - 1) & 1, status, 101) && ok;
+                    if (__any_sync(0xffffffffu, move || !ok)) {
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         fence_after();
-                        if (__any_sync(0xffffffffu, move)) {
+                        if (j > 0) {
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                tmem_ld32(lanes + 2 * kT + c, o);
-                                tmem_wait(o);
-#pragma unroll
-                                for (int e = 0; e < 32; e++) o[e] *= corr;
-                                tmem_st32(lanes + 2 * kT + c, o);
-                            }
+                            for (int c = 0; c < D; c += 16) tmem_scale16(lanes + 2 * kT + c, corr);
                         }
                     }
 #pragma unroll
                     for (int p = 0; p < NP; p++) {
-                        const float fe = fmaxf((float)((int)((mt[p] >> 8) & 255u) - 127) - Ns, -80.f) + 7.f, bias = fe - ms, ks = key_scale(p);
+                        const float fe = fmaxf(value_exp(p) - Ns, -80.f) + 7.f, bias = fe - ms, ks = key_scale(p);
                         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                         for (int c = p * P; c < (p + 1) * P; c += 8) {
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                     fence_before();
                     bar_arrive_warp(&p_full[h]);
                 }
-                if (ok) ok = __all_sync(0xffffffffu, bar_wait(&o_done[h], (uint32_t)(steps - 1) & 1, status, 102));
+                if (ok) ok = bar_wait_warp(&o_done[h], (uint32_t)(steps - 1) & 1, status, 102);
                 if (ok) {
                     fence_after();
                     const float sink = on && a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
@@ -486,79 +489,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                     }
                 }
             }
-        } else if (warp < 11) {
+        } else if (warp < kCopier) {
             // ---- pages to operand tiles ----
-            const int x = tid - 256;
-            const int32_t *tab = a.table + (size_t)b * a.width;
-            auto page_at = [&](int t) {   // of token t, -1 where there is none
-                const int pg = t < seen ? __ldg(tab + t / P) : -1;
-                return pg >= 0 && pg < a.c.n_pages ? pg : -1;
-            };
-            // warp 8, lane p < NP: page p of the step to copy next, read one step ahead
-            int pg = -1, issued = 0, pend_slot = -1;
-            uint32_t pend_k = 0, pend_v = 0, pend_there = 0;   // put together only when they are stored: nothing waits for them here
-            auto fetch = [&]() { pg = warp == 8 && lane < NP && issued < steps ? page_at((step0 + issued) * kT + lane * P) : -1; };
-            auto flush = [&]() {   // the scales, read since the copies went out: the slot's second arrival
-                if (pend_slot < 0) return;
-                if (lane < NP) rmeta[pend_slot][lane] = pend_k | pend_v << 8 | pend_there;
-                __syncwarp();
-                if (lane == 0) bar_arrive(&raw[pend_slot]);
-                pend_slot = -1;
-            };
-            auto issue = [&]() {   // warp 8
-                flush();
-                const int slot = issued % kRaw;
-                const unsigned there = __ballot_sync(0xffffffffu, pg >= 0);
-                if (lane == 0)
-                    asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(smem_u32(&raw[slot])),
-                                 "r"((uint32_t)(__popc(there) * 2 * P * D)) : "memory");
-                __syncwarp();
-                pend_k = pend_v = pend_there = 0;
-                if (pg >= 0) {
-                    const size_t ph = (size_t)pg * a.c.KVH + kvh;
-                    const uint32_t dst = smem_u32(smem + L::kCodes + slot * (2 * kT * D)) + lane * (P * D), bar = smem_u32(&raw[slot]);
-                    bulk_copy(dst, a.c.k + ph * (P * D), P * D, bar);
-                    bulk_copy(dst + kT * D, a.c.v + ph * (P * D), P * D, bar);
-                    pend_k = __ldg(a.c.ks + ph), pend_v = __ldg(a.c.vs + ph), pend_there = 1u << 16;
-                }
-                pend_slot = slot;
-                issued++;
-                fetch();
-            };
-            if (warp == 8) fetch();
+            const int x = tid - kSoftmax * 32;
             bool ok = true;
             for (int j = 0; j < steps; j++) {
                 const int st = j % kStages, slot = j % kRaw, t0 = (step0 + j) * kT;
-                if (warp == 8) {
-                    // a slot is filled again once the step in it, before this one, has been read
-#pragma unroll 1
-                    while (ok && issued < steps && issued - kRaw < j) {
-                        if (issued >= kRaw) ok = __all_sync(0xffffffffu, bar_wait(&raw_empty[issued % kRaw], (uint32_t)(issued / kRaw - 1) & 1, status, 110));
-                        if (ok) issue();
-                    }
-                    if (pend_slot == slot) flush();
-                    if (!ok) break;
-                }
-                ok = bar_wait(&raw[slot], (uint32_t)(j / kRaw) & 1, status, 108);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = bar_wait_warp(&raw[slot], (uint32_t)(j / kRaw) & 1, status, 108);
                 if (!ok) break;
                 if (j >= kStages) {
-                    ok = __all_sync(0xffffffffu, bar_wait(&empty[st], (uint32_t)(j / kStages - 1) & 1, status, 103));
+                    ok = bar_wait_warp(&empty[st], (uint32_t)(j / kStages - 1) & 1, status, 103);
                     if (!ok) break;
                 }
                 const uint32_t mw = x < NP ? rmeta[slot][x] : 0u;
                 uint32_t there = 0;   // pages of the step that are there
 #pragma unroll
                 for (int p = 0; p < NP; p++) there |= (rmeta[slot][p] >> 16) << p;
-                const bool part = !whole(t0, p_first, p_last) || there != (1u << NP) - 1;
+                const bool part = t0 + kT > seen || t0 + kT - 1 > p_first || (a.window && t0 <= p_last - a.window) || there != (1u << NP) - 1;
                 // unit u: keys of token u % 64, dims 16 (u / 64) ..; values of dim u % D, tokens 16 (u / D) ..; what no
                 // page brought is what the slot held before, and never seen
                 const unsigned char *codes = smem + L::kCodes + slot * (2 * kT * D);
                 unsigned char *K = smem + L::kK + st * (kT * D * 2), *V = smem + L::kV + st * (kT * D * 2);
-#pragma unroll kUnroll
+#pragma unroll 2
                 for (int i = 0; i < KU; i++) {
                     const int u = x + kLoaders * i, tok = u % kT, ch = 2 * (u / kT);   // 16-byte chunk of the row: dims 8 ch ..
-                    if (u >= NU) break;
                     const uint4 w = *reinterpret_cast<const uint4 *>(codes + (tok / P) * (P * D) + (u / kT) * (P * 16) + (tok % P) * 16);
                     uint4 c0, c1;
                     decode16(w, true, c0, c1);
@@ -566,10 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                     *reinterpret_cast<uint4 *>(to + swizzled(tok, ch % 8)) = c0;
                     *reinterpret_cast<uint4 *>(to + swizzled(tok, ch % 8 + 1)) = c1;
                 }
-#pragma unroll kUnroll
+#pragma unroll 2
                 for (int i = 0; i < KU; i++) {
                     const int u = x + kLoaders * i, dim = u % D, blk = u / D;
-                    if (u >= NU) break;
                     uint4 v = *reinterpret_cast<const uint4 *>(codes + kT * D + u * 16);
                     if (part) {
                         // tokens that no row sees to zero; a NaN among the others: not all rows see it
@@ -596,22 +549,49 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                 fence_async();
                 bar_arrive_warp(&full[st]);
             }
+        } else if (warp == kCopier) {
+            // ---- pages into shared memory: lane p page p of a step ----
+            const int32_t *tab = a.table + (size_t)b * a.width;
+            auto page_of = [&](int j) {   // -1 where there is none
+                const int t = (step0 + j) * kT + lane * P;
+                const int pg = lane < NP && j < steps && t < seen ? __ldg(tab + t / P) : -1;
+                return pg >= 0 && pg < a.c.n_pages ? pg : -1;
+            };
+            int pg = page_of(0), issued = 0;
+            for (; issued < steps; issued++) {
+                const int slot = issued % kRaw;
+                if (issued >= kRaw && !bar_wait_warp(&raw_empty[slot], (uint32_t)(issued / kRaw - 1) & 1, status, 110)) break;
+                const unsigned there = __ballot_sync(0xffffffffu, pg >= 0);
+                if (lane == 0)
+                    asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(smem_u32(&raw[slot])),
+                                 "r"((uint32_t)(__popc(there) * 2 * P * D)) : "memory");
+                __syncwarp();
+                uint32_t scales = 0;
+                if (pg >= 0) {
+                    const size_t ph = (size_t)pg * a.c.KVH + kvh;
+                    const uint32_t dst = smem_u32(smem + L::kCodes + slot * (2 * kT * D)) + lane * (P * D), bar = smem_u32(&raw[slot]);
+                    bulk_copy(dst, a.c.k + ph * (P * D), P * D, bar);
+                    bulk_copy(dst + kT * D, a.c.v + ph * (P * D), P * D, bar);
+                    scales = (uint32_t)__ldg(a.c.ks + ph) | (uint32_t)__ldg(a.c.vs + ph) << 8 | 1u << 16;
+                }
+                pg = page_of(issued + 1);
+                if (lane < NP) rmeta[slot][lane] = scales;
+                bar_arrive_warp(&raw[slot]);   // the slot's second arrival
+            }
             // copies still in flight land before the shared memory goes
-            flush();
-            if (warp == 8)
-                for (int j = max(0, issued - kRaw); j < issued; j++) bar_wait(&raw[j % kRaw], (uint32_t)(j / kRaw) & 1, status, 109, true);
+            for (int j = max(0, issued - kRaw); j < issued; j++) bar_wait_warp(&raw[j % kRaw], (uint32_t)(j / kRaw) & 1, status, 109, true);
         } else {
-            // ---- the products: the warp together, so that descriptors stay in uniform registers; one lane issues ----
-            const uint64_t Q = tile_desc(smem_u32(smem + L::kQ)), Pt = tile_desc(smem_u32(smem + L::kP));
+            // ---- a half's products: the warp together, so that descriptors stay in uniform registers; one lane issues ----
+            const int h = warp - kIssuer;
+            const uint64_t Q = tile_desc(smem_u32(smem + L::kQ + h * L::kQ1)), Pt = tile_desc(smem_u32(smem + L::kP + h * L::kP1));
             const uint64_t K0 = tile_desc(smem_u32(smem + L::kK)), V0 = tile_desc(smem_u32(smem + L::kV));
+            const uint32_t S = tmem + 256 * h, O = S + 2 * kT;
             constexpr uint64_t kTile16 = kT * D * 2 / 16;   // descriptors count 16 bytes
-            bool ok = true;
-            for (int h = 0; h < halves && ok; h++) ok = __all_sync(0xffffffffu, bar_wait(&q_full[h], 0, status, 104));
-            auto scores = [&](int j, int st, uint32_t parity) {   // into score buffers j & 1
-                if (!__all_sync(0xffffffffu, bar_wait(&full[st], parity, status, 105))) return false;
+            auto scores = [&](int j, int st, uint32_t parity) {   // into score buffer j & 1
+                if (!bar_wait_warp(&full[st], parity, status, 105)) return false;
                 fence_after();
                 const uint64_t K = K0 + st * kTile16;
-                const uint32_t to = tmem + (j & 1) * kT;
+                const uint32_t to = S + (j & 1) * kT;
                 if (elect_one()) {
 #pragma unroll
                     for (int c = 0; c < D / 16; c++) {
@@ -619,48 +599,37 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                         if (c == 0) mma<false>(to, q, k, inst_desc(kT));
                         else mma<true>(to, q, k, inst_desc(kT));
                     }
-                    commit(&s_full[0][j & 1]);
-                    if (halves > 1) {
-#pragma unroll
-                        for (int c = 0; c < D / 16; c++) {
-                            const uint64_t q = Q + L::kQ1 / 16 + (c / 4) * (kM * 8) + (c % 4) * 2, k = K + (c / 4) * (kT * 8) + (c % 4) * 2;
-                            if (c == 0) mma<false>(to + 256, q, k, inst_desc(kT));
-                            else mma<true>(to + 256, q, k, inst_desc(kT));
-                        }
-                        commit(&s_full[1][j & 1]);
-                    }
+                    commit(&s_full[h][j & 1]);
                 }
                 __syncwarp();
                 return true;
             };
             int st = 0, st1 = 0;          // stages of steps j and j + 1
             uint32_t par1 = 0;
+            bool ok = h < halves && bar_wait_warp(&q_full[h], 0, status, 104);
             if (ok) ok = scores(0, 0, 0);
             for (int j = 0; j < steps && ok; j++, st = st1) {
                 if (++st1 == kStages) st1 = 0, par1 ^= 1;
-                // the next scores go ahead of this step's values: their buffers were read before step j - 1's weights were
+                // the next scores go ahead of this step's values: their buffer was read before step j - 1's weights were
                 if (j + 1 < steps) ok = scores(j + 1, st1, par1);
+                if (ok) ok = bar_wait_warp(&p_full[h], (uint32_t)j & 1, status, 106);
+                if (!ok) break;
+                fence_after();
                 const uint64_t V = V0 + st * kTile16;
-                for (int h = 0; h < halves && ok; h++) {
-                    ok = __all_sync(0xffffffffu, bar_wait(&p_full[h], (uint32_t)j & 1, status, 106));
-                    if (!ok) break;
-                    fence_after();
-                    const uint64_t w = Pt + h * (L::kP1 / 16);
-                    const uint32_t to = tmem + 256 * h + 2 * kT;
-                    if (elect_one()) {
-                        if (j == 0) mma<false>(to, w, V, inst_desc(D));
-                        else mma<true>(to, w, V, inst_desc(D));
+                if (elect_one()) {
+                    if (j == 0) mma<false>(O, Pt, V, inst_desc(D));
+                    else mma<true>(O, Pt, V, inst_desc(D));
 #pragma unroll
-                        for (int c = 1; c < kT / 16; c++) mma<true>(to, w + c * 2, V + c * 2, inst_desc(D));
-                        commit(&o_done[h]);
-                        if (h + 1 == halves) commit(&empty[st]);
-                    }
-                    __syncwarp();
+                    for (int c = 1; c < kT / 16; c++) mma<true>(O, Pt + c * 2, V + c * 2, inst_desc(D));
+                    commit(&o_done[h]);
+                    commit(&empty[st]);
+                    if (halves == 1) commit(&empty[st]);   // the other half's
                 }
+                __syncwarp();
             }
-            if (!ok) {   // the products already issued finish before tensor memory is released
-                if (elect_one()) commit(&drain);
-                bar_wait(&drain, 0, status, 107, true);
+            if (!ok && h < halves) {   // the products already issued finish before tensor memory is released
+                if (elect_one()) commit(&drain[h]);
+                bar_wait_warp(&drain[h], 0, status, 107, true);
             }
         }
         __syncthreads();
@@ -673,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
     }
     fence_before();
     __syncthreads();
-    if (warp == 11) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == kIssuer) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 template <int D, int P>
@@ -695,6 +664,6 @@ cudaError_t launch_kv8_prompt(const Kv8Attend &a, int32_t *status, cudaStream_t 
     // row tiles: a sequence's last may be partly filled
     const long long tiles = (long long)a.n_rows * f.G / (2 * kM) + a.n_seqs;
     const long long most = (long long)a.n_seqs * (((long long)a.max_new * f.G + 2 * kM - 1) / (2 * kM));
-    const dim3 grid((unsigned)std::min(tiles, most), a.c.KVH);
+    const dim3 grid((unsigned)(std::min(tiles, most) * a.c.KVH));
     return a.c.D == 64 ? prompt_page<64>(f, grid, st) : prompt_page<128>(f, grid, st);
 }
