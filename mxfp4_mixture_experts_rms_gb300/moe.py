@@ -470,18 +470,20 @@ class AttnPlan:
             pass
 
 
-def _arg(t, itemsize: int, count=None, what="tensor", none=False):
-    """Device address of a dense CUDA tensor of `itemsize` bytes an element and
-    (where given) `count` elements; None passes where `none` allows it."""
+def _arg(t, kind: str, count=None, what="tensor", none=False):
+    """Device address of a dense CUDA tensor of `kind` ("i4", "f4": int32,
+    float32; "u1": bytes) and (where given) `count` elements; None passes where
+    `none` allows it."""
     if t is None and none:
         return None
-    if t is None or not t.is_cuda or t.element_size() != itemsize or not t.is_contiguous() or \
-            (count is not None and t.numel() != count):
-        raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {itemsize}-byte elements"
+    if t is None or not t.is_cuda or t.element_size() != int(kind[1]) or t.is_floating_point() != (kind[0] == "f") or \
+            not t.is_contiguous() or (count is not None and t.numel() != count):
+        raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {_KINDS[kind]}"
                                    + (f" ({count} of them)" if count is not None else "") + " is needed")
     return t.data_ptr()
 
 
+_KINDS = {"i4": "int32", "f4": "float32", "u1": "bytes"}
 _raw_stream = None
 
 
@@ -496,10 +498,21 @@ def _stream(stream):
     return _raw_stream[0](_raw_stream[1]())
 
 
+_bf16 = None
+
+
+def _is_bf16(t):
+    global _bf16
+    if _bf16 is None:
+        import torch
+        _bf16 = torch.bfloat16
+    return t.dtype is _bf16
+
+
 def _head_rows(t, heads: int, dim: int, what: str):
     """(address, row stride) of bf16 rows [n][heads][dim], dense but for the stride from row to row."""
     shape = t.shape
-    if not t.is_cuda or t.element_size() != 2 or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+    if not t.is_cuda or not _is_bf16(t) or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][{heads}][{dim}] is needed")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != dim and heads > 1):
@@ -515,10 +528,10 @@ def pages_assign(page_size: int, cached, fresh, free_pages, counts, counts_out, 
     n, width = table.shape
     tokens = slots.numel()
     rc = (_lib or load()).moe_pages_assign(
-        int(page_size), n, _arg(cached, 4, n, "cached"), _arg(fresh, 4, n, "fresh"), _arg(free_pages, 4, None, "free_pages"),
-        free_pages.numel(), _arg(counts, 4, None, "counts"), _arg(counts_out, 4, 2, "counts_out"), _arg(table, 4, None, "table"),
-        width, _arg(starts, 4, n + 1, "starts"), _arg(lens, 4, n, "lens"), _arg(slots, 4, None, "slots"),
-        _arg(positions, 4, tokens, "positions", none=True), tokens, _stream(stream))
+        int(page_size), n, _arg(cached, "i4", n, "cached"), _arg(fresh, "i4", n, "fresh"), _arg(free_pages, "i4", None, "free_pages"),
+        free_pages.numel(), _arg(counts, "i4", None, "counts"), _arg(counts_out, "i4", 2, "counts_out"), _arg(table, "i4", None, "table"),
+        width, _arg(starts, "i4", n + 1, "starts"), _arg(lens, "i4", n, "lens"), _arg(slots, "i4", None, "slots"),
+        _arg(positions, "i4", tokens, "positions", none=True), tokens, _stream(stream))
     if rc:
         _check(rc)
 
@@ -546,10 +559,10 @@ class Kv8:
         if cache is None:
             cache = [torch.zeros(s, dtype=torch.uint8, device=device) for s in (codes, codes, scales, scales)]
         self.k, self.v, self.k_scale, self.v_scale = cache
-        _check(self.L.moe_kv8_set_cache(self.h, _arg(self.k, 1, n_codes, "k"), _arg(self.v, 1, n_codes, "v"),
-                                        _arg(self.k_scale, 1, n_scales, "k_scale"), _arg(self.v_scale, 1, n_scales, "v_scale")))
+        _check(self.L.moe_kv8_set_cache(self.h, _arg(self.k, "u1", n_codes, "k"), _arg(self.v, "u1", n_codes, "v"),
+                                        _arg(self.k_scale, "u1", n_scales, "k_scale"), _arg(self.v_scale, "u1", n_scales, "v_scale")))
         self.sinks = sinks
-        _check(self.L.moe_kv8_set_sinks(self.h, _arg(sinks, 4, q_heads, "sinks", none=True)))
+        _check(self.L.moe_kv8_set_sinks(self.h, _arg(sinks, "f4", q_heads, "sinks", none=True)))
         n = int(self.L.moe_kv8_workspace_bytes(self.h))
         self.ws = torch.empty(n + 256, dtype=torch.uint8, device=device) if workspace is None else workspace.ws
         if self.ws.numel() < n + 256:
@@ -563,7 +576,7 @@ class Kv8:
         n = k.shape[0]
         if v.shape[0] != n:
             raise MoeError(MOE_EINVAL, "k and v must have the same number of rows")
-        rc = self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, 4, n, "slots"), n, _stream(stream))
+        rc = self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, "i4", n, "slots"), n, _stream(stream))
         if rc:
             _check(rc)
 
@@ -575,8 +588,8 @@ class Kv8:
         n, width = table.shape
         if out.shape[0] != q.shape[0]:
             raise MoeError(MOE_EINVAL, "q and out must have the same number of rows")
-        rc = self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, 4, n + 1, "starts", none=True), _arg(lens, 4, n, "lens"),
-                                   _arg(table, 4, None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream))
+        rc = self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, "i4", n + 1, "starts", none=True), _arg(lens, "i4", n, "lens"),
+                                   _arg(table, "i4", None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream))
         if rc:
             _check(rc)
 
@@ -604,13 +617,13 @@ def sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None,
     int32 [n]; temperature, top_p, min_p float32 [n] and top_k int32 [n], each may be None."""
     shape, size = logits.shape, logits.element_size()
     if not logits.is_cuda or len(shape) != 2 or size not in (2, 4) or not logits.is_floating_point() or \
-            (logits.stride(1) != 1 and shape[1] > 1) or (size == 2 and str(logits.dtype) != "torch.bfloat16"):
+            (logits.stride(1) != 1 and shape[1] > 1) or (size == 2 and not _is_bf16(logits)):
         raise MoeError(MOE_EINVAL, "logits: a CUDA tensor of fp32 or bf16 rows is needed")
     n, vocab = shape
     rc = (_lib or load()).moe_sample(
         logits.data_ptr(), size == 2, n, vocab, logits.stride(0) if n > 1 else vocab,
-        _arg(temperature, 4, n, "temperature", none=True), _arg(top_k, 4, n, "top_k", none=True),
-        _arg(top_p, 4, n, "top_p", none=True), _arg(min_p, 4, n, "min_p", none=True), _arg(u, 4, n, "u"),
-        _arg(ids, 4, n, "ids"), _stream(stream))
+        _arg(temperature, "f4", n, "temperature", none=True), _arg(top_k, "i4", n, "top_k", none=True),
+        _arg(top_p, "f4", n, "top_p", none=True), _arg(min_p, "f4", n, "min_p", none=True), _arg(u, "f4", n, "u"),
+        _arg(ids, "i4", n, "ids"), _stream(stream))
     if rc:
         _check(rc)

@@ -240,7 +240,9 @@ def check_attend(rng, P, D, kv, H, lens, rows, window=0, sinks=True, width=None,
         ref, tol = S.attend(*c, P, q, starts, lens, table, window, s, scale, 2.0 ** -31 if most * (H // kv) > 64 else 2.0 ** -39)
         for b in range(len(lens)):
             a, z = starts[b], min(starts[b] + most, starts[b + 1])
-            far = np.abs(got[a:z] - ref[a:z]) / tol[a:z]
+            nan = np.isnan(ref[a:z])
+            assert np.array_equal(np.isnan(got[a:z]), nan), b
+            far = np.abs(got[a:z] - ref[a:z])[~nan] / tol[a:z][~nan]
             assert not far.size or far.max() <= 1, (b, far.max())
             assert np.all(got[z:starts[b + 1]] == 7.5)
         assert np.all(got[starts[-1]:] == 7.5)          # rows of no sequence
@@ -322,6 +324,22 @@ def test_attend_scales_far_apart(rows):
     check_attend(rng, 16, 64, 2, 8, [100, 70, 333], rows, change=change)
     # scores up to about 100, one key far above the rest, and a sink that takes nearly all
     check_attend(rng, 16, 64, 1, 8, [300, 64, 1000], rows, lo=124, hi=128, spread=0.02, scale=1.0)
+
+
+@pytest.mark.parametrize("P,D", [(16, 64), (64, 128)])
+@pytest.mark.parametrize("rows", [[3, 2, 1], [70, 33, 200]])
+@pytest.mark.parametrize("window", [0, 20])
+def test_attend_nan_values_reach_only_rows_that_see_them(P, D, rows, window):
+    rng = np.random.default_rng(17)
+    lens = [100, 75, 333]
+
+    def change(c, table):
+        kk, vv = S.unpack(c[0], c[1], P, D)
+        for b, t in ((0, 99), (0, 40), (1, 74 - rows[1] // 2), (2, 332 - rows[2] // 2)):   # a last token, ones before
+            vv[table[b, t // P], t % P, b % 2, 3 + b] = 127
+        c[:2] = S.pack(kk, vv)
+
+    check_attend(rng, P, D, 2, 8, lens, rows, window=window, change=change)
 
 
 def test_attend_two_streams_graph_replay_and_repeats():
@@ -427,6 +445,67 @@ def test_sample(V, dtype):
     check_sample(x, u, t=t, k=k, p=p, dtype=dtype, stride=1)
     check_sample(x, u, t=t, k=k, p=p, mp=mp, dtype=dtype)
     check_sample(x, u, t=t, p=p, dtype=dtype)
+
+
+@pytest.mark.parametrize("n,V,dtype", [(16, 200000, "float32"), (21, 40000, "bfloat16"), (45, 130000, "bfloat16"), (80, 131072, "bfloat16"),
+                                       (90, 201000, "float32"), (1, 1 << 22, "float32"), (2, (1 << 22) - 3, "bfloat16"),
+                                       (160, 5000, "float32")])
+def test_sample_batches_of_all_shapes(n, V, dtype):
+    # from one row over many CTAs to rows that share the device, kept in shared memory and not
+    rng = np.random.default_rng(n + V)
+    x = rng.normal(0, 3, (n, V)).astype(np.float32)
+    pick = lambda *v: rng.choice(v, n)   # noqa: E731
+    check_sample(x, rng.random(n), t=pick(0.5, 0.9, 1.3), k=pick(0, 40, 700), p=pick(0.9, 0.3, 1.0), mp=pick(0.0, 0.02), dtype=dtype)
+
+
+def test_two_streams_of_page_tables_and_sampling():
+    import torch
+    rng = np.random.default_rng(23)
+    x = dev(rng.normal(0, 2, (40, 30011)).astype(np.float32))
+    u = dev(rng.random(40).astype(np.float32))
+    k, p = dev(np.full(40, 900, np.int32)), dev(np.full(40, 0.9, np.float32))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = []
+    for _ in range(2):
+        i = lambda *a: torch.zeros(a, dtype=torch.int32, device="cuda")   # noqa: E731
+        out.append(dict(ids=i(40), table=i(700, 9), starts=i(701), lens=i(700), slots=i(9000), free=torch.arange(6000, dtype=torch.int32, device="cuda"),
+                        counts=torch.tensor([6000, 0], dtype=torch.int32, device="cuda")))
+    cached, fresh = i(700), dev(rng.integers(0, 14, 700).astype(np.int32))
+    torch.cuda.synchronize()
+    for turn in range(10):      # no entry point keeps anything of another call's
+        for s, o in zip(streams, out):
+            moe().pages_assign(16, cached, fresh, o["free"], o["counts"], o["counts"], o["table"], o["starts"], o["lens"], o["slots"], stream=s)
+            moe().sample(x, u, o["ids"], top_k=k, top_p=p, stream=s)
+    torch.cuda.synchronize()
+    for n in out[0]:
+        assert torch.equal(out[0][n], out[1][n]), n
+    # 10 times 657 pages of 6000: the last call got 87 of its own
+    pages = int((fresh > 0).sum())
+    assert pages == 657 and out[0]["counts"].tolist() == [0, 10 * pages - 6000]
+    once = torch.zeros_like(out[0]["ids"])
+    moe().sample(x, u, once, top_k=k, top_p=p)
+    assert torch.equal(once, out[0]["ids"])
+
+
+def test_bindings_refuse_other_types():
+    import torch
+    M = moe()
+    z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device="cuda")   # noqa: E731
+    f = lambda *s: z(*s, t=torch.float32)   # noqa: E731
+    calls = [lambda: M.sample(z(2, 8, t=torch.float16), f(2), z(2)), lambda: M.sample(f(2, 8), z(2), z(2)),
+             lambda: M.sample(f(2, 8), f(2), f(2)), lambda: M.sample(f(2, 8), f(2), z(2), top_k=f(2)),
+             lambda: M.sample(f(2, 8), f(2), z(2), temperature=z(2)), lambda: M.sample(f(2, 8), f(2), z(3))]
+    plan = M.Kv8(4, 2, 64, 16, 3)
+    b = lambda n, h, t=torch.bfloat16: z(n, h, 64, t=t)   # noqa: E731
+    calls += [lambda: plan.append(b(2, 2, torch.float16), b(2, 2), z(2)), lambda: plan.append(b(2, 2), b(2, 2), f(2)),
+              lambda: plan.append(b(2, 2), b(3, 2), z(2)), lambda: plan.append(b(2, 4), b(2, 4), z(2)),
+              lambda: plan.attend(b(2, 4, torch.float16), z(2), z(2, 1), b(2, 4)), lambda: plan.attend(b(2, 4), f(2), z(2, 1), b(2, 4)),
+              lambda: plan.attend(b(2, 4), z(2), z(2, 1), b(3, 4)), lambda: plan.attend(b(2, 4), z(2), z(3, 1), b(2, 4))]
+    for n, c in enumerate(calls):
+        with pytest.raises(M.MoeError):
+            c()
+            raise AssertionError(f"call {n} was not refused")
+    assert plan.device_status() == 0
 
 
 def test_sample_equal_and_odd_logits():

@@ -164,6 +164,10 @@ def test_kv8_refusals(L):
     att = lambda q=x, qs=512, st=None, le=s, t=y, w=4, n=2, mn=1, r=2, out=o, os_=512: L.moe_kv8_attend(   # noqa: E731
         h, q, qs, st, le, t, w, n, mn, r, out, os_, None)
     assert app() == moe.MOE_ENOTREADY and att() == moe.MOE_ENOTREADY
+    word = C.c_int(7)
+    assert L.moe_kv8_get_device_status(h, C.byref(word), None) == moe.MOE_ENOTREADY and word.value == 7
+    assert L.moe_kv8_get_device_status(None, C.byref(word), None) == moe.MOE_EINVAL
+    assert L.moe_kv8_get_device_status(h, None, None) == moe.MOE_EINVAL
     assert L.moe_kv8_set_cache(h, x, None, s, s) == moe.MOE_EINVAL
     assert L.moe_kv8_set_cache(h, P(0x10008), y, s, s) == moe.MOE_EINVAL
     assert L.moe_kv8_set_cache(h, x, y, s, P(0x30001)) == moe.MOE_OK          # scales: any byte
