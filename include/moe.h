@@ -496,8 +496,8 @@ void moe_attn_destroy(moe_attn *plan);
  *                 -1, their tokens' slots too).
  *   starts [n_seqs + 1] out: index of each request's first new token, and
  *                 their number; a finished request has none.
- *   lens [n_seqs] out: cached + fresh, 0 for a finished request.  Must not
- *                 overlap cached.
+ *   lens [n_seqs] out: cached + fresh, 0 for a finished request.  starts and
+ *                 lens must not overlap cached or fresh.
  *   slots [max_tokens] out: page * P + place in the page of new token i, -1
  *                 for one without a page or past table_width pages, and from
  *                 starts[n_seqs] on.
@@ -536,8 +536,10 @@ int moe_kv8_set_cache(moe_kv8 *plan, uint8_t *k, uint8_t *v, uint8_t *k_scales, 
 int moe_kv8_set_sinks(moe_kv8 *plan, const float *sinks);
 /* Device workspace of moe_kv8_attend, whatever the call's sizes: caller-owned,
  * 256-byte aligned, borrowed (moe_kv8_set_workspace clears its tickets; it
- * synchronises the device).  Plans whose attends follow one another on one
- * stream may share it; attends that can overlap on the GPU need one each. */
+ * synchronises the device, so it is not called while a stream is captured, nor
+ * while an attend of a plan that shares the workspace runs).  Plans whose
+ * attends follow one another on one stream may share it; attends that can
+ * overlap on the GPU need one each. */
 size_t moe_kv8_workspace_bytes(const moe_kv8 *plan);
 int moe_kv8_set_workspace(moe_kv8 *plan, void *dev_ptr, size_t bytes);
 /* n_tokens tokens' keys and values (bf16, [n_tokens] rows of [kv_heads]

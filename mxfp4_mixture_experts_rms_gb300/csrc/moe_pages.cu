@@ -173,7 +173,10 @@ __global__ void __launch_bounds__(T) moe_pages_push_kernel(const PagesArgs a) {
     __shared__ int wsum[T / 32], told[kCluster], s_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int rank = 0, C = 1;
-    if (!SMALL) rank = (int)cg::this_cluster().block_rank(), C = (int)cg::this_cluster().num_blocks();
+    if (!SMALL) {
+        rank = (int)cg::this_cluster().block_rank(), C = (int)cg::this_cluster().num_blocks();
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // waited for before the first write to another CTA
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // (after the wait: the second kernel reads the request lengths before its own)
     asm volatile("griddepcontrol.launch_dependents;");
@@ -207,6 +210,7 @@ __global__ void __launch_bounds__(T) moe_pages_push_kernel(const PagesArgs a) {
         if (lane == 0) wsum[warp] = c;
         __syncthreads();
         c = __reduce_add_sync(0xffffffffu, lane < T / 32 ? wsum[lane] : 0);
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA runs
         if (tid < C) cg::this_cluster().map_shared_rank(told, tid)[rank] = c;
         cg::this_cluster().sync();
         for (int x = 0; x < C; x++) {
@@ -311,8 +315,9 @@ extern "C" int moe_pages_assign(int page_size, int n_seqs, const int32_t *cached
     if (((uintptr_t)cached | (uintptr_t)fresh | (uintptr_t)free_pages | (uintptr_t)counts | (uintptr_t)counts_out |
          (uintptr_t)table | (uintptr_t)starts | (uintptr_t)lens | (uintptr_t)slots | (uintptr_t)positions) & 3u)
         return moe_fail_status(MOE_EINVAL, "pointers must be 4-byte aligned");
-    if (n_seqs && cached < lens + n_seqs && lens < cached + n_seqs)
-        return moe_fail_status(MOE_EINVAL, "lens must not overlap cached");
+    for (const int32_t *in : {cached, fresh})
+        if (n_seqs && ((in < lens + n_seqs && lens < in + n_seqs) || (in < starts + n_seqs + 1 && starts < in + n_seqs)))
+            return moe_fail_status(MOE_EINVAL, "starts and lens must not overlap cached or fresh");
     int shift = -1;
     if ((page_size & (page_size - 1)) == 0)
         for (shift = 0; (1 << shift) < page_size; shift++) {

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), C = (int)cl.num_blocks();
     const int row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // waited for before the first write to another CTA
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     if (lane == 0) red[warp] = km;
     __syncthreads();
     km = __reduce_max_sync(0xffffffffu, red[lane % NW]);
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA of the row runs
     tell({km, 0, 0, 0});
     for (int c = 0; c < C; c++) km = max(km, told[turn][c].key);
     if (km == 0) {   // nothing to choose

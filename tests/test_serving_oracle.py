@@ -147,7 +147,7 @@ def test_pages_assign_refusals(L):
     for bad in (dict(page=0), dict(page=65537), dict(n=-1), dict(n=4097), dict(cap=-1), dict(w=-1), dict(mt=-1),
                 dict(n=4096, w=2 ** 20), dict(cached=None), dict(fresh=None), dict(free=None), dict(counts=None), dict(co=None),
                 dict(table=None), dict(starts=None), dict(lens=None), dict(slots=None), dict(cached=P(0x1002)),
-                dict(pos=P(0x2001)), dict(lens=a[0])):
+                dict(pos=P(0x2001)), dict(lens=a[0]), dict(lens=a[1]), dict(starts=a[0]), dict(starts=P(0x1ffc)), dict(starts=P(0x1ff8))):
         assert call(**bad) == moe.MOE_EINVAL, bad
         assert L.moe_last_error()
 
