@@ -37,6 +37,10 @@ constexpr int kSmemSeqs = 512;       // sequences whose lengths are held in shar
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Measured: 16 x 4096 tokens of 8 heads of 64 (67 MB) 23.7 us: lengths and
+// table 1.4, the first pages 2.8, units 8.0 (HBM's rate), joins 4.7, the launch
+// the rest; 96 ragged sequences of up to 12 K, 8 heads of 128 (591 MB), 109 us:
+// 0.80 of a copy's rate; one sequence of 131 tokens 7.4 us.
 // Warps, and units in each one's ring.  What bounds the kernel is latency at
 // the instructions of a unit, so as many warps as registers and the 227 KB of
 // shared memory allow come before a deeper ring: a warp's own copies are in
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
     __shared__ uint32_t meta[W][S][NP];           // per stage and page: key exponent byte, value's, 1 if it is there
     __shared__ int scan[W];
     __shared__ Seg segs[2 * W];                   // head and tail of each warp
-    __shared__ int list[2 * W], shared_seg[2], s_last[2];
+    __shared__ int list[2 * W], group_at[2 * W + 1], group_seg[2 * W], shared_seg[2], s_first[2], s_count[2];
     const Kv8Attend &a = f.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     unsigned char *ring = smem_raw + (size_t)warp * S * ST;
@@ -413,6 +417,7 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                     nan |= ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy into the stage
                 // a NaN that only some rows see: those rows' values apart (below)
                 odd = __any_sync(0xffffffffu, nan != 0 && pmin != pmax);
             }
@@ -595,101 +600,107 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
             if (s < iu - u0) bar_wait(smem_u32(&bars[warp][s]), (uint32_t)((iu - u0 - 1 - s) / S) & 1, f.status, 91);
     __syncthreads();
 
-    // Joining: the CTA's segments in order (those of one job are neighbours),
-    // then, of the jobs that other CTAs share (at most the first and the last),
-    // those whose other partials are all there.  A join: the partials' m, l and
-    // N side by side in shared memory, then a thread for each row and pair of
-    // dims.
-    const int my_seg = lane < 2 * W ? segs[lane].u0 : -1;
-    unsigned todo = __ballot_sync(0xffffffffu, my_seg >= 0);
+    // Joining: the CTA's segments in order, those of one job a group (they are
+    // neighbours); then, of the jobs that other CTAs share (at most the first
+    // and the last), those whose other partials are all there.  Either time all
+    // groups at once: the partials' m, l and N side by side in shared memory,
+    // then a thread for each group, row and pair of dims (16 x 4096 tokens: 23.7
+    // us, 26.3 with the groups one after the other).
     auto scal = [&](int k) {   // 3 R floats, behind the tails in the rings
         return reinterpret_cast<float *>(smem_raw + (size_t)(k % W) * S * ST) + PF + k / W * (3 * R);
     };
-    static_assert((PF + (kMaxCtas + W - 1) / W * 3 * R) * 4 <= S * ST, "room for the scalars of a join");
-    for (int across = 0;;) {
-        Seg sg;
-        int n, fc = 0;
-        if (todo) {
-            const int first_seg = __ffs(todo) - 1;
-            sg = segs[first_seg];
-            const unsigned members = __ballot_sync(0xffffffffu, my_seg == sg.u0);
-            todo &= ~members;
-            n = __popc(members);
-            if (members >> lane & 1) list[__popc(members & ((1u << lane) - 1))] = lane;   // every warp the same
-            if (tid == 0 && !(sg.u0 >= c0 && sg.u0 + sg.nt <= c1)) shared_seg[sg.u0 >= c0 ? 1 : 0] = first_seg;
-        } else {
-            if (across == 0) {
-                __threadfence();
-                __syncthreads();
-                if (tid < 2) {
-                    s_last[tid] = 0;
-                    if (shared_seg[tid] >= 0) {
-                        // the CTAs that share the job, by the even cuts (no cut inside it was moved)
-                        const Seg x = segs[shared_seg[tid]];
-                        const int c_first = (int)(((long long)(x.u0 + 1) * ctas - 1) / units), c_last = (int)(((long long)(x.u0 + x.nt) * ctas - 1) / units);
-                        if (atomicAdd(f.tickets + c_first, 1) == (uint32_t)(c_last - c_first)) {
-                            f.tickets[c_first] = 0;   // as the next call finds it
-                            s_last[tid] = 1 + c_first;
-                            list[tid] = c_last - c_first + 1;
-                        }
-                    }
-                    __threadfence();
-                }
-                __syncthreads();
-            }
-            if (across < 2 && !s_last[across]) across++;
-            if (across < 2 && !s_last[across]) across++;
-            if (across >= 2) break;
-            sg = segs[shared_seg[across]];
-            fc = s_last[across] - 1, n = list[across];
-            across++;
-        }
-        const bool here = !across;
-        auto src = [&](int k) -> const float * {
-            if (!here) return f.parts + ((size_t)(fc + k) * 2 + (k == 0 ? 1 : 0)) * PF;
-            const int x = list[k];
-            return x & 1 ? reinterpret_cast<const float *>(smem_raw + (size_t)(x >> 1) * S * ST) : part + (size_t)(x >> 1) * PF;
-        };
-        if (here) __syncthreads();   // list
-        for (int x = tid; x < n * 3 * R; x += W * 32) {
-            const int k = x / (3 * R), y = x % (3 * R);
-            scal(k)[y] = *(volatile const float *)(src(k) + R * PAD + y);
-        }
-        __syncthreads();
+    static_assert((PF + (kMaxCtas + W) / W * 3 * R) * 4 <= S * ST, "room for the scalars of a join: kMaxCtas + 1 partials at most");
+    auto scalars = [&](int k, const float *from) {
+        for (int y = lane; y < 3 * R; y += 32) scal(k)[y] = *(volatile const float *)(from + R * PAD + y);
+    };
+    // partials k0 .. k0 + n - 1 (at(k)) of segment sg's job: row r, dims d, d + 1
+    auto join = [&](const Seg &sg, int k0, int n, auto at, bool done, int r, int d) {
         int row0, nr, pos0;
         kv8_rows(a, sg.b, row0, nr, pos0);
-        const int rows = min(kRows, nr * f.G - sg.rt * kRows);
-        const bool done = !here || (sg.u0 >= c0 && sg.u0 + sg.nt <= c1);
-        float *mine_p = f.parts + ((size_t)blockIdx.x * 2 + (sg.u0 >= c0 ? 1 : 0)) * PF;
-        for (int x = tid; x < rows * (D / 2); x += W * 32) {
-            const int r = x / (D / 2), d = 2 * (x % (D / 2));
-            float mm = -INFINITY, NN = -INFINITY, ll = 0.f;
+        if (r >= min(kRows, nr * f.G - sg.rt * kRows)) return;
+        float mm = -INFINITY, NN = -INFINITY, ll = 0.f;
 #pragma unroll 4
-            for (int k = 0; k < n; k++) mm = fmaxf(mm, scal(k)[r]);
-            const float ms = mm == -INFINITY ? 0.f : mm;
+        for (int k = k0; k < k0 + n; k++) mm = fmaxf(mm, scal(k)[r]);
+        const float ms = mm == -INFINITY ? 0.f : mm;
 #pragma unroll 4
-            for (int k = 0; k < n; k++) NN = fmaxf(NN, scal(k)[r] - ms + scal(k)[2 * R + r]);
-            const float Ns = NN == -INFINITY ? 0.f : NN;
-            float2 v = make_float2(0.f, 0.f);
+        for (int k = k0; k < k0 + n; k++) NN = fmaxf(NN, scal(k)[r] - ms + scal(k)[2 * R + r]);
+        const float Ns = NN == -INFINITY ? 0.f : NN;
+        float2 v = make_float2(0.f, 0.f);
 #pragma unroll 8
-            for (int k = 0; k < n; k++) {
-                const float km = scal(k)[r], kl = scal(k)[R + r], kn = scal(k)[2 * R + r];
-                const float c = ex2(km - ms + kn - Ns);   // no tokens: 2^-inf
-                volatile const float *p = src(k) + r * PAD + d;
-                v.x = fmaf(c, p[0], v.x), v.y = fmaf(c, p[1], v.y);
-                ll += kl * (km == -INFINITY ? 1.f : ex2(km - ms));   // the l of NaN scores has no maximum
-            }
-            if (done) {
-                const int rr = sg.rt * kRows + r, i2 = rr / f.G, head = sg.h * f.G + rr - i2 * f.G;
-                const float k = row_factor(mm, ll, NN, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
-                *reinterpret_cast<__nv_bfloat162 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D + d) =
-                    __floats2bfloat162_rn(v.x * k, v.y * k);
-            } else {
-                *reinterpret_cast<float2 *>(mine_p + r * PAD + d) = v;
-                if (d == 0) mine_p[R * PAD + r] = mm, mine_p[R * PAD + R + r] = ll, mine_p[R * PAD + 2 * R + r] = NN;
+        for (int k = k0; k < k0 + n; k++) {
+            const float km = scal(k)[r], kl = scal(k)[R + r], kn = scal(k)[2 * R + r];
+            const float c = ex2(km - ms + kn - Ns);   // no tokens: 2^-inf
+            volatile const float *p = at(k) + r * PAD + d;
+            v.x = fmaf(c, p[0], v.x), v.y = fmaf(c, p[1], v.y);
+            ll += kl * (km == -INFINITY ? 1.f : ex2(km - ms));   // the l of NaN scores has no maximum
+        }
+        if (done) {
+            const int rr = sg.rt * kRows + r, i2 = rr / f.G, head = sg.h * f.G + rr - i2 * f.G;
+            const float k = row_factor(mm, ll, NN, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+            *reinterpret_cast<__nv_bfloat162 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D + d) =
+                __floats2bfloat162_rn(v.x * k, v.y * k);
+        } else {
+            float *mine_p = f.parts + ((size_t)blockIdx.x * 2 + (sg.u0 >= c0 ? 1 : 0)) * PF;
+            *reinterpret_cast<float2 *>(mine_p + r * PAD + d) = v;
+            if (d == 0) mine_p[R * PAD + r] = mm, mine_p[R * PAD + R + r] = ll, mine_p[R * PAD + 2 * R + r] = NN;
+        }
+    };
+    constexpr int kCell = R * (D / 2);   // threads of a group
+    const int my_seg = lane < 2 * W ? segs[lane].u0 : -1;
+    const unsigned valid = __ballot_sync(0xffffffffu, my_seg >= 0), lower = valid & ((1u << lane) - 1);
+    const int before = __shfl_sync(0xffffffffu, my_seg, lower ? 31 - __clz(lower) : 0);
+    const bool leads = my_seg >= 0 && (!lower || before != my_seg);
+    const unsigned leaders = __ballot_sync(0xffffffffu, leads);
+    const int groups = __popc(leaders), partials = __popc(valid);
+    auto whole_job = [&](const Seg &sg) { return sg.u0 >= c0 && sg.u0 + sg.nt <= c1; };
+    // every warp writes the same
+    if (my_seg >= 0) list[__popc(lower)] = lane;
+    if (leads) {
+        const int gi = __popc(leaders & ((1u << lane) - 1));
+        group_at[gi] = __popc(lower), group_seg[gi] = lane;
+        if (!whole_job(segs[lane])) shared_seg[my_seg >= c0 ? 1 : 0] = lane;
+    }
+    if (lane == 0) group_at[groups] = partials;
+    __syncwarp();
+    auto here = [&](int k) -> const float * {
+        const int x = list[k];
+        return x & 1 ? reinterpret_cast<const float *>(smem_raw + (size_t)(x >> 1) * S * ST) : part + (size_t)(x >> 1) * PF;
+    };
+    for (int k = warp; k < partials; k += W) scalars(k, here(k));
+    __syncthreads();
+    for (int x = tid; x < groups * kCell; x += W * 32) {
+        const int gi = x / kCell, k0 = group_at[gi];
+        const Seg sg = segs[group_seg[gi]];
+        join(sg, k0, group_at[gi + 1] - k0, here, whole_job(sg), x % kCell / (D / 2), 2 * (x % (D / 2)));
+    }
+    if (shared_seg[0] < 0 && shared_seg[1] < 0) return;   // the same for the whole CTA
+
+    __threadfence();
+    __syncthreads();
+    if (tid < 2) {
+        s_count[tid] = 0;
+        if (shared_seg[tid] >= 0) {
+            // the CTAs that share the job, by the even cuts (no cut inside it was moved)
+            const Seg x = segs[shared_seg[tid]];
+            const int c_first = (int)(((long long)(x.u0 + 1) * ctas - 1) / units), c_last = (int)(((long long)(x.u0 + x.nt) * ctas - 1) / units);
+            if (atomicAdd(f.tickets + c_first, 1) == (uint32_t)(c_last - c_first)) {
+                f.tickets[c_first] = 0;   // as the next call finds it
+                s_first[tid] = c_first, s_count[tid] = c_last - c_first + 1;
             }
         }
-        __syncthreads();   // the scratch is the next join's
+        __threadfence();
+    }
+    __syncthreads();
+    const int n0 = s_count[0], n1 = s_count[1];
+    auto there_at = [&](int k) -> const float * {
+        const int i = k >= n0, kk = k - (i ? n0 : 0);
+        return f.parts + ((size_t)(s_first[i] + kk) * 2 + (kk == 0 ? 1 : 0)) * PF;
+    };
+    for (int k = warp; k < n0 + n1; k += W) scalars(k, there_at(k));
+    __syncthreads();
+    for (int x = tid; x < 2 * kCell; x += W * 32) {
+        const int i = x / kCell, n = i ? n1 : n0;
+        if (n) join(segs[shared_seg[i]], i ? n0 : 0, n, there_at, true, x % kCell / (D / 2), 2 * (x % (D / 2)));
     }
 }
 
