@@ -22,13 +22,15 @@ namespace {
 //
 // A run that fills its page (all but the ends of a prompt) is read once, into
 // registers, 16 bytes a load; values' codes are turned through shared memory.
-// Other runs are read twice and keep the bytes around them; all 16 tokens of a
-// group of values are loaded before the first is used, since the few CTAs with
-// such runs end a prompts' launch (47 us with one load after another).
+// Other runs are read likewise, a page's places with those of others left out,
+// and merged into the words that hold them.
 // Bound by HBM for prompts (4 bytes read, 2 written a value pair; 22 559 tokens
-// of 8 heads of 128: 39 us, 21 at HBM's rate, the rest each CTA's chain of
-// slots, reads and writes at 20 warps an SM); a decode step is a chain of four
-// dependent loads (48 tokens: 4.9 us).
+// of 8 heads of 128: 30 us, 21 at HBM's rate).  What is above it is the CTAs
+// with a page's part: the pages that are filled are done after 25 us, and a CTA
+// with the end of one prompt and the beginning of the next takes 11 (47 us when
+// those loaded value after value, 39 with a group of values at a time).  Four
+// CTAs an SM that hold a page in registers: 30.0 us, five that hold less 31.7.
+// A decode step is a chain of four dependent loads (48 tokens: 4.3 us).
 __device__ __forceinline__ int kv8_exponent(float amax) {
     const uint32_t b = min(max(__float_as_uint(amax), 0x04E00000u), 0x7F7FFFFFu);  // at least 448 * 2^-126, finite
     return (int)(b >> 23) - 135 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
@@ -68,6 +70,22 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float f) {
 
 constexpr int kAppendWarps = 4;
 constexpr int kMaxWindow = 64;  // tokens of one CTA
+
+// 16 tokens of 4 dims from [token][dim] bytes to the page's words: word q of a
+// dim holds tokens 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q.
+template <int D>
+__device__ __forceinline__ void turn_words(const uint8_t *from, uint32_t (&out)[4][4]) {
+    uint32_t in[16];
+#pragma unroll
+    for (int t = 0; t < 16; t++) in[t] = *reinterpret_cast<const uint32_t *>(from + t * D);
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const uint32_t a0 = __byte_perm(in[2 * q], in[2 * q + 1], 0x5140), a1 = __byte_perm(in[2 * q], in[2 * q + 1], 0x7362);
+        const uint32_t b0 = __byte_perm(in[8 + 2 * q], in[9 + 2 * q], 0x5140), b1 = __byte_perm(in[8 + 2 * q], in[9 + 2 * q], 0x7362);
+        out[0][q] = __byte_perm(a0, b0, 0x5410), out[1][q] = __byte_perm(a0, b0, 0x7632);
+        out[2][q] = __byte_perm(a1, b1, 0x5410), out[3][q] = __byte_perm(a1, b1, 0x7632);
+    }
+}
 
 // A page's run; x: its first row, at this kv head; base: the page's codes;
 // turn: P * D bytes of the warp's own; returns the scale byte.
@@ -109,17 +127,8 @@ __device__ __forceinline__ int append_page(bool keys, const uint16_t *x, long lo
 #pragma unroll 1
         for (int w = lane; w < P / 16 * (D / 4); w += 32) {
             const int g = w / (D / 4), d = 4 * (w % (D / 4));
-            uint32_t in[16];
-#pragma unroll
-            for (int t = 0; t < 16; t++) in[t] = *reinterpret_cast<const uint32_t *>(turn + (16 * g + t) * D + d);
             uint32_t out[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; q++) {   // tokens 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q
-                const uint32_t a0 = __byte_perm(in[2 * q], in[2 * q + 1], 0x5140), a1 = __byte_perm(in[2 * q], in[2 * q + 1], 0x7362);
-                const uint32_t b0 = __byte_perm(in[8 + 2 * q], in[9 + 2 * q], 0x5140), b1 = __byte_perm(in[8 + 2 * q], in[9 + 2 * q], 0x7362);
-                out[0][q] = __byte_perm(a0, b0, 0x5410), out[1][q] = __byte_perm(a0, b0, 0x7632);
-                out[2][q] = __byte_perm(a1, b1, 0x5410), out[3][q] = __byte_perm(a1, b1, 0x7632);
-            }
+            turn_words<D>(turn + 16 * g * D + d, out);
             uint4 *o = reinterpret_cast<uint4 *>(base + g * (D * 16) + d * 16);
 #pragma unroll
             for (int e = 0; e < 4; e++) o[e] = make_uint4(out[e][0], out[e][1], out[e][2], out[e][3]);
@@ -131,75 +140,95 @@ __device__ __forceinline__ int append_page(bool keys, const uint16_t *x, long lo
 
 // A run of len tokens from place o0 on; old: the page's scale byte (0: it starts here).
 template <int D, int P>
-__device__ __forceinline__ int append_run(bool keys, const uint16_t *x, long long stride, uint8_t *base, int o0, int len, int old, int lane) {
-    float am = 0.f;
+__device__ __forceinline__ int append_run(bool keys, const uint16_t *x, long long stride, uint8_t *base, uint8_t *turn, int o0, int len, int old, int lane) {
+    // places as append_page has them, loaded where they are the run's
+    constexpr int kTok = 256 / D, N = P / kTok, HELD = N < 16 ? N : 16;
+    const int tok = lane / (D / 8), ch = lane % (D / 8);
+    const uint16_t *p = x + (long long)(tok - o0) * stride + 8 * ch;
+    const long long step = kTok * stride;
+    auto mine = [&](int i) { return (unsigned)(i * kTok + tok - o0) < (unsigned)len; };
+    auto load = [&](int i) { return mine(i) ? __ldg(reinterpret_cast<const uint4 *>(p + i * step)) : make_uint4(0, 0, 0, 0); };
+    const int i0 = o0 / kTok, i1 = (o0 + len - 1) / kTok + 1;   // of any lane
+    uint4 v[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; i++) v[i] = load(i);
+    uint32_t m = 0;
 #pragma unroll 4
-    for (int u = lane; u < len * (D / 8); u += 32)
-        am = amax8(am, __ldg(reinterpret_cast<const uint4 *>(x + (long long)(u / (D / 8)) * stride) + u % (D / 8)));
-    const int now = max(kv8_exponent(warp_max(am)) + 127, old);
+    for (int i = HELD; i < N; i++) m = bits8(m, load(i));
+#pragma unroll
+    for (int i = 0; i < HELD; i++) m = bits8(m, v[i]);
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    float am = __uint_as_float(m << 16);
+    if (m > 0x7F80u) {
+        am = 0.f;
+#pragma unroll 1
+        for (int i = i0; i < i1; i++) am = amax8(am, load(i));
+        am = warp_max(am);
+    }
+    const int now = max(kv8_exponent(am) + 127, old);
     const float inv = pow2i(127 - now), shrink = pow2i(old - now);
     const bool again = o0 > 0 && now > old;
+    uint8_t *to = keys ? base + (ch / 2) * (P * 16) + tok * 16 + (ch % 2) * 8 : turn + tok * D + ch * 8;
+    const int next = keys ? kTok * 16 : kTok * D;
+#pragma unroll
+    for (int i = 0; i < HELD; i++)
+        if (mine(i)) *reinterpret_cast<uint2 *>(to + i * next) = encode8(v[i], inv);
+#pragma unroll 4
+    for (int i = HELD; i < N; i++)
+        if (mine(i)) *reinterpret_cast<uint2 *>(to + i * next) = encode8(load(i), inv);
     if (keys) {
         if (again)
+#pragma unroll 4
             for (int u = lane; u < o0 * (D / 16); u += 32) {
-                uint4 *p = reinterpret_cast<uint4 *>(base + (size_t)(u % (D / 16)) * P * 16 + u / (D / 16) * 16);
-                uint4 w = *p;
+                uint4 *q = reinterpret_cast<uint4 *>(base + (size_t)(u % (D / 16)) * P * 16 + u / (D / 16) * 16);
+                uint4 w = *q;
                 w.x = requant4(w.x, shrink), w.y = requant4(w.y, shrink);
                 w.z = requant4(w.z, shrink), w.w = requant4(w.w, shrink);
-                *p = w;
+                *q = w;
             }
-#pragma unroll 2
-        for (int u = lane; u < len * (D / 8); u += 32) {
-            const int j = u / (D / 8), ch = u % (D / 8);
-            *reinterpret_cast<uint2 *>(base + (ch / 2) * (P * 16) + (o0 + j) * 16 + (ch % 2) * 8) =
-                encode8(__ldg(reinterpret_cast<const uint4 *>(x + (long long)j * stride) + ch), inv);
-        }
         return now;
     }
-    // (16 tokens, 2 dims) at a time: bytes of tokens outside the run keep
-    // their codes (re-rounded if the exponent rose)
+    // values: 4 dims and 16 tokens a lane; bytes of tokens outside the run keep
+    // their codes (earlier ones re-rounded if the exponent rose)
+    __syncwarp();
     const int g0 = again ? 0 : o0 / 16, g1 = (o0 + len + 15) / 16;
-    for (int u = lane; u < (g1 - g0) * (D / 2); u += 32) {
-        const int gr = g0 + u / (D / 2), d = 2 * (u % (D / 2));
-        uint4 *p = reinterpret_cast<uint4 *>(base + (size_t)gr * D * 16 + d * 16);
-        uint32_t in[16];   // the run's tokens of the group, all on their way at once
+#pragma unroll 1
+    for (int w = lane; w < (g1 - g0) * (D / 4); w += 32) {
+        const int g = g0 + w / (D / 4), d = 4 * (w % (D / 4));
+        uint4 *o = reinterpret_cast<uint4 *>(base + g * (D * 16) + d * 16);
+        uint4 was[4];
 #pragma unroll
-        for (int t = 0; t < 16; t++) {
-            const int j = gr * 16 + t - o0;
-            in[t] = j >= 0 && j < len ? __ldg(reinterpret_cast<const uint32_t *>(x + (long long)j * stride + d)) : 0u;
-        }
-        const uint4 a = p[0], b = p[1];
-        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        for (int e = 0; e < 4; e++) was[e] = o[e];
+        uint32_t out[4][4], fresh[4], past[4];   // of the words' bytes: the run's, those before
+        turn_words<D>(turn + 16 * g * D + d, out);
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            // tokens 2q, 2q + 1, 8 + 2q, 9 + 2q of the group in byte order
-            uint32_t n0 = w[q], n1 = w[4 + q];
-            const uint32_t r0 = again ? requant4(n0, shrink) : n0, r1 = again ? requant4(n1, shrink) : n1;
+            fresh[q] = past[q] = 0;
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const int place = 2 * q + (e & 1) + 8 * (e >> 1), tok = gr * 16 + place, sh = 8 * e;
-                const uint32_t mask = 0xFFu << sh;
-                if (tok >= o0 && tok < o0 + len) {
-                    const uint32_t pr = in[place];
-                    const uint32_t cd = f32x2_to_e4m3(bf16_lo(pr) * inv, bf16_hi(pr) * inv);
-                    n0 = (n0 & ~mask) | ((cd & 0xFFu) << sh);
-                    n1 = (n1 & ~mask) | ((cd >> 8) << sh);
-                } else if (tok < o0) {
-                    n0 = (n0 & ~mask) | (r0 & mask);
-                    n1 = (n1 & ~mask) | (r1 & mask);
-                }
+                const int place = 16 * g + 2 * q + (e & 1) + 8 * (e >> 1);
+                if ((unsigned)(place - o0) < (unsigned)len) fresh[q] |= 0xFFu << (8 * e);
+                if (place < o0) past[q] |= 0xFFu << (8 * e);
             }
-            w[q] = n0, w[4 + q] = n1;
         }
-        p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            uint32_t x4[4] = {was[e].x, was[e].y, was[e].z, was[e].w};
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                if (again) x4[q] = (x4[q] & ~past[q]) | (requant4(x4[q], shrink) & past[q]);
+                x4[q] = (x4[q] & ~fresh[q]) | (out[e][q] & fresh[q]);
+            }
+            o[e] = make_uint4(x4[0], x4[1], x4[2], x4[3]);
+        }
     }
+    __syncwarp();   // the buffer is the next run's
     return now;
 }
 
 // Window of tokens blockIdx.x; warps over (kv head, side) pairs.
 template <int D, int P>
-__global__ void __launch_bounds__(kAppendWarps * 32, 5) moe_kv8_append_kernel(Kv8Cache c, const uint16_t *k, const uint16_t *v,
+__global__ void __launch_bounds__(kAppendWarps * 32, 4) moe_kv8_append_kernel(Kv8Cache c, const uint16_t *k, const uint16_t *v,
                                                                            long long k_stride, long long v_stride,
                                                                            const int32_t *slots, int n, int window) {
     __shared__ __align__(16) uint8_t turn[kAppendWarps][P * D];
@@ -236,7 +265,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 5) moe_kv8_append_kernel(Kv
             const uint16_t *row = x + (long long)(t0 + at) * stride;
             uint8_t *base = codes + ph * (size_t)(P * D);
             const int byte = len == P ? append_page<D, P>(keys, row, stride, base, turn[tid >> 5], lane)
-                                      : append_run<D, P>(keys, row, stride, base, o0, len, o0 ? scales[ph] : 0, lane);
+                                      : append_run<D, P>(keys, row, stride, base, turn[tid >> 5], o0, len, o0 ? scales[ph] : 0, lane);
             __syncwarp();
             if (lane == 0) scales[ph] = (uint8_t)byte;
         }

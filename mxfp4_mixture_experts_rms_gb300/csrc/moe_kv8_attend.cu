@@ -39,8 +39,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Measured: 16 x 4096 tokens of 8 heads of 64 (67 MB) 23.7 us: lengths and
 // table 1.4, the first pages 2.8, units 8.0 (HBM's rate), joins 4.7, the launch
-// the rest; 96 ragged sequences of up to 12 K, 8 heads of 128 (591 MB), 109 us:
-// 0.80 of a copy's rate; one sequence of 131 tokens 7.4 us.
+// the rest; 96 ragged sequences of up to 12 K, 4 heads of 128 (612 MB), 109 us:
+// 0.82 of a copy's rate; one sequence of 131 tokens 7.4 us.
 // Warps, and units in each one's ring.  What bounds the kernel is latency at
 // the instructions of a unit, so as many warps as registers and the 227 KB of
 // shared memory allow come before a deeper ring: a warp's own copies are in
