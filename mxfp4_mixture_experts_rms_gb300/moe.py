@@ -470,49 +470,47 @@ class AttnPlan:
             pass
 
 
+_DTYPES = {}    # "i4", "f4", "u1", "b2": int32, float32, uint8, bfloat16
+
+
+def _dtypes():
+    import torch
+    _DTYPES.update(i4=torch.int32, f4=torch.float32, u1=torch.uint8, b2=torch.bfloat16)
+    return _DTYPES
+
+
 def _arg(t, kind: str, count=None, what="tensor", none=False):
-    """Device address of a dense CUDA tensor of `kind` ("i4", "f4": int32,
-    float32; "u1": bytes) and (where given) `count` elements; None passes where
-    `none` allows it."""
+    """Device address of a dense CUDA tensor of type `kind` and (where given)
+    `count` elements; None passes where `none` allows it."""
     if t is None and none:
         return None
-    if t is None or not t.is_cuda or t.element_size() != int(kind[1]) or t.is_floating_point() != (kind[0] == "f") or \
-            not t.is_contiguous() or (count is not None and t.numel() != count):
-        raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {_KINDS[kind]}"
-                                   + (f" ({count} of them)" if count is not None else "") + " is needed")
+    if t is None or t.dtype is not (_DTYPES or _dtypes())[kind] or not t.is_cuda or not t.is_contiguous() or \
+            (count is not None and t.numel() != count):
+        raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {_dtypes()[kind]}"
+                                   + (f" ({count} elements)" if count is not None else "") + " is needed")
     return t.data_ptr()
 
 
-_KINDS = {"i4": "int32", "f4": "float32", "u1": "bytes"}
 _raw_stream = None
 
 
-def _stream(stream):
-    """cudaStream_t of `stream`, or of the current device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
+def _stream(stream, t):
+    """cudaStream_t of `stream`, or of the current one; `t`, a tensor of the
+    call, must be on the current device."""
     global _raw_stream
     if _raw_stream is None:
         import torch
         _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
-    return _raw_stream[0](_raw_stream[1]())
-
-
-_bf16 = None
-
-
-def _is_bf16(t):
-    global _bf16
-    if _bf16 is None:
-        import torch
-        _bf16 = torch.bfloat16
-    return t.dtype is _bf16
+    device = _raw_stream[1]()
+    if t.get_device() != device:
+        raise MoeError(MOE_EINVAL, f"tensors on device {t.get_device()}, the current device is {device}")
+    return _raw_stream[0](device) if stream is None else stream.cuda_stream
 
 
 def _head_rows(t, heads: int, dim: int, what: str):
     """(address, row stride) of bf16 rows [n][heads][dim], dense but for the stride from row to row."""
     shape = t.shape
-    if not t.is_cuda or not _is_bf16(t) or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+    if not t.is_cuda or t.dtype is not (_DTYPES or _dtypes())["b2"] or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][{heads}][{dim}] is needed")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != dim and heads > 1):
@@ -531,7 +529,7 @@ def pages_assign(page_size: int, cached, fresh, free_pages, counts, counts_out, 
         int(page_size), n, _arg(cached, "i4", n, "cached"), _arg(fresh, "i4", n, "fresh"), _arg(free_pages, "i4", None, "free_pages"),
         free_pages.numel(), _arg(counts, "i4", None, "counts"), _arg(counts_out, "i4", 2, "counts_out"), _arg(table, "i4", None, "table"),
         width, _arg(starts, "i4", n + 1, "starts"), _arg(lens, "i4", n, "lens"), _arg(slots, "i4", None, "slots"),
-        _arg(positions, "i4", tokens, "positions", none=True), tokens, _stream(stream))
+        _arg(positions, "i4", tokens, "positions", none=True), tokens, _stream(stream, table))
     if rc:
         _check(rc)
 
@@ -576,7 +574,7 @@ class Kv8:
         n = k.shape[0]
         if v.shape[0] != n:
             raise MoeError(MOE_EINVAL, "k and v must have the same number of rows")
-        rc = self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, "i4", n, "slots"), n, _stream(stream))
+        rc = self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, "i4", n, "slots"), n, _stream(stream, k))
         if rc:
             _check(rc)
 
@@ -589,13 +587,13 @@ class Kv8:
         if out.shape[0] != q.shape[0]:
             raise MoeError(MOE_EINVAL, "q and out must have the same number of rows")
         rc = self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, "i4", n + 1, "starts", none=True), _arg(lens, "i4", n, "lens"),
-                                   _arg(table, "i4", None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream))
+                                   _arg(table, "i4", None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream, q))
         if rc:
             _check(rc)
 
     def device_status(self, stream=None) -> int:
         s = C.c_int(0)
-        rc = self.L.moe_kv8_get_device_status(self.h, C.byref(s), _stream(stream))
+        rc = self.L.moe_kv8_get_device_status(self.h, C.byref(s), _stream(stream, self.ws))
         if rc not in (MOE_OK, MOE_EDEVICE):
             _check(rc)
         return s.value
@@ -615,15 +613,15 @@ class Kv8:
 def sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
     """Next tokens (moe_sample): logits [n][vocab] fp32 or bf16 (rows may be strided), u float32 [n] in [0, 1), ids
     int32 [n]; temperature, top_p, min_p float32 [n] and top_k int32 [n], each may be None."""
-    shape, size = logits.shape, logits.element_size()
-    if not logits.is_cuda or len(shape) != 2 or size not in (2, 4) or not logits.is_floating_point() or \
-            (logits.stride(1) != 1 and shape[1] > 1) or (size == 2 and not _is_bf16(logits)):
+    shape, kinds = logits.shape, _DTYPES or _dtypes()
+    bf16 = logits.dtype is kinds["b2"]
+    if not logits.is_cuda or len(shape) != 2 or not (bf16 or logits.dtype is kinds["f4"]) or (logits.stride(1) != 1 and shape[1] > 1):
         raise MoeError(MOE_EINVAL, "logits: a CUDA tensor of fp32 or bf16 rows is needed")
     n, vocab = shape
     rc = (_lib or load()).moe_sample(
-        logits.data_ptr(), size == 2, n, vocab, logits.stride(0) if n > 1 else vocab,
+        logits.data_ptr(), bf16, n, vocab, logits.stride(0) if n > 1 else vocab,
         _arg(temperature, "f4", n, "temperature", none=True), _arg(top_k, "i4", n, "top_k", none=True),
         _arg(top_p, "f4", n, "top_p", none=True), _arg(min_p, "f4", n, "min_p", none=True), _arg(u, "f4", n, "u"),
-        _arg(ids, "i4", n, "ids"), _stream(stream))
+        _arg(ids, "i4", n, "ids"), _stream(stream, logits))
     if rc:
         _check(rc)

@@ -508,6 +508,21 @@ def test_bindings_refuse_other_types():
     assert plan.device_status() == 0
 
 
+def test_bindings_refuse_tensors_of_another_device(monkeypatch):
+    import torch
+    M = moe()
+    z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device="cuda")   # noqa: E731
+    b = lambda n, h: z(n, h, 64, t=torch.bfloat16)   # noqa: E731
+    plan = M.Kv8(4, 2, 64, 16, 3)
+    plan.append(b(1, 2), b(1, 2), z(1))
+    monkeypatch.setattr(M, "_raw_stream", (M._raw_stream[0], lambda: 1))     # as where the current device is the second
+    for call in (lambda: plan.append(b(1, 2), b(1, 2), z(1)), lambda: plan.attend(b(1, 4), z(1), z(1, 1), b(1, 4)),
+                 lambda: M.sample(z(1, 4, t=torch.float32), z(1, t=torch.float32), z(1)), plan.device_status,
+                 lambda: M.pages_assign(16, z(1), z(1), z(4), z(2), z(2), z(1, 2), z(2), torch.ones(1, dtype=torch.int32, device="cuda"), z(3))):
+        with pytest.raises(M.MoeError, match="device"):
+            call()
+
+
 def test_sample_equal_and_odd_logits():
     rng = np.random.default_rng(1)
     V = 3001
