@@ -71,7 +71,7 @@ struct Kv8Attend {
 // of the first (lens - the sequence's rows; negative: those see nothing).
 // Whatever starts holds, the rows stay inside 0 .. n_rows - 1.
 __device__ __forceinline__ void kv8_rows(const Kv8Attend &a, int b, int &row0, int &n, int &pos0) {
-    const int len = a.lens[b];
+    const int len = max(a.lens[b], 0);
     if (!a.starts) {
         row0 = b, n = 1, pos0 = len - 1;
         return;

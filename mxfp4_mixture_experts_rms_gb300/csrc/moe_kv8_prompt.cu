@@ -621,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                     else mma<true>(O, Pt, V, inst_desc(D));
 #pragma unroll
                     for (int c = 1; c < kT / 16; c++) mma<true>(O, Pt + c * 2, V + c * 2, inst_desc(D));
-                    commit(&o_done[h]);
                     commit(&empty[st]);
                     if (halves == 1) commit(&empty[st]);   // the other half's
+                    commit(&o_done[h]);   // (last: the one that is waited for before the CTA ends)
                 }
                 __syncwarp();
             }

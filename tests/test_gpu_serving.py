@@ -291,6 +291,31 @@ def test_attend_rows_that_see_nothing():
     assert np.all(got[:2] == 0) and np.all(got[5:8] == 0) and np.all(got[8:28] == 0)
 
 
+@pytest.mark.parametrize("rows", [[1, 1, 1], [5, 60, 2]])
+def test_attend_lengths_and_starts_out_of_range(rows):
+    import torch
+    rng = np.random.default_rng(18)
+    P, D, kv, H, n = 16, 64, 2, 8, sum(rows)
+    c, table = sequences(rng, P, [64, 64, 64], rows, 4, 20, kv, D, poison=False)
+    plan = moe().Kv8(H, kv, D, P, 20, cache=[dev(x) for x in c])
+    qd, q = bf16(rng.normal(0, 0.25, (n, H, D)))
+    out = torch.full((n, H, D), 7.5, dtype=torch.bfloat16, device="cuda")
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    # a length below 0 is none; the sequence between keeps its own
+    plan.attend(qd, dev(np.array([-2 ** 31, 64, -5], np.int32)), dev(table), out, starts=dev(starts), max_new=max(rows))
+    got = out.double().cpu().numpy()
+    ref, tol = S.attend(*c, P, q, starts, [0, 64, 0], table, floor=2.0 ** -31)
+    assert (np.abs(got - ref) / tol).max() <= 1
+    assert np.all(got[:starts[1]] == 0) and np.all(got[starts[2]:] == 0)
+    # starts past the rows, before them and going back: nothing outside out's rows is written
+    guard = torch.full((n + 40, H, D), 7.5, dtype=torch.bfloat16, device="cuda")
+    for bad in ([0, n + 5, 2 * n, 2 ** 31 - 1], [-7, -3, 1, n], [n, 2, 1, 0], [2 ** 31 - 1] * 4):
+        guard.fill_(7.5)
+        plan.attend(qd, dev(np.array([64, 64, 64], np.int32)), dev(table), guard[20:20 + n], starts=dev(np.array(bad, np.int32)), max_new=max(rows))
+        assert bool((guard[:20] == 7.5).all()) and bool((guard[20 + n:] == 7.5).all())
+    assert plan.device_status() == 0
+
+
 def test_attend_pages_that_are_not_there():
     rng = np.random.default_rng(13)
 
