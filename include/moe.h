@@ -606,6 +606,9 @@ void moe_kv8_destroy(moe_kv8 *plan);
  *   3. min_p (above 1: 1) keeps those with w >= min_p
  *   4. the token is the first, in order of index, at which the running sum of
  *      the kept weights exceeds u times their total
+ * Weights are fp32 (one below 2^-126 is 0), sums of them within 2^-20 of the
+ * row's total; however little a kept token weighs next to the others, it has its
+ * share of u.
  * t <= 0 (or NaN) takes the first token in descending order.  temperature, top_k,
  * top_p, min_p: device arrays [n_rows], each may be NULL (1, all, 1, 0).
  * ids int32 [n_rows]; -1 for a row without a token to choose. */

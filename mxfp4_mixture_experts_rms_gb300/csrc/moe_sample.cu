@@ -88,6 +88,16 @@ __device__ __forceinline__ uint32_t order_key(float l) {
 __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
+// n tokens of weight w (0 .. 1; n at most 2^22) in units of 2^-(40 + up), up at
+// least 0, rounded up: what can be chosen has a unit.  The caller sees to it
+// that the result fits.
+__device__ __forceinline__ u64 units(u64 n, float w, int up = 0) {
+    const uint32_t b = __float_as_uint(w);
+    if (b < 0x800000u || n == 0) return 0;   // 0, and below 2^-126 (which ex2 makes 0)
+    const int s = (int)(b >> 23) - 110 + up;   // mantissa times 2^(exponent - 150) = units times 2^s
+    const u64 m = n * ((b & 0x7FFFFFu) | 0x800000u);
+    return s >= 0 ? m << s : (m + (1ull << min(-s, 47)) - 1) >> min(-s, 47);   // (m is below 2^47)
+}
 // A weight (0 .. 1) in units of 2^-40, by its bits.
 __device__ __forceinline__ u64 fixed40(float w) {
     const uint32_t b = __float_as_uint(w);
@@ -410,7 +420,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                         const uint2 o = all[j];
                         mine += o.x > me.x || (o.x == me.x && o.y < me.y);
                     }
-                    if (mine < k) w = fixed40(weight(key_logit(me.x)));
+                    if (mine < k) w = units(1, weight(key_logit(me.x)), 13);   // kRank of them are below 2^63
                     ranks[tid] = mine, hist[tid] = w;
                 }
                 const u64 kept = total(w);
@@ -606,10 +616,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         cl.sync();   // lists, histograms and what was told are read no more
     }
 
-    // the kept weight of each warp's part, and its tokens at T
+    // the kept weight of each warp's part, and its tokens at T.  Sums are
+    // rounded up, lane by lane and over the tokens at T (the n-th of them adds
+    // at_T(n) - at_T(n - 1)): a part with a token to choose is never nothing.
     const float xT = T ? key_logit(T) : -INFINITY;
     const float wT = T ? weight(xT) : 0.f;
-    const u64 fT = wT >= least ? fixed40(wT) : 0;
+    auto at_T = [&](u64 n) { return wT >= least ? units(min(n, r), wT) : 0; };
     float sum = 0.f;
     int ties = 0;
     d.each([&](float (&x)[VE], int) {
@@ -621,7 +633,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             ties += x[e] == xT;   // (-inf where no logit is at T: not counted below, as r is 0)
         }
     });
-    u64 mass = warp_sum(fixed_sum(sum));
+    u64 mass = warp_sum(__float2ull_ru(sum * 0x1p40f));
     ties = __reduce_add_sync(0xffffffffu, ties);
     if (lane == 0) wmass[warp] = mass, wties[warp] = ties;
     __syncthreads();
@@ -629,11 +641,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     mass = lane < NW ? wmass[lane] : 0, ties = lane < NW ? wties[lane] : 0;
     tell({0, 0, (int)__reduce_add_sync(0xffffffffu, ties), warp_sum(mass)});
     // in order of index: kept weight before each CTA, warp, lane, logit
-    u64 kept = 0, base = 0, tb = 0, tsum = 0, own = 0;
+    u64 kept = 0, base = 0, tb = 0, tsum = 0, own = 0, upto = 0;   // (upto: at_T(tsum))
     for (int c = 0; c < C; c++) {
-        const u64 ct = told[turn][c].ties, keep_t = tsum < r ? min(r - tsum, ct) : 0;
-        const u64 m = told[turn][c].sum + keep_t * fT;
-        if (c == rank) base = kept, tb = tsum, own = m;
+        const u64 ct = told[turn][c].ties;
+        u64 m = told[turn][c].sum;
+        if (c == rank) base = kept, tb = tsum;
+        if (ct && tsum < r) {
+            const u64 f = at_T(tsum + ct);
+            m += f - upto, upto = f;
+        }
+        if (c == rank) own = m;
         kept += m, tsum += ct;
     }
     u64 target = (u64)((double)u * (double)kept);   // the first token whose running sum exceeds u times the total
@@ -641,15 +658,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     if (target < base || target >= base + own) return;
     {
         const u64 t0 = tb + scan((u64)ties) - ties;   // tokens at T before the lane's warp
-        mass += (t0 < r ? min(r - t0, (u64)ties) : 0) * fT;
+        if (ties && t0 < r) mass += at_T(t0 + ties) - at_T(t0);
         const u64 m0 = base + scan(mass) - mass;
         const unsigned hit = __ballot_sync(0xffffffffu, target >= m0 && target < m0 + mass);
         if (warp != __ffs(hit) - 1) return;
-        base = __shfl_sync(0xffffffffu, m0, warp), tb = __shfl_sync(0xffffffffu, t0, warp);
+        target -= __shfl_sync(0xffffffffu, m0, warp), tb = __shfl_sync(0xffffffffu, t0, warp);
+        mass = __shfl_sync(0xffffffffu, mass, warp);
     }
-    // this warp's: 32 vectors at a time.  Its sum was rounded lane by lane, a
-    // token's weight here is not: where the running sum stays below the
+    // this warp's: 32 vectors at a time, in units in which its sum is about
+    // 2^62, so that it has a token to choose however little it weighs.  Its
+    // lanes' sums were rounded otherwise: where the running sum stays below the
     // target to the end, the last kept token is the one.
+    const int up = max(__clzll((long long)mass) - 2, 0);
+    target <<= up, base = 0;
     int last = -1;
     for (int v = d.v0; v < d.v1; v += 32) {
         float x[VE];
@@ -673,27 +694,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             rt += it - mt;
             tb += __shfl_sync(0xffffffffu, it, 31);
         }
-        u64 we[VE], m = 0;
+        // the lane's weight at once, its tokens' only where the choice is among them
+        float w[VE], mine = 0.f;
+        uint32_t keep = 0;
 #pragma unroll
         for (int e = 0; e < VE; e++) {
-            const float w = weight(x[e]);
-            we[e] = x[e] > xT && w >= least ? fixed40(w) : 0;
-            if (mt && x[e] == xT) we[e] = rt++ < r ? fT : 0;
-            m += we[e];
-            if (we[e]) last = (v + lane) * VE - d.off + e;
+            w[e] = weight(x[e]);
+            const bool in = mt && x[e] == xT ? rt++ < r : x[e] > xT;
+            if (in && w[e] >= least && w[e] > 0.f) keep |= 1u << e, mine += w[e];
         }
-        const u64 here = warp_sum(m);
+        if (keep) last = (v + lane) * VE - d.off + 31 - __clz(keep);
+        const u64 m = units(1, mine, up), here = warp_sum(m);
         if (target >= base + here) {
             base += here;
             continue;
         }
         u64 at = base + scan(m) - m;
         if (target >= at && target < at + m) {
-            int id = 0;
+            int id = last;
 #pragma unroll
             for (int e = 0; e < VE; e++) {
-                if (target >= at && target < at + we[e]) id = (v + lane) * VE - d.off + e;
-                at += we[e];
+                const u64 one = keep >> e & 1 ? units(1, w[e], up) : 0;
+                if (target >= at && target < at + one) id = (v + lane) * VE - d.off + e;
+                at += one;
             }
             a.ids[row] = id;
         }

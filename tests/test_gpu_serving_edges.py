@@ -1,0 +1,37 @@
+"""The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
+nothing beside another.
+
+Tolerances are those of test_gpu_serving.py."""
+import numpy as np
+import pytest
+
+import test_gpu_serving as base
+from oracle import serving as S
+
+pytestmark = pytest.mark.gpu
+LAST = np.float32(1 - 2.0 ** -24)       # the largest u
+
+
+# ---------------------------------------------------------------- sampling
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("V,top,n", [(128000, 29.5, 6), (200000, 31.0, 6), (5000, 35.0, 6), (20000, 40.0, 200), (1200000, 30.0, 2)])
+def test_sample_tokens_far_below_another(V, top, n, dtype):
+    rng = np.random.default_rng(V)
+    x = rng.normal(0, 0.25, (n, V)).astype(np.float32)
+    x[np.arange(n), V - 1 - np.arange(n) * 7] = top
+    vals = base.bf16(x)[1] if dtype == "bfloat16" else x
+    for kw in (dict(), dict(k=V // 2), dict(mp=1e-25), dict(k=V - 1, t=0.9)):
+        got = base.check_sample(x, 0.0, dtype=dtype, **kw)
+        for r in range(n):      # at u = 0 the first kept token, however little it weighs
+            w = S.kept(vals[r], kw.get("t", 1.0), kw.get("k", 0), 1.0, kw.get("mp", 0.0))
+            assert got[r] == np.flatnonzero(w)[0]
+        base.check_sample(x, np.resize(np.float32([1e-30, 2.0 ** -24, LAST, 0.5, 2.0 ** -60]), n), dtype=dtype, **kw)
+
+
+def test_sample_ranked_tokens_far_below_the_first():
+    rng = np.random.default_rng(1)
+    x = rng.normal(0, 0.25, (8, 3000)).astype(np.float32)
+    x[:, 2990] = 36.0
+    got = base.check_sample(x, 0.0, k=100)
+    assert all(got[r] == np.flatnonzero(S.kept(x[r], 1.0, 100, 1.0, 0.0))[0] for r in range(8))
