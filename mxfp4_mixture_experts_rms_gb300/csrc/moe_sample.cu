@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         const int c1 = min(d.c0 + a.seg, vecs), per = (c1 - d.c0 + NW - 1) / NW;
         d.v0 = min(d.c0 + warp * per, c1), d.v1 = min(d.v0 + per, c1);
     }
-    const float t = a.temperature ? fminf(a.temperature[row], 3.402823466e38f) : 1.f;
+    float t = a.temperature ? a.temperature[row] : 1.f;
+    if (t == INFINITY) t = 3.402823466e38f;   // (NaN stays NaN: the first token, as t > 0 is false)
     const int k = a.top_k ? a.top_k[row] : 0;
     const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? fminf(a.min_p[row], 1.f) : 0.f;
     const float u = a.u[row];

@@ -1,5 +1,5 @@
 """The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
-nothing beside another.
+nothing beside another, parameters that are not numbers.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -35,3 +35,14 @@ def test_sample_ranked_tokens_far_below_the_first():
     x[:, 2990] = 36.0
     got = base.check_sample(x, 0.0, k=100)
     assert all(got[r] == np.flatnonzero(S.kept(x[r], 1.0, 100, 1.0, 0.0))[0] for r in range(8))
+
+
+@pytest.mark.parametrize("n", [3, 300])
+def test_sample_nan_temperature_takes_the_first_token(n):
+    rng = np.random.default_rng(2)
+    x = rng.normal(0, 1, (n, 3000))
+    t = np.where(np.arange(n) % 3 == 1, 0.8, np.nan)
+    got = base.check_sample(x, rng.random(n), t=t, p=0.9)
+    nan = np.isnan(t)
+    assert np.array_equal(got[nan], np.argmax(np.float32(x), 1)[nan])
+    base.check_sample(x[:3], rng.random(3), t=[np.inf, -np.inf, np.nan], k=50)
