@@ -17,13 +17,12 @@
 //     keys until one key is left.
 // A top-k of few tokens lists all of them in step 2 instead, and a CTA ranks
 // the list by comparing each with each: top-k, top-p and the choice itself
-// need nothing more of the row.  Where a bin's list does not fit, step 3 counts
-// the bin's keys in the row, taking a sub-bin's weight as its count times one
-// of its weights; then, and where step 1's rounding named a neighbour of T's
-// bin, T moves by single keys until the exact sums hold.  A T below the 32
-// octaves is looked for by exact weights over the row.  Sums are fp32 over a
-// lane's logits and whole multiples of 2^-40 above that, so they do not depend
-// on their order.
+// need nothing more of the row.  Where a bin's list does not fit, step 3 goes
+// over the row, and where step 1's rounding named a neighbour of T's bin or T
+// lies below the 32 octaves over all its keys (16 x 200 K logits within 0.1 of
+// one another: 189 us).  Sums are fp32 over a lane's
+// logits and whole multiples of 2^-40 above that, so they do not depend on
+// their order.
 //
 // A row is a cluster's: each CTA keeps its part in shared memory (read from
 // memory once) where it fits, and meets the others through distributed shared
@@ -98,12 +97,12 @@ __device__ __forceinline__ u64 units(u64 n, float w, int up = 0) {
     const u64 m = n * ((b & 0x7FFFFFu) | 0x800000u);
     return s >= 0 ? m << s : (m + (1ull << min(-s, 47)) - 1) >> min(-s, 47);   // (m is below 2^47)
 }
-// A weight (0 .. 1) in units of 2^-40, by its bits.
+// A weight (0 .. 1) in units of 2^-40, by its bits, the nearest.
 __device__ __forceinline__ u64 fixed40(float w) {
     const uint32_t b = __float_as_uint(w);
-    const int s = (int)(b >> 23) - 110;   // mantissa times 2^(exponent - 150) = units of 2^-40 times 2^s
-    const uint32_t m = (b & 0x7FFFFFu) | 0x800000u;
-    return s >= 0 ? (u64)m << s : (u64)(m >> min(-s, 31));
+    const int s = (int)(b >> 23) - 110;   // as above
+    const uint32_t m = (b & 0x7FFFFFu) | 0x800000u, down = min(max(-s, 0), 31);
+    return s >= 0 ? (u64)m << s : (u64)((m + (1u << down >> 1)) >> down);
 }
 
 // What the CTAs of a row tell one another, each its slot.
@@ -359,10 +358,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             const int shift = 40 - 23 + a.drop + (int)(((0x3F800000u >> kBinShift) - (unsigned)tid) >> (23 - kBinShift)) - 127;
             if (by_weight) h = shift >= 0 ? h << shift : h >> -shift;
         }
-        int bin = find(h, goal);
+        const int bin = find(h, goal);
         // 2. what lies above the bin, and the bin's keys; few tokens: all of them
-        u64 above = 0;
-        uint32_t lo = 1, hi = km;   // T is among these keys
+        u64 above = 0, rest = 0;   // the goal's part that the tokens at T fill
+        uint32_t T_new = 0;
+        bool found = false, in_bin = false;
         if (bin >= 0) {
             if (tid == bin) s_n = (int)min(s_above + h, (u64)INT_MAX);   // by count: tokens up to the bin
             __syncthreads();
@@ -448,30 +448,70 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 if (w && target >= run && target < run + w) a.ids[row] = (int)me.y;
                 return;
             }
-            listed = listed && above < goal && n <= kKeys;
-            bool step = by_weight;   // does T still have to be moved by exact sums?
+            in_bin = above < goal;
             // 3. by keys: of the lists (every CTA all of them), else of the row
-            if (listed) {
+            if (listed && in_bin && n <= kKeys) {
                 // into this CTA's own copy, a warp a list at a time
                 uint32_t l = 0xFFFFFFFFu, m = 0;
-                int at = 0;
+                int to = 0;
                 for (int c = 0; c < C; c++) {
                     const uint32_t q = remote(list, c);
                     const int nc = told[turn][c].n;
                     if (warp % C == c)
                         for (int i = warp / C * 32 + lane; i < nc; i += (NW + C - 1 - c) / C * 32) {
                             const uint32_t key = remote_u32(q + 8 * i);
-                            keys[at + i] = key;
+                            keys[to + i] = key;
                             l = min(l, key), m = max(m, key);
                         }
-                    at += nc;
+                    to += nc;
                 }
                 l = __reduce_min_sync(0xffffffffu, l), m = __reduce_max_sync(0xffffffffu, m);
                 if (lane == 0) atomicMin(&s_lo, l), atomicMax(&s_hi, m);
                 __syncthreads();
-                lo = s_lo, hi = s_hi;
-            } else {
-                // too many to list, or a neighbour's bin: its keys' range
+                uint32_t lo = s_lo, hi = s_hi;
+                u64 at = above;
+                for (int shift = 1; shift;) {
+                    shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
+                    __syncthreads();
+                    for (int b = tid; b < kBins; b += NT) hist[b] = 0;
+                    __syncthreads();
+                    // exact weights in two limbs of 20 bits, at most 2^31 of 2^11 keys: 32-bit additions are the fast
+                    // ones where many keys are equal
+                    uint32_t *const limbs = reinterpret_cast<uint32_t *>(hist);
+                    for (int i = tid; i < n; i += NT) {
+                        const uint32_t key = keys[i];
+                        if (key < lo || key > hi) continue;
+                        const u64 w = by_weight ? fixed40(weight(key_logit(key))) : 1;
+                        const int b = (int)((hi - key) >> shift);
+                        atomicAdd(&limbs[2 * b], (uint32_t)(w & 0xFFFFFu));
+                        if (w >> 20) atomicAdd(&limbs[2 * b + 1], (uint32_t)(w >> 20));
+                    }
+                    __syncthreads();
+                    h = tid < kBins ? limbs[2 * tid] + ((u64)limbs[2 * tid + 1] << 20) : 0;
+                    const int sub = find(h, goal - at);
+                    if (sub < 0) break;
+                    at += s_above;
+                    const uint32_t width = (1u << shift) - 1, top_key = hi - ((uint32_t)sub << shift);
+                    lo = max(lo, top_key - min(width, top_key)), hi = top_key;
+                    found = !shift;
+                }
+                T_new = hi, rest = goal - at;
+                in_bin = false;   // where the goal is not reached in the list, it lies in another bin
+            }
+        }
+        // The row's own keys, in steps of 2^9 sub-bins that end at single keys:
+        // those of the bin, where they are too many to list; then, where step 1's
+        // rounding named a neighbour of T's bin and where T is below the octaves,
+        // all.  A sub-bin's weight is exact: the sum of its tokens', or where it
+        // is one key their count times its weight.
+        constexpr int KS = BF16 ? 16 : 0;   // a bf16 logit's key is its upper half
+        auto full = [](uint32_t q) { return BF16 ? q << 16 | (q & 0x8000u ? 0u : 0xFFFFu) : q; };
+#pragma unroll 1
+        for (int whole = in_bin ? 0 : 1; whole < 2 && !found; whole++) {
+            uint32_t lo = 1 >> KS, hi = km >> KS;
+            u64 at = 0;
+            cl.sync();   // what was read of other CTAs is read no more
+            if (!whole) {
                 uint32_t l = 0xFFFFFFFFu, m = 0;
                 d.each([&](float (&x)[VE], int) {
 #pragma unroll
@@ -482,138 +522,51 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 if (lane == 0) atomicMin(&s_lo, l), atomicMax(&s_hi, m);
                 __syncthreads();
                 tell({s_lo, (int)s_hi, 0, 0});
-                lo = 0xFFFFFFFFu, hi = 0;
-                for (int c = 0; c < C; c++) lo = min(lo, told[turn][c].key), hi = max(hi, (uint32_t)told[turn][c].n);
+                lo = 0xFFFFFFFFu, hi = 0, at = above;
+                for (int c = 0; c < C; c++) lo = min(lo, told[turn][c].key >> KS), hi = max(hi, (uint32_t)told[turn][c].n >> KS);
             }
-            u64 at = above;
-            for (int shift = 1; shift && above < goal;) {
-                shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
-                __syncthreads();
-                for (int b = tid; b < kBins; b += NT) hist[b] = 0;
-                __syncthreads();
-                uint32_t *const limbs = reinterpret_cast<uint32_t *>(hist);
-                h = 0;
-                if (listed) {
-                    // exact weights in two limbs of 20 bits, at most 2^31 of 2^11 keys: 32-bit additions are the fast
-                    // ones where many keys are equal
-                    for (int i = tid; i < n; i += NT) {
-                        const uint32_t key = keys[i];
-                        if (key < lo || key > hi) continue;
-                        const u64 w = by_weight ? fixed40(weight(key_logit(key))) : 1;
-                        const int b = (int)((hi - key) >> shift);
-                        atomicAdd(&limbs[2 * b], (uint32_t)(w & 0xFFFFFu));
-                        if (w >> 20) atomicAdd(&limbs[2 * b + 1], (uint32_t)(w >> 20));
-                    }
-                    __syncthreads();
-                    if (tid < kBins) h = limbs[2 * tid] + ((u64)limbs[2 * tid + 1] << 20);
-                } else {
-                    // counts, times the weight of the sub-bin's largest key
-                    d.each([&](float (&x)[VE], int) {
-#pragma unroll
-                        for (int e = 0; e < VE; e++) {
-                            const uint32_t key = order_key(x[e]);
-                            if (key >= lo && key <= hi) atomicAdd(&limbs[2 * ((hi - key) >> shift)], 1u);
-                        }
-                    });
-                    cl.sync();
-                    if (tid < kBins) {
-#pragma unroll
-                        for (int c = 0; c < kMaxCluster; c++)
-                            if (c < C) h += remote_u32(remote(limbs + 2 * tid, c));
-                        if (by_weight && h) h *= fixed40(weight(key_logit(hi - min((uint32_t)tid << shift, hi - 1))));
-                    }
-                }
-                bin = find(h, goal - at);
-                if (!listed) cl.sync();
-                if (bin < 0) break;
-                at += s_above;
-                const uint32_t width = (1u << shift) - 1, top_key = hi - ((uint32_t)bin << shift);
-                lo = max(lo, top_key - min(width, top_key)), hi = top_key;
-            }
-            T = above < goal && bin < 0 ? lo : hi, r = above < goal && goal > at ? goal - at : 1;
-            if (by_weight) {
-                const u64 w = fixed40(weight(key_logit(T)));
-                r = w ? (r + w - 1) / w : 1;
-                step = !listed || bin < 0;
-            }
-            // to the key whose tokens reach the goal
-#pragma unroll 1
-            for (int tries = 0; step && tries < 16; tries++) {
-                const float xT = key_logit(T);
-                float sums = 0.f;
-                int ties = 0;
-                uint32_t below = 0, next = 0xFFFFFFFFu;
-                d.each([&](float (&x)[VE], int) {
-                    float w[VE];
-                    weights(x, w);
-#pragma unroll
-                    for (int e = 0; e < VE; e++) {
-                        if (!(x[e] > over)) continue;
-                        const uint32_t key = order_key(x[e]);
-                        sums += x[e] > xT ? w[e] : 0.f;
-                        ties += x[e] == xT;
-                        if (key < T) below = max(below, key);
-                        if (key > T) next = min(next, key);
-                    }
-                });
-                const u64 mine_sum = total(fixed_sum(sums));
-                const int mine_ties = (int)total((u64)ties);
-                if (tid == 0) s_lo = 0xFFFFFFFFu, s_hi = 0;
-                __syncthreads();
-                below = __reduce_max_sync(0xffffffffu, below), next = __reduce_min_sync(0xffffffffu, next);
-                if (lane == 0) atomicMin(&s_lo, next), atomicMax(&s_hi, below);
-                __syncthreads();
-                tell({s_hi, (int)s_lo, mine_ties, mine_sum});
-                u64 exact = 0, tied = 0;
-                below = 0, next = 0xFFFFFFFFu;
-                for (int c = 0; c < C; c++) {
-                    exact += told[turn][c].sum, tied += told[turn][c].ties;
-                    below = max(below, told[turn][c].key), next = min(next, (uint32_t)told[turn][c].n);
-                }
-                const u64 w = fixed40(weight(xT));
-                r = w && goal > exact ? (goal - exact + w - 1) / w : 1;
-                if (exact >= goal && next != 0xFFFFFFFFu) T = next;
-                else if (exact + tied * w < goal && below) T = below;
-                else step = false;
-            }
-        } else {
-            // below the histogram's octaves: exact weights (or counts) by keys of the row
-            cl.sync();   // the first histograms are read no more
-            u64 at = 0;
             for (int shift = 1; shift;) {
                 shift = max(0, 32 - __clz((hi - lo) | 1) - 9);
+                const bool sums = by_weight && shift;
                 __syncthreads();
                 for (int b = tid; b < kBins; b += NT) hist[b] = 0;
+                for (int b = tid; b < kBins; b += NT) hist32[b] = 0;
                 __syncthreads();
                 d.each([&](float (&x)[VE], int) {
 #pragma unroll
                     for (int e = 0; e < VE; e++) {
-                        const uint32_t key = order_key(x[e]);
-                        if (x[e] > over && key >= lo && key <= hi)
-                            atomicAdd(&hist[(hi - key) >> shift], by_weight ? fixed40(weight(x[e])) : 1ull);
+                        const uint32_t key = order_key(x[e]) >> KS;
+                        if (!(x[e] > over) || key < lo || key > hi) continue;
+                        const float w = weight(x[e]);
+                        if (!whole && bin_of(w) != bin) continue;
+                        if (sums) atomicAdd(&hist[(hi - key) >> shift], fixed40(w));
+                        else atomicAdd(&hist32[(hi - key) >> shift], 1u);
                     }
                 });
                 cl.sync();
                 h = 0;
-                if (tid < kBins)
+                if (tid < kBins) {
 #pragma unroll
                     for (int c = 0; c < kMaxCluster; c++)
-                        if (c < C) h += remote_u64(remote(hist + tid, c));
-                bin = find(h, goal - at);
+                        if (c < C) h += sums ? remote_u64(remote(hist + tid, c)) : remote_u32(remote(hist32 + tid, c));
+                    if (by_weight && !shift && h) h *= fixed40(weight(key_logit(full(hi - tid))));
+                }
+                const int sub = find(h, goal - at);
                 cl.sync();
-                if (bin < 0) break;
+                if (sub < 0) break;
                 at += s_above;
-                const uint32_t width = (1u << shift) - 1, top_key = hi - ((uint32_t)bin << shift);
+                const uint32_t width = (1u << shift) - 1, top_key = hi - ((uint32_t)sub << shift);
                 lo = max(lo, top_key - min(width, top_key)), hi = top_key;
+                found = !shift;
             }
-            if (bin >= 0) {
-                T = hi;
-                const u64 w = by_weight ? fixed40(weight(key_logit(T))) : 1;
-                r = w ? (goal - at + w - 1) / w : 1;
-            } else if (!by_weight) {
-                T = 0, r = 0;   // fewer than k tokens
-            }                   // (a goal beyond the rounding of the sum: all that top-k left)
+            T_new = full(hi), rest = goal - at;
         }
+        if (found) {
+            const u64 w = by_weight ? fixed40(weight(key_logit(T_new))) : 1;
+            T = T_new, r = (rest + w - 1) / w;
+        } else if (!by_weight) {
+            T = 0, r = 0;   // fewer than k tokens
+        }                   // (by weight: the goal is beyond the sum's rounding, and all that top-k left is kept)
         cl.sync();   // lists, histograms and what was told are read no more
     }
 

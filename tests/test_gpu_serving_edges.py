@@ -1,5 +1,5 @@
 """The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
-nothing beside another, parameters that are not numbers.
+nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -46,3 +46,29 @@ def test_sample_nan_temperature_takes_the_first_token(n):
     nan = np.isnan(t)
     assert np.array_equal(got[nan], np.argmax(np.float32(x), 1)[nan])
     base.check_sample(x[:3], rng.random(3), t=[np.inf, -np.inf, np.nan], k=50)
+
+
+@pytest.mark.parametrize("V,std,t,p", [(128000, 0.02, 1.0, 0.5), (128000, 0.02, 1.0, 0.4), (200000, 2.5, 30.0, 0.5), (128000, 2.5, 200.0, 0.8),
+                                       (60000, 1e-3, 1.0, 0.5), (1000003, 0.5, 3.0, 0.6), (1 << 22, 0.3, 2.0, 0.7)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_sample_nucleus_of_nearly_equal_tokens(V, std, t, p, dtype):
+    # the border's bin holds more than a list does, on both sides of 0: with a border a few tokens off, most draws are others
+    rng = np.random.default_rng(V)
+    n = 24 if V < 10 ** 6 else 4
+    x = rng.normal(0, std, (n, V)).astype(np.float32)
+    u = rng.random(n)
+    base.check_sample(x, u, t=t, p=p, dtype=dtype)
+    base.check_sample(x, u, t=t, p=p, k=V * 3 // 4, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_sample_nucleus_at_the_edges_of_bins(dtype):
+    # equal tokens whose weights are 2^(-i / 16), p where their sums end: the first histogram's rounding may name the bin next to it
+    rng = np.random.default_rng(7)
+    V, n = 20000, 24
+    level = -np.log(2) / 16 * rng.integers(0, 40, (n, V))
+    w = np.sort(np.exp(level), 1)[:, ::-1]
+    for shift in (-1e-6, 0.0, 1e-6):
+        at = rng.integers(50, V - 50, n)
+        p = np.cumsum(w, 1)[np.arange(n), at] / w.sum(1) + shift
+        base.check_sample(level, rng.random(n), p=p, dtype=dtype)
