@@ -105,6 +105,16 @@ __device__ __forceinline__ u64 fixed40(float w) {
     return s >= 0 ? (u64)m << s : (u64)((m + (1u << down >> 1)) >> down);
 }
 
+// p or u (0 .. 1 - 2^-24; NaN: 0) in units of 2^-64, and a part of a sum: all
+// threads need it, and 64-bit floats are the GPU's slowest numbers.
+__device__ __forceinline__ u64 fraction(float p) {
+    const uint32_t b = __float_as_uint(fminf(fmaxf(p, 0.f), 0.99999994f));
+    const int s = (int)(b >> 23) - 86;
+    const uint32_t m = (b & 0x7FFFFFu) | 0x800000u;
+    return s >= 0 ? (u64)m << s : (u64)(m >> min(-s, 31));
+}
+__device__ __forceinline__ u64 part_up(u64 sum, u64 f) { return __umul64hi(sum, f) + (sum * f != 0); }
+
 // What the CTAs of a row tell one another, each its slot.
 struct Told {
     uint32_t key;
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     const float least = mp * weight(top);   // min-p is relative to the largest weight
     // 0 - the bin of weight 1 - downwards; NaN is never asked for
     auto bin_of = [](float w) { return max((0x3F800000 >> kBinShift) - (int)(__float_as_uint(w) >> kBinShift), 0); };
-    auto fixed_sum = [](float sum) { return (u64)(sum * 0x1p40f); };
+    auto fixed_sum = [](float sum) { return __float2ull_rn(sum * 0x1p40f); };
     auto warp_sum = [](u64 v) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -338,16 +348,25 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             }
         });
         u64 goal = (u64)k, everything = 0;
+        u64 drop = 0;   // weight that top-p may leave out, in units of 2^-64
         tell({0, 0, 0, by_weight ? total(fixed_sum(sum)) : 0});   // and the histograms are there
         if (by_weight) {
-            const u64 at_T = T ? fixed40(weight(key_logit(T))) : 0;
             for (int c = 0; c < C; c++) everything += told[turn][c].sum;
-            goal = max((u64)ceil((double)fmaxf(p, 0.f) * (double)(everything + r * at_T)), (u64)1);
-            if (goal > everything && T) {   // among the tokens at T
-                if (at_T) r = min(r, (goal - everything + at_T - 1) / at_T);
-                cl.sync();                  // the histograms are read no more
-                continue;
+            if (T) {
+                const double at_T = (double)weight(key_logit(T)) * 0x1p40, ties = (double)r * at_T, all = (double)everything + ties;
+                const double out = (1. - (double)fmaxf(p, 0.f)) * all - ties;   // of the tokens above T
+                if (out < 0.) {   // among the tokens at T
+                    r -= min((u64)((out + ties) / at_T), r - 1);
+                    cl.sync();     // the histograms are read no more
+                    continue;
+                }
+                goal = (u64)ceil((double)fmaxf(p, 0.f) * all), drop = (u64)fmin(out * 0x1p24, 0x1p62);
+            } else {
+                goal = part_up(everything, fraction(p));
+                const u64 not_p = ~fraction(p) + 1, hi = __umul64hi(everything, not_p);
+                drop = hi >> 38 || !not_p ? 1ull << 62 : hi << 24 | (everything * not_p) >> 40;
             }
+            goal = max(goal, (u64)1);
         }
         u64 h = 0;
         if (tid < kBins) {
@@ -427,7 +446,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 const u64 kept = total(w);
                 bool keep = tid < n && mine < k;
                 if (p < 1.f) {
-                    const u64 g = max((u64)ceil((double)fmaxf(p, 0.f) * (double)kept), (u64)1);
+                    const u64 g = max(part_up(kept, fraction(p)), (u64)1);
                     u64 ahead = 0;
                     if (keep)
 #pragma unroll 4
@@ -439,8 +458,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 w = keep ? w : 0;
                 if (tid < n) hist[tid] = w;
                 const u64 all_kept = total(w);
-                u64 target = (u64)((double)u * (double)all_kept);
-                if (target >= all_kept) target = all_kept - 1;
+                const u64 target = __umul64hi(all_kept, fraction(u));
                 u64 run = 0;
                 if (w)
 #pragma unroll 4
@@ -503,13 +521,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         // those of the bin, where they are too many to list; then, where step 1's
         // rounding named a neighbour of T's bin and where T is below the octaves,
         // all.  A sub-bin's weight is exact: the sum of its tokens', or where it
-        // is one key their count times its weight.
+        // is one key their count times its weight.  Tokens below the octaves are
+        // held in units of 2^-64, and what is left out of them is what counts: the
+        // goal itself, next to 1, has no bits for them.
         constexpr int KS = BF16 ? 16 : 0;   // a bf16 logit's key is its upper half
         auto full = [](uint32_t q) { return BF16 ? q << 16 | (q & 0x8000u ? 0u : 0xFFFFu) : q; };
 #pragma unroll 1
         for (int whole = in_bin ? 0 : 1; whole < 2 && !found; whole++) {
             uint32_t lo = 1 >> KS, hi = km >> KS;
-            u64 at = 0;
+            u64 at = 0, need = goal;
+            const bool tail = by_weight && bin < 0;
+            bool look = tail;   // is the sum of the tokens below the octaves still to be seen?
+            auto exact = [&](float w) { return tail ? units(1, w, 24) : fixed40(w); };
             cl.sync();   // what was read of other CTAs is read no more
             if (!whole) {
                 uint32_t l = 0xFFFFFFFFu, m = 0;
@@ -538,8 +561,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                         const uint32_t key = order_key(x[e]) >> KS;
                         if (!(x[e] > over) || key < lo || key > hi) continue;
                         const float w = weight(x[e]);
-                        if (!whole && bin_of(w) != bin) continue;
-                        if (sums) atomicAdd(&hist[(hi - key) >> shift], fixed40(w));
+                        if (tail ? bin_of(w) < kBins : !whole && bin_of(w) != bin) continue;
+                        if (sums) atomicAdd(&hist[(hi - key) >> shift], exact(w));
                         else atomicAdd(&hist32[(hi - key) >> shift], 1u);
                     }
                 });
@@ -549,9 +572,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
 #pragma unroll
                     for (int c = 0; c < kMaxCluster; c++)
                         if (c < C) h += sums ? remote_u64(remote(hist + tid, c)) : remote_u32(remote(hist32 + tid, c));
-                    if (by_weight && !shift && h) h *= fixed40(weight(key_logit(full(hi - tid))));
+                    if (by_weight && !shift && h) h *= exact(weight(key_logit(full(hi - tid))));
                 }
-                const int sub = find(h, goal - at);
+                if (look) {
+                    look = false;
+                    const u64 of_tail = total(h);
+                    need = of_tail > drop ? of_tail - drop : 1;
+                }
+                const int sub = find(h, need - at);
                 cl.sync();
                 if (sub < 0) break;
                 at += s_above;
@@ -559,10 +587,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 lo = max(lo, top_key - min(width, top_key)), hi = top_key;
                 found = !shift;
             }
-            T_new = full(hi), rest = goal - at;
+            T_new = full(hi), rest = need - at;
         }
         if (found) {
-            const u64 w = by_weight ? fixed40(weight(key_logit(T_new))) : 1;
+            const float w_T = weight(key_logit(T_new));
+            const u64 w = !by_weight ? 1 : bin < 0 ? units(1, w_T, 24) : fixed40(w_T);
             T = T_new, r = (rest + w - 1) / w;
         } else if (!by_weight) {
             T = 0, r = 0;   // fewer than k tokens
@@ -570,9 +599,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         cl.sync();   // lists, histograms and what was told are read no more
     }
 
-    // the kept weight of each warp's part, and its tokens at T.  Sums are
-    // rounded up, lane by lane and over the tokens at T (the n-th of them adds
-    // at_T(n) - at_T(n - 1)): a part with a token to choose is never nothing.
+    // the kept weight of each warp's part, and its tokens at T.  A lane's sum is
+    // at least one unit, the sum over the tokens at T is rounded up (the n-th of
+    // them adds at_T(n) - at_T(n - 1)): a part with a token to choose is never
+    // nothing.
     const float xT = T ? key_logit(T) : -INFINITY;
     const float wT = T ? weight(xT) : 0.f;
     auto at_T = [&](u64 n) { return wT >= least ? units(min(n, r), wT) : 0; };
@@ -587,7 +617,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             ties += x[e] == xT;   // (-inf where no logit is at T: not counted below, as r is 0)
         }
     });
-    u64 mass = warp_sum(__float2ull_ru(sum * 0x1p40f));
+    u64 mass = warp_sum(max(fixed_sum(sum), (u64)(sum > 0.f)));
     ties = __reduce_add_sync(0xffffffffu, ties);
     if (lane == 0) wmass[warp] = mass, wties[warp] = ties;
     __syncthreads();
@@ -607,8 +637,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         if (c == rank) own = m;
         kept += m, tsum += ct;
     }
-    u64 target = (u64)((double)u * (double)kept);   // the first token whose running sum exceeds u times the total
-    if (target >= kept) target = kept - 1;          // (u = 1 - 2^-24 rounds up to the total at most)
+    u64 target = __umul64hi(kept, fraction(u));   // the first token whose running sum exceeds u times the total
     if (target < base || target >= base + own) return;
     {
         const u64 t0 = tb + scan((u64)ties) - ties;   // tokens at T before the lane's warp

@@ -72,3 +72,36 @@ def test_sample_nucleus_at_the_edges_of_bins(dtype):
         at = rng.integers(50, V - 50, n)
         p = np.cumsum(w, 1)[np.arange(n), at] / w.sum(1) + shift
         base.check_sample(level, rng.random(n), p=p, dtype=dtype)
+
+
+@pytest.mark.parametrize("gap,steps", [(22.5, 150), (23.0, 90), (25.0, 15), (26.5, 4), (27.2, 2)])
+@pytest.mark.parametrize("k", [0, 100000])
+def test_sample_nucleus_that_ends_far_below_the_first(gap, steps, k):
+    # one token next to 1, the others e^-gap each, 1 - p about half of them; the largest u then falls just before the
+    # last kept ones.  Of their sum: weights are within 2^-21 of themselves and the first token's lane (of at least
+    # 512) loses what others it has, V / 512 of V: 2^-9 in all.
+    rng = np.random.default_rng(3)
+    V, n = 128000, 4
+    x = rng.normal(0, 0.3, (n, V)).astype(np.float32) - np.float32(gap)
+    x[:, 0] = 0.0
+    p = np.float32(1 - steps * 2.0 ** -24)
+    got = base.check_sample(x, LAST, p=p, k=k)
+    for r in range(n):
+        w = S.kept(x[r], 1.0, k, float(p), 0.0)
+        c = np.cumsum(w) - 1                                # of the others, up to each token
+        goal = max(float(LAST) * (1 + c[-1]) - 1, 0.0)      # 0: the first token itself
+        assert abs(c[got[r]] - goal) <= 2.0 ** -9 * c[-1], r
+
+
+@pytest.mark.parametrize("gap", [20.0, 24.0, 30.0])
+def test_sample_nucleus_cuts_equal_tokens_far_below_the_first(gap):
+    # top-k ends among equal tokens, and top-p leaves half of the kept ones of them: counted by u at their ends
+    V, n, k = 40000, 4, 30000
+    x = np.full((n, V), -gap, np.float32)
+    x[:, 0] = 0.0
+    tail = (k - 1) * np.exp(-gap)
+    p = np.float32(1 - 0.5 * tail)
+    got = base.check_sample(x, LAST, p=p, k=k)
+    c = np.cumsum(S.kept(x[0], 1.0, k, float(p), 0.0)) - 1
+    goal = max(float(LAST) * (1 + c[-1]) - 1, 0.0)
+    assert np.all(np.abs(c[got] - goal) <= 2.0 ** -9 * c[-1])
