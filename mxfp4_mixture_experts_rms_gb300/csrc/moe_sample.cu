@@ -17,10 +17,12 @@
 //     keys until one key is left.
 // A top-k of few tokens lists all of them in step 2 instead, and a CTA ranks
 // the list by comparing each with each: top-k, top-p and the choice itself
-// need nothing more of the row.  Where a bin's list does not fit, step 3 goes
-// over the row, and where step 1's rounding named a neighbour of T's bin or T
-// lies below the 32 octaves over all its keys (16 x 200 K logits within 0.1 of
-// one another: 189 us).  Sums are fp32 over a lane's
+// need nothing more of the row.  A bin with more tokens than a list holds is cut
+// into 512 by its weights' further bits, and listed then; only where a sub-bin
+// holds too many again, or T lies below the 32 octaves, the row is searched by
+// its keys (16 x 200 K logits within 0.1 of one another: 59 us).  Where step
+// 1's rounding named a neighbour of T's bin, that one is looked at next.  Sums
+// are fp32 over a lane's
 // logits and whole multiples of 2^-40 above that, so they do not depend on
 // their order.
 //
@@ -326,7 +328,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     uint32_t T = 0;
     u64 r = 0;
     if (!(t > 0.f)) T = km, r = 1;
-    for (int stage = 0; stage < 2 && t > 0.f; stage++) {
+#pragma unroll
+    for (int stage = 0; stage < 2 && t > 0.f; stage++) {   // (each its own code)
         const bool by_weight = stage == 1;
         if (by_weight ? !(p < 1.f) : !(k > 0 && k < a.V)) continue;
         const float over = T ? key_logit(T) : -INFINITY;   // what top-k left lies above, and r tokens at it
@@ -380,20 +383,23 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         const int bin = find(h, goal);
         // 2. what lies above the bin, and the bin's keys; few tokens: all of them
         u64 above = 0, rest = 0;   // the goal's part that the tokens at T fill
-        uint32_t T_new = 0;
-        bool found = false, in_bin = false;
-        if (bin >= 0) {
-            if (tid == bin) s_n = (int)min(s_above + h, (u64)INT_MAX);   // by count: tokens up to the bin
+        uint32_t T_new = 0, from = 0, span = 0;   // the bin's weights by their bits: from .. from + 2^span - 1
+        bool found = false, in_bin = bin >= 0, many = false;
+        if (in_bin) from = (uint32_t)((0x3F800000 >> kBinShift) - bin) << kBinShift, span = kBinShift;
+        // (step 1's rounding may name a neighbour of T's bin: the next ones then, a few times)
+#pragma unroll 1
+        for (int look = 0; look < 6 && in_bin && !found; look++) {
+            if (look == 0 && tid == bin) s_n = (int)min(s_above + h, (u64)INT_MAX);   // by count: tokens up to the bin
             __syncthreads();
-            const bool few = !by_weight && s_n <= kRank;
+            const bool few = look == 0 && !by_weight && s_n <= kRank;
             __syncthreads();
             if (tid == 0) s_n = 0, s_lo = 0xFFFFFFFFu, s_hi = 0;
             __syncthreads();
             float before = 0.f;
             int count = 0;
             // the bin's weights: from w_in up to w_up; listed: from w_in, up to w_end (NaN nowhere)
-            const float w_in = __uint_as_float((uint32_t)((0x3F800000 >> kBinShift) - bin) << kBinShift);
-            const float w_up = bin ? __uint_as_float((uint32_t)((0x3F800000 >> kBinShift) - bin + 1) << kBinShift) : INFINITY;
+            const bool first = span == kBinShift && from >= 0x3F800000u;   // with all weights of 1 and (by rounding) above
+            const float w_in = __uint_as_float(from), w_up = first ? INFINITY : __uint_as_float(from + (1u << span));
             const float w_end = few ? INFINITY : w_up;
             d.each([&](float (&x)[VE], int i) {
                 float w[VE];
@@ -419,11 +425,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             tell({0, s_n, 0, mine});
             bool listed = true;
             int n = 0, base = 0;
+            u64 sum = 0;
             for (int c = 0; c < C; c++) {
-                above += told[turn][c].sum, listed = listed && told[turn][c].n <= kList;
+                sum += told[turn][c].sum, listed = listed && told[turn][c].n <= kList;
                 if (c < rank) base += told[turn][c].n;
                 n += told[turn][c].n;
             }
+            if (span == kBinShift) above = sum;   // (of a sub-bin it has been summed)
             if (few && n <= kRank) {
                 // all that top-k can keep, in the first CTA: each token against each
                 uint2 *to = cl.map_shared_rank(all, 0);
@@ -466,9 +474,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 if (w && target >= run && target < run + w) a.ids[row] = (int)me.y;
                 return;
             }
-            in_bin = above < goal;
-            // 3. by keys: of the lists (every CTA all of them), else of the row
-            if (listed && in_bin && n <= kKeys) {
+            // 3. by keys: of the lists (every CTA all of them)
+            if (above >= goal) {
+                in_bin = span == kBinShift && !first;
+                from += 1u << kBinShift;
+            } else if (listed && n <= kKeys) {
                 // into this CTA's own copy, a warp a list at a time
                 uint32_t l = 0xFFFFFFFFu, m = 0;
                 int to = 0;
@@ -514,24 +524,65 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                     found = !shift;
                 }
                 T_new = hi, rest = goal - at;
-                in_bin = false;   // where the goal is not reached in the list, it lies in another bin
+                if (found) break;
+                in_bin = span == kBinShift;
+                from -= 1u << kBinShift;
+                cl.sync();   // the lists are read no more
+            } else if (span < kBinShift) {
+                many = true, in_bin = false;
+            } else {
+                // too many: 512 sub-bins of the weights, and the one that holds T is listed.  Their sums are exact, by
+                // count and by what the bits that are left add.
+                const int s = kBinShift - 9;
+                uint32_t *const low = reinterpret_cast<uint32_t *>(hist);
+                for (int b = tid; b < kBins; b += NT) hist32[b] = low[b] = 0;
+                __syncthreads();
+                d.each([&](float (&x)[VE], int) {
+                    float w[VE];
+                    weights(x, w);
+#pragma unroll
+                    for (int e = 0; e < VE; e++) {
+                        const uint32_t bits = __float_as_uint(w[e]) - from;
+                        if (!(x[e] > over) || bits >> kBinShift) continue;
+                        atomicAdd(&hist32[(bits >> s) ^ (kBins - 1)], 1u);   // downwards
+                        if (by_weight) atomicAdd(&low[(bits >> s) ^ (kBins - 1)], bits & ((1u << s) - 1));   // of at most 2^22 tokens
+                    }
+                });
+                cl.sync();
+                h = 0;
+                const uint32_t w0 = from + ((uint32_t)(tid ^ (kBins - 1)) << s);   // the sub-bin's least weight
+                if (tid < kBins) {
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; c++)
+                        if (c < C) {
+                            const u64 in = remote_u32(remote(hist32 + tid, c));
+                            h += by_weight ? in * ((w0 & 0x7FFFFFu) | 0x800000u) + remote_u32(remote(low + tid, c)) : in;
+                        }
+                    const int up = (int)(w0 >> 23) - 110;   // from units of the octave to 2^-40
+                    if (by_weight) h = up >= 0 ? h << up : (h + (1ull << -up >> 1)) >> -up;
+                }
+                const int sub = find(h, goal - above);
+                cl.sync();
+                in_bin = sub >= 0;
+                if (in_bin) above += s_above, from += (uint32_t)(sub ^ (kBins - 1)) << s, span = s;
             }
         }
         // The row's own keys, in steps of 2^9 sub-bins that end at single keys:
-        // those of the bin, where they are too many to list; then, where step 1's
-        // rounding named a neighbour of T's bin and where T is below the octaves,
-        // all.  A sub-bin's weight is exact: the sum of its tokens', or where it
-        // is one key their count times its weight.  Tokens below the octaves are
-        // held in units of 2^-64, and what is left out of them is what counts: the
-        // goal itself, next to 1, has no bits for them.
+        // those of the sub-bin, where even they are too many to list; where T is
+        // below the octaves, or has not been found, all.  A sub-bin's weight is
+        // exact: the sum of its tokens', or where it is one key their count times
+        // its weight.  Tokens below the octaves are held in units of 2^-64, and
+        // what is left out of them is what counts: the goal itself, next to 1, has
+        // no bits for them.
         constexpr int KS = BF16 ? 16 : 0;   // a bf16 logit's key is its upper half
+        auto in_span = [&](float w) { return (__float_as_uint(w) - from) >> span == 0; };
         auto full = [](uint32_t q) { return BF16 ? q << 16 | (q & 0x8000u ? 0u : 0xFFFFu) : q; };
 #pragma unroll 1
-        for (int whole = in_bin ? 0 : 1; whole < 2 && !found; whole++) {
+        for (int whole = many ? 0 : 1; whole < 2 && !found; whole++) {
             uint32_t lo = 1 >> KS, hi = km >> KS;
             u64 at = 0, need = goal;
             const bool tail = by_weight && bin < 0;
-            bool look = tail;   // is the sum of the tokens below the octaves still to be seen?
+            bool unseen = tail;   // is the sum of the tokens below the octaves still to be seen?
             auto exact = [&](float w) { return tail ? units(1, w, 24) : fixed40(w); };
             cl.sync();   // what was read of other CTAs is read no more
             if (!whole) {
@@ -539,7 +590,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 d.each([&](float (&x)[VE], int) {
 #pragma unroll
                     for (int e = 0; e < VE; e++)
-                        if (x[e] > over && bin_of(weight(x[e])) == bin) l = min(l, order_key(x[e])), m = max(m, order_key(x[e]));
+                        if (x[e] > over && in_span(weight(x[e]))) l = min(l, order_key(x[e])), m = max(m, order_key(x[e]));
                 });
                 l = __reduce_min_sync(0xffffffffu, l), m = __reduce_max_sync(0xffffffffu, m);
                 if (lane == 0) atomicMin(&s_lo, l), atomicMax(&s_hi, m);
@@ -561,7 +612,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                         const uint32_t key = order_key(x[e]) >> KS;
                         if (!(x[e] > over) || key < lo || key > hi) continue;
                         const float w = weight(x[e]);
-                        if (tail ? bin_of(w) < kBins : !whole && bin_of(w) != bin) continue;
+                        if (tail ? bin_of(w) < kBins : !whole && !in_span(w)) continue;
                         if (sums) atomicAdd(&hist[(hi - key) >> shift], exact(w));
                         else atomicAdd(&hist32[(hi - key) >> shift], 1u);
                     }
@@ -574,8 +625,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                         if (c < C) h += sums ? remote_u64(remote(hist + tid, c)) : remote_u32(remote(hist32 + tid, c));
                     if (by_weight && !shift && h) h *= exact(weight(key_logit(full(hi - tid))));
                 }
-                if (look) {
-                    look = false;
+                if (unseen) {
+                    unseen = false;
                     const u64 of_tail = total(h);
                     need = of_tail > drop ? of_tail - drop : 1;
                 }
