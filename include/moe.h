@@ -535,9 +535,10 @@ int moe_kv8_set_cache(moe_kv8 *plan, uint8_t *k, uint8_t *v, uint8_t *k_scales, 
  * [q_heads], device, borrowed); NULL: none. */
 int moe_kv8_set_sinks(moe_kv8 *plan, const float *sinks);
 /* Device workspace of moe_kv8_attend, whatever the call's sizes: caller-owned,
- * 256-byte aligned, borrowed (moe_kv8_set_workspace clears its tickets; it
- * synchronises the device, so it is not called while a stream is captured, nor
- * while an attend of a plan that shares the workspace runs).  Plans whose
+ * 256-byte aligned, borrowed (moe_kv8_set_workspace clears its tickets, after
+ * all that is queued on the device and before it returns: it synchronises the
+ * device, so it is not called while a stream is captured, nor while another
+ * thread launches an attend of a plan that shares the workspace).  Plans whose
  * attends follow one another on one stream may share it; attends that can
  * overlap on the GPU need one each. */
 size_t moe_kv8_workspace_bytes(const moe_kv8 *plan);

@@ -385,7 +385,11 @@ int moe_kv8_set_workspace(moe_kv8 *p, void *dev, size_t bytes) {
     if ((uintptr_t)dev & 255u) return moe_fail_status(MOE_EINVAL, "the workspace must be 256-byte aligned");
     const size_t need = kv8_workspace_bytes(p->c.D);
     if (bytes < need) return moe_fail_status(MOE_ENOMEM, "workspace of %zu bytes, %zu needed", bytes, need);
-    const cudaError_t e = cudaMemset(dev, 0, kKv8ClearBytes);
+    // what is queued on any stream may still use the memory, and what is queued
+    // next may be on a stream that does not wait for the one of the memset
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemset(dev, 0, kKv8ClearBytes);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return moe_fail_status(MOE_ECUDA, "moe_kv8_set_workspace: %s", cudaGetErrorString(e));
     p->ws = static_cast<unsigned char *>(dev);
     return MOE_OK;

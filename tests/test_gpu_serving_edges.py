@@ -1,5 +1,6 @@
 """The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
-nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens.
+nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens;
+plans made while streams are busy.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -105,3 +106,33 @@ def test_sample_nucleus_cuts_equal_tokens_far_below_the_first(gap):
     c = np.cumsum(S.kept(x[0], 1.0, k, float(p), 0.0)) - 1
     goal = max(float(LAST) * (1 + c[-1]) - 1, 0.0)
     assert np.all(np.abs(c[got] - goal) <= 2.0 ** -9 * c[-1])
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("busy", ["default", "own"])
+def test_a_plan_made_while_streams_are_busy(busy):
+    # its workspace is cleared after what is queued on the block of memory that it gets, and before its own first call
+    import torch
+    rng = np.random.default_rng(8)
+    P, D, kv, H, lens = 64, 64, 1, 8, [9000, 20, 4000]
+    c, table = base.sequences(rng, P, lens, [1] * 3, 141, 220, kv, D, poison=False)
+    d, ld, td = [base.dev(x) for x in c], base.dev(np.array(lens, np.int32)), base.dev(table)
+    qd, q = base.bf16(rng.normal(0, 0.25, (3, H, D)))
+    size = base.moe().Kv8(H, kv, D, P, 220, cache=d).ws.numel()
+    ref, tol = S.attend(*c, P, q, range(4), lens, table)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            old = torch.empty(size, dtype=torch.uint8, device="cuda")
+            with torch.cuda.stream(torch.cuda.default_stream() if busy == "default" else side):
+                torch.cuda._sleep(20_000_000)               # some 10 ms
+            old.fill_(255)
+            del old
+            plan = base.moe().Kv8(H, kv, D, P, 220, cache=d)
+            out = torch.zeros((3, H, D), dtype=torch.bfloat16, device="cuda")
+            plan.attend(qd, ld, td, out)
+        side.synchronize()
+        assert (np.abs(out.double().cpu().numpy() - ref) / tol).max() <= 1
+        assert plan.device_status() == 0
