@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy into the stage
+                __syncwarp();                                                  // and before other lanes read the values
                 // a NaN that only some rows see: those rows' values apart (below)
                 odd = __any_sync(0xffffffffu, nan != 0 && pmin != pmax);
             }
@@ -505,7 +506,6 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                     }
             } else {
                 // one position's rows at a time, with only the values that they see
-                __syncwarp();
 #pragma unroll 1
                 for (int p = pmin; p <= pmax; p++) {
                     uint32_t keep[2] = {0, 0};

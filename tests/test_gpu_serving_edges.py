@@ -1,6 +1,6 @@
 """The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
 nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens;
-plans made while streams are busy.
+plans made while streams are busy; NaN in every hidden place.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -136,3 +136,13 @@ def test_a_plan_made_while_streams_are_busy(busy):
         side.synchronize()
         assert (np.abs(out.double().cpu().numpy() - ref) / tol).max() <= 1
         assert plan.device_status() == 0
+
+
+@pytest.mark.parametrize("P,D", [(16, 64), (32, 128), (64, 64)])
+@pytest.mark.parametrize("H", [4, 16])
+def test_attend_nan_in_every_place_behind_a_sequence(P, D, H):
+    # what a sequence does not see is set to 0 in shared memory by other lanes than those that read it
+    rng = np.random.default_rng(9)
+    base.check_attend(rng, P, D, 1, H, list(range(1, 130)), [1] * 129)
+    base.check_attend(rng, P, D, 1, H, list(range(40, 140)), [1] * 100, window=37)
+    base.check_attend(rng, P, D, 1, H, list(range(4, 70)), [3] * 66, sinks=False)
