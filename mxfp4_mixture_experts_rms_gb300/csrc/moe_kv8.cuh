@@ -83,6 +83,9 @@ __device__ __forceinline__ void kv8_rows(const Kv8Attend &a, int b, int &row0, i
     pos0 = len - all;
 }
 
+// The first token that a row at position pos sees (one below 0 sees none).
+__device__ __forceinline__ int kv8_first(int pos, int window) { return window > 0 ? max(0, max(pos, 0) - window + 1) : 0; }
+
 cudaError_t launch_kv8_append(const Kv8Cache &c, const uint16_t *k, const uint16_t *v, long long k_stride,
                               long long v_stride, const int32_t *slots, int n, cudaStream_t st);
 cudaError_t launch_kv8_attend(const Kv8Attend &a, unsigned char *ws, cudaStream_t st);

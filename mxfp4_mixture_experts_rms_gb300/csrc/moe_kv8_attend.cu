@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
         int row0, n, pos0;
         kv8_rows(a, b, row0, n, pos0);
         seen = (int)max(0ll, min((long long)a.lens[b], (long long)a.width * P));
-        first = a.window > 0 ? max(0, pos0 - a.window + 1) / kTile : 0;
+        first = kv8_first(pos0, a.window) / kTile;
         return n > 0 ? max(1, (seen + kTile - 1) / kTile - first) * ((n * f.G + kRows - 1) / kRows) : 0;
     };
     int mine = 0, first, seen_b;
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
 #pragma unroll
                         for (int r = 0; r < (TOP ? 2 : 1); r++)
                             if (!(there(n, t) && sees(t, pos[r]))) s[n][2 * r + e] = -INFINITY;
-                        if (there(n, t) && t <= pmax && (a.window == 0 || t > pmin - a.window)) keep[n / 2] |= 0xFFu << (16 * (n & 1) + 8 * e);
+                        if (there(n, t) && t <= pmax && t >= kv8_first(pmin, a.window)) keep[n / 2] |= 0xFFu << (16 * (n & 1) + 8 * e);
                     }
                 // values that no row sees to zero: nothing they hold may meet a weight of 0
                 uint32_t nan = 0;

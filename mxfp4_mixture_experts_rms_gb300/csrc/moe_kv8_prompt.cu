@@ -219,7 +219,7 @@ __device__ void slow_row(const Kv8Attend &a, int b, int kvh, int head, int row, 
     float *qs = scratch, *p = qs + D, *vsc = p + 128, *red = vsc + 128;
     const uint8_t **vat = reinterpret_cast<const uint8_t **>(red + 128);
     auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    const int last = (int)min((long long)pos, (long long)a.width * P - 1), first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    const int last = (int)min((long long)pos, (long long)a.width * P - 1), first = kv8_first(pos, a.window);
     const uint16_t *q = a.q + (long long)row * a.q_stride + head * D;
     sync();
     for (int d = tid; d < D; d += 128) qs[d] = bf16_to_f32(q[d]) * a.scale;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
         const int p_first = pos0 + r0 / f.G, p_last = pos0 + (r0 + rows - 1) / f.G;
         // tokens that any row sees, and the steps over them (aligned to 64)
         const int seen = (int)max(0ll, min((long long)p_last + 1, (long long)a.width * P));
-        const int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+        const int lo = kv8_first(p_first, a.window);
         const int step0 = lo / kT, steps = max(1, (seen + kT - 1) / kT - step0);
         int32_t *status = f.status;
 
@@ -350,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                 const int r = tid & (kM - 1), rr = r0 + h * kM + r, i2 = rr / f.G, head = kvh * f.G + rr - i2 * f.G;
                 const bool on = h * kM + r < rows;
                 // tokens from .. to that the row sees, and all_from .. all_to that all rows of the half see (where their pages are)
-                const int to = on ? min(seen - 1, pos0 + i2) : -1, from = a.window ? pos0 + i2 - a.window + 1 : 0;
+                const int to = on ? min(seen - 1, pos0 + i2) : -1, from = kv8_first(pos0 + i2, a.window);
                 const int all_to = min(seen - 1, pos0 + (r0 + h * kM) / f.G);
-                const int all_from = a.window ? pos0 + (r0 + min(rows, (h + 1) * kM) - 1) / f.G - a.window + 1 : 0;
+                const int all_from = kv8_first(pos0 + (r0 + min(rows, (h + 1) * kM) - 1) / f.G, a.window);
                 int up;
                 {
                     // the row's queries, scaled by a power of two: largest magnitude in [2^14, 2^15)

@@ -1,6 +1,7 @@
 """The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
 nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens;
-plans made while streams are busy; NaN in every hidden place.
+plans made while streams are busy; NaN in every hidden place; the largest
+windows.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -146,3 +147,12 @@ def test_attend_nan_in_every_place_behind_a_sequence(P, D, H):
     base.check_attend(rng, P, D, 1, H, list(range(1, 130)), [1] * 129)
     base.check_attend(rng, P, D, 1, H, list(range(40, 140)), [1] * 100, window=37)
     base.check_attend(rng, P, D, 1, H, list(range(4, 70)), [3] * 66, sinks=False)
+
+
+@pytest.mark.parametrize("rows", [[6, 1], [40, 3]])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 30])
+def test_attend_the_largest_windows(rows, window):
+    # with rows before the sequence's beginning: position - window goes past 32 bits
+    rng = np.random.default_rng(4)
+    base.check_attend(rng, 16, 64, 2, 8, [3, 200], rows, window=window)
+    base.check_attend(rng, 64, 128, 2, 8, [rows[0] - 1, 200], rows, window=window, sinks=False)
