@@ -581,7 +581,8 @@ int moe_kv8_append(moe_kv8 *plan, const uint16_t *k, const uint16_t *v, long lon
  * rounded to bf16; 0 for a row that sees no token.  What a row does not see
  * does not touch its result, whatever it holds.  max_new: rows of a sequence
  * that are computed, at most 65535; rows past it, rows of no sequence, and
- * rows from n_rows on are left as they are.  A sequence of one row among long
+ * rows from n_rows on are left as they are (starts may go past n_rows: the rows
+ * before it keep their positions).  A sequence of one row among long
  * prompts is better served by a call of its own kind: the kernel and its split
  * of the work are chosen by max_new. */
 int moe_kv8_attend(moe_kv8 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,

@@ -68,19 +68,19 @@ struct Kv8Attend {
 };
 
 // The rows of sequence b: first row, rows that are computed, and the position
-// of the first (lens - the sequence's rows; negative: those see nothing).
-// Whatever starts holds, the rows stay inside 0 .. n_rows - 1.
+// of the first (lens - the sequence's rows from it on, past n_rows too;
+// negative: those see nothing).  Whatever starts holds, the rows stay inside
+// 0 .. n_rows - 1.
 __device__ __forceinline__ void kv8_rows(const Kv8Attend &a, int b, int &row0, int &n, int &pos0) {
     const int len = max(a.lens[b], 0);
     if (!a.starts) {
         row0 = b, n = 1, pos0 = len - 1;
         return;
     }
-    const int s = a.starts[b], e = a.starts[b + 1];
-    row0 = min(max(s, 0), a.n_rows);
-    const int all = min(max(e, row0), a.n_rows) - row0;
-    n = min(all, a.max_new);
-    pos0 = len - all;
+    row0 = min(max(a.starts[b], 0), a.n_rows);
+    const int e = max(a.starts[b + 1], row0);
+    n = min(min(e, a.n_rows) - row0, a.max_new);
+    pos0 = len - (e - row0);
 }
 
 // The first token that a row at position pos sees (one below 0 sees none).

@@ -1,7 +1,7 @@
 """The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
 nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens;
 plans made while streams are busy; NaN in every hidden place; the largest
-windows.
+windows; a sequence that goes on past the rows.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -156,3 +156,23 @@ def test_attend_the_largest_windows(rows, window):
     rng = np.random.default_rng(4)
     base.check_attend(rng, 16, 64, 2, 8, [3, 200], rows, window=window)
     base.check_attend(rng, 64, 128, 2, 8, [rows[0] - 1, 200], rows, window=window, sinks=False)
+
+
+@pytest.mark.parametrize("rows", [[5, 7, 4], [30, 90, 8]])
+@pytest.mark.parametrize("window", [0, 20])
+def test_attend_a_sequence_that_goes_on_past_the_rows(rows, window):
+    # as where the page tables had room for fewer tokens than there are: the rows that are there keep their positions
+    import torch
+    rng = np.random.default_rng(5)
+    P, D, kv, H, lens = 16, 64, 2, 8, [50, 130, 70]
+    c, table = base.sequences(rng, P, lens, rows, 9, 30, kv, D, poison=False)
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    qd, q = base.bf16(rng.normal(0, 0.25, (starts[-1], H, D)))
+    plan = base.moe().Kv8(H, kv, D, P, 30, sliding_window=window, cache=[base.dev(x) for x in c])
+    ref, tol = S.attend(*c, P, q, starts, lens, table, window, floor=2.0 ** -31)
+    for n in (starts[1] + 2, starts[2] - 1, starts[2] + 1):
+        out = torch.full((starts[-1], H, D), 7.5, dtype=torch.bfloat16, device="cuda")
+        plan.attend(qd[:n], base.dev(np.array(lens, np.int32)), base.dev(table), out[:n], starts=base.dev(starts), max_new=max(rows))
+        got = out.double().cpu().numpy()
+        assert (np.abs(got[:n] - ref[:n]) / tol[:n]).max() <= 1
+        assert np.all(got[n:] == 7.5)
