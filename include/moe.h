@@ -578,7 +578,8 @@ int moe_kv8_append(moe_kv8 *plan, const uint16_t *k, const uint16_t *v, long lon
  * head
  *   out = sum_t p_t v_t,  p = softmax over the seen tokens' softmax_scale q . k_t
  *                             and the head's sink logit, if the plan has sinks
- * rounded to bf16; 0 for a row that sees no token.  What a row does not see
+ * rounded to bf16; 0 for a row that sees no token (scores beyond fp32's range:
+ * NaN).  What a row does not see
  * does not touch its result, whatever it holds.  max_new: rows of a sequence
  * that are computed, at most 65535; rows past it, rows of no sequence, and
  * rows from n_rows on are left as they are (starts may go past n_rows: the rows

@@ -455,7 +455,8 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                     const float fac = ex2(fminf((float)((int)((mt[p] >> 8) & 255u) - 112) - Ns, 126.f));
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        const float w = ex2(fmaf(s[n][2 * r + e], ks[p], -ms));
+                        // the product rounded as the maximum was: a score past 2^24 is off by more than 1 otherwise
+                        const float w = ex2(__fsub_rn(__fmul_rn(s[n][2 * r + e], ks[p]), ms));
                         sum += w;
                         s[n][2 * r + e] = w * fac;
                     }

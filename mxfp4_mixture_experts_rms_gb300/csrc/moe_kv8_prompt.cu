@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                     }
                     auto key_scale = [&](int p) { return fmaxf(pow2i((int)(mt[p] & 255u) - 127 - up) * sc, 1e-37f); };   // > 0: -inf stays
                     auto value_exp = [&](int p) { return (float)((int)((mt[p] >> 8) & 255u) - 127); };
-                    float mx = -INFINITY, mv = -INFINITY;
+                    float mx = -INFINITY, mv = -INFINITY, pm[NP];   // mv: over m
 #pragma unroll
                     for (int p = 0; p < NP; p++) {
                         float x[4];   // four chains
@@ -419,19 +419,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                             if (c + 4 < P && (c / 4) % 2 == 1) x[c % 4] = max3(x[c % 4], s[p * P + c], s[p * P + c + 4]);
                             else if (c + 4 >= P && (c / 4) % 2 == 1) x[c % 4] = fmaxf(x[c % 4], s[p * P + c]);
                         }
-                        const float pm = fmaxf(max3(x[0], x[1], x[2]), x[3]) * key_scale(p);
-                        mx = fmaxf(mx, pm), mv = fmaxf(mv, pm + value_exp(p));
+                        pm[p] = fmaxf(max3(x[0], x[1], x[2]), x[3]) * key_scale(p);
+                        mx = fmaxf(mx, pm[p]), mv = fmaxf(mv, pm[p] - m + value_exp(p));   // (-inf - -inf passes over)
                     }
                     // the references follow when passed by more than 2^8
                     float corr = 1.f;
-                    const bool move = mx > m + 8.f || mv > N + 8.f + (m == -INFINITY ? 0.f : m);
+                    const bool move = mx > m + 8.f || mv > N + 8.f;
                     if (move) {
-                        const float mn = fmaxf(m, mx), was = N + (m - mn), nn = fmaxf(was, mv - mn);
+                        const float mn = fmaxf(m, mx), was = N + (m - mn);
+                        float nn = was;
+#pragma unroll
+                        for (int p = 0; p < NP; p++) nn = fmaxf(nn, pm[p] - mn + value_exp(p));
                         l *= ex2(m - mn);
                         corr = ex2(was - nn);
                         m = mn, N = nn;
                     }
                     const float ms = m == -INFINITY ? 0.f : m, Ns = N == -INFINITY ? 0.f : N;
+                    // large scores: differences first, each product rounded as the maximum was
+                    const bool large = __any_sync(0xffffffffu, fabsf(ms) >= 0x1p17f);
+                    if (large) {
+#pragma unroll
+                        for (int c = 0; c < kT; c++) s[c] = __fsub_rn(__fmul_rn(s[c], key_scale(c / P)), ms);
+                    }
                     // the products of the step before have read the P tile
                     if (j > 0) ok = bar_wait(&o_done[h], (uint32_t)(j - 1) & 1, status, 101) && ok;
                     if (__any_sync(0xffffffffu, move || !ok)) {
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                     }
 #pragma unroll
                     for (int p = 0; p < NP; p++) {
-                        const float fe = fmaxf(value_exp(p) - Ns, -80.f) + 7.f, bias = fe - ms, ks = key_scale(p);
+                        const float fe = fmaxf(value_exp(p) - Ns, -80.f) + 7.f, bias = large ? fe : fe - ms, ks = large ? 1.f : key_scale(p);
                         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                         for (int c = p * P; c < (p + 1) * P; c += 8) {

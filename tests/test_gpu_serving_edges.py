@@ -1,7 +1,8 @@
 """The serving operators on the GPU where they are easily wrong, against oracle/serving.py: tokens that weigh next to
 nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens;
 plans made while streams are busy; NaN in every hidden place; the largest
-windows; a sequence that goes on past the rows.
+windows; a sequence that goes on past the rows;
+scores that need more than 24 bits.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -176,3 +177,44 @@ def test_attend_a_sequence_that_goes_on_past_the_rows(rows, window):
         got = out.double().cpu().numpy()
         assert (np.abs(got[:n] - ref[:n]) / tol[:n]).max() <= 1
         assert np.all(got[n:] == 7.5)
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [3, 2], [40, 70]])
+@pytest.mark.parametrize("P,D,lo", [(16, 64, 135), (16, 64, 150), (64, 128, 155), (32, 64, 170)])
+def test_attend_large_scores(rows, P, D, lo):
+    # up to 2^60: their rounding is more than 1, and the largest one's weight still 1
+    rng = np.random.default_rng(6)
+
+    def change(c, table):
+        c[3][...] = rng.integers(120, 130, c[3].shape)      # the values' scales as usual
+
+    base.check_attend(rng, P, D, 2, 8, [100, 333], rows, lo=lo, hi=lo + 3, change=change, spread=4.0)
+    base.check_attend(rng, P, D, 1, 8, [100, 333], rows, lo=lo, hi=lo + 3, change=change, spread=4.0, window=70)
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [40, 30]])
+@pytest.mark.parametrize("P", [16, 64])
+def test_attend_one_large_score_takes_all(rows, P):
+    # every query and key a multiple of one direction: the last seen key is the longest by far, and its value the result
+    import torch
+    rng = np.random.default_rng(10)
+    D, lens = 64, [90, 120]
+    c, table = base.sequences(rng, P, lens, rows, 8, 20, 1, D, poison=False)
+    kk, vv = S.unpack(c[0], c[1], P, D)
+    for b, L in enumerate(lens):
+        for t in range(L):
+            kk[table[b, t // P], t % P] = 0x38 + t % 8          # 1 .. 1.875 times the page's scale
+            c[2][table[b, t // P]] = 127 + 24 + 2 * (t // P)
+    vv[...] = rng.integers(0x30, 0x40, vv.shape)                # values of one sign and size
+    c[:2] = S.pack(kk, vv)
+    c[3][...] = 127
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    n = int(starts[-1])
+    qd, q = base.bf16(np.full((n, 4, D), 3.0))
+    plan = base.moe().Kv8(4, 1, D, P, 20, cache=[base.dev(x) for x in c])
+    out = torch.zeros((n, 4, D), dtype=torch.bfloat16, device="cuda")
+    plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out, starts=base.dev(starts), max_new=max(rows))
+    got = out.double().cpu().numpy()
+    ref, _ = S.attend(*c, P, q, starts, lens, table)
+    # scores differ by 2^24 and more or not at all: sums of values and weights of exactly 1, and one division, in fp32
+    assert (np.abs(got - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -16)).all()
