@@ -126,8 +126,8 @@ __device__ __forceinline__ int request_from(const int *sum, int n, int x, int b)
 // Tables of wanted pages first, first + step, .. and slots and positions of
 // tokens likewise, four neighbours at a time.  n1: free pages before the pops.
 __device__ __forceinline__ void fill(const PagesArgs &a, const Requests &q, const Sums &total, int n1, int first, int step) {
-    for (int p = first; p < total.want; p += step) {
-        const int b = request_of(q.want, a.n, p), src = n1 - 1 - p;
+    for (unsigned at = first; at < (unsigned)total.want; at += step) {   // (at + step may pass 2^31)
+        const int p = (int)at, b = request_of(q.want, a.n, p), src = n1 - 1 - p;
         a.table[(size_t)b * a.width + pages_of(q.have[b], a) + (p - q.want[b])] = src >= 0 ? a.free_pages[src] : -1;
     }
     const int tokens = clamp_int(total.tok), most = INT_MAX / a.P;   // pages whose slots are 32-bit
@@ -170,7 +170,8 @@ template <bool SMALL, int T>
 __global__ void __launch_bounds__(T) moe_pages_push_kernel(const PagesArgs a) {
     extern __shared__ int smem[];
     __shared__ Sums part[T / 32];
-    __shared__ int wsum[T / 32], told[kCluster], s_base;
+    __shared__ int wsum[T / 32], told[kCluster];
+    __shared__ unsigned s_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int rank = 0, C = 1;
     if (!SMALL) {
@@ -191,21 +192,22 @@ __global__ void __launch_bounds__(T) moe_pages_push_kernel(const PagesArgs a) {
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             id[i] = -1;
-            if (x0 + i >= e1) continue;
+            if (i >= e1 - x0) continue;
             b = request_from(q.back, a.n, x0 + i, b);
             id[i] = a.table[(size_t)b * a.width + (x0 + i - q.back[b])];
             c += id[i] >= 0;
         }
         return c;
     };
-    int base = n_free, all = 0, id[kPer], got = 0;
+    int id[kPer], got = 0;
+    unsigned base = n_free, all = 0;   // places in the free list, with those past its end: up to 2^32 - 2
     const bool once = C > 1 && e1 - e0 <= kPer * T;   // what the first look loads is kept
     if (C > 1) {
         // entries that are there in each CTA's share
         int c = 0;
 #pragma unroll
         for (int i = 0; i < kPer; i++) id[i] = -1;
-        for (int x = e0 + kPer * tid; x < e1; x += kPer * T) c += got = load(x, id);
+        for (unsigned x = e0 + kPer * tid; x < (unsigned)e1; x += kPer * T) c += got = load((int)x, id);
         c = __reduce_add_sync(0xffffffffu, c);
         if (lane == 0) wsum[warp] = c;
         __syncthreads();
@@ -220,8 +222,8 @@ __global__ void __launch_bounds__(T) moe_pages_push_kernel(const PagesArgs a) {
     }
     if (tid == 0) s_base = base;
     __syncthreads();
-    for (int x = e0; x < e1; x += kPer * T) {
-        const int c = once ? got : load(x + kPer * tid, id);
+    for (unsigned x = e0; x < (unsigned)e1; x += kPer * T) {
+        const int c = once ? got : load((int)min(x + kPer * tid, (unsigned)e1), id);
         int inc = c;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -232,18 +234,18 @@ __global__ void __launch_bounds__(T) moe_pages_push_kernel(const PagesArgs a) {
         __syncthreads();
         const int ws = lane < T / 32 ? wsum[lane] : 0;
         const int sum = __reduce_add_sync(0xffffffffu, ws);
-        int at = s_base + inc - c + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
+        unsigned at = s_base + inc - c + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
 #pragma unroll
         for (int i = 0; i < kPer; i++)
             if (id[i] >= 0) {
-                if (at < a.cap) a.free_pages[at] = id[i];
+                if (at < (unsigned)a.cap) a.free_pages[at] = id[i];
                 at++;
             }
         __syncthreads();
         if (tid == 0) s_base += sum;
         __syncthreads();
     }
-    const int n1 = min(C > 1 ? n_free + all : s_base, a.cap);
+    const int n1 = (int)min(C > 1 ? n_free + all : s_base, (unsigned)a.cap);
     if (rank == 0) {
         for (int b = tid; b < a.n; b += T) {
             a.starts[b] = q.start[b];

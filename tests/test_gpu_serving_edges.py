@@ -2,7 +2,8 @@
 nothing beside another, parameters that are not numbers, thresholds among nearly equal tokens;
 plans made while streams are busy; NaN in every hidden place; the largest
 windows; a sequence that goes on past the rows;
-scores that need more than 24 bits.
+scores that need more than 24 bits; page
+tables and free lists of nearly 2^31 entries.
 
 Tolerances are those of test_gpu_serving.py."""
 import numpy as np
@@ -13,6 +14,60 @@ from oracle import serving as S
 
 pytestmark = pytest.mark.gpu
 LAST = np.float32(1 - 2.0 ** -24)       # the largest u
+
+
+# ---------------------------------------------------------------- page tables
+
+def big_pages(n, width, cached, fresh, table_fill, capacity, n_free, tokens):
+    """A call with P = 1; -> (table, free, counts_out, starts, lens, slots) on the GPU, and the table's and list's given tails."""
+    import torch
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")   # noqa: E731
+    table = torch.full((n, width), table_fill, dtype=torch.int32, device="cuda")
+    free = torch.full((capacity,), 5, dtype=torch.int32, device="cuda")
+    free[:min(n_free, 3000)] = torch.arange(min(n_free, 3000), dtype=torch.int32, device="cuda")
+    counts, out = i([n_free, 0]), i([0, 0])
+    cached, fresh = i([cached] * n), i([fresh] * n)
+    starts, lens, slots = i([9] * (n + 1)), i([9] * n), i([9] * tokens)
+    return table, free, counts, out, cached, fresh, starts, lens, slots
+
+
+WIDE = (2 ** 31 - 1) // 4096
+
+
+def test_pages_assign_of_nearly_2_31_wanted_pages():
+    import torch
+    table, free, counts, out, cached, fresh, starts, lens, slots = big_pages(4096, WIDE, 0, WIDE, 7, 1000, 1000, 1500)
+    base.moe().pages_assign(1, cached, fresh, free, counts, out, table, starts, lens, slots)
+    flat = table.view(-1)
+    assert out.tolist() == [0, 4096 * WIDE - 1000]
+    assert torch.equal(flat[:1000], torch.arange(999, -1, -1, dtype=torch.int32, device="cuda"))
+    assert bool((flat[1000:] == -1).all())
+    assert torch.equal(slots[:1000], flat[:1000]) and bool((slots[1000:] == -1).all())
+    assert starts[-1].item() == 4096 * WIDE and bool((lens == WIDE).all())
+
+
+def test_pages_assign_of_nearly_2_31_entries_given_back():
+    import torch
+    table, free, counts, out, cached, fresh, starts, lens, slots = big_pages(4096, WIDE, WIDE, -1, -1, 5000, 4, 10)
+    places = [0, 1, WIDE - 1, WIDE, 2000 * WIDE + 17, 4096 * WIDE - 2, 4096 * WIDE - 1]
+    table.view(-1)[torch.tensor(places, device="cuda")] = torch.arange(100, 107, dtype=torch.int32, device="cuda")
+    base.moe().pages_assign(1, cached, fresh, free, counts, out, table, starts, lens, slots)
+    assert out.tolist() == [11, 0] and free[:13].tolist() == [0, 1, 2, 3, *range(100, 107), 5, 5]
+    assert bool((starts == 0).all()) and bool((lens == 0).all()) and bool((slots == -1).all())
+
+
+def test_pages_assign_with_a_full_free_list_of_2_31_entries():
+    import torch
+    most = 2 ** 31 - 1
+    for n in (40, 3000):        # one kernel, and two
+        table, free, counts, out, cached, fresh, starts, lens, slots = big_pages(n, 20, 16, -1, 77, most, most, 30)
+        cached[-1], fresh[-1] = 0, 3
+        free[-3:] = torch.tensor([21, 22, 23], dtype=torch.int32, device="cuda")
+        base.moe().pages_assign(1, cached, fresh, free, counts, out, table, starts, lens, slots)
+        assert out.tolist() == [most - 3, 0]                    # what was given back had no room
+        assert table[-1, :4].tolist() == [23, 22, 21, 77] and slots[:4].tolist() == [23, 22, 21, -1]
+        assert free[-3:].tolist() == [21, 22, 23] and bool((free[3000:-3] == 5).all())
+        del table, free
 
 
 # ---------------------------------------------------------------- sampling
