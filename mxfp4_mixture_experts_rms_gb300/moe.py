@@ -479,39 +479,49 @@ def _dtypes():
     return _DTYPES
 
 
-def _arg(t, kind: str, count=None, what="tensor", none=False):
-    """Device address of a dense CUDA tensor of type `kind` and (where given)
-    `count` elements; None passes where `none` allows it."""
-    if t is None and none:
-        return None
-    if t is None or t.dtype is not (_DTYPES or _dtypes())[kind] or not t.is_cuda or not t.is_contiguous() or \
-            (count is not None and t.numel() != count):
-        raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {_dtypes()[kind]}"
-                                   + (f" ({count} elements)" if count is not None else "") + " is needed")
-    return t.data_ptr()
-
-
 _raw_stream = None
 
 
-def _stream(stream, t):
-    """cudaStream_t of `stream`, or of the current one; `t`, a tensor of the
-    call, must be on the current device."""
+def _device(t, what: str) -> int:
+    """The current device; `t`, a tensor of the call, must be on it."""
     global _raw_stream
+    if t is None or not t.is_cuda:
+        raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor is needed")
     if _raw_stream is None:
         import torch
         _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
     device = _raw_stream[1]()
     if t.get_device() != device:
-        raise MoeError(MOE_EINVAL, f"tensors on device {t.get_device()}, the current device is {device}")
-    return _raw_stream[0](device) if stream is None else stream.cuda_stream
+        raise MoeError(MOE_EINVAL, f"{what} is on device {t.get_device()}, the current device is {device}")
+    return device
 
 
-def _head_rows(t, heads: int, dim: int, what: str):
+def _arg(t, kind: str, device: int, count=None, what="tensor", none=False):
+    """Address of a dense tensor on `device` of type `kind` and (where given)
+    `count` elements; None passes where `none` allows it."""
+    if t is None and none:
+        return None
+    if t is None or t.dtype is not (_DTYPES or _dtypes())[kind] or t.get_device() != device or not t.is_contiguous() or \
+            (count is not None and t.numel() != count):
+        raise MoeError(MOE_EINVAL, f"{what}: a contiguous CUDA tensor of {_dtypes()[kind]} on device {device}"
+                                   + (f" ({count} elements)" if count is not None else "") + " is needed")
+    return t.data_ptr()
+
+
+def _stream(stream, device: int):
+    """cudaStream_t of `stream`, one of `device`, or of the current one."""
+    if stream is None:
+        return _raw_stream[0](device)
+    if stream.device.index != device:
+        raise MoeError(MOE_EINVAL, f"the stream is of device {stream.device.index}, the current device is {device}")
+    return stream.cuda_stream
+
+
+def _head_rows(t, heads: int, dim: int, device: int, what: str):
     """(address, row stride) of bf16 rows [n][heads][dim], dense but for the stride from row to row."""
     shape = t.shape
-    if not t.is_cuda or t.dtype is not (_DTYPES or _dtypes())["b2"] or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][{heads}][{dim}] is needed")
+    if t.get_device() != device or t.dtype is not (_DTYPES or _dtypes())["b2"] or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][{heads}][{dim}] on device {device} is needed")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != dim and heads > 1):
         raise MoeError(MOE_EINVAL, f"{what}: the heads of a row must lie side by side")
@@ -524,12 +534,13 @@ def pages_assign(page_size: int, cached, fresh, free_pages, counts, counts_out, 
     fresh [n] (below 0: finished), free_pages [capacity], counts [>= 1], counts_out [2], table [n][width],
     starts [n + 1], lens [n], slots [max_tokens], positions [max_tokens] or None."""
     n, width = table.shape
-    tokens = slots.numel()
+    tokens, d = slots.numel(), _device(table, "table")
     rc = (_lib or load()).moe_pages_assign(
-        int(page_size), n, _arg(cached, "i4", n, "cached"), _arg(fresh, "i4", n, "fresh"), _arg(free_pages, "i4", None, "free_pages"),
-        free_pages.numel(), _arg(counts, "i4", None, "counts"), _arg(counts_out, "i4", 2, "counts_out"), _arg(table, "i4", None, "table"),
-        width, _arg(starts, "i4", n + 1, "starts"), _arg(lens, "i4", n, "lens"), _arg(slots, "i4", None, "slots"),
-        _arg(positions, "i4", tokens, "positions", none=True), tokens, _stream(stream, table))
+        int(page_size), n, _arg(cached, "i4", d, n, "cached"), _arg(fresh, "i4", d, n, "fresh"),
+        _arg(free_pages, "i4", d, None, "free_pages"), free_pages.numel(), _arg(counts, "i4", d, None, "counts"),
+        _arg(counts_out, "i4", d, 2, "counts_out"), _arg(table, "i4", d, None, "table"), width, _arg(starts, "i4", d, n + 1, "starts"),
+        _arg(lens, "i4", d, n, "lens"), _arg(slots, "i4", d, None, "slots"), _arg(positions, "i4", d, tokens, "positions", none=True),
+        tokens, _stream(stream, d))
     if rc:
         _check(rc)
 
@@ -538,7 +549,8 @@ class Kv8:
     """One layer's paged key/value cache in 8 bits (moe_kv8_*): the plan, its workspace, and the arrays of
     codes and scales k, v [n_pages][kv_heads][page_size * head_dim], k_scale, v_scale [n_pages][kv_heads]
     (uint8; `cache` = (k, v, k_scale, v_scale) to use given ones).  `workspace`: another plan, used on the
-    same stream, whose workspace this one shares."""
+    same stream, whose workspace this one shares.  All of a plan's arrays are on one device, which is the
+    current one where its methods are called."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, n_pages: int, sliding_window: int = 0,
                  softmax_scale: float | None = None, sinks=None, cache=None, workspace: "Kv8 | None" = None, device="cuda"):
@@ -557,43 +569,57 @@ class Kv8:
         if cache is None:
             cache = [torch.zeros(s, dtype=torch.uint8, device=device) for s in (codes, codes, scales, scales)]
         self.k, self.v, self.k_scale, self.v_scale = cache
-        _check(self.L.moe_kv8_set_cache(self.h, _arg(self.k, "u1", n_codes, "k"), _arg(self.v, "u1", n_codes, "v"),
-                                        _arg(self.k_scale, "u1", n_scales, "k_scale"), _arg(self.v_scale, "u1", n_scales, "v_scale")))
+        d = self.device = self.k.get_device()   # whose tensors and streams the calls take
+        if d < 0:
+            raise MoeError(MOE_EINVAL, "k: a CUDA tensor is needed")
+        _check(self.L.moe_kv8_set_cache(self.h, _arg(self.k, "u1", d, n_codes, "k"), _arg(self.v, "u1", d, n_codes, "v"),
+                                        _arg(self.k_scale, "u1", d, n_scales, "k_scale"), _arg(self.v_scale, "u1", d, n_scales, "v_scale")))
         self.sinks = sinks
-        _check(self.L.moe_kv8_set_sinks(self.h, _arg(sinks, "f4", q_heads, "sinks", none=True)))
+        _check(self.L.moe_kv8_set_sinks(self.h, _arg(sinks, "f4", d, q_heads, "sinks", none=True)))
         n = int(self.L.moe_kv8_workspace_bytes(self.h))
-        self.ws = torch.empty(n + 256, dtype=torch.uint8, device=device) if workspace is None else workspace.ws
+        self.ws = torch.empty(n + 256, dtype=torch.uint8, device=self.k.device) if workspace is None else workspace.ws
         if self.ws.numel() < n + 256:
             raise MoeError(MOE_ENOMEM, "the shared workspace is too small for this plan")
-        _check(self.L.moe_kv8_set_workspace(self.h, self.ws.data_ptr() + (-self.ws.data_ptr()) % 256, n))
+        at = _arg(self.ws, "u1", d, None, "workspace")
+        with torch.cuda.device(d):
+            _check(self.L.moe_kv8_set_workspace(self.h, at + (-at) % 256, n))
+
+    def _on(self, t, what: str) -> int:
+        """The current device; `t` must be on it, and the plan too."""
+        d = _device(t, what)
+        if d != self.device:
+            raise MoeError(MOE_EINVAL, f"the cache is on device {self.device}, the current device is {d}")
+        return d
 
     def append(self, k, v, slots, stream=None):
         """k, v: bf16 [n][kv_heads][head_dim] (rows may be strided); slots: int32 [n]."""
-        kp, ks = _head_rows(k, self.kv_heads, self.head_dim, "k")
-        vp, vs = _head_rows(v, self.kv_heads, self.head_dim, "v")
+        d = self._on(k, "k")
+        kp, ks = _head_rows(k, self.kv_heads, self.head_dim, d, "k")
+        vp, vs = _head_rows(v, self.kv_heads, self.head_dim, d, "v")
         n = k.shape[0]
         if v.shape[0] != n:
             raise MoeError(MOE_EINVAL, "k and v must have the same number of rows")
-        rc = self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, "i4", n, "slots"), n, _stream(stream, k))
+        rc = self.L.moe_kv8_append(self.h, kp, vp, ks, vs, _arg(slots, "i4", d, n, "slots"), n, _stream(stream, d))
         if rc:
             _check(rc)
 
     def attend(self, q, lens, table, out, starts=None, max_new: int = 1, stream=None):
         """q, out: bf16 [n_rows][q_heads][head_dim] (rows may be strided); lens int32 [n_seqs]; table int32
         [n_seqs][width]; starts int32 [n_seqs + 1] (None: one row a sequence); max_new: most rows of a sequence."""
-        qp, qs = _head_rows(q, self.q_heads, self.head_dim, "q")
-        op, os_ = _head_rows(out, self.q_heads, self.head_dim, "out")
+        d = self._on(q, "q")
+        qp, qs = _head_rows(q, self.q_heads, self.head_dim, d, "q")
+        op, os_ = _head_rows(out, self.q_heads, self.head_dim, d, "out")
         n, width = table.shape
         if out.shape[0] != q.shape[0]:
             raise MoeError(MOE_EINVAL, "q and out must have the same number of rows")
-        rc = self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, "i4", n + 1, "starts", none=True), _arg(lens, "i4", n, "lens"),
-                                   _arg(table, "i4", None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream, q))
+        rc = self.L.moe_kv8_attend(self.h, qp, qs, _arg(starts, "i4", d, n + 1, "starts", none=True), _arg(lens, "i4", d, n, "lens"),
+                                   _arg(table, "i4", d, None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream, d))
         if rc:
             _check(rc)
 
     def device_status(self, stream=None) -> int:
         s = C.c_int(0)
-        rc = self.L.moe_kv8_get_device_status(self.h, C.byref(s), _stream(stream, self.ws))
+        rc = self.L.moe_kv8_get_device_status(self.h, C.byref(s), _stream(stream, self._on(self.ws, "the plan")))
         if rc not in (MOE_OK, MOE_EDEVICE):
             _check(rc)
         return s.value
@@ -615,13 +641,14 @@ def sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None,
     int32 [n]; temperature, top_p, min_p float32 [n] and top_k int32 [n], each may be None."""
     shape, kinds = logits.shape, _DTYPES or _dtypes()
     bf16 = logits.dtype is kinds["b2"]
-    if not logits.is_cuda or len(shape) != 2 or not (bf16 or logits.dtype is kinds["f4"]) or (logits.stride(1) != 1 and shape[1] > 1):
+    d = _device(logits, "logits")
+    if len(shape) != 2 or not (bf16 or logits.dtype is kinds["f4"]) or (logits.stride(1) != 1 and shape[1] > 1):
         raise MoeError(MOE_EINVAL, "logits: a CUDA tensor of fp32 or bf16 rows is needed")
     n, vocab = shape
     rc = (_lib or load()).moe_sample(
         logits.data_ptr(), bf16, n, vocab, logits.stride(0) if n > 1 else vocab,
-        _arg(temperature, "f4", n, "temperature", none=True), _arg(top_k, "i4", n, "top_k", none=True),
-        _arg(top_p, "f4", n, "top_p", none=True), _arg(min_p, "f4", n, "min_p", none=True), _arg(u, "f4", n, "u"),
-        _arg(ids, "i4", n, "ids"), _stream(stream, logits))
+        _arg(temperature, "f4", d, n, "temperature", none=True), _arg(top_k, "i4", d, n, "top_k", none=True),
+        _arg(top_p, "f4", d, n, "top_p", none=True), _arg(min_p, "f4", d, n, "min_p", none=True), _arg(u, "f4", d, n, "u"),
+        _arg(ids, "i4", d, n, "ids"), _stream(stream, d))
     if rc:
         _check(rc)
