@@ -563,8 +563,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 }
                 const int sub = find(h, goal - above);
                 cl.sync();
-                in_bin = sub >= 0;
-                if (in_bin) above += s_above, from += (uint32_t)(sub ^ (kBins - 1)) << s, span = s;
+                if (sub >= 0) above += s_above, from += (uint32_t)(sub ^ (kBins - 1)) << s, span = s;
+                else from -= 1u << kBinShift;
             }
         }
         // The row's own keys, in steps of 2^9 sub-bins that end at single keys:
