@@ -828,8 +828,14 @@ cudaError_t sample_plan(SampleArgs a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     int C = kMaxCluster;
     while (C > 1 && (a.rows > fits->n[C] || vecs / C < 128)) C--;
-    const bool alone = a.rows <= fits->n[C];   // one CTA an SM
+    const bool alone = a.rows <= fits->n[C] && vecs * 16 / C <= kAloneBytes - 16;   // one CTA an SM
     while (!alone && C < kMaxCluster && vecs * 16 / C > kSharedBytes) C++;
+    // Rows that no cluster holds are read anew by every pass: as many CTAs as
+    // two an SM allow, four at least (fp32 rows of 200 K, C = 1, 2, 4, 8: 24 of
+    // them 156, 84, 57, 47 us, 100 of them 184, 119, 99, 115, 256 of them 281,
+    // 249, 224, 278; bf16 rows of 1 M: 24 of them 771, 400, 263, 196, 256 of
+    // them 1489, 1266, 1186, 1204).
+    if (!alone && vecs * 16 / C > kSharedBytes) C = std::min(std::max(2 * fits->n[1] / a.rows, 4), kMaxCluster);
     a.seg = (int)((vecs + C - 1) / C);
     const size_t smem = (size_t)a.seg * 16;
     a.drop = 0;

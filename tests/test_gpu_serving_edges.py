@@ -295,3 +295,12 @@ def test_attend_one_large_score_takes_all(rows, P):
     ref, _ = S.attend(*c, P, q, starts, lens, table)
     # scores differ by 2^24 and more or not at all: sums of values and weights of exactly 1, and one division, in fp32
     assert (np.abs(got - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -16)).all()
+
+
+@pytest.mark.parametrize("n,V,dtype", [(76, 90000, "float32"), (100, 60000, "float32"), (120, 131072, "bfloat16"), (152, 43000, "float32"),
+                                       (30, 210000, "float32"), (310, 170000, "float32")])
+def test_sample_row_counts_between_one_and_two_ctas_an_sm(n, V, dtype):
+    rng = np.random.default_rng(n)
+    x = rng.normal(0, 3, (n, V)).astype(np.float32)
+    pick = lambda *v: rng.choice(v, n)   # noqa: E731
+    base.check_sample(x, rng.random(n), t=pick(0.5, 0.9), k=pick(0, 40, 700), p=pick(0.9, 0.3, 1.0), mp=pick(0.0, 0.02), dtype=dtype)
