@@ -35,9 +35,15 @@ constexpr int kMaxSeqs = 4096;
 constexpr int kPushThreads = 512, kSmallThreads = 256;
 constexpr int kFillThreads = 256;
 constexpr int kCluster = 8;
-// One CTA does it all up to so many requests, tokens and table entries; above,
-// the second kernel's parallel writes gain more than its launch costs.
-constexpr int kSmallSeqs = 1024, kSmallTokens = 8192, kSmallTable = 65536;
+// One CTA does it all up to so many requests, tokens that there is room for and
+// table entries; above, the second kernel's parallel writes gain more than its
+// launch costs.  One CTA and two kernels, us: 64 requests with 899, 2022, 2891,
+// 5785 new tokens 6.7 and 9.5, 8.0 and 9.1, 10.5 and 9.3, 15.3 and 9.2 (room for
+// 4096 and 8192 with 60 there: 7.2 and 9.6, 8.1 and 9.4); 512, 1024, 2048
+// requests of one token 9.3 and 10.6, 11.4 and 11.3, 19.1 and 12.4; 256 requests
+// with tables of 16 K and 128 K entries 7.3 and 10.4, 11.3 and 10.3, 1024 with
+// 513 K (many finished) 30.9 and 11.9.
+constexpr int kSmallSeqs = 1024, kSmallTokens = 2048, kSmallTable = 65536;
 
 struct PagesArgs {
     int P, shift, n, width, cap, max_tokens;   // shift: log2 P where P is a power of two, else -1

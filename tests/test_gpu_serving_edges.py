@@ -31,6 +31,15 @@ def big_pages(n, width, cached, fresh, table_fill, capacity, n_free, tokens):
     return table, free, counts, out, cached, fresh, starts, lens, slots
 
 
+@pytest.mark.parametrize("room", [2047, 2048, 2049, 5000])
+@pytest.mark.parametrize("n", [40, 1024, 1025])
+def test_pages_assign_around_the_sizes_of_one_cta(n, room):
+    rng = np.random.default_rng(n + room)
+    c = base.pages_case(rng, n, 16, 64, 900, 1 if n > 100 else 100, 0.2)
+    base.check_pages(16, *c[:5], room)
+    base.check_pages(16, *c[:5], room, in_place=True)
+
+
 WIDE = (2 ** 31 - 1) // 4096
 
 
