@@ -567,7 +567,7 @@ int moe_kv8_append(moe_kv8 *plan, const uint16_t *k, const uint16_t *v, long lon
 /* Attention of new tokens over the cache (their own keys and values appended
  * before): q bf16 rows of [q_heads][head_dim], out likewise, q_stride /
  * out_stride elements from row to row (multiples of 8), 16-byte aligned, not
- * overlapping.  Sequence b (of 0..4096) has rows starts[b] .. starts[b + 1] - 1
+ * overlapping (they may be places of the same rows, at one stride).  Sequence b (of 0..4096) has rows starts[b] .. starts[b + 1] - 1
  * (int32 [n_seqs + 1], device; NULL: row b alone, then n_rows = n_seqs and
  * max_new = 1), the last of them at position lens[b] - 1; the row at position
  * p sees the tokens 0 .. p, on a plan with a sliding window the last

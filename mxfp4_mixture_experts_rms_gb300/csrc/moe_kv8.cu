@@ -434,8 +434,11 @@ int moe_kv8_attend(moe_kv8 *p, const uint16_t *q, long long q_stride, const int3
     const long long row = (long long)p->QH * p->c.D;
     if (q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8)
         return moe_fail_status(MOE_EINVAL, "row strides must be multiples of 8 and at least %lld elements", row);
+    // their extents lie apart, or (rows of one array) their places in a row do
     const uint16_t *qe = q + (long long)(n_rows - 1) * q_stride + row, *oe = out + (long long)(n_rows - 1) * out_stride + row;
-    if (q < oe && out < qe) return moe_fail_status(MOE_EINVAL, "q and out must not overlap");
+    const long long apart = q_stride == out_stride ? (((long long)(out - q)) % q_stride + q_stride) % q_stride : 0;
+    if (q < oe && out < qe && (apart < row || apart > q_stride - row))
+        return moe_fail_status(MOE_EINVAL, "q and out must not overlap");
     Kv8Attend a{};
     a.c = p->c;
     a.QH = p->QH, a.window = p->window, a.n_seqs = n_seqs, a.n_rows = n_rows, a.max_new = max_new, a.width = table_width;

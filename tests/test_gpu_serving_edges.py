@@ -313,3 +313,27 @@ def test_sample_row_counts_between_one_and_two_ctas_an_sm(n, V, dtype):
     x = rng.normal(0, 3, (n, V)).astype(np.float32)
     pick = lambda *v: rng.choice(v, n)   # noqa: E731
     base.check_sample(x, rng.random(n), t=pick(0.5, 0.9), k=pick(0, 40, 700), p=pick(0.9, 0.3, 1.0), mp=pick(0.0, 0.02), dtype=dtype)
+
+
+@pytest.mark.parametrize("rows", [1, 30])
+def test_attend_out_beside_q_in_one_array(rows):
+    import torch
+    rng = np.random.default_rng(11)
+    P, D, kv, H, lens = 16, 64, 2, 4, [50, 130]
+    c, table = base.sequences(rng, P, lens, [rows] * 2, 9, 30, kv, D, poison=False)
+    plan = base.moe().Kv8(H, kv, D, P, 30, cache=[base.dev(x) for x in c])
+    ld, td, n = base.dev(np.array(lens, np.int32)), base.dev(table), 2 * rows
+    starts = np.array([0, rows, n], np.int32)
+    for first in (0, 1):        # q before out and behind it
+        both, vals = base.bf16(rng.normal(0, 0.25, (n, 2 * H + 1, D)))
+        q, out = (both[:, :H], both[:, H + 1:]) if first == 0 else (both[:, H + 1:], both[:, :H])
+        qv = vals[:, :H] if first == 0 else vals[:, H + 1:]
+        plan.attend(q, ld, td, out, starts=base.dev(starts), max_new=rows)
+        ref, tol = S.attend(*c, P, qv, starts, lens, table, floor=2.0 ** -31)
+        assert (np.abs(out.double().cpu().numpy() - ref) / tol).max() <= 1
+        assert np.array_equal(q.double().cpu().numpy(), qv) and np.array_equal(both[:, H].double().cpu().numpy(), vals[:, H])
+    both = torch.zeros((n, 2 * H, D), dtype=torch.bfloat16, device="cuda")
+    for off in (0, 1, H - 1):   # overlapping in every row
+        if n > 1:
+            with pytest.raises(base.moe().MoeError, match="overlap"):
+                plan.attend(both[:, :H], ld, td, both[:, off:off + H], starts=base.dev(starts), max_new=rows)
