@@ -138,11 +138,13 @@ struct Seg {
 };
 
 // What turns a row's accumulator into its output (sink: the head's logit in
-// units of log2, -inf without one).
-__device__ __forceinline__ float row_factor(float m, float l, float N, float sink) {
+// units of log2, -inf without one): two factors, as their product may be below
+// 2^-126 where the output is not.
+__device__ __forceinline__ float2 row_factor(float m, float l, float N, float sink) {
     const float top = fmaxf(m, sink);
     const float den = top == -INFINITY ? l : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sink - top);
-    return den == 0.f || N == -INFINITY ? 0.f : ex2(N - 15.f + (m - top)) / den;   // an empty row: 0; NaN stays NaN
+    const float half = ex2(0.5f * (N - 15.f + (m - top)));
+    return den == 0.f || N == -INFINITY ? make_float2(0.f, 0.f) : make_float2(half, half / den);   // an empty row: 0; NaN stays NaN
 }
 
 // One warp's place in its units: where the next unit's pages come from.
@@ -548,13 +550,15 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                 // the whole job was this warp's
                 int row0, n, pos0;
                 kv8_rows(a, j.b, row0, n, pos0);
-                float k[2];
+                float2 k[2];
 #pragma unroll
                 for (int r = 0; r < (TOP ? 2 : 1); r++)
                     k[r] = row_factor(m[r], quad_sum(l[r]), N[r], sink[r]);
                 if (!TOP) {
-                    k[1] = __shfl_sync(0xffffffffu, k[0], 8 * t4 + 4);
-                    k[0] = __shfl_sync(0xffffffffu, k[0], 8 * t4);
+                    const float2 own = k[0];
+#pragma unroll
+                    for (int r = 0; r < 2; r++)
+                        k[r] = make_float2(__shfl_sync(0xffffffffu, own.x, 8 * t4 + 4 * r), __shfl_sync(0xffffffffu, own.y, 8 * t4 + 4 * r));
                 }
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
@@ -565,10 +569,10 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
 #pragma unroll
                     for (int d = 0; d < NA; d++) {
                         if (TOP) {
-                            *reinterpret_cast<__nv_bfloat162 *>(o + 8 * d) = __floats2bfloat162_rn(acc[d][2 * r] * k[r], acc[d][2 * r + 1] * k[r]);
+                            *reinterpret_cast<__nv_bfloat162 *>(o + 8 * d) = __floats2bfloat162_rn(acc[d][2 * r] * k[r].x * k[r].y, acc[d][2 * r + 1] * k[r].x * k[r].y);
                         } else {
-                            o[16 * d] = __float2bfloat16_rn(acc[d][r] * k[r]);
-                            o[16 * d + 8] = __float2bfloat16_rn(acc[d][2 + r] * k[r]);
+                            o[16 * d] = __float2bfloat16_rn(acc[d][r] * k[r].x * k[r].y);
+                            o[16 * d + 8] = __float2bfloat16_rn(acc[d][2 + r] * k[r].x * k[r].y);
                         }
                     }
                 }
@@ -637,9 +641,9 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
         }
         if (done) {
             const int rr = sg.rt * kRows + r, i2 = rr / f.G, head = sg.h * f.G + rr - i2 * f.G;
-            const float k = row_factor(mm, ll, NN, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+            const float2 k = row_factor(mm, ll, NN, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
             *reinterpret_cast<__nv_bfloat162 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D + d) =
-                __floats2bfloat162_rn(v.x * k, v.y * k);
+                __floats2bfloat162_rn(v.x * k.x * k.y, v.y * k.x * k.y);
         } else {
             float *mine_p = f.parts + ((size_t)blockIdx.x * 2 + (sg.u0 >= c0 ? 1 : 0)) * PF;
             *reinterpret_cast<float2 *>(mine_p + r * PAD + d) = v;

@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                     const float sink = on && a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
                     const float top = fmaxf(m, sink);
                     const float den = top == -INFINITY ? l : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sink - top);
-                    const float k = den == 0.f || N == -INFINITY ? 0.f : ex2(N - 7.f + (m - top)) / den;
+                    // two factors: their product may be below 2^-126 where the output is not
+                    const float k1 = den == 0.f || N == -INFINITY ? 0.f : ex2(0.5f * (N - 7.f + (m - top))), k2 = k1 == 0.f ? 0.f : k1 / den;
                     uint4 *o = reinterpret_cast<uint4 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
@@ -490,11 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv8_prompt_kernel(const __gri
                         tmem_wait(v);
                         if (!on) continue;
 #pragma unroll
+                        for (int x = 0; x < 32; x++) v[x] = v[x] * k1 * k2;
+#pragma unroll
                         for (int x = 0; x < 4; x++)
-                            o[c / 8 + x] = make_uint4(bits_of(__floats2bfloat162_rn(v[8 * x] * k, v[8 * x + 1] * k)),
-                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 2] * k, v[8 * x + 3] * k)),
-                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 4] * k, v[8 * x + 5] * k)),
-                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 6] * k, v[8 * x + 7] * k)));
+                            o[c / 8 + x] = make_uint4(bits_of(__floats2bfloat162_rn(v[8 * x], v[8 * x + 1])),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 2], v[8 * x + 3])),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 4], v[8 * x + 5])),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 6], v[8 * x + 7])));
                     }
                 }
             }

@@ -337,3 +337,26 @@ def test_attend_out_beside_q_in_one_array(rows):
         if n > 1:
             with pytest.raises(base.moe().MoeError, match="overlap"):
                 plan.attend(both[:, :H], ld, td, both[:, off:off + H], starts=base.dev(starts), max_new=rows)
+
+
+@pytest.mark.parametrize("lens,rows", [([100, 70], [1, 1]), ([900, 20], [1, 1]), ([100, 70], [40, 30])])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_attend_values_of_the_smallest_scales(lens, rows, sinks):
+    # pages from 2^-127 on; outputs are bf16 numbers still (2^-126, its smallest normal one, absolutely)
+    import torch
+    rng = np.random.default_rng(12)
+    P, D, kv, H = 16, 64, 2, 4
+    c, table = base.sequences(rng, P, lens, rows, 64, 80, kv, D, poison=False)
+    for lo, hi in ((0, 6), (4, 12), (12, 40)):
+        c[3][...] = rng.integers(lo, hi, c[3].shape)
+        s = rng.normal(0, 2, H).astype(np.float32) if sinks else None
+        starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        qd, q = base.bf16(rng.normal(0, 0.25, (starts[-1], H, D)))
+        plan = base.moe().Kv8(H, kv, D, P, 80, sinks=None if s is None else base.dev(s), cache=[base.dev(x) for x in c])
+        out = torch.zeros((int(starts[-1]), H, D), dtype=torch.bfloat16, device="cuda")
+        plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out, starts=base.dev(starts), max_new=max(rows))
+        # the oracle's absolute 1e-30 is not for these: its other terms at the same scores, values scaled by 2^90
+        up = [*c[:3], (c[3] + 90).astype(np.uint8)]
+        ref, tol = S.attend(*up, P, q, starts, lens, table, 0, s, None, 2.0 ** -31)
+        got = out.double().cpu().numpy() * 2.0 ** 90
+        assert (np.abs(got - ref) <= tol + 2.0 ** (90 - 126 - 8)).all(), (lo, (np.abs(got - ref) / tol).max())
