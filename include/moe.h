@@ -613,7 +613,8 @@ void moe_kv8_destroy(moe_kv8 *plan);
  * row's total; however little a kept token weighs next to the others, it has its
  * share of u.
  * t <= 0 (or NaN) takes the first token in descending order.  temperature, top_k,
- * top_p, min_p: device arrays [n_rows], each may be NULL (1, all, 1, 0).
+ * top_p, min_p: device arrays [n_rows], each may be NULL (1, all, 1, 0); a NaN
+ * in top_p or min_p is as none.
  * ids int32 [n_rows]; -1 for a row without a token to choose. */
 int moe_sample(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride, const float *temperature,
                const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *ids, void *stream);

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     float t = a.temperature ? a.temperature[row] : 1.f;
     if (t == INFINITY) t = 3.402823466e38f;   // (NaN stays NaN: the first token, as t > 0 is false)
     const int k = a.top_k ? a.top_k[row] : 0;
-    const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? fminf(a.min_p[row], 1.f) : 0.f;
+    const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? fminf(fmaxf(a.min_p[row], 0.f), 1.f) : 0.f;   // (NaN: 0)
     const float u = a.u[row];
     int turn = 0;
     // every CTA's value to every CTA; all of them are there after it

@@ -115,6 +115,21 @@ def test_sample_nan_temperature_takes_the_first_token(n):
     base.check_sample(x[:3], rng.random(3), t=[np.inf, -np.inf, np.nan], k=50)
 
 
+def test_sample_nan_top_p_and_min_p_are_none():
+    import torch
+    rng = np.random.default_rng(13)
+    for k in (0, 40, 900):
+        x, u = base.dev(rng.normal(0, 2, (9, 5000)).astype(np.float32)), base.dev(rng.random(9).astype(np.float32))
+        nan, some = np.full(9, np.nan, np.float32), np.where(np.arange(9) % 2, np.nan, 0.02).astype(np.float32)
+        kk = base.dev(np.full(9, k, np.int32))
+        ids = [torch.zeros(9, dtype=torch.int32, device="cuda") for _ in range(4)]
+        base.moe().sample(x, u, ids[0], top_k=kk)
+        base.moe().sample(x, u, ids[1], top_k=kk, top_p=base.dev(nan), min_p=base.dev(nan))
+        base.moe().sample(x, u, ids[2], top_k=kk, top_p=base.dev(nan), min_p=base.dev(some))
+        base.moe().sample(x, u, ids[3], top_k=kk, min_p=base.dev(np.nan_to_num(some)))
+        assert torch.equal(ids[0], ids[1]) and torch.equal(ids[2], ids[3])
+
+
 @pytest.mark.parametrize("V,std,t,p", [(128000, 0.02, 1.0, 0.5), (128000, 0.02, 1.0, 0.4), (200000, 2.5, 30.0, 0.5), (128000, 2.5, 200.0, 0.8),
                                        (60000, 1e-3, 1.0, 0.5), (1000003, 0.5, 3.0, 0.6), (1 << 22, 0.3, 2.0, 0.7)])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
