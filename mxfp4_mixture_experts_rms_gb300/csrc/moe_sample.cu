@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             if (T) {
                 const double at_T = (double)weight(key_logit(T)) * 0x1p40, ties = (double)r * at_T, all = (double)everything + ties;
                 const double out = (1. - (double)fmaxf(p, 0.f)) * all - ties;   // of the tokens above T
-                if (out < 0.) {   // among the tokens at T
+                if (out < 0. || everything == 0) {   // among the tokens at T
                     r -= min((u64)((out + ties) / at_T), r - 1);
                     cl.sync();     // the histograms are read no more
                     continue;

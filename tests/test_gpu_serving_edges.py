@@ -375,3 +375,12 @@ def test_attend_values_of_the_smallest_scales(lens, rows, sinks):
         ref, tol = S.attend(*up, P, q, starts, lens, table, 0, s, None, 2.0 ** -31)
         got = out.double().cpu().numpy() * 2.0 ** 90
         assert (np.abs(got - ref) <= tol + 2.0 ** (90 - 126 - 8)).all(), (lo, (np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("p", [0.0, 1e-9, 1e-4, 0.3, 0.999])
+@pytest.mark.parametrize("k", [2, 40, 511, 512, 900, 1500])
+def test_sample_nucleus_among_the_equal_tokens_that_top_k_left(p, k):
+    rng = np.random.default_rng(14)
+    base.check_sample(rng.integers(-2, 3, (8, 4909)), rng.random(8), k=k, p=p)
+    base.check_sample(np.zeros((8, 1448)), rng.random(8), k=k, p=p, dtype="bfloat16")
+    base.check_sample(np.full((8, 20000), 9984.0), rng.random(8), t=0.1, k=k, p=p)
