@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                         for (int j = 0; j < n; j++) ahead += ranks[j] < mine ? hist[j] : 0;
                     keep = keep && ahead < g;
                 }
-                keep = keep && weight(key_logit(me.x)) >= least;
+                keep = keep && (mp < 1.f ? weight(key_logit(me.x)) >= least : me.x == km);
                 __syncthreads();
                 w = keep ? w : 0;
                 if (tid < n) hist[tid] = w;
@@ -650,6 +650,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         cl.sync();   // lists, histograms and what was told are read no more
     }
 
+    // min-p of 1: the largest logit's tokens, not those whose weight rounds to 1
+    if (!(mp < 1.f) && T != km) T = km, r = a.V;
     // the kept weight of each warp's part, and its tokens at T.  A lane's sum is
     // at least one unit, the sum over the tokens at T is rounded up (the n-th of
     // them adds at_T(n) - at_T(n - 1)): a part with a token to choose is never

@@ -384,3 +384,18 @@ def test_sample_nucleus_among_the_equal_tokens_that_top_k_left(p, k):
     base.check_sample(rng.integers(-2, 3, (8, 4909)), rng.random(8), k=k, p=p)
     base.check_sample(np.zeros((8, 1448)), rng.random(8), k=k, p=p, dtype="bfloat16")
     base.check_sample(np.full((8, 20000), 9984.0), rng.random(8), t=0.1, k=k, p=p)
+
+
+@pytest.mark.parametrize("V", [2, 30, 700, 30000])
+@pytest.mark.parametrize("mp", [1.0, 2.0])
+def test_sample_min_p_of_one_keeps_the_largest_only(V, mp):
+    # weights of the others within 2^-24 of 1
+    rng = np.random.default_rng(15)
+    x = -np.abs(rng.normal(0, 1e-7, (12, V))).astype(np.float32)
+    x[6:, ::3] = x[6:].max(1, keepdims=True)            # and with many that are the largest
+    u = rng.random(12)
+    want = [S.sample(np.where(r == r.max(), 1.0, 0.0), float(np.float32(v))) for r, v in zip(x, u)]
+    for kw in (dict(), dict(t=0.7), dict(k=V // 2 + 1), dict(k=600), dict(p=0.999), dict(k=5, p=0.9)):
+        got = base.check_sample(x, u, mp=mp, **kw)
+        if not kw or "t" in kw:
+            assert list(got) == want
