@@ -523,7 +523,7 @@ def _head_rows(t, heads: int, dim: int, device: int, what: str):
     if t.get_device() != device or t.dtype is not (_DTYPES or _dtypes())["b2"] or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][{heads}][{dim}] on device {device} is needed")
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != dim and heads > 1):
+    if shape[0] and (s2 != 1 or (s1 != dim and heads > 1)):     # (an empty tensor's strides say nothing)
         raise MoeError(MOE_EINVAL, f"{what}: the heads of a row must lie side by side")
     return t.data_ptr(), s0 if shape[0] > 1 else heads * dim
 

@@ -137,3 +137,13 @@ def test_a_plan_s_arrays_are_on_one_device(lib):
             lib.moe_kv8_create = lambda *a: 99
             lib.moe_kv8_workspace_bytes = lambda *a: 256
             make(**bad)
+
+
+def test_rows_of_an_empty_batch_have_any_strides(lib):
+    p = plan(lib)
+    q, k, i = Tensor(B2, 0, 4, 64), Tensor(B2, 0, 2, 64), Tensor(I4, 0)
+    for t in (q, k):
+        t.stride = lambda n=None: (0, 1, 1) if n is None else (0, 1, 1)[n]
+    p.attend(q, i, Tensor(I4, 0, 3), q)
+    p.append(k, k, i)
+    assert lib.calls == 2
