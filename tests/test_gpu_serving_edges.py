@@ -399,3 +399,54 @@ def test_sample_min_p_of_one_keeps_the_largest_only(V, mp):
         got = base.check_sample(x, u, mp=mp, **kw)
         if not kw or "t" in kw:
             assert list(got) == want
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [40, 33]])
+def test_append_and_attend_past_32_bit_offsets(rows):
+    # the last pages of a cache of 4.6 GB a side: byte offsets past 2^32, against a cache of those pages alone
+    import torch
+    rng = np.random.default_rng(16)
+    P, D, kv, H, pages, lens = 64, 128, 8, 16, 70000, [200, 130]
+    plan = base.moe().Kv8(H, kv, D, P, pages)
+    used = np.array([69999, 69998, 40000, 65537, 65536, 32769, 1])
+    c = base.random_cache(rng, len(used), kv, P, D)
+    at = torch.from_numpy(used).cuda()
+    for t, x in zip((plan.k, plan.v, plan.k_scale, plan.v_scale), c):
+        t[at] = base.dev(x)
+    small = np.array([[0, 1, 2, 3], [4, 5, 6, -1]], np.int32)
+    table = np.where(small < 0, -1, used[small]).astype(np.int32)
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    n = int(starts[-1])
+    pos = [np.arange(L - r, L) for L, r in zip(lens, rows)]
+    near = np.concatenate([small[b, p // P] * P + p % P for b, p in enumerate(pos)])
+    far = np.concatenate([table[b, p // P] * P + p % P for b, p in enumerate(pos)]).astype(np.int32)
+    kd, k = base.bf16(rng.normal(0, 1, (n, kv, D)))
+    vd, v = base.bf16(rng.normal(0, 1, (n, kv, D)))
+    plan.append(kd, vd, base.dev(far))
+    ref = S.append(*c, P, k, v, near)
+    for t, x in zip((plan.k, plan.v, plan.k_scale, plan.v_scale), ref):
+        assert np.array_equal(t[at].cpu().numpy(), x)
+    qd, q = base.bf16(rng.normal(0, 0.25, (n, H, D)))
+    out = torch.zeros((n, H, D), dtype=torch.bfloat16, device="cuda")
+    plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out, starts=base.dev(starts), max_new=max(rows))
+    want, tol = S.attend(*ref, P, q, starts, lens, small, floor=2.0 ** -31)
+    assert (np.abs(out.double().cpu().numpy() - want) / tol).max() <= 1
+
+
+def test_a_status_that_was_set_is_told_once_and_clears_the_tickets():
+    # as a wait that gave up leaves the workspace: the status word, and tickets of jobs that were not joined
+    import torch
+    rng = np.random.default_rng(17)
+    P, D, kv, H, lens = 64, 64, 1, 8, [9000, 5000]
+    c, table = base.sequences(rng, P, lens, [1] * 2, 141, 230, kv, D, poison=False)
+    plan = base.moe().Kv8(H, kv, D, P, 230, cache=[base.dev(x) for x in c])
+    head = plan.ws[(-plan.ws.data_ptr()) % 256:][:8192].view(torch.int32)
+    assert plan.device_status() == 0
+    head[0], head[1] = 1, 90
+    head[16:16 + 160] = 1
+    assert plan.device_status() == 1 and plan.device_status() == 0 and bool((head == 0).all())
+    qd, q = base.bf16(rng.normal(0, 0.25, (2, H, D)))
+    out = torch.zeros((2, H, D), dtype=torch.bfloat16, device="cuda")
+    plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out)
+    ref, tol = S.attend(*c, P, q, range(3), lens, table)
+    assert (np.abs(out.double().cpu().numpy() - ref) / tol).max() <= 1 and bool((head == 0).all())
