@@ -28,6 +28,9 @@ namespace {
 // holds sum 2^(15 + s + e - M) * code over value codes with
 // page exponent e, so that the fp16 weights 2^(15 + s + e - M) <= 2^15 keep 11
 // bits down to 2^-29 of the largest, however far the pages' scales are apart.
+// 11 bits, where a sum takes fp32 weights in the plain form: one product instead
+// of two, and results still 1.6e-3 from those in 64 bits (relative, over an
+// output), as is a form in fp32 that is rounded to bf16 at its end.
 // q is scaled per row by a power of two into fp16's range: exact for a bf16
 // row's values down to 2^-28 of its largest.
 constexpr int kTile = 64;             // tokens of a unit
@@ -37,10 +40,10 @@ constexpr int kSmemSeqs = 512;       // sequences whose lengths are held in shar
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Measured: 16 x 4096 tokens of 8 heads of 64 (67 MB) 23.7 us: lengths and
+// Measured: 16 x 4096 tokens of 8 heads of 64 (67 MB) 23.8 us: lengths and
 // table 1.4, the first pages 2.8, units 8.0 (HBM's rate), joins 4.7, the launch
-// the rest; 96 ragged sequences of up to 12 K, 4 heads of 128 (612 MB), 109 us:
-// 0.82 of a copy's rate; one sequence of 131 tokens 7.4 us.
+// the rest; 96 ragged sequences of up to 12 K, 4 heads of 128 (612 MB), 110 us:
+// 0.82 of a copy's rate; one sequence of 131 tokens 7.3 us.
 // Warps, and units in each one's ring.  What bounds the kernel is latency at
 // the instructions of a unit, so as many warps as registers and the 227 KB of
 // shared memory allow come before a deeper ring: a warp's own copies are in
@@ -745,6 +748,12 @@ cudaError_t sm_count(int *n) {
 size_t kv8_workspace_bytes(int D) { return kPartOffset + (size_t)kMaxCtas * 2 * partial_floats(kRows, D) * 4; }
 
 cudaError_t launch_kv8_attend(const Kv8Attend &a, unsigned char *ws, cudaStream_t st) {
+    // Up to 64 rows of a kv head the streaming kernel: its work grows by the row
+    // tile of 16, that of the kernel for prompts, 256 rows a CTA, does not.  us at
+    // 32, 64, 128 rows, 8 kv heads of 64, streaming and prompts: 32 sequences of
+    // 4096 tokens 76 and 113, 133 and 110, 243 and 111; 8 of them 33 and 57, 46
+    // and 55, 75 and 56.  Not so where the prompts' CTAs are few, as they walk all
+    // keys: one sequence of 32 K tokens 36 and 415, 50 and 402, 73 and 403.
     const int G = a.QH / a.c.KVH;
     if (a.max_new * G <= 64) {
         FewArgs f{};

@@ -21,7 +21,7 @@
 // Bound by the softmax warps' chains: a step takes them about 2050 cycles (wait
 // for the scores 400, read 200, maxima 250, wait for the products 250, weights
 // 750, hand over 150), the tensor cores about 540 of them and the exponentials
-// 512.  2430 new tokens of 3 sequences over 6416 cached, 64 / 8 heads of 64: 163 us
+// 512.  2430 new tokens of 3 sequences over 6416 cached, 64 / 8 heads of 64: 159 us
 // (205 with one issuing warp for both halves and page copies by a decoder;
 // 193 with 16 softmax warps of 32 scores a thread, whose fixed work a step is
 // the same for half the scores; 170 before a tile's heads came together).

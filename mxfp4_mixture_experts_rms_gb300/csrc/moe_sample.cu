@@ -21,10 +21,12 @@
 // into 512 by its weights' further bits, and listed then; only where a sub-bin
 // holds too many again, or T lies below the 32 octaves, the row is searched by
 // its keys (16 x 200 K logits within 0.1 of one another: 59 us).  Where step
-// 1's rounding named a neighbour of T's bin, that one is looked at next.  Sums
-// are fp32 over a lane's
-// logits and whole multiples of 2^-40 above that, so they do not depend on
-// their order.
+// 1's rounding named a neighbour of T's bin, that one is looked at next.
+//
+// Weights are fp32: those below 2^-126 are 0.  Sums are fp32 over a lane's logits
+// and whole multiples of 2^-40 above that, so they do not depend on their order;
+// below the octaves, and in the part of a row that holds the chosen token, units
+// are as small as the weights there.
 //
 // A row is a cluster's: each CTA keeps its part in shared memory (read from
 // memory once) where it fits, and meets the others through distributed shared
@@ -818,13 +820,13 @@ cudaError_t sample_plan(SampleArgs a, cudaStream_t st) {
     const int VE = BF16 ? 8 : 4;
     const long long vecs = ((long long)a.V + VE - 1) / VE + 1;   // one more where the first is cut
     // CTAs of a row: as many as run at once with one an SM, each with at least
-    // 128 vectors (one row of 32 K fp32: 19, 15, 11, 10 us with 1, 2, 4, 8; 16 x
-    // 200 K: 52 with 8, where the 16th cluster had to wait for another's SMs, 29
-    // with the most that all fit),
+    // 128 vectors (one row of 32 K fp32: 19, 15, 11, 10 us with 1, 2, 4, 8, before
+    // the other steps to 9; 16 x 200 K: 52 with 8, where the 16th cluster had to
+    // wait for another's SMs, 28 with the most that all fit),
     // and where there are more rows, as many as two an SM need to keep their
     // parts in shared memory (256 x 128 K bf16, mixed: 143 and 108 us with 1 and
     // 2 that read it from L2 again, 95 with 4, 124 with 8, before the other
-    // steps to 87).
+    // steps to 88).
     const Fits *fits;
     const cudaError_t e = sample_fits<BF16>(fits);
     if (e != cudaSuccess) return e;
