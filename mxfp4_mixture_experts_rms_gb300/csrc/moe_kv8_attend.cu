@@ -553,18 +553,10 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
                 // the whole job was this warp's
                 int row0, n, pos0;
                 kv8_rows(a, j.b, row0, n, pos0);
-                float2 k[2];
-#pragma unroll
-                for (int r = 0; r < (TOP ? 2 : 1); r++)
-                    k[r] = row_factor(m[r], quad_sum(l[r]), N[r], sink[r]);
-                if (!TOP) {
-                    const float2 own = k[0];
-#pragma unroll
-                    for (int r = 0; r < 2; r++)
-                        k[r] = make_float2(__shfl_sync(0xffffffffu, own.x, 8 * t4 + 4 * r), __shfl_sync(0xffffffffu, own.y, 8 * t4 + 4 * r));
-                }
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
+                    float2 k = row_factor(m[TOP ? r : 0], quad_sum(l[TOP ? r : 0]), N[TOP ? r : 0], sink[TOP ? r : 0]);
+                    if (!TOP) k = make_float2(__shfl_sync(0xffffffffu, k.x, 8 * t4 + 4 * r), __shfl_sync(0xffffffffu, k.y, 8 * t4 + 4 * r));
                     const int rr = j.rt * kRows + (TOP ? g + 8 * r : 2 * t4 + r);
                     if (rr >= n * f.G) continue;
                     __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(a.out) + (long long)(row0 + rr / f.G) * a.o_stride +
@@ -572,10 +564,10 @@ __global__ void __launch_bounds__(Few<D, TOP>::kWarps * 32, 1) moe_kv8_few_kerne
 #pragma unroll
                     for (int d = 0; d < NA; d++) {
                         if (TOP) {
-                            *reinterpret_cast<__nv_bfloat162 *>(o + 8 * d) = __floats2bfloat162_rn(acc[d][2 * r] * k[r].x * k[r].y, acc[d][2 * r + 1] * k[r].x * k[r].y);
+                            *reinterpret_cast<__nv_bfloat162 *>(o + 8 * d) = __floats2bfloat162_rn(acc[d][2 * r] * k.x * k.y, acc[d][2 * r + 1] * k.x * k.y);
                         } else {
-                            o[16 * d] = __float2bfloat16_rn(acc[d][r] * k[r].x * k[r].y);
-                            o[16 * d + 8] = __float2bfloat16_rn(acc[d][2 + r] * k[r].x * k[r].y);
+                            o[16 * d] = __float2bfloat16_rn(acc[d][r] * k.x * k.y);
+                            o[16 * d + 8] = __float2bfloat16_rn(acc[d][2 + r] * k.x * k.y);
                         }
                     }
                 }
