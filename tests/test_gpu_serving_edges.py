@@ -450,3 +450,22 @@ def test_a_status_that_was_set_is_told_once_and_clears_the_tickets():
     plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out)
     ref, tol = S.attend(*c, P, q, range(3), lens, table)
     assert (np.abs(out.double().cpu().numpy() - ref) / tol).max() <= 1 and bool((head == 0).all())
+
+
+@pytest.mark.parametrize("lens,rows", [([9000, 20, 4000, 700], [1] * 4), ([3000, 50, 900, 1], [8, 3, 5, 1]), ([700, 333, 90, 1500], [300, 33, 90, 1])])
+def test_attend_repeats_itself_exactly(lens, rows):
+    # joins in a fixed order, whichever CTA comes last
+    import torch
+    rng = np.random.default_rng(18)
+    P, D, kv, H = 32, 64, 2, 16
+    c, table = base.sequences(rng, P, lens, rows, -(-max(lens) // P), sum(-(-n // P) for n in lens) + 1, kv, D, poison=False)
+    plan = base.moe().Kv8(H, kv, D, P, c[2].shape[0], cache=[base.dev(x) for x in c])
+    qd, _ = base.bf16(rng.normal(0, 0.25, (sum(rows), H, D)))
+    ld, td = base.dev(np.array(lens, np.int32)), base.dev(table)
+    starts = base.dev(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32))
+    outs = [torch.zeros((sum(rows), H, D), dtype=torch.bfloat16, device="cuda") for _ in range(12)]
+    for i, o in enumerate(outs):
+        if i % 3 == 2:      # other work beside it
+            torch.randn(1 << 22, device="cuda").sort()
+        plan.attend(qd, ld, td, o, starts=starts, max_new=max(rows))
+    assert all(torch.equal(o, outs[0]) for o in outs)
