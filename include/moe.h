@@ -619,6 +619,119 @@ void moe_kv8_destroy(moe_kv8 *plan);
 int moe_sample(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride, const float *temperature,
                const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *ids, void *stream);
 
+/* Queries and keys before a cache: each head's norm and the rotation by its
+ * token's positions, from a projection's rows, in one pass.  Per head of
+ * head_dim values x, in fp32:
+ *   x' = x / sqrt(mean(x^2) + eps) * gamma      on a side that has a gamma
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin)
+ *             for its n_pairs pairs (a, b), the angle of pair i being
+ *             positions[axes[i]][token] * freqs[i]
+ * rounded once, to bf16; dims in no pair are x'.  Pairs are dims i and
+ * i + n_pairs, or 2 i and 2 i + 1 (interleaved = 1).  Angles are exact to
+ * 2^-32 of a turn at any position. */
+typedef struct moe_rotary moe_rotary;
+/* head_dim 64, 128 or 256; n_pairs a multiple of 8, 0 .. head_dim / 2; n_axes
+ * 1 .. 4 (time, height and width of images and video, say).  Defaults: no
+ * norms, eps 1e-5, factor 1.  NULL on bad arguments. */
+moe_rotary *moe_rotary_create(int head_dim, int n_pairs, int n_axes, int interleaved);
+/* "eps" (0 .. 1e30), "factor" (1e-30 .. 1e30). */
+int moe_rotary_set_f(moe_rotary *plan, const char *key, double value);
+/* Radians a position (f64 [n_pairs], device, borrowed) and the axis of each
+ * pair (uint8 [n_pairs], device, borrowed; NULL: the first; one past the last
+ * counts as the last). */
+int moe_rotary_set_freqs(moe_rotary *plan, const double *freqs, const uint8_t *axes);
+/* The norms' gammas (f32 [head_dim], device, borrowed, 16-byte aligned); NULL:
+ * that side is not normed. */
+int moe_rotary_set_norm(moe_rotary *plan, const float *q_gamma, const float *k_gamma);
+/* n_tokens rows of q_heads queries and of kv_heads keys (bf16, strides in
+ * elements from row to row, multiples of 4; 8-byte aligned; a side of 0 heads
+ * may be NULL) into q_out and k_out, which may be their inputs (the same
+ * pointer and stride) and overlap nothing else (they may be places of the same
+ * rows, at one stride).  positions int32 [n_axes] rows of pos_stride (device).
+ * A token with a negative position on any axis is left out: its output rows
+ * stay as they are. */
+int moe_rotary_apply(moe_rotary *plan, const uint16_t *q, long long q_stride, int q_heads, const uint16_t *k,
+                     long long k_stride, int kv_heads, const int32_t *positions, long long pos_stride, int n_tokens,
+                     uint16_t *q_out, long long q_out_stride, uint16_t *k_out, long long k_out_stride, void *stream);
+void moe_rotary_destroy(moe_rotary *plan);
+
+/* One layer's paged cache in 4 bits, MXFP4: E2M1 codes and an E8M0 scale
+ * (value 2^(s - 127)) for each token, kv head, side (keys, values) and block of
+ * 32 dims.  One device array, borrowed, 16-byte aligned, [n_pages][kv_heads] of
+ * P * head_dim * 17 / 16 bytes, in them
+ *   key codes   [head_dim / 32][P][16]: byte i of a token's block holds its dims
+ *               2 i (low nibble) and 2 i + 1
+ *   value codes the same
+ *   key scales  [head_dim / 32][P], of 16 tokens token 2 t + e (t < 4, e < 2)
+ *               at byte 4 t + e, token 8 + 2 t + e at byte 4 t + 2 + e
+ *   value scales the same
+ * A slot is page * P + place in the page. */
+typedef struct moe_kv4 moe_kv4;
+/* Arguments and options as for moe_kv8_create and what follows it. */
+moe_kv4 *moe_kv4_create(int q_heads, int kv_heads, int head_dim, int page_size, int n_pages);
+int moe_kv4_set_i(moe_kv4 *plan, const char *key, long long value);
+int moe_kv4_set_f(moe_kv4 *plan, const char *key, double value);
+/* Bytes of a page of all kv heads. */
+size_t moe_kv4_page_bytes(const moe_kv4 *plan);
+int moe_kv4_set_cache(moe_kv4 *plan, uint8_t *cache);
+int moe_kv4_set_sinks(moe_kv4 *plan, const float *sinks);
+size_t moe_kv4_workspace_bytes(const moe_kv4 *plan);
+int moe_kv4_set_workspace(moe_kv4 *plan, void *dev_ptr, size_t bytes);
+/* n_tokens tokens' keys and values (bf16, as moe_kv8_append takes them) into
+ * the cache at slots (int32, device), in any order.  A slot outside 0 ..
+ * n_pages * P - 1 appends nothing; of one that a call names twice the contents
+ * are unspecified.  A block's scale and codes are those of moe_mx_quantize_fp4
+ * (k = ceil(log2(amax / 6)), the nearest E2M1 value to x / 2^k, ties to the
+ * even code, infinities +-6, NaN +6) but for k, which is at most 125, so that
+ * every value is a finite bf16. */
+int moe_kv4_append(moe_kv4 *plan, const uint16_t *k, const uint16_t *v, long long k_stride, long long v_stride,
+                   const int32_t *slots, int n_tokens, void *stream);
+/* What the cache holds at slots (int32, device), as bf16 rows (exact) of the
+ * form that append takes; k and v must not overlap (they may be places of the
+ * same rows, at one stride).  Rows of slots outside 0 .. n_pages * P - 1 are
+ * left as they are.  A scale byte that no append writes, 0 or above 252, counts
+ * as a scale of 0 or as 252, here and in moe_kv4_attend. */
+int moe_kv4_read(moe_kv4 *plan, const int32_t *slots, int n_tokens, uint16_t *k, uint16_t *v, long long k_stride,
+                 long long v_stride, void *stream);
+/* Attention of new tokens over the cache: all of moe_kv8_attend's arguments,
+ * rules and limits. */
+int moe_kv4_attend(moe_kv4 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
+                   const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
+                   long long out_stride, void *stream);
+int moe_kv4_get_device_status(moe_kv4 *plan, int *status, void *stream);
+void moe_kv4_destroy(moe_kv4 *plan);
+
+/* Drafted tokens against the target model's logits.  Sequence b (of 0..65536)
+ * has the rows starts[b] .. starts[b + 1] - 1 (int32 [n_seqs + 1], device, not
+ * decreasing; what lies past n_rows is not there), logits as moe_sample takes
+ * them: n - 1 drafted tokens, drafts[row] (int32 [n_rows], device) at each but
+ * the last, whose logits are of the token after them.  With p the probabilities
+ * from which moe_sample draws at a row, at the sequence's settings (temperature,
+ * top_k, top_p, min_p: device arrays [n_seqs], each may be NULL), and q those
+ * that its drafted token was drawn from (draft_probs, fp32 rows probs_stride
+ * elements apart, device, taken into 0 .. 1, NaN 0; NULL: 1 at the drafted
+ * token, 0 elsewhere):
+ *   1. the first rows whose tokens x have u[row] q(x) < p(x) are accepted
+ *      (u f32 [n_rows], device, uniform in [0, 1)); a token outside the
+ *      vocabulary is not
+ *   2. at the row behind them a token is drawn, the first in order of index at
+ *      which the running sum of max(p - q, 0) - of p at the last row, and where
+ *      p is nowhere above q - exceeds draws[b] times its total (draws f32
+ *      [n_seqs], device, uniform in [0, 1))
+ * so that a token of a sequence has the probability that p gives it.
+ * accepted[b] (int32 [n_seqs]) is the number of accepted tokens; ids (int32
+ * [n_rows]) gets those, the drawn token (-1 where the row has none to choose)
+ * and -1 behind it; rows of no sequence are left as they are.  Of a sequence of
+ * one row the token is drawn as moe_sample would.  Weights are fp32, sums
+ * within 2^-20 of their totals.  draft_probs is read at tokens that p keeps,
+ * never at a sequence's last row.  The workspace (device, 16-byte aligned) holds
+ * nothing between calls; calls that can overlap on the GPU need one each. */
+size_t moe_verify_workspace_bytes(int n_rows);
+int moe_verify(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride, const int32_t *drafts,
+               const float *draft_probs, long long probs_stride, const int32_t *starts, int n_seqs, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p, const float *u, const float *draws, int32_t *ids,
+               int32_t *accepted, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Text of the last failure on this thread ("" if none) (goosedump gpt_oss.rs:
  * every `ensure!` carries a message). */
 const char *moe_last_error(void);

@@ -33,7 +33,7 @@
 // memory.  Large batches are bound by the passes' instructions (about eleven a
 // logit in step 1, three where a pass skips it), single rows by the cluster's
 // meetings, about half a microsecond each.
-#include "moe_common.cuh"
+#include "moe_sample.cuh"
 #include "../../include/moe.h"
 
 #include <cooperative_groups.h>
@@ -69,28 +69,7 @@ constexpr int kKeys = 2048;           // listed keys of a row that a CTA has roo
 constexpr int kRank = 512;            // tokens that are ranked by comparing each with each
 constexpr int kAloneBytes = 170000, kSharedBytes = 80000;   // of a row's part in shared memory: one CTA an SM, two
 constexpr int kBinShift = 19;         // a weight's bits above: exponent and four bits of mantissa
-constexpr float kLog2e = 1.4426950408889634f;
 
-struct SampleArgs {
-    const void *x;
-    int rows, V;
-    long long stride;
-    const float *temperature;
-    const int32_t *top_k;
-    const float *top_p, *min_p, *u;
-    int32_t *ids;
-    int seg;         // 16-byte vectors of a row's part
-    int drop;        // mantissa bits that a sum of V weights in 32 bits has no room for
-};
-
-// Larger logit, larger key; NaN and -inf (never chosen): 0.
-__device__ __forceinline__ uint32_t order_key(float l) {
-    const uint32_t b = __float_as_uint(l + 0.f);  // -0 becomes +0
-    return l > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
-}
-__device__ __forceinline__ float key_logit(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
 // n tokens of weight w (0 .. 1; n at most 2^22) in units of 2^-(40 + up), up at
 // least 0, rounded up: what can be chosen has a unit.  The caller sees to it
 // that the result fits.
@@ -126,63 +105,8 @@ struct Told {
     u64 sum;
 };
 
-template <bool BF16, bool RES, int NT>
-struct Row {
-    static constexpr int VE = BF16 ? 8 : 4;   // logits of a 16-byte vector
-    const uint4 *g;       // the row's vectors in memory, from the one that holds its first logit
-    const uint4 *s;       // this CTA's in shared memory (RES)
-    int off, V;           // logits of the first vector that are not the row's; the row's logits
-    int v0, v1;           // this warp's vectors
-    int c0;               // the CTA's first vector
-
-    __device__ __forceinline__ uint4 fetch(int v) const {   // from memory, -inf outside the row
-        const int i = v * VE - off;
-        if (i >= 0 && i + VE <= V) return __ldg(g + v);
-        uint32_t w[4];
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            if (BF16) {
-                const uint16_t *p = reinterpret_cast<const uint16_t *>(g) + (size_t)v * VE + 2 * q;
-                const uint32_t lo = i + 2 * q >= 0 && i + 2 * q < V ? p[0] : 0xFF80u;
-                const uint32_t hi = i + 2 * q + 1 >= 0 && i + 2 * q + 1 < V ? p[1] : 0xFF80u;
-                w[q] = lo | hi << 16;
-            } else {
-                w[q] = i + q >= 0 && i + q < V ? reinterpret_cast<const uint32_t *>(g)[(size_t)v * VE + q] : 0xFF800000u;
-            }
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    static __device__ __forceinline__ void values(uint4 w, float (&x)[VE]) {
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            if (BF16) {
-                x[2 * q] = __uint_as_float(a[q] << 16), x[2 * q + 1] = __uint_as_float(a[q] & 0xFFFF0000u);
-            } else {
-                x[q] = __uint_as_float(a[q]);
-            }
-        }
-    }
-    __device__ __forceinline__ uint4 vec(int v) const { return RES ? s[v - c0] : fetch(v); }
-    // f(logits, first one's index) for the warp's vectors, a lane a vector; in
-    // order of index; the next vector is read ahead
-    template <class F>
-    __device__ __forceinline__ void each(F f) const {
-        int v = v0 + (threadIdx.x & 31);
-        if (v >= v1) return;
-        uint4 next = vec(v);
-#pragma unroll 1
-        for (; v < v1; v += 32) {
-            const uint4 w = next;
-            if (v + 32 < v1) next = vec(v + 32);
-            float x[VE];
-            values(w, x);
-            f(x, v * VE - off);
-        }
-    }
-};
-
-template <bool BF16, bool RES, int NT>
+// LIMITS: tells what the row's token would be chosen from (SampleLimits) instead of choosing it.
+template <bool BF16, bool RES, int NT, bool LIMITS>
 __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleArgs a) {
     typedef Row<BF16, RES, NT> R;
     constexpr int VE = R::VE, NW = NT / 32;
@@ -216,11 +140,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         const int c1 = min(d.c0 + a.seg, vecs), per = (c1 - d.c0 + NW - 1) / NW;
         d.v0 = min(d.c0 + warp * per, c1), d.v1 = min(d.v0 + per, c1);
     }
-    float t = a.temperature ? a.temperature[row] : 1.f;
-    if (t == INFINITY) t = 3.402823466e38f;   // (NaN stays NaN: the first token, as t > 0 is false)
-    const int k = a.top_k ? a.top_k[row] : 0;
-    const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? fminf(fmaxf(a.min_p[row], 0.f), 1.f) : 0.f;   // (NaN: 0)
-    const float u = a.u[row];
+    float t, p, mp, u;
+    int k, of = row;
+    auto settings = [&](int of) {
+        t = used_temperature(a.temperature ? a.temperature[of] : 1.f);
+        k = a.top_k ? a.top_k[of] : 0;
+        p = a.top_p ? a.top_p[of] : 1.f, mp = a.min_p ? used_min_p(a.min_p[of]) : 0.f;
+        u = LIMITS ? 0.f : a.u[of];
+    };
+    if (!LIMITS) settings(row);
     int turn = 0;
     // every CTA's value to every CTA; all of them are there after it
     auto tell = [&](Told mine) {
@@ -252,27 +180,25 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     }
     km = __reduce_max_sync(0xffffffffu, km);
     if (lane == 0) red[warp] = km;
+    if (LIMITS) {
+        of = sequence_of(a.starts, a.n_seqs, row);
+        settings(max(of, 0));
+    }
     __syncthreads();
     km = __reduce_max_sync(0xffffffffu, red[lane % NW]);
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA of the row runs
     tell({km, 0, 0, 0});
     for (int c = 0; c < C; c++) km = max(km, told[turn][c].key);
-    if (km == 0) {   // nothing to choose
-        if (rank == 0 && tid == 0) a.ids[row] = -1;
+    if (km == 0 || of < 0) {   // nothing to choose
+        if (rank == 0 && tid == 0) {
+            if (LIMITS) a.limits[row] = {0u, 0u, 0, 0, 0.};
+            else a.ids[row] = -1;
+        }
         return;
     }
-    const float top = key_logit(km), scale = t > 0.f ? fminf(kLog2e / t, 1e30f) : 0.f;
-    // An infinite largest logit: then only infinite ones weigh anything.  A
-    // row of steep scale: differences first, so that 0 stays 0.  Else the
-    // weights are 2^(x scale - top scale), the constant rounded: one factor,
-    // within 2^-14 of 1, on all of them.
-    const bool endless = top == INFINITY, steep = !(fabsf(top * scale) < 1000.f);
-    const float shift_w = endless || steep ? 0.f : -top * scale;
-    auto weight = [&](float x) {
-        float w;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(steep ? (x - top) * scale : fmaf(x, scale, shift_w)));
-        return endless ? (x == top ? 1.f : 0.f) : w;
-    };
+    const Weight weight(key_logit(km), t);
+    const float top = weight.top, scale = weight.scale, shift_w = weight.shift;
+    const bool endless = weight.endless, steep = weight.steep;
     auto weights = [&](const float (&x)[VE], float (&w)[VE]) {
         if (endless || steep) {
 #pragma unroll
@@ -468,6 +394,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                 w = keep ? w : 0;
                 if (tid < n) hist[tid] = w;
                 const u64 all_kept = total(w);
+                if (LIMITS) {
+                    if (keep) atomicMin(&s_lo, me.x);
+                    __syncthreads();
+                    const uint32_t least_key = s_lo;
+                    const int at_it = __syncthreads_count(keep && me.x == least_key), cut = __syncthreads_or(tid < n && !keep && me.x == least_key);
+                    if (tid == 0) a.limits[row] = {km, least_key, at_it, cut, (double)all_kept * 0x1p-53};
+                    return;
+                }
                 const u64 target = __umul64hi(all_kept, fraction(u));
                 u64 run = 0;
                 if (w)
@@ -692,6 +626,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         if (c == rank) own = m;
         kept += m, tsum += ct;
     }
+    if (LIMITS) {
+        // (T is 0 where all tokens are kept: the least key is that of -inf, which weighs nothing)
+        if (rank == 0 && tid == 0) a.limits[row] = {km, T, (int)min(r, (u64)INT_MAX), T && tsum > r, (double)kept * 0x1p-40};
+        return;
+    }
     u64 target = __umul64hi(kept, fraction(u));   // the first token whose running sum exceeds u times the total
     if (target < base || target >= base + own) return;
     {
@@ -781,7 +720,7 @@ cudaError_t sample_fits(const Fits *&out) {
     Fits &f = fits.v[dev];
     out = &f;
     if (f.known) return cudaSuccess;
-    e = smem_optin_once(moe_sample_kernel<BF16, true, 1024>, opted);
+    e = smem_optin_once(moe_sample_kernel<BF16, true, 1024, false>, opted);
     for (int C = 1; C <= kMaxCluster && e == cudaSuccess; C++) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(C), cfg.blockDim = dim3(1024), cfg.dynamicSmemBytes = kAloneBytes;
@@ -789,16 +728,16 @@ cudaError_t sample_fits(const Fits *&out) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = C, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr, cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&f.n[C], moe_sample_kernel<BF16, true, 1024>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&f.n[C], moe_sample_kernel<BF16, true, 1024, false>, &cfg);
     }
     f.known = e == cudaSuccess;
     return e;
 }
 
-template <bool BF16, bool RES, int NT>
+template <bool BF16, bool RES, int NT, bool LIMITS>
 cudaError_t sample_launch(const SampleArgs &a, int C, size_t smem, cudaStream_t st) {
     static PerDevice<bool> opted;
-    cudaError_t e = smem_optin_once(moe_sample_kernel<BF16, RES, NT>, opted);
+    cudaError_t e = smem_optin_once(moe_sample_kernel<BF16, RES, NT, LIMITS>, opted);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.rows * C);
@@ -812,10 +751,10 @@ cudaError_t sample_launch(const SampleArgs &a, int C, size_t smem, cudaStream_t 
     attr[1].val.clusterDim.x = C, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, moe_sample_kernel<BF16, RES, NT>, a);
+    return cudaLaunchKernelEx(&cfg, moe_sample_kernel<BF16, RES, NT, LIMITS>, a);
 }
 
-template <bool BF16>
+template <bool BF16, bool LIMITS>
 cudaError_t sample_plan(SampleArgs a, cudaStream_t st) {
     const int VE = BF16 ? 8 : 4;
     const long long vecs = ((long long)a.V + VE - 1) / VE + 1;   // one more where the first is cut
@@ -844,12 +783,16 @@ cudaError_t sample_plan(SampleArgs a, cudaStream_t st) {
     const size_t smem = (size_t)a.seg * 16;
     a.drop = 0;
     while (((long long)a.V << 24) >> a.drop > 0xFFFFFFFFll - a.V) a.drop++;
-    if (smem > (alone ? kAloneBytes : kSharedBytes)) return sample_launch<BF16, false, 512>(a, C, 0, st);
+    if (smem > (alone ? kAloneBytes : kSharedBytes)) return sample_launch<BF16, false, 512, LIMITS>(a, C, 0, st);
     // (alone, with much to do: all its warps)
-    return alone && a.seg >= 2048 ? sample_launch<BF16, true, 1024>(a, C, smem, st) : sample_launch<BF16, true, 512>(a, C, smem, st);
+    return alone && a.seg >= 2048 ? sample_launch<BF16, true, 1024, LIMITS>(a, C, smem, st) : sample_launch<BF16, true, 512, LIMITS>(a, C, smem, st);
 }
 
 }  // namespace
+
+cudaError_t launch_sample_limits(const SampleArgs &a, bool bf16, cudaStream_t st) {
+    return bf16 ? sample_plan<true, true>(a, st) : sample_plan<false, true>(a, st);
+}
 
 extern "C" int moe_sample(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride,
                           const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
@@ -867,6 +810,6 @@ extern "C" int moe_sample(const void *logits, int is_bf16, int n_rows, int vocab
     a.x = logits, a.rows = n_rows, a.V = vocab, a.stride = row_stride;
     a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p, a.u = u, a.ids = ids;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = is_bf16 ? sample_plan<true>(a, st) : sample_plan<false>(a, st);
+    const cudaError_t e = is_bf16 ? sample_plan<true, false>(a, st) : sample_plan<false, false>(a, st);
     return e == cudaSuccess ? MOE_OK : moe_fail_status(MOE_ECUDA, "moe_sample: %s", cudaGetErrorString(e));
 }

@@ -32,7 +32,11 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_plan_set_i", "moe_plan_se
            "moe_attn_destroy", "moe_attn_get_device_status", "moe_pages_assign", "moe_kv8_create", "moe_kv8_set_i",
            "moe_kv8_set_f", "moe_kv8_set_cache", "moe_kv8_set_sinks", "moe_kv8_workspace_bytes",
            "moe_kv8_set_workspace", "moe_kv8_append", "moe_kv8_attend", "moe_kv8_destroy", "moe_kv8_get_device_status",
-           "moe_sample",
+           "moe_sample", "moe_rotary_create", "moe_rotary_set_f", "moe_rotary_set_freqs", "moe_rotary_set_norm",
+           "moe_rotary_apply", "moe_rotary_destroy", "moe_kv4_create", "moe_kv4_set_i", "moe_kv4_set_f", "moe_kv4_page_bytes",
+           "moe_kv4_set_cache", "moe_kv4_set_sinks", "moe_kv4_workspace_bytes", "moe_kv4_set_workspace", "moe_kv4_append",
+           "moe_kv4_read", "moe_kv4_attend", "moe_kv4_get_device_status", "moe_kv4_destroy", "moe_verify_workspace_bytes",
+           "moe_verify",
            "moe_last_error"]
 
 
@@ -140,6 +144,34 @@ def load(build_if_missing: bool = True):
     L.moe_kv8_destroy.restype = None
     L.moe_kv8_destroy.argtypes = [P]
     L.moe_sample.argtypes = [P, I, I, I, LL, P, P, P, P, P, P, P]
+    L.moe_rotary_create.restype = P
+    L.moe_rotary_create.argtypes = [I, I, I, I]
+    L.moe_rotary_set_f.argtypes = [P, C.c_char_p, D]
+    L.moe_rotary_set_freqs.argtypes = [P, P, P]
+    L.moe_rotary_set_norm.argtypes = [P, P, P]
+    L.moe_rotary_apply.argtypes = [P, P, LL, I, P, LL, I, P, LL, I, P, LL, P, LL, P]
+    L.moe_rotary_destroy.restype = None
+    L.moe_rotary_destroy.argtypes = [P]
+    L.moe_kv4_create.restype = P
+    L.moe_kv4_create.argtypes = [I, I, I, I, I]
+    L.moe_kv4_set_i.argtypes = [P, C.c_char_p, LL]
+    L.moe_kv4_set_f.argtypes = [P, C.c_char_p, D]
+    L.moe_kv4_page_bytes.restype = SZ
+    L.moe_kv4_page_bytes.argtypes = [P]
+    L.moe_kv4_set_cache.argtypes = [P, P]
+    L.moe_kv4_set_sinks.argtypes = [P, P]
+    L.moe_kv4_workspace_bytes.restype = SZ
+    L.moe_kv4_workspace_bytes.argtypes = [P]
+    L.moe_kv4_set_workspace.argtypes = [P, P, SZ]
+    L.moe_kv4_append.argtypes = [P, P, P, LL, LL, P, I, P]
+    L.moe_kv4_read.argtypes = [P, P, I, P, P, LL, LL, P]
+    L.moe_kv4_attend.argtypes = [P, P, LL, P, P, P, I, I, I, I, P, LL, P]
+    L.moe_kv4_get_device_status.argtypes = [P, C.POINTER(I), P]
+    L.moe_kv4_destroy.restype = None
+    L.moe_kv4_destroy.argtypes = [P]
+    L.moe_verify_workspace_bytes.restype = SZ
+    L.moe_verify_workspace_bytes.argtypes = [I]
+    L.moe_verify.argtypes = [P, I, I, I, LL, P, P, LL, P, I, P, P, P, P, P, P, P, P, P, SZ, P]
     L.moe_last_error.restype = C.c_char_p
     L.moe_last_error.argtypes = []
     for name in EXPORTS:
@@ -470,12 +502,12 @@ class AttnPlan:
             pass
 
 
-_DTYPES = {}    # "i4", "f4", "u1", "b2": int32, float32, uint8, bfloat16
+_DTYPES = {}    # "i4", "f4", "f8", "u1", "b2": int32, float32, float64, uint8, bfloat16
 
 
 def _dtypes():
     import torch
-    _DTYPES.update(i4=torch.int32, f4=torch.float32, u1=torch.uint8, b2=torch.bfloat16)
+    _DTYPES.update(i4=torch.int32, f4=torch.float32, f8=torch.float64, u1=torch.uint8, b2=torch.bfloat16)
     return _DTYPES
 
 
@@ -652,3 +684,220 @@ def sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None,
         _arg(ids, "i4", d, n, "ids"), _stream(stream, d))
     if rc:
         _check(rc)
+
+
+class Rotary:
+    """Norms and rotary positions of queries and keys (moe_rotary_*): the plan and its table.  freqs: radians a
+    position of each pair of dims (host, float64; a multiple of 8 of them, at most head_dim / 2); axes: the axis
+    of positions that turns each pair (host; None: one axis); pairs are dims i and i + len(freqs), or with
+    `interleaved` 2 i and 2 i + 1.  q_gamma, k_gamma: float32 [head_dim] device tensors, None: that side is not
+    normed.  factor: of the sines and cosines.  All arrays are on one device, which is the current one where
+    apply is called."""
+
+    def __init__(self, head_dim: int, freqs, axes=None, n_axes: int | None = None, interleaved: bool = False, q_gamma=None,
+                 k_gamma=None, eps: float = 1e-5, factor: float = 1.0, device="cuda"):
+        import torch
+        self.L = load()
+        freqs = np.ascontiguousarray(freqs, np.float64).reshape(-1)
+        if axes is not None:
+            axes = np.asarray(axes).reshape(-1)
+            if len(axes) != len(freqs) or (len(axes) and (axes.min() < 0 or axes.max() > 255)):
+                raise MoeError(MOE_EINVAL, "axes: one of 0 .. 255 for each of freqs is needed")
+        most = 0 if axes is None or not len(axes) else int(axes.max())
+        self.head_dim, self.n_axes = int(head_dim), most + 1 if n_axes is None else int(n_axes)
+        if self.n_axes <= most:
+            raise MoeError(MOE_EINVAL, f"axes: one is {most}, there are {self.n_axes}")
+        h = self.L.moe_rotary_create(self.head_dim, len(freqs), self.n_axes, int(bool(interleaved)))
+        if not h:
+            raise MoeError(MOE_EINVAL, self.L.moe_last_error().decode())
+        self.h = C.c_void_p(h)
+        _check(self.L.moe_rotary_set_f(self.h, b"eps", float(eps)))
+        _check(self.L.moe_rotary_set_f(self.h, b"factor", float(factor)))
+        self.freqs = torch.from_numpy(freqs if len(freqs) else np.zeros(1)).to(device)
+        self.axes = None if axes is None else torch.from_numpy(np.ascontiguousarray(axes, np.uint8)).to(device)
+        self.q_gamma, self.k_gamma = q_gamma, k_gamma
+        d = self.device = self.freqs.get_device()
+        if d < 0:
+            raise MoeError(MOE_EINVAL, "the table: a CUDA device is needed")
+        _check(self.L.moe_rotary_set_freqs(self.h, _arg(self.freqs, "f8", d, None, "freqs"), _arg(self.axes, "u1", d, None, "axes", none=True)))
+        _check(self.L.moe_rotary_set_norm(self.h, _arg(q_gamma, "f4", d, self.head_dim, "q_gamma", none=True),
+                                          _arg(k_gamma, "f4", d, self.head_dim, "k_gamma", none=True)))
+
+    def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """q, k: bf16 [n][heads][head_dim] (rows may be strided; k may be None); positions: int32 [n], or
+        [n_axes][n]; q_out, k_out: likewise, None: in place."""
+        d = _device(q, "q")
+        if d != self.device:
+            raise MoeError(MOE_EINVAL, f"the table is on device {self.device}, the current device is {d}")
+        n = q.shape[0]
+        if positions.shape != ((n,) if self.n_axes == 1 and len(positions.shape) == 1 else (self.n_axes, n)):
+            raise MoeError(MOE_EINVAL, f"positions: shape ({self.n_axes}, {n})" + (f" or ({n},)" if self.n_axes == 1 else "") + " is needed")
+        sides = []
+        for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
+            if x is None and out is None and what == "k":
+                sides.append((None, 0, 0, None, 0))
+                continue
+            if x is None or len(x.shape) != 3:
+                raise MoeError(MOE_EINVAL, f"{what}: a CUDA tensor of bf16 rows [n][heads][{self.head_dim}] is needed")
+            heads, out = x.shape[1], x if out is None else out
+            xp, xs = _head_rows(x, heads, self.head_dim, d, what)
+            op, os_ = _head_rows(out, heads, self.head_dim, d, what + "_out")
+            if x.shape[0] != n or out.shape[0] != n:
+                raise MoeError(MOE_EINVAL, "q, k and the outputs must have the same number of rows")
+            sides.append((xp, xs, heads, op, os_))
+        (qp, qs, qh, qop, qos), (kp, ks, kh, kop, kos) = sides
+        rc = self.L.moe_rotary_apply(self.h, qp, qs, qh, kp, ks, kh, _arg(positions, "i4", d, None, "positions"), n, n, qop, qos, kop, kos,
+                                     _stream(stream, d))
+        if rc:
+            _check(rc)
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.L.moe_rotary_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Kv4:
+    """One layer's paged key/value cache in 4 bits (moe_kv4_*): the plan, its workspace, and the cache, uint8
+    [n_pages][kv_heads][page_size * head_dim * 17 / 16] (`cache` to use a given one).  `workspace`: another plan,
+    used on the same stream, whose workspace this one shares.  All of a plan's arrays are on one device, which is
+    the current one where its methods are called."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, n_pages: int, sliding_window: int = 0,
+                 softmax_scale: float | None = None, sinks=None, cache=None, workspace: "Kv4 | None" = None, device="cuda"):
+        import torch
+        self.L = load()
+        h = self.L.moe_kv4_create(q_heads, kv_heads, head_dim, page_size, n_pages)
+        if not h:
+            raise MoeError(MOE_EINVAL, self.L.moe_last_error().decode())
+        self.h = C.c_void_p(h)
+        self.q_heads, self.kv_heads, self.head_dim, self.page_size, self.n_pages = q_heads, kv_heads, head_dim, page_size, n_pages
+        _check(self.L.moe_kv4_set_i(self.h, b"sliding_window", int(sliding_window)))
+        if softmax_scale is not None:
+            _check(self.L.moe_kv4_set_f(self.h, b"softmax_scale", float(softmax_scale)))
+        page = int(self.L.moe_kv4_page_bytes(self.h))
+        if cache is None:
+            cache = torch.zeros((n_pages, kv_heads, page // kv_heads), dtype=torch.uint8, device=device)
+        self.cache = cache
+        d = self.device = cache.get_device()   # whose tensors and streams the calls take
+        if d < 0:
+            raise MoeError(MOE_EINVAL, "cache: a CUDA tensor is needed")
+        _check(self.L.moe_kv4_set_cache(self.h, _arg(cache, "u1", d, n_pages * page, "cache")))
+        self.sinks = sinks
+        _check(self.L.moe_kv4_set_sinks(self.h, _arg(sinks, "f4", d, q_heads, "sinks", none=True)))
+        n = int(self.L.moe_kv4_workspace_bytes(self.h))
+        self.ws = torch.empty(n + 256, dtype=torch.uint8, device=cache.device) if workspace is None else workspace.ws
+        if self.ws.numel() < n + 256:
+            raise MoeError(MOE_ENOMEM, "the shared workspace is too small for this plan")
+        at = _arg(self.ws, "u1", d, None, "workspace")
+        with torch.cuda.device(d):
+            _check(self.L.moe_kv4_set_workspace(self.h, at + (-at) % 256, n))
+
+    _on = Kv8._on
+
+    def _rows(self, k, v, slots, d):
+        kp, ks = _head_rows(k, self.kv_heads, self.head_dim, d, "k")
+        vp, vs = _head_rows(v, self.kv_heads, self.head_dim, d, "v")
+        n = k.shape[0]
+        if v.shape[0] != n:
+            raise MoeError(MOE_EINVAL, "k and v must have the same number of rows")
+        return kp, vp, ks, vs, _arg(slots, "i4", d, n, "slots"), n
+
+    def append(self, k, v, slots, stream=None):
+        """k, v: bf16 [n][kv_heads][head_dim] (rows may be strided); slots: int32 [n]."""
+        d = self._on(k, "k")
+        kp, vp, ks, vs, at, n = self._rows(k, v, slots, d)
+        rc = self.L.moe_kv4_append(self.h, kp, vp, ks, vs, at, n, _stream(stream, d))
+        if rc:
+            _check(rc)
+
+    def read(self, slots, k, v, stream=None):
+        """What the cache holds at slots into k, v, as append takes them."""
+        d = self._on(k, "k")
+        kp, vp, ks, vs, at, n = self._rows(k, v, slots, d)
+        rc = self.L.moe_kv4_read(self.h, at, n, kp, vp, ks, vs, _stream(stream, d))
+        if rc:
+            _check(rc)
+
+    def attend(self, q, lens, table, out, starts=None, max_new: int = 1, stream=None):
+        """q, out: bf16 [n_rows][q_heads][head_dim] (rows may be strided); lens int32 [n_seqs]; table int32
+        [n_seqs][width]; starts int32 [n_seqs + 1] (None: one row a sequence); max_new: most rows of a sequence."""
+        d = self._on(q, "q")
+        qp, qs = _head_rows(q, self.q_heads, self.head_dim, d, "q")
+        op, os_ = _head_rows(out, self.q_heads, self.head_dim, d, "out")
+        n, width = table.shape
+        if out.shape[0] != q.shape[0]:
+            raise MoeError(MOE_EINVAL, "q and out must have the same number of rows")
+        rc = self.L.moe_kv4_attend(self.h, qp, qs, _arg(starts, "i4", d, n + 1, "starts", none=True), _arg(lens, "i4", d, n, "lens"),
+                                   _arg(table, "i4", d, None, "table"), width, n, max_new, q.shape[0], op, os_, _stream(stream, d))
+        if rc:
+            _check(rc)
+
+    def device_status(self, stream=None) -> int:
+        s = C.c_int(0)
+        rc = self.L.moe_kv4_get_device_status(self.h, C.byref(s), _stream(stream, self._on(self.ws, "the plan")))
+        if rc not in (MOE_OK, MOE_EDEVICE):
+            _check(rc)
+        return s.value
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.L.moe_kv4_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Verify:
+    """Verification of drafted tokens (moe_verify) in calls of at most max_rows rows: holds their workspace, which
+    is on the device that is current where it is made.  Calls that can overlap on the GPU need one each."""
+
+    def __init__(self, max_rows: int, device="cuda"):
+        import torch
+        self.L, self.max_rows = load(), int(max_rows)
+        n = int(self.L.moe_verify_workspace_bytes(self.max_rows))
+        self.ws = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+        self.bytes, self.device = n, self.ws.get_device()
+        if self.device < 0:
+            raise MoeError(MOE_EINVAL, "the workspace: a CUDA device is needed")
+
+    def run(self, logits, drafts, u, draws, starts, ids, accepted, draft_probs=None, temperature=None, top_k=None, top_p=None,
+            min_p=None, stream=None):
+        """logits [n][vocab] fp32 or bf16 (rows may be strided): sequence b's rows are starts[b] .. starts[b + 1] - 1
+        (int32 [n_seqs + 1]); drafts int32 [n], draft_probs fp32 [n][vocab] (rows may be strided; None: drafted tokens
+        were certain), u float32 [n], draws float32 [n_seqs], in [0, 1); temperature, top_p, min_p float32 [n_seqs]
+        and top_k int32 [n_seqs], each may be None.  Writes ids int32 [n] and accepted int32 [n_seqs]."""
+        shape, kinds = logits.shape, _DTYPES or _dtypes()
+        bf16 = logits.dtype is kinds["b2"]
+        d = _device(logits, "logits")
+        if d != self.device:
+            raise MoeError(MOE_EINVAL, f"the workspace is on device {self.device}, the current device is {d}")
+        if len(shape) != 2 or not (bf16 or logits.dtype is kinds["f4"]) or (shape[0] and logits.stride(1) != 1 and shape[1] > 1):
+            raise MoeError(MOE_EINVAL, "logits: a CUDA tensor of fp32 or bf16 rows is needed")
+        n, vocab = shape
+        probs, probs_stride = None, 0
+        if draft_probs is not None:
+            if draft_probs.dtype is not kinds["f4"] or draft_probs.get_device() != d or draft_probs.shape != shape or \
+                    (n and draft_probs.stride(1) != 1 and vocab > 1):
+                raise MoeError(MOE_EINVAL, f"draft_probs: a CUDA tensor of fp32 rows [{n}][{vocab}] on device {d} is needed")
+            probs, probs_stride = draft_probs.data_ptr(), draft_probs.stride(0) if n > 1 else vocab
+        S = starts.numel() - 1
+        rc = self.L.moe_verify(
+            logits.data_ptr(), bf16, n, vocab, logits.stride(0) if n > 1 else vocab, _arg(drafts, "i4", d, n, "drafts"), probs, probs_stride,
+            _arg(starts, "i4", d, None, "starts"), S, _arg(temperature, "f4", d, S, "temperature", none=True),
+            _arg(top_k, "i4", d, S, "top_k", none=True), _arg(top_p, "f4", d, S, "top_p", none=True),
+            _arg(min_p, "f4", d, S, "min_p", none=True), _arg(u, "f4", d, n, "u"), _arg(draws, "f4", d, S, "draws"),
+            _arg(ids, "i4", d, n, "ids"), _arg(accepted, "i4", d, S, "accepted"), _arg(self.ws, "u1", d, None, "workspace"), self.bytes,
+            _stream(stream, d))
+        if rc:
+            _check(rc)
