@@ -1,7 +1,7 @@
 // moe_kv8_attend.cu -- attention over the 8-bit paged key/value cache for a few
 // new tokens a sequence (decode steps), and the choice between this kernel and
 // that for prompts (moe_kv8_prompt.cu).
-#include "moe_kv8.cuh"
+#include "moe_kv_few.cuh"
 
 #include <algorithm>
 
@@ -33,12 +33,6 @@ namespace {
 // output), as is a form in fp32 that is rounded to bf16 at its end.
 // q is scaled per row by a power of two into fp16's range: exact for a bf16
 // row's values down to 2^-28 of its largest.
-constexpr int kTile = 64;             // tokens of a unit
-constexpr int kRows = 16;             // rows of a unit
-constexpr int kMaxCtas = 160;         // the tickets and partials there are room for
-constexpr int kSmemSeqs = 512;       // sequences whose lengths are held in shared memory
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Measured: 16 x 4096 tokens of 8 heads of 64 (67 MB) 23.8 us: lengths and
 // table 1.4, the first pages 2.8, units 8.0 (HBM's rate), joins 4.7, the launch
@@ -72,72 +66,6 @@ struct FewArgs {
     uint32_t *tickets;         // [kMaxCtas], zero between calls
     float *parts;              // [kMaxCtas][2][partial_floats]
     int *seqs;                 // [3][n_seqs], or null: in shared memory
-};
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-// Bounded wait of a whole warp: false (and the status word set) after about 2 s.
-__device__ bool bar_wait(uint32_t bar, uint32_t parity, int32_t *status, int where) {
-    if (bar_try(bar, parity)) return true;
-    uint64_t t0, t1;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    for (uint32_t i = 1;; i++) {
-        if (bar_try(bar, parity)) return true;
-        if ((i & 63) == 0) {
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
-            if (t1 - t0 > kWaitNs) {
-                set_device_error(status, MOE_DEV_WAIT_TIMEOUT, where);
-                return false;
-            }
-        }
-    }
-}
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
-}
-
-struct Job {
-    int b, h, rt, nt;  // sequence, kv head, row tile, units
-    int u0;            // its first unit
-};
-
-// One of the CTA's pieces of a job: partials that lie side by side in it.
-struct Seg {
-    int u0;             // the job's first unit, -1: none
-    int nt, b, h, rt;
 };
 
 // What turns a row's accumulator into its output (sink: the head's logit in
@@ -724,15 +652,6 @@ template <int D>
 cudaError_t few_page(const FewArgs &f, bool top, int ctas, cudaStream_t st) {
     return f.a.c.P == 16 ? few_rows<D, 16>(f, top, ctas, st) : f.a.c.P == 32 ? few_rows<D, 32>(f, top, ctas, st)
                                                                              : few_rows<D, 64>(f, top, ctas, st);
-}
-
-cudaError_t sm_count(int *n) {
-    static PerDevice<int> sms;
-    int dev = 0;
-    cudaError_t e = current_device_slot(&dev);
-    if (e == cudaSuccess && !sms.v[dev]) e = cudaDeviceGetAttribute(&sms.v[dev], cudaDevAttrMultiProcessorCount, dev);
-    *n = sms.v[dev];
-    return e;
 }
 
 }  // namespace
