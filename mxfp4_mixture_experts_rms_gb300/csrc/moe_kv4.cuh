@@ -41,4 +41,5 @@ struct Kv4Attend {
 };
 
 cudaError_t launch_kv4_attend(const Kv4Attend &a, unsigned char *ws, cudaStream_t st);
+cudaError_t launch_kv4_prompt(const Kv4Attend &a, int32_t *status, cudaStream_t st);
 size_t kv4_workspace_bytes(int head_dim);

@@ -1,0 +1,420 @@
+// moe_kv4_prompt.cu -- attention over the 4-bit paged cache for many new tokens
+// a sequence (prompts, or pieces of them): tensor-core products on tcgen05 with
+// accumulators in tensor memory.
+//
+// The CTA is that of the 8-bit cache's kernel (moe_kv8_prompt.cu): one per
+// (sequence, kv head, 256 rows), 64 cached tokens a step, eight softmax warps,
+// four that turn codes into operand tiles, one that copies pages, two that issue
+// a half's products.  What differs:
+//  * Keys and values become bf16, scale included: exact (E2M1 times a power of
+//    two), so that no reference is needed however far the scales are apart.
+//    Both tiles are [token][D], the same conversion; V's is read turned.
+//  * Weights are bf16, 8 bits where a sum takes fp32 weights in the plain form:
+//    with fp16 ones values would need a reference for each block of 32 dims.
+//    Results are 2.0e-3 from those in 64 bits (relative, over an output), 1.6e-3
+//    of it their own rounding to bf16; the sum of the weights is fp32's.
+//  * One softmax reference m, moved (to 8 above the largest score) only when a
+//    score passes it, so that weights are at most 1 and the accumulator in tensor
+//    memory is rarely rescaled.
+//  * The values of a block are finite whatever the cache holds, so that a token
+//    that a row does not see adds nothing to it.
+#include "moe_kv_prompt.cuh"
+#include "moe_kv4.cuh"
+
+#include <algorithm>
+
+namespace {
+
+template <int D>
+struct Smem {   // offsets from a 1024-byte boundary
+    static constexpr int kStages = D == 64 ? 4 : 3, kRaw = D == 64 ? 4 : 2;   // operand tiles; steps of copied pages
+    static constexpr int kStep = kT * D / 16 * 17;          // bytes of one
+    static constexpr int kQ = 0;
+    static constexpr int kQ1 = kM * D * 2;                  // of a half: Q [128][D], P [128][64]
+    static constexpr int kP = 2 * kQ1, kP1 = kM * kT * 2;
+    static constexpr int kK = kP + 2 * kP1;                 // kStages x [64][D]
+    static constexpr int kV = kK + kStages * kT * D * 2;    // kStages x [64][D]
+    static constexpr int kCodes = kV + kStages * kT * D * 2; // kRaw x pages
+    static constexpr int kBytes = kCodes + kRaw * kStep;
+};
+
+// V's tile [64][D], read with its rows as K: halves of 64 dims kT * 128 bytes
+// apart, groups of eight rows 1024.
+__device__ __forceinline__ uint64_t turned_desc(uint32_t at) {
+    return (uint64_t)((at >> 4) & 0x3FFFu) | (uint64_t)(kT * 128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+struct PromptArgs {
+    Kv4Attend a;
+    int G;
+    int32_t *status;
+};
+
+// A block of 32 codes with its scale -> 64 bytes of bf16.  The fp16 pattern of an
+// E2M1 value, shifted to bf16's places, is the value times 2^-112.
+__device__ __forceinline__ void decode32(uint4 codes, uint32_t byte, uint4 (&out)[4]) {
+    const int e = min((int)byte, kKv4MaxByte) - 127 + 112;   // at most 237
+    const float f0 = byte ? pow2i(min(e, 127)) : 0.f, f1 = pow2i(max(e - 127, 0));
+    const __nv_bfloat162 k0 = __floats2bfloat162_rn(f0, f0), k1 = __floats2bfloat162_rn(f1, f1);
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        uint32_t h[4];
+        e2m1x8_to_f16(w[c], h);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t x = (h[i] >> 3 & 0x0FFF0FFFu) | (h[i] & 0x80008000u);
+            h[i] = bits_of(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), k0));
+        }
+        out[c] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    if (e > 127) {
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            uint32_t h[4] = {out[c].x, out[c].y, out[c].z, out[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) h[i] = bits_of(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&h[i]), k1));
+            out[c] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+}
+
+template <int D, int P>
+__global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __grid_constant__ PromptArgs f) {
+    constexpr int NP = kT / P, NB = D / 32, PB = kv4_page_bytes(P, D);
+    typedef Smem<D> L;
+    constexpr int kStages = L::kStages, kRaw = L::kRaw;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2], drain[2];
+    __shared__ uint32_t rmeta[kRaw], meta[kStages];   // the pages that are there
+    __shared__ uint32_t tmem_slot;
+    __shared__ int job[2];
+    const Kv4Attend &a = f.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.x % a.c.KVH;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; s++) bar_init(&full[s], kLoaders / 32), bar_init(&empty[s], 2);
+        for (int s = 0; s < kRaw; s++) bar_init(&raw[s], 2), bar_init(&raw_empty[s], kLoaders / 32);
+        for (int h = 0; h < 2; h++)
+            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], kSoftmax / 2), bar_init(&p_full[h], kSoftmax / 2), bar_init(&o_done[h], 1), bar_init(&drain[h], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {
+        // a tile of 256 rows: sequences in order, a sequence's last (longest)
+        // tile first, its heads together, so that the last to start are short
+        int x = blockIdx.x / a.c.KVH, found = -1, rt = 0;
+        for (int b0 = 0; b0 < a.n_seqs && found < 0; b0 += 32) {
+            int row0, n = 0, pos0;
+            if (b0 + lane < a.n_seqs) kv8_rows(a, b0 + lane, row0, n, pos0);
+            const int mine = (n * f.G + 2 * kM - 1) / (2 * kM);
+            int inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, x < inc);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                found = b0 + at;
+                rt = __shfl_sync(0xffffffffu, inc, at) - 1 - x;
+            } else {
+                x -= __shfl_sync(0xffffffffu, inc, 31);
+            }
+        }
+        if (lane == 0) job[0] = found, job[1] = rt;
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    // only now: a dependent's CTA that got tensor memory first would wait for
+    // this grid, and this grid for it
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t tmem = tmem_slot;
+    const int b = job[0];
+    if (b >= 0) {
+        int row0, n, pos0;
+        kv8_rows(a, b, row0, n, pos0);
+        const int r0 = job[1] * 2 * kM, rows = min(2 * kM, n * f.G - r0), halves = rows > kM ? 2 : 1;
+        const int p_first = pos0 + r0 / f.G, p_last = pos0 + (r0 + rows - 1) / f.G;
+        // tokens that any row sees, and the steps over them (aligned to 64)
+        const int seen = (int)max(0ll, min((long long)p_last + 1, (long long)a.width * P));
+        const int lo = kv8_first(p_first, a.window);
+        const int step0 = lo / kT, steps = max(1, (seen + kT - 1) / kT - step0);
+        int32_t *status = f.status;
+
+        if (warp < kSoftmax) {
+            // ---- the softmax ----
+            const int h = warp >> 2;
+            if (h < halves) {
+                const int r = tid & (kM - 1), rr = r0 + h * kM + r, i2 = rr / f.G, head = kvh * f.G + rr - i2 * f.G;
+                const bool on = h * kM + r < rows;
+                // tokens from .. to that the row sees (where their pages are)
+                const int to = on ? min(seen - 1, pos0 + i2) : -1, from = kv8_first(pos0 + i2, a.window);
+                {
+                    const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (long long)(row0 + i2) * a.q_stride + head * D);
+#pragma unroll 8
+                    for (int c = 0; c < D / 8; c++)
+                        *reinterpret_cast<uint4 *>(smem + L::kQ + h * L::kQ1 + (c / 8) * (kM * 128) + swizzled(r, c % 8)) = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+                    fence_async();
+                    bar_arrive_warp(&q_full[h]);
+                }
+                const float sc = a.scale * kLog2e;
+                float m = -INFINITY, l = 0.f;
+                const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * h;
+                unsigned char *pt = smem + L::kP + h * L::kP1;
+                bool ok = true;
+                for (int j = 0; j < steps; j++) {
+                    const int st = j % kStages, t0 = (step0 + j) * kT;
+                    // (a wait that gave up is only found out below: what it waited for is then read as it is)
+                    ok = bar_wait(&s_full[h][j & 1], (uint32_t)(j >> 1) & 1, status, 100);
+                    __syncwarp();
+                    fence_after();
+                    float s[kT];
+                    tmem_ld32(lanes + (j & 1) * kT, s);
+                    tmem_ld32(lanes + (j & 1) * kT + 32, s + 32);
+                    const uint32_t there = meta[st];
+                    tmem_wait(s);
+                    tmem_wait(s + 32);
+                    if (!(t0 >= from && t0 + kT - 1 <= to && there == (1u << NP) - 1)) {
+                        const int c0 = max(from - t0, 0), c1 = min(to - t0, kT - 1);   // columns that the row sees
+                        uint64_t sees = c1 < c0 ? 0 : ~0ull >> (kT - 1 - c1) & ~0ull << c0;
+#pragma unroll
+                        for (int p = 0; p < NP; p++)
+                            if (!(there >> p & 1)) sees &= ~(~0ull >> (64 - P) << (p * P));
+#pragma unroll
+                        for (int c = 0; c < kT; c++)
+                            if (!(sees >> c & 1)) s[c] = -INFINITY;
+                    }
+                    float x[4];   // four chains
+#pragma unroll
+                    for (int c = 0; c < 4; c++) x[c] = fmaxf(s[c], s[4 + c]);
+#pragma unroll
+                    for (int c = 8; c < kT; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) x[e] = max3(x[e], s[c + e], s[c + 4 + e]);
+                    const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * sc;
+                    float corr = 1.f;
+                    const bool move = mx > m;
+                    if (move) {
+                        const float mn = mx + 8.f;
+                        corr = ex2(m - mn);
+                        l *= corr, m = mn;
+                    }
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    // large scores: products rounded as the maximum was
+                    float ks = sc;
+                    if (__any_sync(0xffffffffu, fabsf(ms) >= 0x1p17f)) {
+#pragma unroll
+                        for (int c = 0; c < kT; c++) s[c] = __fmul_rn(s[c], sc);
+                        ks = 1.f;
+                    }
+                    // the products of the step before have read the P tile
+                    if (j > 0) ok = bar_wait(&o_done[h], (uint32_t)(j - 1) & 1, status, 101) && ok;
+                    if (__any_sync(0xffffffffu, move || !ok)) {
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        fence_after();
+                        if (j > 0) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) tmem_scale16(lanes + 2 * kT + c, corr);
+                        }
+                    }
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kT; c += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            float w0, w1;
+                            fma2(w0, w1, s[c + 2 * e], s[c + 2 * e + 1], ks, -ms);
+                            w0 = ex2(w0), w1 = ex2(w1);
+                            add2(s0, s1, w0, w1);
+                            y[e] = bits_of(__floats2bfloat162_rn(w0, w1));
+                        }
+                        *reinterpret_cast<uint4 *>(pt + swizzled(r, c / 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                    l += s0 + s1;
+                    fence_async();
+                    fence_before();
+                    bar_arrive_warp(&p_full[h]);
+                }
+                if (ok) ok = bar_wait_warp(&o_done[h], (uint32_t)(steps - 1) & 1, status, 102);
+                if (ok) {
+                    fence_after();
+                    // (the row anew, so that no registers hold it meanwhile)
+                    uint32_t r;
+                    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(r));
+                    r &= kM - 1;
+                    int row0, n, pos0;
+                    kv8_rows(a, *(volatile int *)&job[0], row0, n, pos0);
+                    const int rr = (*(volatile int *)&job[1] * 2 + h) * kM + (int)r, i2 = rr / f.G, head = kvh * f.G + rr - i2 * f.G;
+                    const bool on = rr < n * f.G;
+                    const float sink = on && a.sinks ? a.sinks[head] * kLog2e : -INFINITY;
+                    const float top = fmaxf(m, sink);
+                    const float den = top == -INFINITY ? l : (m == -INFINITY ? l : l * ex2(m - top)) + ex2(sink - top);
+                    // two factors: their product may be below 2^-126 where the output is not
+                    const float k1 = den == 0.f || m == -INFINITY ? 0.f : ex2(0.5f * (m - top)), k2 = k1 == 0.f ? 0.f : k1 / den;
+                    uint4 *o = reinterpret_cast<uint4 *>(a.out + (long long)(row0 + i2) * a.o_stride + head * D);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float v[32];
+                        tmem_ld32(lanes + 2 * kT + c, v);
+                        tmem_wait(v);
+                        if (!on) continue;
+#pragma unroll
+                        for (int x = 0; x < 32; x++) v[x] = v[x] * k1 * k2;
+#pragma unroll
+                        for (int x = 0; x < 4; x++)
+                            o[c / 8 + x] = make_uint4(bits_of(__floats2bfloat162_rn(v[8 * x], v[8 * x + 1])),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 2], v[8 * x + 3])),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 4], v[8 * x + 5])),
+                                                      bits_of(__floats2bfloat162_rn(v[8 * x + 6], v[8 * x + 7])));
+                    }
+                }
+            }
+        } else if (warp < kCopier) {
+            // ---- pages to operand tiles ----
+            const int x = tid - kSoftmax * 32;
+            bool ok = true;
+            for (int j = 0; j < steps; j++) {
+                const int st = j % kStages, slot = j % kRaw;
+                ok = bar_wait_warp(&raw[slot], (uint32_t)(j / kRaw) & 1, status, 108);
+                if (!ok) break;
+                if (j >= kStages) {
+                    ok = bar_wait_warp(&empty[st], (uint32_t)(j / kStages - 1) & 1, status, 103);
+                    if (!ok) break;
+                }
+                const uint32_t there = rmeta[slot];
+                // a block a thread: tokens side by side, so that a tile's rows are stored without conflicts; what no page
+                // brought is what the slot held before, and never seen
+                const unsigned char *codes = smem + L::kCodes + slot * L::kStep;
+                unsigned char *K = smem + L::kK + st * (kT * D * 2), *V = smem + L::kV + st * (kT * D * 2);
+#pragma unroll 2
+                for (int i = x; i < 2 * NB * kT; i += kLoaders) {
+                    const int tok = i % kT, b = i / kT % NB, side = i / kT / NB;
+                    const unsigned char *page = codes + tok / P * PB;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(page + side * (P * D / 2) + (b * P + tok % P) * 16);
+                    uint4 y[4];
+                    decode32(w, page[P * D + (side * NB + b) * P + tok % P / 16 * 16 + kv4_scale_byte(tok % 16)], y);
+                    unsigned char *tile = (side ? V : K) + b / 2 * (kT * 128);
+#pragma unroll
+                    for (int c = 0; c < 4; c++) *reinterpret_cast<uint4 *>(tile + swizzled(tok, b % 2 * 4 + c)) = y[c];
+                }
+                bar_arrive_warp(&raw_empty[slot]);
+                if (x == 0) meta[st] = there;
+                fence_async();
+                bar_arrive_warp(&full[st]);
+            }
+        } else if (warp == kCopier) {
+            // ---- pages into shared memory: lane p page p of a step ----
+            const int32_t *tab = a.table + (size_t)b * a.width;
+            auto page_of = [&](int j) {   // -1 where there is none
+                const int t = (step0 + j) * kT + lane * P;
+                const int pg = lane < NP && j < steps && t < seen ? __ldg(tab + t / P) : -1;
+                return pg >= 0 && pg < a.c.n_pages ? pg : -1;
+            };
+            int pg = page_of(0), issued = 0;
+            for (; issued < steps; issued++) {
+                const int slot = issued % kRaw;
+                if (issued >= kRaw && !bar_wait_warp(&raw_empty[slot], (uint32_t)(issued / kRaw - 1) & 1, status, 110)) break;
+                const unsigned there = __ballot_sync(0xffffffffu, pg >= 0);
+                if (lane == 0)
+                    asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(smem_u32(&raw[slot])),
+                                 "r"((uint32_t)(__popc(there) * PB)) : "memory");
+                __syncwarp();
+                if (pg >= 0)
+                    bulk_copy(smem_u32(smem + L::kCodes + slot * L::kStep) + lane * PB, a.c.c + ((size_t)pg * a.c.KVH + kvh) * PB, PB, smem_u32(&raw[slot]));
+                pg = page_of(issued + 1);
+                if (lane == 0) rmeta[slot] = there;
+                bar_arrive_warp(&raw[slot]);   // the slot's second arrival
+            }
+            // copies still in flight land before the shared memory goes
+            for (int j = max(0, issued - kRaw); j < issued; j++) bar_wait_warp(&raw[j % kRaw], (uint32_t)(j / kRaw) & 1, status, 109, true);
+        } else {
+            // ---- a half's products: the warp together, so that descriptors stay in uniform registers; one lane issues ----
+            const int h = warp - kIssuer;
+            const uint64_t Q = tile_desc(smem_u32(smem + L::kQ + h * L::kQ1)), Pt = tile_desc(smem_u32(smem + L::kP + h * L::kP1));
+            const uint64_t K0 = tile_desc(smem_u32(smem + L::kK)), V0 = turned_desc(smem_u32(smem + L::kV));
+            const uint32_t S = tmem + 256 * h, O = S + 2 * kT;
+            constexpr uint64_t kTile16 = kT * D * 2 / 16;   // descriptors count 16 bytes
+            auto scores = [&](int j, int st, uint32_t parity) {   // into score buffer j & 1
+                if (!bar_wait_warp(&full[st], parity, status, 105)) return false;
+                fence_after();
+                const uint64_t K = K0 + st * kTile16;
+                const uint32_t to = S + (j & 1) * kT;
+                if (elect_one()) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; c++) {
+                        const uint64_t q = Q + (c / 4) * (kM * 8) + (c % 4) * 2, k = K + (c / 4) * (kT * 8) + (c % 4) * 2;
+                        if (c == 0) mma<false>(to, q, k, inst_desc(kT, true));
+                        else mma<true>(to, q, k, inst_desc(kT, true));
+                    }
+                    commit(&s_full[h][j & 1]);
+                }
+                __syncwarp();
+                return true;
+            };
+            int st = 0, st1 = 0;          // stages of steps j and j + 1
+            uint32_t par1 = 0;
+            bool ok = h < halves && bar_wait_warp(&q_full[h], 0, status, 104);
+            if (ok) ok = scores(0, 0, 0);
+            for (int j = 0; j < steps && ok; j++, st = st1) {
+                if (++st1 == kStages) st1 = 0, par1 ^= 1;
+                // the next scores go ahead of this step's values: their buffer was read before step j - 1's weights were
+                if (j + 1 < steps) ok = scores(j + 1, st1, par1);
+                if (ok) ok = bar_wait_warp(&p_full[h], (uint32_t)j & 1, status, 106);
+                if (!ok) break;
+                fence_after();
+                const uint64_t V = V0 + st * kTile16;
+                if (elect_one()) {
+                    // 16 tokens are two groups of eight rows of the tile, 1024 bytes each
+                    if (j == 0) mma<false>(O, Pt, V, inst_desc(D, true, true));
+                    else mma<true>(O, Pt, V, inst_desc(D, true, true));
+#pragma unroll
+                    for (int c = 1; c < kT / 16; c++) mma<true>(O, Pt + c * 2, V + c * 128, inst_desc(D, true, true));
+                    commit(&empty[st]);
+                    if (halves == 1) commit(&empty[st]);   // the other half's
+                    commit(&o_done[h]);   // (last: the one that is waited for before the CTA ends)
+                }
+                __syncwarp();
+            }
+            if (!ok && h < halves) {   // the products already issued finish before tensor memory is released
+                if (elect_one()) commit(&drain[h]);
+                bar_wait_warp(&drain[h], 0, status, 107, true);
+            }
+        }
+        __syncthreads();
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kIssuer) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D, int P>
+cudaError_t prompt_launch(const PromptArgs &f, dim3 grid, cudaStream_t st) {
+    static PerDevice<bool> opted;
+    const cudaError_t e = smem_optin_once(moe_kv4_prompt_kernel<D, P>, opted);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(moe_kv4_prompt_kernel<D, P>, grid, dim3(kThreads), (size_t)Smem<D>::kBytes + 1024, st, f);
+}
+template <int D>
+cudaError_t prompt_page(const PromptArgs &f, dim3 grid, cudaStream_t st) {
+    return f.a.c.P == 16 ? prompt_launch<D, 16>(f, grid, st) : f.a.c.P == 32 ? prompt_launch<D, 32>(f, grid, st) : prompt_launch<D, 64>(f, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_prompt(const Kv4Attend &a, int32_t *status, cudaStream_t st) {
+    PromptArgs f{a, a.QH / a.c.KVH, status};
+    // row tiles: a sequence's last may be partly filled
+    const long long tiles = (long long)a.n_rows * f.G / (2 * kM) + a.n_seqs;
+    const long long most = (long long)a.n_seqs * (((long long)a.max_new * f.G + 2 * kM - 1) / (2 * kM));
+    const dim3 grid((unsigned)(std::min(tiles, most) * a.c.KVH));
+    return a.c.D == 64 ? prompt_page<64>(f, grid, st) : prompt_page<128>(f, grid, st);
+}

@@ -29,20 +29,11 @@
 // A NaN value that only some of a tile's rows see would reach the others as
 // 0 * NaN: where the pages hold one in a step that not all rows see, the CTA's
 // rows are computed once more, one at a time.
-#include "moe_kv8.cuh"
+#include "moe_kv_prompt.cuh"
 
 #include <algorithm>
 
 namespace {
-
-constexpr int kM = 128;         // rows of a half
-constexpr int kT = 64;          // tokens of a step
-constexpr int kSoftmax = 8;     // warps
-constexpr int kLoaders = 128;   // threads that turn pages into operands
-constexpr int kCopier = kSoftmax + kLoaders / 32, kIssuer = kCopier + 1;   // warps
-constexpr int kThreads = (kIssuer + 2) * 32;
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Smem {   // offsets from a 1024-byte boundary
@@ -55,142 +46,6 @@ struct Smem {   // offsets from a 1024-byte boundary
     static constexpr int kCodes = kV + kStages * kT * D * 2; // kRaw x keys, values as they lie in the pages
     static constexpr int kBytes = kCodes + kRaw * kT * D * 2;
 };
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
-    return ok != 0;
-}
-// Bounded wait: false (and the status word set) after about 2 s, or when a
-// failure was reported elsewhere first; drain: only the time limit ends it.
-__device__ __noinline__ bool bar_wait_long(uint64_t *b, uint32_t parity, int32_t *status, int where, bool drain) {
-    const uint64_t t0 = now_ns();
-    for (uint32_t i = 1;; i++) {
-        if (bar_try(b, parity)) return true;
-        if ((i & 63) == 0) {
-            if (!drain && *(volatile int32_t *)status != 0) return false;
-            if (now_ns() - t0 > kWaitNs) {
-                set_device_error(status, MOE_DEV_WAIT_TIMEOUT, where);
-                return false;
-            }
-        }
-    }
-}
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *status, int where, bool drain = false) {
-#pragma unroll 1
-    for (int i = 0; i < 16; i++)
-        if (bar_try(b, parity)) return true;
-    return bar_wait_long(b, parity, status, where, drain);
-}
-__device__ __forceinline__ bool bar_wait_warp(uint64_t *b, uint32_t parity, int32_t *status, int where, bool drain = false) {
-    return __all_sync(0xffffffffu, bar_wait(b, parity, status, where, drain));
-}
-__device__ __forceinline__ void bar_init(uint64_t *b, uint32_t n) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n));
-}
-__device__ __forceinline__ void bar_arrive(uint64_t *b) {
-    asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_u32(b)) : "memory");
-}
-// One arrival a warp: 32 of one warp on a barrier are taken one after another
-// (several hundred cycles).
-__device__ __forceinline__ void bar_arrive_warp(uint64_t *b) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) bar_arrive(b);
-}
-__device__ __forceinline__ void commit(uint64_t *b) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-// Operand tile: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t at) {
-    return (uint64_t)((at >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-__device__ __forceinline__ uint32_t swizzled(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
-// fp16 operands, fp32 accumulator, M = 128.
-constexpr uint32_t inst_desc(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kM >> 4) << 24); }
-template <bool ACC>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
-}
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-    return p != 0;
-}
-// 32 consecutive columns of the thread's TMEM lane; tmem_wait before their use.
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
-          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
-          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
-          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(at));
-}
-// The wait takes the registers in and out, so that no use of them moves above it.
-__device__ __forceinline__ void tmem_wait(float *v) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-        : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
-          "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
-          "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
-          "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
-}
-// Packed fp32: (x0, x1) * k + c, and sums.
-__device__ __forceinline__ void fma2(float &y0, float &y1, float x0, float x1, float k, float c) {
-    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 d, {%5, %5}; fma.rn.f32x2 a, a, b, d; mov.b64 {%0, %1}, a; }"
-        : "=f"(y0), "=f"(y1) : "f"(x0), "f"(x1), "f"(k), "f"(c));
-}
-__device__ __forceinline__ void add2(float &s0, float &s1, float x0, float x1) {
-    asm("{ .reg .b64 a, b; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
-        : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-// 16 columns, to be scaled.
-__device__ __forceinline__ void tmem_scale16(uint32_t at, float k) {
-    float v[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16]; tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
-          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-        : "r"(at) : "memory");
-#pragma unroll
-    for (int e = 0; e < 16; e++) v[e] *= k;
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16}; tcgen05.wait::st.sync.aligned;" ::"r"(at),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
-        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-        : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); }
 
 struct PromptArgs {
     Kv8Attend a;
