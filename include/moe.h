@@ -644,7 +644,7 @@ int moe_rotary_set_freqs(moe_rotary *plan, const double *freqs, const uint8_t *a
  * that side is not normed. */
 int moe_rotary_set_norm(moe_rotary *plan, const float *q_gamma, const float *k_gamma);
 /* n_tokens rows of q_heads queries and of kv_heads keys (bf16, strides in
- * elements from row to row, multiples of 4; 8-byte aligned; a side of 0 heads
+ * elements from row to row, multiples of 8; 16-byte aligned; a side of 0 heads
  * may be NULL) into q_out and k_out, which may be their inputs (the same
  * pointer and stride) and overlap nothing else (they may be places of the same
  * rows, at one stride).  positions int32 [n_axes] rows of pos_stride (device).

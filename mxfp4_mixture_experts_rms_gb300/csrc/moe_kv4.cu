@@ -5,9 +5,11 @@
 //
 // A block does not depend on other tokens, so tokens may come in any order and
 // nothing that the cache holds is rounded twice (the 8-bit cache's pages share a
-// scale).  Four lanes hold a block, eight dims each, and a warp the blocks of
-// eight tokens at one place: it reads 64 bytes of each token, and where the
-// slots follow one another writes 128 in a row.  Bound by HBM.
+// scale).  Four lanes hold a block, eight dims each, and a warp 128 dims of one
+// side of eight tokens: it reads 64 bytes of each token at a time, and where the
+// slots follow one another writes 128 in a row.  Bound by HBM, as long as no
+// place is found by division (the append of 22 559 tokens, 8 heads of 128, took
+// 47 us with them).
 #include "moe_kv4.cuh"
 #include "../../include/moe.h"
 
@@ -20,7 +22,7 @@
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBlocks = 4;     // blocks of a warp's tokens, loaded before any is encoded
+constexpr int kBlocks = 4;     // of a warp's tokens: 128 dims
 
 struct RowArgs {
     Kv4Cache c;
@@ -28,81 +30,91 @@ struct RowArgs {
     uint16_t *ko, *vo;         // read: the same
     long long ks, vs;          // elements from row to row
     const int32_t *slots;
-    int n;
+    int n, shift;              // P = 1 << shift
 };
 
-// Where the block `x` (side, kv head, 32 dims) of the token at `slot` lies:
-// codes and scale, from the cache's start.
-__device__ __forceinline__ void block_at(const Kv4Cache &c, int slot, int x, size_t &codes, size_t &scale) {
-    const int nb = c.D / 32, side = x / (c.KVH * nb), h = x / nb % c.KVH, b = x % nb;
-    const int page = slot / c.P, tok = slot % c.P;
-    const size_t at = ((size_t)page * c.KVH + h) * kv4_page_bytes(c.P, c.D);
-    codes = at + (size_t)side * (c.P * c.D / 2) + (b * c.P + tok) * 16;
-    scale = at + c.P * c.D + side * (c.P * nb) + b * c.P + (tok & ~15) + kv4_scale_byte(tok & 15);
-}
+// A lane's token and its slot (-1: none), the side and first kv head of its
+// warp's 128 dims, and where they lie.
+template <int D>
+struct Place {
+    static constexpr int NB = D / 32;
+    int tok, slot, quarter, h;
+    bool values, on;           // on: is the warp's part one of the heads'?
+    size_t codes, scale;       // of block 0; block b of head h + x: + x * page bytes + b * P * 16 (codes), + b * P (scales)
+    int page_bytes, P;
+    __device__ __forceinline__ Place(const RowArgs &a) {
+        const int lane = threadIdx.x & 31, part = blockIdx.y * kWarps + (threadIdx.x >> 5), parts = (a.c.KVH * D + 127) / 128;   // of a side
+        quarter = lane & 3;
+        values = part >= parts, on = part < 2 * parts;
+        h = (part - (values ? parts : 0)) * (128 / D);
+        tok = blockIdx.x * 8 + (lane >> 2);
+        P = 1 << a.shift, page_bytes = kv4_page_bytes(P, D);
+        const int s = tok < a.n ? __ldg(a.slots + tok) : -1;
+        slot = s >= 0 && s < a.c.n_pages << a.shift ? s : -1;
+        const int page = max(slot, 0) >> a.shift, place = max(slot, 0) & (P - 1);
+        const size_t at = ((size_t)page * a.c.KVH + h) * page_bytes;
+        codes = at + (values ? P * D / 2 : 0) + place * 16 + 4 * quarter;
+        scale = at + P * D + (values ? P * NB : 0) + (place & ~15) + kv4_scale_byte(place & 15);
+    }
+    __device__ __forceinline__ bool has(const RowArgs &a, int i) const { return on && slot >= 0 && h + i / NB < a.c.KVH; }   // block i of the 128 dims
+    __device__ __forceinline__ size_t code_at(int i) const { return codes + (size_t)(i / NB) * page_bytes + (i % NB) * P * 16; }
+    __device__ __forceinline__ size_t scale_at(int i) const { return scale + (size_t)(i / NB) * page_bytes + (i % NB) * P; }
+};
 
+template <int D>
 __global__ void __launch_bounds__(kWarps * 32) moe_kv4_append_kernel(const RowArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tok = blockIdx.x * 8 + (lane >> 2), quarter = lane & 3;
-    const int blocks = 2 * a.c.KVH * (a.c.D / 32), x0 = (blockIdx.y * kWarps + warp) * kBlocks, side = blocks / 2;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int slot = tok < a.n ? a.slots[tok] : -1;
-    if (slot < 0 || slot >= a.c.n_pages * a.c.P) slot = -1;
+    const Place<D> p(a);
+    const uint4 *row = reinterpret_cast<const uint4 *>((p.values ? a.v + p.tok * a.vs : a.k + p.tok * a.ks) + p.h * D) + p.quarter;
     uint4 w[kBlocks];
 #pragma unroll
-    for (int i = 0; i < kBlocks; i++) {
-        const int x = x0 + i;
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (slot >= 0 && x < blocks) {
-            const uint16_t *row = x < side ? a.k + tok * a.ks + x * 32 : a.v + tok * a.vs + (x - side) * 32;
-            w[i] = __ldg(reinterpret_cast<const uint4 *>(row) + quarter);
-        }
-    }
+    for (int i = 0; i < kBlocks; i++) w[i] = p.has(a, i) ? __ldg(row + 4 * i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kBlocks; i++) {
         const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        float f[8], am = 0.f;
+        float f[8];
 #pragma unroll
         for (int q = 0; q < 4; q++) f[2 * q] = __uint_as_float(u[q] << 16), f[2 * q + 1] = __uint_as_float(u[q] & 0xFFFF0000u);
+        // the largest magnitude by its bits, two at a time; a NaN shows as more than infinity
+        uint32_t m = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = max(m & 0xFFFFu, m >> 16);
+        float am = __uint_as_float(m << 16);
+        if (__any_sync(0xffffffffu, m > 0x7F80u)) {
+            am = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; e++) am = fmaxf(am, fabsf(f[e]));   // NaN passes over
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+            for (int e = 0; e < 8; e++) am = fmaxf(am, fabsf(f[e]));   // NaN passes over
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        }
         const int k = min(mxq_exponent(am), kKv4MaxByte - 127);
         const float inv = mxq_inv_scale(k);
 #pragma unroll
         for (int e = 0; e < 8; e++) f[e] = fminf(fmaf(f[e], inv, 0.0f), 6.0f);   // as the activation encoder: -0 is 0, NaN 6
         const uint32_t codes = e2m1x4(f[0], f[1], f[2], f[3]) | (e2m1x4(f[4], f[5], f[6], f[7]) << 16);
-        if (slot >= 0 && x0 + i < blocks) {
-            size_t to, scale;
-            block_at(a.c, slot, x0 + i, to, scale);
-            *reinterpret_cast<uint32_t *>(a.c.c + to + 4 * quarter) = codes;
-            if (quarter == 0) a.c.c[scale] = (uint8_t)(k + 127);
+        if (p.has(a, i)) {
+            *reinterpret_cast<uint32_t *>(a.c.c + p.code_at(i)) = codes;
+            if (p.quarter == 0) a.c.c[p.scale_at(i)] = (uint8_t)(k + 127);
         }
     }
 }
 
+template <int D>
 __global__ void __launch_bounds__(kWarps * 32) moe_kv4_read_kernel(const RowArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tok = blockIdx.x * 8 + (lane >> 2), quarter = lane & 3;
-    const int blocks = 2 * a.c.KVH * (a.c.D / 32), x0 = (blockIdx.y * kWarps + warp) * kBlocks, side = blocks / 2;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int slot = tok < a.n ? a.slots[tok] : -1;
-    if (slot < 0 || slot >= a.c.n_pages * a.c.P) return;
+    const Place<D> p(a);
     uint32_t w[kBlocks], s[kBlocks];
 #pragma unroll
     for (int i = 0; i < kBlocks; i++) {
         w[i] = s[i] = 0;
-        if (x0 + i < blocks) {
-            size_t at, scale;
-            block_at(a.c, slot, x0 + i, at, scale);
-            w[i] = *reinterpret_cast<const uint32_t *>(a.c.c + at + 4 * quarter), s[i] = a.c.c[scale];
-        }
+        if (p.has(a, i)) w[i] = *reinterpret_cast<const uint32_t *>(a.c.c + p.code_at(i)), s[i] = a.c.c[p.scale_at(i)];
     }
+    uint4 *row = reinterpret_cast<uint4 *>((p.values ? a.vo + p.tok * a.vs : a.ko + p.tok * a.ks) + p.h * D) + p.quarter;
 #pragma unroll
     for (int i = 0; i < kBlocks; i++) {
-        const int x = x0 + i;
-        if (x >= blocks) break;
         uint32_t h[4], o[4];
         e2m1x8_to_f16(w[i], h);
         const float f = kv4_scale(s[i]);
@@ -112,14 +124,16 @@ __global__ void __launch_bounds__(kWarps * 32) moe_kv4_read_kernel(const RowArgs
             const __nv_bfloat162 r = __floats2bfloat162_rn(y.x * f, y.y * f);   // exact
             o[q] = *reinterpret_cast<const uint32_t *>(&r);
         }
-        uint16_t *row = x < side ? a.ko + tok * a.ks + x * 32 : a.vo + tok * a.vs + (x - side) * 32;
-        reinterpret_cast<uint4 *>(row)[quarter] = make_uint4(o[0], o[1], o[2], o[3]);
+        if (p.has(a, i)) row[4 * i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
-dim3 row_grid(const RowArgs &a) {
-    const int blocks = 2 * a.c.KVH * (a.c.D / 32);
-    return dim3((a.n + 7) / 8, (blocks + kWarps * kBlocks - 1) / (kWarps * kBlocks));
+cudaError_t launch_rows(bool append, RowArgs a, cudaStream_t st) {
+    a.shift = a.c.P == 16 ? 4 : a.c.P == 32 ? 5 : 6;
+    const int parts = 2 * ((a.c.KVH * a.c.D + 127) / 128);
+    const dim3 grid((a.n + 7) / 8, (parts + kWarps - 1) / kWarps), block(kWarps * 32);
+    if (append) return a.c.D == 64 ? launch_pdl(moe_kv4_append_kernel<64>, grid, block, 0, st, a) : launch_pdl(moe_kv4_append_kernel<128>, grid, block, 0, st, a);
+    return a.c.D == 64 ? launch_pdl(moe_kv4_read_kernel<64>, grid, block, 0, st, a) : launch_pdl(moe_kv4_read_kernel<128>, grid, block, 0, st, a);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -246,7 +260,7 @@ int moe_kv4_append(moe_kv4 *p, const uint16_t *k, const uint16_t *v, long long k
     if (rc) return rc;
     RowArgs a{};
     a.c = p->c, a.k = k, a.v = v, a.ks = k_stride, a.vs = v_stride, a.slots = slots, a.n = n_tokens;
-    const cudaError_t e = launch_pdl(moe_kv4_append_kernel, row_grid(a), dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = launch_rows(true, a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : moe_fail_status(MOE_ECUDA, "moe_kv4_append: %s", cudaGetErrorString(e));
 }
 
@@ -265,7 +279,7 @@ int moe_kv4_read(moe_kv4 *p, const int32_t *slots, int n_tokens, uint16_t *k, ui
     if (k < ve && v < ke && (apart < row || apart > k_stride - row)) return moe_fail_status(MOE_EINVAL, "k and v must not overlap");
     RowArgs a{};
     a.c = p->c, a.ko = k, a.vo = v, a.ks = k_stride, a.vs = v_stride, a.slots = slots, a.n = n_tokens;
-    const cudaError_t e = launch_pdl(moe_kv4_read_kernel, row_grid(a), dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = launch_rows(false, a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : moe_fail_status(MOE_ECUDA, "moe_kv4_read: %s", cudaGetErrorString(e));
 }
 

@@ -10,10 +10,14 @@
 // of position * F are the turn's fraction, exact to 2^-33 of a turn wherever the
 // position is (an fp32 product is off by whole radians at 2^24).
 //
-// Bound by HBM: 4 bytes an element.  A CTA takes the tokens' angles first, once
-// for all heads, then a group of D / 8 lanes a head: a lane holds four dims of
-// each half, so that no pair crosses lanes and the norm's sum is the only
-// exchange.
+// Bound by HBM: 4 bytes an element.  A CTA takes its tokens' angles first, once
+// for all heads, then a group of D / 16 lanes has two heads of each token: a lane
+// holds eight dims of each half, so that no pair crosses lanes and the norm's sum
+// is the only exchange.  As many groups as the heads need; a head's places move on
+// by a stride from token to token, and the next token is loaded before this one
+// is computed.  fp32 by twos.  (A warp's instructions are the next bound: with
+// eight dims a lane and heads' places found anew for each, 15 001 tokens of 32
+// heads of 128 took 71 us.)
 #include "moe_common.cuh"
 #include "../../include/moe.h"
 
@@ -24,9 +28,10 @@
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kMaxThreads = 256;
+constexpr int kHeads = 2;       // of a group
 constexpr int kMaxAxes = 4;
-constexpr int kTokens = 2;      // of a CTA, at most
+constexpr int kTokens = 4;      // of a CTA, at most
 
 struct RotaryArgs {
     const uint16_t *q, *k;      // rows of heads
@@ -41,130 +46,181 @@ struct RotaryArgs {
     float eps, factor;
 };
 
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
+typedef unsigned long long u64;   // (also: two fp32)
+__device__ __forceinline__ u64 two(float x, float y) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
 }
-__device__ __forceinline__ void unpack(uint2 w, float *x) { x[0] = lo16(w.x), x[1] = hi16(w.x), x[2] = lo16(w.y), x[3] = hi16(w.y); }
+__device__ __forceinline__ float2 of_two(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 x, u64 y) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 x, u64 y, u64 z) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ u64 unpack(uint32_t w) { return two(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ uint32_t pack(u64 v) {
+    const float2 f = of_two(v);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ void lds2(const float *p, u64 (&v)[4]) {   // eight floats
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p), b = *reinterpret_cast<const ulonglong2 *>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) moe_rotary_kernel(const RotaryArgs a) {
-    constexpr int L = D / 8, G = kThreads / L, U = 4;   // lanes of a head; heads at once; heads a group loads ahead
-    __shared__ float2 table[kTokens * D / 2];            // factor * (cos, sin)
+__global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const RotaryArgs a) {
+    constexpr int L = D / 16, U = kHeads;                 // lanes of a head
+    __shared__ u64 turns[D / 2];                          // of a position, in units of 2^-64
+    __shared__ __align__(16) float cosines[kTokens][D / 2], sines[kTokens][D / 2];   // times the factor
+    __shared__ __align__(16) float gammas[2][D];
     __shared__ int skip[kTokens];
-    const int tid = threadIdx.x, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
+    const int tid = threadIdx.x, threads = blockDim.x, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid < kTokens) {
-        int s = 0;
-        if (tid < nt)
-            for (int x = 0; x < a.axes; x++) s |= a.pos[x * a.pos_stride + t0 + tid] < 0;
-        skip[tid] = s;
+    for (int i = tid; i < a.pairs; i += threads) {        // (the plan's own, no earlier kernel's)
+        double t = a.freqs[i] * 0.15915494309189533577;
+        t -= floor(t);
+        turns[i] = __double2ull_rn(t * 18446744073709551616.0);
     }
-    for (int i = tid; i < nt * a.pairs; i += kThreads) {
-        const int t = i / a.pairs, p = i - t * a.pairs;
-        const int axis = a.of ? min((int)a.of[p], a.axes - 1) : 0;
-        double turns = a.freqs[p] * 0.15915494309189533577;
-        turns -= floor(turns);
-        const unsigned long long f = __double2ull_rn(turns * 18446744073709551616.0);
-        const unsigned long long at = (unsigned long long)(long long)a.pos[axis * a.pos_stride + t0 + t] * f;
-        float s, c;
-        sincospif((float)(int)(at >> 32) * 0x1p-31f, &s, &c);
-        table[i] = make_float2(c * a.factor, s * a.factor);
+    const bool norms = a.qg || a.kg;
+    if (norms)
+        for (int i = tid; i < 2 * D; i += threads) {
+            const float *gamma = i < D ? a.qg : a.kg;
+            gammas[i / D][i % D] = gamma ? gamma[i % D] : 1.f;
+        }
+    // the lane's dims: d0 .. d0 + 7 and d1 .. d1 + 7; its pairs 8 l .. 8 l + 7 (from a.pairs on: not rotated)
+    const int l = tid % L, g = tid / L, groups = threads / L;
+    const bool turned = l < a.pairs / 8;
+    int d0 = 16 * l, d1 = d0 + 8;   // (halves: what lies behind the pairs' dims, too)
+    if (!INTER && turned) d0 = 8 * l, d1 = a.pairs + 8 * l;
+    // the group's heads, queries before keys, and where its lane's dims of the running token are
+    const uint16_t *in[U];
+    uint16_t *out[U];
+    long long in_step[U], out_step[U];
+    int side[U];
+    bool on[U], norm[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int h = (blockIdx.y * U + u) * groups + g, x = h >= a.QH;
+        side[u] = x, on[u] = h < a.QH + a.KVH, norm[u] = (x ? a.kg : a.qg) != nullptr;
+        in_step[u] = x ? a.ks : a.qs, out_step[u] = x ? a.kos : a.qos;
+        in[u] = (x ? a.k - a.QH * D : a.q) + t0 * in_step[u] + h * D, out[u] = (x ? a.ko - a.QH * D : a.qo) + t0 * out_step[u] + h * D;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint4 next[U][2];
+    auto load = [&](bool more) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            next[u][0] = next[u][1] = make_uint4(0, 0, 0, 0);
+            if (more && on[u]) next[u][0] = *reinterpret_cast<const uint4 *>(in[u] + d0), next[u][1] = *reinterpret_cast<const uint4 *>(in[u] + d1);
+            in[u] += in_step[u];
+        }
+    };
+    load(true);
+    for (int t = tid; t < nt; t += threads) {
+        int s = 0;
+        for (int x = 0; x < a.axes; x++) s |= a.pos[x * a.pos_stride + t0 + t];
+        skip[t] = s < 0;
     }
     __syncthreads();
-
-    // the lane's dims: d0 .. d0 + 3 and d1 .. d1 + 3; its pairs p0 .. p0 + 3 (past a.pairs: not rotated)
-    const int l = tid % L, g = tid / L;
-    const int quads = a.pairs / 4;
-    int d0, d1;
-    const bool turned = l < quads;
-    if (INTER || !turned) {
-        d0 = 8 * l, d1 = d0 + 4;
-        // (halves: what lies behind the pairs' dims, two quads a lane, is at 8 l as well)
-    } else {
-        d0 = 4 * l, d1 = a.pairs + 4 * l;
-    }
-    const int heads = a.QH + a.KVH, items = nt * heads;
-    const bool norm = a.qg || a.kg;
-    for (int base = blockIdx.y * G; base < items; base += U * G * gridDim.y) {   // the same for the whole CTA
-        const int i0 = base + g;
-        uint2 w[U][2];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int i = i0 + u * G * gridDim.y;
-            if (i < items) {
-                const int t = i / heads, h = i - t * heads;
-                const uint16_t *row = h < a.QH ? a.q + (long long)(t0 + t) * a.qs + h * D : a.k + (long long)(t0 + t) * a.ks + (h - a.QH) * D;
-                w[u][0] = *reinterpret_cast<const uint2 *>(row + d0), w[u][1] = *reinterpret_cast<const uint2 *>(row + d1);
-            } else {
-                w[u][0] = w[u][1] = make_uint2(0, 0);
-            }
+    for (int t = 0; t < nt; t++)
+        for (int i = tid; i < a.pairs; i += threads) {
+            const int axis = a.of ? min((int)__ldg(a.of + i), a.axes - 1) : 0;
+            const u64 at = (u64)(long long)a.pos[axis * a.pos_stride + t0 + t] * turns[i];
+            float s, c;
+            sincospif((float)(int)(at >> 32) * 0x1p-31f, &s, &c);
+            cosines[t][i] = c * a.factor, sines[t][i] = s * a.factor;
         }
+    __syncthreads();
+#pragma unroll 1
+    for (int t = 0; t < nt; t++) {
+        uint4 w[U][2];
+#pragma unroll
+        for (int u = 0; u < U; u++) w[u][0] = next[u][0], w[u][1] = next[u][1];
+        load(t + 1 < nt);
+        const bool live = !skip[t];
+        u64 cs[4], sn[4];
+        if (turned) lds2(&cosines[t][8 * l], cs), lds2(&sines[t][8 * l], sn);
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int i = i0 + u * G * gridDim.y;
-            const bool on = i < items;
-            const int ii = on ? i : 0, t = ii / heads, h = ii - t * heads;
-            const bool is_q = h < a.QH;
-            float x[8];
-            unpack(w[u][0], x), unpack(w[u][1], x + 4);
-            const float *gamma = is_q ? a.qg : a.kg;
-            float ss = 0.f;
-            if (norm) {
+            u64 x[4] = {unpack(w[u][0].x), unpack(w[u][0].y), unpack(w[u][0].z), unpack(w[u][0].w)};
+            u64 y[4] = {unpack(w[u][1].x), unpack(w[u][1].y), unpack(w[u][1].z), unpack(w[u][1].w)};
+            if (norms) {
+                auto squares = [&](unsigned lanes) {
+                    u64 sq = mul2(x[0], x[0]), sr = mul2(y[0], y[0]);
 #pragma unroll
-                for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
+                    for (int e = 1; e < 4; e++) sq = fma2(x[e], x[e], sq), sr = fma2(y[e], y[e], sr);
+                    const float2 f = of_two(sq), h = of_two(sr);
+                    float ss = (f.x + f.y) + (h.x + h.y);
 #pragma unroll
-                for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            }
-            if (gamma) {
-                const float mean = ss * (1.f / D) + a.eps;
-                const float4 g0 = __ldg(reinterpret_cast<const float4 *>(gamma + d0)), g1 = __ldg(reinterpret_cast<const float4 *>(gamma + d1));
-                if (mean > 1e-30f && mean < 1e37f) {
+                    for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
+                    return ss * (1.f / D);
+                };
+                float mean = squares(0xffffffffu) + a.eps;
+                if (norm[u]) {
+                    if (!(mean > 1e-30f && mean < 1e37f)) {
+                        // squares that fp32 does not hold, or the norm of next to nothing: 2^100 times or 2^-100 of the head
+                        // (its lanes have one mean, so they come here together)
+                        const float k = mean < 1.f ? 0x1p100f : 0x1p-100f;
+                        const u64 k2 = two(k, k);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) x[e] = mul2(x[e], k2), y[e] = mul2(y[e], k2);
+                        mean = squares(((1u << L) - 1) << (tid & 31 & ~(L - 1))) + a.eps * k * k;
+                    }
                     const float inv = rsqrtf(mean);
+                    const u64 inv2 = two(inv, inv);
+                    u64 ga[4], gb[4];
+                    lds2(&gammas[side[u]][d0], ga), lds2(&gammas[side[u]][d1], gb);
 #pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] *= inv;
-                } else {
-                    // squares beyond fp32: the head again, in 64 bits (its lanes have one mean, so they come here together)
-                    const unsigned mask = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << (tid & 31 & ~(L - 1));
-                    double sd = 0.;
-#pragma unroll 1
-                    for (int e = 0; e < 8; e++) sd += (double)x[e] * x[e];
-#pragma unroll 1
-                    for (int o = L / 2; o; o >>= 1) sd += __shfl_xor_sync(mask, sd, o);
-                    const double inv = 1. / sqrt(sd / D + (double)a.eps);
-#pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] = (float)(x[e] * inv);
+                    for (int e = 0; e < 4; e++) x[e] = mul2(mul2(x[e], inv2), ga[e]), y[e] = mul2(mul2(y[e], inv2), gb[e]);
                 }
-                x[0] *= g0.x, x[1] *= g0.y, x[2] *= g0.z, x[3] *= g0.w;
-                x[4] *= g1.x, x[5] *= g1.y, x[6] *= g1.z, x[7] *= g1.w;
             }
             if (turned) {
-                const float4 *cs = reinterpret_cast<const float4 *>(table + t * a.pairs + 4 * l);   // two pairs each
-                const float4 c0 = cs[0], c1 = cs[1];
-                const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
+                auto turn = [](u64 &a, u64 &b, u64 c, u64 s) {
+                    const u64 y = fma2(b, s ^ 0x8000000080000000ull, mul2(a, c));
+                    b = fma2(a, s, mul2(b, c));
+                    a = y;
+                };
+                if (INTER) {
+                    // pairs side by side: (a, b) apart, and back
+                    auto apart = [&](u64 &a, u64 &b, u64 c, u64 s) {
+                        const float2 f = of_two(a), h = of_two(b);
+                        u64 p = two(f.x, h.x), q = two(f.y, h.y);
+                        turn(p, q, c, s);
+                        const float2 v = of_two(p), z = of_two(q);
+                        a = two(v.x, z.x), b = two(v.y, z.y);
+                    };
+                    apart(x[0], x[1], cs[0], sn[0]), apart(x[2], x[3], cs[1], sn[1]);
+                    apart(y[0], y[1], cs[2], sn[2]), apart(y[2], y[3], cs[3], sn[3]);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    float &A = INTER ? x[2 * e] : x[e], &B = INTER ? x[2 * e + 1] : x[4 + e];
-                    const float y = A * c[e] - B * s[e], z = B * c[e] + A * s[e];
-                    A = y, B = z;
+                    for (int e = 0; e < 4; e++) turn(x[e], y[e], cs[e], sn[e]);
                 }
             }
-            if (on && !skip[t]) {
-                uint16_t *row = is_q ? a.qo + (long long)(t0 + t) * a.qos + h * D : a.ko + (long long)(t0 + t) * a.kos + (h - a.QH) * D;
-                *reinterpret_cast<uint2 *>(row + d0) = make_uint2(pack(x[0], x[1]), pack(x[2], x[3]));
-                *reinterpret_cast<uint2 *>(row + d1) = make_uint2(pack(x[4], x[5]), pack(x[6], x[7]));
+            if (live && on[u]) {
+                *reinterpret_cast<uint4 *>(out[u] + d0) = make_uint4(pack(x[0]), pack(x[1]), pack(x[2]), pack(x[3]));
+                *reinterpret_cast<uint4 *>(out[u] + d1) = make_uint4(pack(y[0]), pack(y[1]), pack(y[2]), pack(y[3]));
             }
+            out[u] += out_step[u];
         }
     }
 }
 
 template <int D>
-cudaError_t rotary_launch(const RotaryArgs &a, bool inter, dim3 grid, cudaStream_t st) {
-    return inter ? launch_pdl(moe_rotary_kernel<D, true>, grid, dim3(kThreads), 0, st, a)
-                 : launch_pdl(moe_rotary_kernel<D, false>, grid, dim3(kThreads), 0, st, a);
+cudaError_t rotary_launch(const RotaryArgs &a, bool inter, dim3 grid, int threads, cudaStream_t st) {
+    return inter ? launch_pdl(moe_rotary_kernel<D, true>, grid, dim3(threads), 0, st, a)
+                 : launch_pdl(moe_rotary_kernel<D, false>, grid, dim3(threads), 0, st, a);
 }
 
 }  // namespace
@@ -247,9 +303,9 @@ int moe_rotary_apply(moe_rotary *p, const uint16_t *q, long long q_stride, int q
     } sides[2] = {{q, q_stride, q_out, q_out_stride, (long long)q_heads * p->D}, {k, k_stride, k_out, k_out_stride, (long long)kv_heads * p->D}};
     for (const Side &s : sides) {
         if (!s.row) continue;
-        if (((uintptr_t)s.x | (uintptr_t)s.o) & 7u) return moe_fail_status(MOE_EINVAL, "rows must be 8-byte aligned");
-        if (s.xs < s.row || s.os < s.row || s.xs % 4 || s.os % 4)
-            return moe_fail_status(MOE_EINVAL, "row strides must be multiples of 4 and at least %lld elements", s.row);
+        if (((uintptr_t)s.x | (uintptr_t)s.o) & 15u) return moe_fail_status(MOE_EINVAL, "rows must be 16-byte aligned");
+        if (s.xs < s.row || s.os < s.row || s.xs % 8 || s.os % 8)
+            return moe_fail_status(MOE_EINVAL, "row strides must be multiples of 8 and at least %lld elements", s.row);
     }
     // An output lies apart from every input and from the other output, or in rows
     // of one stride at other places, or on its own input exactly.
@@ -275,14 +331,15 @@ int moe_rotary_apply(moe_rotary *p, const uint16_t *q, long long q_stride, int q
     a.QH = q_heads, a.KVH = kv_heads, a.n = n_tokens, a.pairs = p->pairs, a.axes = p->axes;
     a.pos = positions, a.pos_stride = pos_stride, a.freqs = p->freqs, a.of = p->of, a.qg = p->qg, a.kg = p->kg;
     a.eps = p->eps, a.factor = p->factor;
-    a.tokens = n_tokens >= 1024 ? kTokens : 1;
-    const int groups = kThreads / (p->D / 8), per = groups * 4;   // heads that a CTA loads at once
-    const long long items = (long long)a.tokens * (q_heads + kv_heads);
-    const int split = n_tokens >= 512 ? 1 : (int)((items + per - 1) / per);
-    const dim3 grid((unsigned)((n_tokens + a.tokens - 1) / a.tokens), (unsigned)(split < 1024 ? split : 1024));
+    // several tokens a CTA where there are enough for all SMs' CTAs; few tokens:
+    // heads over CTAs, a warp or two each
+    a.tokens = n_tokens >= 4096 ? kTokens : n_tokens >= 1024 ? 2 : 1;
+    const int lanes = p->D / 16, groups = (q_heads + kv_heads + kHeads - 1) / kHeads, most = (n_tokens >= 512 ? kMaxThreads : 64) / lanes;
+    const int parts = (groups + most - 1) / most, threads = (((groups + parts - 1) / parts) * lanes + 31) / 32 * 32;
+    const dim3 grid((unsigned)((n_tokens + a.tokens - 1) / a.tokens), (unsigned)parts);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = p->D == 64 ? rotary_launch<64>(a, p->inter, grid, st) : p->D == 128 ? rotary_launch<128>(a, p->inter, grid, st)
-                                                                                              : rotary_launch<256>(a, p->inter, grid, st);
+    const cudaError_t e = p->D == 64 ? rotary_launch<64>(a, p->inter, grid, threads, st) : p->D == 128 ? rotary_launch<128>(a, p->inter, grid, threads, st)
+                                                                                              : rotary_launch<256>(a, p->inter, grid, threads, st);
     return e == cudaSuccess ? MOE_OK : moe_fail_status(MOE_ECUDA, "moe_rotary_apply: %s", cudaGetErrorString(e));
 }
 
