@@ -88,22 +88,12 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
     __shared__ int skip[kTokens];
     const int tid = threadIdx.x, threads = blockDim.x, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
     asm volatile("griddepcontrol.launch_dependents;");
-    for (int i = tid; i < a.pairs; i += threads) {        // (the plan's own, no earlier kernel's)
-        double t = a.freqs[i] * 0.15915494309189533577;
-        t -= floor(t);
-        turns[i] = __double2ull_rn(t * 18446744073709551616.0);
-    }
-    const bool norms = a.qg || a.kg;
-    if (norms)
-        for (int i = tid; i < 2 * D; i += threads) {
-            const float *gamma = i < D ? a.qg : a.kg;
-            gammas[i / D][i % D] = gamma ? gamma[i % D] : 1.f;
-        }
     // the lane's dims: d0 .. d0 + 7 and d1 .. d1 + 7; its pairs 8 l .. 8 l + 7 (from a.pairs on: not rotated)
     const int l = tid % L, g = tid / L, groups = threads / L;
     const bool turned = l < a.pairs / 8;
     int d0 = 16 * l, d1 = d0 + 8;   // (halves: what lies behind the pairs' dims, too)
     if (!INTER && turned) d0 = 8 * l, d1 = a.pairs + 8 * l;
+    const bool norms = a.qg || a.kg;
     // the group's heads, queries before keys, and where its lane's dims of the running token are
     const uint16_t *in[U];
     uint16_t *out[U];
@@ -128,6 +118,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
         }
     };
     load(true);
+    for (int i = tid; i < a.pairs; i += threads) {
+        double t = a.freqs[i] * 0.15915494309189533577;
+        t -= floor(t);
+        turns[i] = __double2ull_rn(t * 18446744073709551616.0);
+    }
+    if (norms)
+        for (int i = tid; i < 2 * D; i += threads) {
+            const float *gamma = i < D ? a.qg : a.kg;
+            gammas[i / D][i % D] = gamma ? gamma[i % D] : 1.f;
+        }
     for (int t = tid; t < nt; t += threads) {
         int s = 0;
         for (int x = 0; x < a.axes; x++) s |= a.pos[x * a.pos_stride + t0 + t];

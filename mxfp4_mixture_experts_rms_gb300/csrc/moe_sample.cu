@@ -125,8 +125,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     const int rank = (int)cl.block_rank(), C = (int)cl.num_blocks();
     const int row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // waited for before the first write to another CTA
-    asm volatile("griddepcontrol.launch_dependents;");
+    if (!LIMITS) asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (LIMITS) asm volatile("griddepcontrol.launch_dependents;");   // the dependent reads what earlier kernels wrote before it waits
 
     R d;
     {
@@ -191,12 +192,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     for (int c = 0; c < C; c++) km = max(km, told[turn][c].key);
     if (km == 0 || of < 0) {   // nothing to choose
         if (rank == 0 && tid == 0) {
-            if (LIMITS) a.limits[row] = {0u, 0u, 0, 0, 0.};
+            if (LIMITS) a.limits[row] = {0u, 0u, 0, 0.f, 0.f, 0.f};
             else a.ids[row] = -1;
         }
         return;
     }
-    const Weight weight(key_logit(km), t);
+    const Weight<LIMITS> weight(key_logit(km), t);
     const float top = weight.top, scale = weight.scale, shift_w = weight.shift;
     const bool endless = weight.endless, steep = weight.steep;
     auto weights = [&](const float (&x)[VE], float (&w)[VE]) {
@@ -209,11 +210,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         for (int e = 0; e < VE; e += 2) {
             asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5}; fma.rn.f32x2 a, a, b, c; "
                 "mov.b64 {%0, %1}, a; }" : "=f"(w[e]), "=f"(w[e + 1]) : "f"(x[e]), "f"(x[e + 1]), "f"(scale), "f"(shift_w));
+            if (LIMITS)   // (x lo - top lo)
+                asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5}; mov.b64 d, {%0, %1}; fma.rn.f32x2 a, a, b, c; "
+                    "add.rn.f32x2 d, d, a; mov.b64 {%0, %1}, d; }" : "+f"(w[e]), "+f"(w[e + 1]) : "f"(x[e]), "f"(x[e + 1]), "f"(weight.lo), "f"(-top * weight.lo));
             asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(w[e]));
             asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(w[e + 1]));
         }
     };
     const float least = mp * weight(top);   // min-p is relative to the largest weight
+    auto tell_limits = [&](uint32_t T, int cut, double sum) {   // by one thread
+        const double inv = 1. / sum;
+        a.limits[row] = {km, T, cut, least, (float)inv, (float)(inv - (float)inv)};
+    };
     // 0 - the bin of weight 1 - downwards; NaN is never asked for
     auto bin_of = [](float w) { return max((0x3F800000 >> kBinShift) - (int)(__float_as_uint(w) >> kBinShift), 0); };
     auto fixed_sum = [](float sum) { return __float2ull_rn(sum * 0x1p40f); };
@@ -398,8 +406,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                     if (keep) atomicMin(&s_lo, me.x);
                     __syncthreads();
                     const uint32_t least_key = s_lo;
-                    const int at_it = __syncthreads_count(keep && me.x == least_key), cut = __syncthreads_or(tid < n && !keep && me.x == least_key);
-                    if (tid == 0) a.limits[row] = {km, least_key, at_it, cut, (double)all_kept * 0x1p-53};
+                    if (keep && me.x == least_key) atomicMax(&s_hi, me.y);   // the last of its tokens that is kept (all ahead of it are)
+                    __syncthreads();
+                    if (tid == 0) tell_limits(least_key, (int)s_hi + 1, (double)all_kept * 0x1p-53);
                     return;
                 }
                 const u64 target = __umul64hi(all_kept, fraction(u));
@@ -627,8 +636,44 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         kept += m, tsum += ct;
     }
     if (LIMITS) {
-        // (T is 0 where all tokens are kept: the least key is that of -inf, which weighs nothing)
-        if (rank == 0 && tid == 0) a.limits[row] = {km, T, (int)min(r, (u64)INT_MAX), T && tsum > r, (double)kept * 0x1p-40};
+        const double sum = (double)kept * 0x1p-40;
+        if (!T || tsum <= r) {
+            if (rank == 0 && tid == 0) tell_limits(T, a.V, sum);
+            return;
+        }
+        // where the r-th token at T is: one warp's part
+        const u64 t0 = tb + scan((u64)ties) - ties;
+        const unsigned hit = __ballot_sync(0xffffffffu, t0 < r && r <= t0 + ties);
+        if (!hit || warp != __ffs(hit) - 1) return;
+        int left = (int)(r - __shfl_sync(0xffffffffu, t0, warp));
+        for (int v = d.v0; v < d.v1; v += 32) {
+            float x[VE];
+            if (v + lane < d.v1) {
+                R::values(d.vec(v + lane), x);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; e++) x[e] = -INFINITY;
+            }
+            int n = 0;
+#pragma unroll
+            for (int e = 0; e < VE; e++) n += x[e] == xT;
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const int all = __shfl_sync(0xffffffffu, inc, 31);
+            if (left > all) {
+                left -= all;
+                continue;
+            }
+            int at = inc - n;   // before the lane's
+#pragma unroll
+            for (int e = 0; e < VE; e++)
+                if (x[e] == xT && ++at == left) tell_limits(T, (v + lane) * VE - d.off + e + 1, sum);
+            return;
+        }
         return;
     }
     u64 target = __umul64hi(kept, fraction(u));   // the first token whose running sum exceeds u times the total

@@ -23,12 +23,12 @@ struct SampleArgs {
 };
 
 // The tokens of a row that may be chosen: those whose logit's key is above T,
-// and the first r whose key is T; of these the ones that min-p keeps.
+// and those whose key is T below index `cut`; of these the ones that min-p keeps.
 struct SampleLimits {
     uint32_t top, T;   // keys of the largest logit (0: no token) and of the least that is kept
-    int r;
-    int cut;           // whether a token at T is left out
-    double total;      // their weights' sum, the largest logit's being 1
+    int cut;
+    float least;       // min-p's least weight, the largest logit's being 1
+    float inv, inv_lo; // 1 over their weights' sum, in two parts
 };
 
 namespace {
@@ -47,18 +47,23 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // The weight 2^((l - top) scale) of a logit.  An infinite largest logit: then
 // only infinite ones weigh anything.  A row of steep scale: differences first,
 // so that 0 stays 0.  Else the weights are 2^(x scale - top scale), the constant
-// rounded: one factor, within 2^-14 of 1, on all of them.
+// rounded: one factor, within 2^-14 of 1, on all of them.  FINE: with what
+// log2(e) / t has beyond fp32, so that no error grows with the distance from the
+// largest logit.
+template <bool FINE>
 struct Weight {
-    float top, scale, shift;
+    float top, scale, shift, lo;
     bool endless, steep;
-    __device__ __forceinline__ Weight(float top_, float t) : top(top_) {
+    __device__ __forceinline__ Weight(float top_, float t) : top(top_), lo(0.f) {
         scale = t > 0.f ? fminf(kLog2e / t, 1e30f) : 0.f;
         endless = top == INFINITY, steep = !(fabsf(top * scale) < 1000.f);
         shift = endless || steep ? 0.f : -top * scale;
+        if (FINE && t > 0.f && scale < 1e30f && scale > 1e-30f) lo = (fmaf(-scale, t, kLog2e) + 1.925963033500e-8f) / t;   // log2(e) less its fp32
     }
     __device__ __forceinline__ float operator()(float x) const {
-        float w;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(steep ? (x - top) * scale : fmaf(x, scale, shift)));
+        float w, e = steep ? (x - top) * scale : fmaf(x, scale, shift);
+        if (FINE && !endless && !steep) e += fmaf(x, lo, -top * lo);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(e));
         return endless ? (x == top ? 1.f : 0.f) : w;
     }
 };

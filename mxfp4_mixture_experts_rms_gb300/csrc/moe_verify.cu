@@ -10,8 +10,10 @@
 // the sums of each warp's part, and in the part that holds the chosen token.
 // q is read at kept tokens only.
 //
-// Sums are exact to about 2^-45 of the total: fp32 over the tokens that a lane
-// reads at once, those in two fp32 parts, a lane's and a warp's in 64 bits.
+// Sums are whole numbers of units of 2^-52, at least one where there is anything:
+// of a lane's tokens, summed in two fp32 parts.  (64-bit floats are the GPU's
+// slowest numbers: sums and quotients in them took two thirds of the second
+// kernel's 76 us at 64 sequences of 128 K logits.)
 #include "moe_sample.cuh"
 #include "../../include/moe.h"
 
@@ -37,110 +39,111 @@ struct VerifyArgs {
     int32_t *ids, *accepted;
 };
 
-struct Part {
-    double sum;
-    long long ties;
-};
-
-__device__ __forceinline__ double warp_sum(double v) {
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// x (0 .. 1 and a little more) in units of 2^-52, at least one of them if it is not 0.
+__device__ __forceinline__ u64 units(float x) {
+    const uint32_t b = __float_as_uint(x);
+    const int s = (int)(b >> 23) - 98;   // mantissa times 2^(exponent - 150)
+    const u64 m = (b & 0x7FFFFFu) | 0x800000u;
+    return x > 0.f ? max(s >= 0 ? m << min(s, 32) : m >> min(-s, 63), (u64)1) : 0;
+}
+// u (0 .. 1 - 2^-24; NaN: 0) in units of 2^-64.
+__device__ __forceinline__ u64 fraction(float u) {
+    const uint32_t b = __float_as_uint(fminf(fmaxf(u, 0.f), 0.99999994f));
+    const int s = (int)(b >> 23) - 86;
+    const u64 m = (b & 0x7FFFFFu) | 0x800000u;
+    return s >= 0 ? m << s : m >> min(-s, 63);
+}
 __device__ __forceinline__ float used_prob(float q) { return fminf(fmaxf(q, 0.f), 1.f); }   // NaN: 0
 
-// Rows of a cluster's CTAs in 16-byte vectors, each warp's side by side.
+// A cluster a sequence; of the row of the draw each CTA has a part, each of its
+// warps one of that.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) moe_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArgs a) {
     typedef Row<BF16, false, kThreads> R;
-    constexpr int VE = R::VE;
-    __shared__ Part parts[2][kMaxCluster];
-    __shared__ double sums[kWarps];
-    __shared__ int ties[kWarps], s_count;
+    constexpr int VE = R::VE, U = BF16 ? 2 : 4;   // logits of a vector; vectors that a lane loads at once
+    __shared__ u64 parts[2][kMaxCluster], sums[kWarps];
+    __shared__ int s_row;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), C = (int)cl.num_blocks();
     const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;");
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // What the first kernel does not write is read before it has ended: it lets
+    // this one start only when all before it are done.
     const int s0 = min(max(a.s.starts[b], 0), a.s.rows), s1 = min(max(a.s.starts[b + 1], s0), a.s.rows);
     const float t = used_temperature(a.s.temperature ? a.s.temperature[b] : 1.f);
     const float mp = a.s.min_p ? used_min_p(a.s.min_p[b]) : 0.f;
     const int n = s1 - s0;
+    const u64 draw = n > 0 ? fraction(a.draws[b]) : 0;
+    // of row s0 + j: the drafted token (-1: none, or not in the vocabulary), its logit and probability, the random number
+    struct Draft {
+        int x;
+        float l, q, u;
+    };
+    auto draft = [&](int j) {
+        Draft d{-1, 0.f, 0.f, 0.f};
+        if (j < n - 1) {
+            const int row = s0 + j;
+            d.x = a.drafts[row], d.u = a.u[row];
+            if (d.x < 0 || d.x >= a.s.V) d.x = -1;
+            if (d.x >= 0) {
+                const long long at = row * a.s.stride + d.x;
+                d.l = BF16 ? bf16_to_f32(__ldg(reinterpret_cast<const uint16_t *>(a.s.x) + at)) : __ldg(reinterpret_cast<const float *>(a.s.x) + at);
+                d.q = a.probs ? used_prob(__ldg(a.probs + row * a.probs_stride + d.x)) : 1.f;
+            }
+        }
+        return d;
+    };
+    Draft d{-1, 0.f, 0.f, 0.f};
+    if (warp == 0) d = draft(lane);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA of the sequence runs
     if (n == 0) {
         if (rank == 0 && tid == 0) a.accepted[b] = 0;
         return;
     }
-    auto logit = [&](int row, int i) {
-        const long long at = row * a.s.stride + i;
-        return BF16 ? bf16_to_f32(__ldg(reinterpret_cast<const uint16_t *>(a.s.x) + at)) : __ldg(reinterpret_cast<const float *>(a.s.x) + at);
-    };
-    auto row_of = [&](int row) {
-        R d;
-        const uintptr_t at = (uintptr_t)a.s.x + (size_t)row * a.s.stride * (BF16 ? 2 : 4);
-        d.g = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
-        d.off = (int)(at & 15) / (BF16 ? 2 : 4);
-        d.V = a.s.V, d.s = nullptr;
-        return d;
-    };
-
-    // the drafted tokens, 32 rows at a time: accepted, not, or (2) among the tokens at T, of which some are left out
-    int j0 = 0;
-    for (bool more = true; more && j0 < n - 1;) {
-        const int j = j0 + lane;
-        int state = 0;
-        if (j < n - 1) {
-            const SampleLimits lim = a.s.limits[s0 + j];
-            const int x = a.drafts[s0 + j];
-            if (x >= 0 && x < a.s.V && lim.top) {
-                const float l = logit(s0 + j, x);
-                const uint32_t key = order_key(l);
-                const Weight weight(key_logit(lim.top), t);
-                const float w = weight(l), q = a.probs ? used_prob(__ldg(a.probs + (s0 + j) * a.probs_stride + x)) : 1.f;
-                const bool in = key >= max(lim.T, 1u) && w > 0.f && (mp < 1.f ? w >= mp * weight(weight.top) : key == lim.top);
-                if (in && (double)a.u[s0 + j] * q * lim.total < w) state = key == lim.T && lim.cut ? 2 : 1;
+    // the first row whose token is not accepted, 32 rows at a time
+    if (warp == 0) {
+        for (int j = 0;; j += 32, d = draft(j + lane)) {
+            bool ok = false;
+            if (d.x >= 0) {
+                const SampleLimits lim = a.s.limits[s0 + j + lane];
+                const uint32_t key = order_key(d.l);
+                if (lim.top) {
+                    const Weight<true> weight(key_logit(lim.top), t);
+                    const float w = weight(d.l), uq = d.u * d.q;
+                    const bool in = (key > lim.T || (key == lim.T && d.x < lim.cut)) && key && w > 0.f && (mp < 1.f ? w >= lim.least : key == lim.top);
+                    ok = in && fmaf(w, lim.inv, -uq) + fmaf(w, lim.inv_lo, -fmaf(d.u, d.q, -uq)) > 0.f;   // u q < w inv
+                }
+            }
+            const unsigned stop = __ballot_sync(0xffffffffu, !ok);
+            if (stop) {
+                if (lane == 0) s_row = j + __ffs(stop) - 1;
+                break;
             }
         }
-        const unsigned stop = __ballot_sync(0xffffffffu, state != 1);
-        if (!stop) {
-            j0 += 32;
-            continue;
-        }
-        const int at = __ffs(stop) - 1;
-        j0 += at;
-        if (j0 >= n - 1 || __shfl_sync(0xffffffffu, state, at) == 0) break;
-        // is it among the first r tokens at T?
-        const SampleLimits lim = a.s.limits[s0 + j0];
-        const int x = a.drafts[s0 + j0];
-        const float xT = key_logit(lim.T);
-        __syncthreads();
-        if (tid == 0) s_count = 0;
-        __syncthreads();
-        R d = row_of(s0 + j0);
-        int found = 0;
-        for (int v = tid; v * VE - d.off < x; v += kThreads) {
-            float y[VE];
-            R::values(d.fetch(v), y);
-#pragma unroll
-            for (int e = 0; e < VE; e++) found += y[e] == xT && v * VE - d.off + e < x;
-        }
-        found = __reduce_add_sync(0xffffffffu, found);
-        if (lane == 0) atomicAdd(&s_count, found);
-        __syncthreads();
-        more = s_count < lim.r;
-        j0 += more;
     }
-    j0 = min(j0, n - 1);
+    __syncthreads();
+    const int j0 = s_row;
 
-    // the draw at row j0
+    // the draw at row j0 (at most n - 1)
     const int row = s0 + j0;
     const SampleLimits lim = a.s.limits[row];
-    R d = row_of(row);
+    R r;
     {
-        const int vecs = (d.off + d.V + VE - 1) / VE, each = (vecs + C - 1) / C;
+        const uintptr_t at = (uintptr_t)a.s.x + (size_t)row * a.s.stride * (BF16 ? 2 : 4);
+        r.g = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
+        r.off = (int)(at & 15) / (BF16 ? 2 : 4);
+        r.V = a.s.V, r.s = nullptr;
+        const int vecs = (r.off + r.V + VE - 1) / VE, each = (vecs + C - 1) / C;
         const int c0 = min(rank * each, vecs), c1 = min(c0 + each, vecs), per = (c1 - c0 + kWarps - 1) / kWarps;
-        d.c0 = c0, d.v0 = min(c0 + warp * per, c1), d.v1 = min(d.v0 + per, c1);
+        r.c0 = c0, r.v0 = min(c0 + warp * per, c1), r.v1 = min(r.v0 + per, c1);
     }
     if (rank == 0) {
         for (int j = tid; j < n; j += kThreads)
@@ -148,105 +151,90 @@ __global__ void __launch_bounds__(kThreads) moe_verify_kernel(const VerifyArgs a
         if (tid == 0) a.accepted[b] = j0;
     }
     if (!lim.top) return;   // nothing to draw
-    const Weight weight(key_logit(lim.top), t);
-    const float xT = lim.T ? key_logit(lim.T) : -INFINITY, least = mp * weight(weight.top);
-    const float per_weight = (float)(1. / lim.total);
-    const int x0 = a.drafts[row];
+    const Weight<true> weight(key_logit(lim.top), t);
+    const float xT = lim.T ? key_logit(lim.T) : -INFINITY;
+    const int cut = lim.T ? lim.cut : 0;   // (of logits of -inf none)
+    const int x0 = j0 < n - 1 ? a.drafts[row] : -1;
     const float *probs = a.probs + row * a.probs_stride;
-    int turn = 0;
     bool minus = j0 < n - 1;   // less what the draft's probabilities are
-    // what token i with logit x adds; rank_T: tokens at T before it
-    auto adds = [&](float x, int i, int &rank_T) {
-        bool in = x > xT;
-        if (x == xT && lim.T) in = rank_T++ < lim.r;
-        if (!in) return 0.f;
-        const float w = weight(x);
-        if (!(mp < 1.f ? w >= least : x == weight.top)) return 0.f;
-        const float q = !minus ? 0.f : a.probs ? used_prob(__ldg(probs + i)) : i == x0 ? 1.f : 0.f;
-        return fmaxf(fmaf(w, per_weight, -q), 0.f);
-    };
-    int tie0 = 0;   // tokens at T before this warp's part, where that counts
-    if (lim.cut) {
-        int mine = 0;
-        d.each([&](float (&x)[VE], int) {
+    const bool whole = a.probs && ((uintptr_t)(probs - r.off) & 15u) == 0;   // a vector's probabilities are vectors
+    // the draft's probabilities of a vector's tokens, the first being i
+    auto drafted_q = [&](int i, float (&q)[VE]) {
+        if (whole && i >= 0 && i + VE <= r.V) {
 #pragma unroll
-            for (int e = 0; e < VE; e++) mine += x[e] == xT;
-        });
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) ties[warp] = mine;
-        __syncthreads();
-        int all = 0;
-        for (int w = 0; w < kWarps; w++) {
-            if (w < warp) tie0 += ties[w];
-            all += ties[w];
-        }
-        if (tid < C) cl.map_shared_rank(&parts[turn][rank], tid)->ties = all;
-        cl.sync();
-        for (int c = 0; c < rank; c++) tie0 += (int)parts[turn][c].ties;
-    }
-    for (int attempt = 0; attempt < 2; attempt++) {
-        // 32 vectors at a time, a lane a vector, f(the lane's sum, its tokens' shares)
-        auto walk = [&](auto f) {
-            int rank_T = tie0;
-            for (int v = d.v0; v < d.v1; v += 32) {
-                float x[VE], y[VE];
-                if (v + lane < d.v1) {
-                    R::values(d.fetch(v + lane), x);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VE; e++) x[e] = -INFINITY;
-                }
-                int mine = 0;
-                if (lim.cut) {
-                    int at = 0;
-#pragma unroll
-                    for (int e = 0; e < VE; e++) at += x[e] == xT;
-                    mine = rank_T;
-                    if (__any_sync(0xffffffffu, at)) {
-                        int inc = at;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const int z = __shfl_up_sync(0xffffffffu, inc, o);
-                            if (lane >= o) inc += z;
-                        }
-                        mine += inc - at;
-                        rank_T += __shfl_sync(0xffffffffu, inc, 31);
-                    }
-                }
-                float sum = 0.f;
-                const int i = (v + lane) * VE - d.off;
-#pragma unroll
-                for (int e = 0; e < VE; e++) y[e] = adds(x[e], i + e, mine), sum += y[e];
-                if (f(sum, y, i)) return;
+            for (int e = 0; e < VE; e += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(probs + i + e));
+                q[e] = f.x, q[e + 1] = f.y, q[e + 2] = f.z, q[e + 3] = f.w;
             }
-        };
+        } else {
+#pragma unroll
+            for (int e = 0; e < VE; e++) q[e] = i + e >= 0 && i + e < r.V ? __ldg(probs + i + e) : 0.f;
+        }
+    };
+    // U vectors a lane at a time: f(index of the first token, what its tokens add, and their sum)
+    auto walk = [&](auto f) {
+        for (int v = r.v0; v < r.v1; v += 32 * U) {
+            uint4 w[U];
+            float q[U][VE];
+            bool some[U];   // are there tokens that may be kept?
+#pragma unroll
+            for (int u = 0; u < U; u++) w[u] = v + 32 * u + lane < r.v1 ? r.fetch(v + 32 * u + lane) : BF16 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
+                                                                                                             : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                float x[VE], top = -INFINITY;
+                R::values(w[u], x);
+#pragma unroll
+                for (int e = 0; e < VE; e++) top = fmaxf(top, x[e]);   // NaN passes over
+                some[u] = top > -INFINITY && top >= xT;
+                const int i = (v + 32 * u + lane) * VE - r.off;
+#pragma unroll
+                for (int e = 0; e < VE; e++) q[u][e] = minus && i + e == x0 && !a.probs ? 1.f : 0.f;
+                if (some[u] && minus && a.probs) drafted_q(i, q[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int i = (v + 32 * u + lane) * VE - r.off;
+                float x[VE], y[VE], sum = 0.f;
+                R::values(w[u], x);
+#pragma unroll
+                for (int e = 0; e < VE; e++) {
+                    y[e] = 0.f;
+                    if (some[u] && (x[e] > xT || (x[e] == xT && i + e < cut))) {
+                        const float w = weight(x[e]);
+                        if (mp < 1.f ? w >= lim.least : x[e] == weight.top) y[e] = fmaxf(fmaf(w, lim.inv, fmaf(w, lim.inv_lo, -used_prob(q[u][e]))), 0.f);
+                    }
+                    sum += y[e];
+                }
+                if (f(i, y, sum)) return;
+            }
+        }
+    };
+    for (int turn = 0; turn < 2; turn++) {
         float hi = 0.f, lo = 0.f;
-        walk([&](float sum, const float (&)[VE], int) {
+        walk([&](int, const float (&)[VE], float sum) {
             const float s = hi + sum, z = s - hi;
             lo += (hi - (s - z)) + (sum - z);
             hi = s;
             return false;
         });
-        const double mine = warp_sum((double)hi + lo);
+        // (lo is a correction of either sign, below half a unit in hi's last place)
+        const u64 mine = warp_sum(lo >= 0.f ? units(hi) + (lo > 0.f ? units(lo) : 0) : max(units(hi) - min(units(-lo), units(hi)), (u64)1));
         if (lane == 0) sums[warp] = mine;
         __syncthreads();
-        turn ^= 1;
-        // where the CTA's share of the running sum begins, and the warp's: sums in
-        // one order, so that each ends where the next begins
-        double at = 0., end = 0.;
+        u64 at = 0, all = 0;
         for (int w = 0; w < kWarps; w++) {
             if (w < warp) at += sums[w];
-            end += sums[w];
+            all += sums[w];
         }
-        if (tid < C) cl.map_shared_rank(&parts[turn][rank], tid)->sum = end;
+        if (tid < C) *cl.map_shared_rank(&parts[turn][rank], tid) = all;
         cl.sync();
-        double total = 0., base = 0., next = 0.;
+        u64 total = 0;
         for (int c = 0; c < C; c++) {
-            if (c == rank) base = total;
-            total += parts[turn][c].sum;
-            if (c == rank) next = total;
+            if (c < rank) at += parts[turn][c];
+            total += parts[turn][c];
         }
-        if (!(total > 0.)) {
+        if (total == 0) {
             if (minus) {   // p is nowhere above q: from p
                 minus = false;
                 continue;
@@ -254,31 +242,31 @@ __global__ void __launch_bounds__(kThreads) moe_verify_kernel(const VerifyArgs a
             if (rank == 0 && tid == 0) a.ids[row] = -1;
             return;
         }
-        end = warp == kWarps - 1 ? next : base + (at + sums[warp]);
-        at = base + at;
-        const double target = (double)fminf(fmaxf(a.draws[b], 0.f), 0.99999994f) * total;   // below the total
-        if (target < at || target >= end) return;
+        const u64 target = __umul64hi(total, draw);   // below the total
+        if (target < at || target >= at + mine) return;
         int last = -1, id = -1;
-        walk([&](float, const float (&y)[VE], int i) {
-            double s = 0.;
+        walk([&](int i, const float (&y)[VE], float sum) {
+            if (!__any_sync(0xffffffffu, sum > 0.f)) return false;
+            u64 s = 0;
 #pragma unroll
             for (int e = 0; e < VE; e++) {
-                s += y[e];
+                s += units(y[e]);
                 if (y[e] > 0.f) last = i + e;
             }
-            double inc = s;
+            u64 inc = s;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double z = __shfl_up_sync(0xffffffffu, inc, o);
+                const u64 z = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += z;
             }
-            double run = at + inc - s;
-            bool hit = false;
-            if (target < at + inc && s > 0.)
+            u64 run = at + inc - s;
+            const bool hit = target >= run && target < run + s;
+            if (hit)
 #pragma unroll
                 for (int e = 0; e < VE; e++) {
-                    run += y[e];
-                    if (!hit && y[e] > 0.f && target < run) hit = true, id = i + e;
+                    const u64 one = units(y[e]);
+                    if (target >= run && target < run + one) id = i + e;
+                    run += one;
                 }
             const unsigned who = __ballot_sync(0xffffffffu, hit);
             at += __shfl_sync(0xffffffffu, inc, 31);
