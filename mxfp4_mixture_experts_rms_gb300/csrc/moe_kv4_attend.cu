@@ -47,21 +47,30 @@ namespace {
 // RT: eights of rows of a unit.  Warps, and units in each one's ring: as many
 // warps as registers and shared memory allow (a multiple of 4: registers are
 // given to four at a time).
-template <int D, int RT>
+template <int D, int P, int RT>
 struct Few {
-    static constexpr int kWarps = D == 64 ? (RT == 1 ? 16 : RT == 2 ? 12 : 8) : (RT == 1 ? 12 : 8);
+    static constexpr int kWarps = D == 64 ? 16 : (RT == 1 ? (P == 32 ? 16 : 12) : 8);
     static constexpr int kStages = D == 128 ? 1 : 2;
     static constexpr int kStage = kTile * D / 16 * 17;   // bytes of one unit
     static constexpr int kPad = D + 8;                   // floats of a partial's row
     static constexpr int kUnitRows = 8 * RT;
+    static constexpr int kHalves = RT == 1 ? 2 : 1;      // halves of a unit that are computed together
     // a partial: acc [rows][D + 8], then m, l [rows], the accumulator's exponent [blocks][rows]
     static constexpr int kPartial = kUnitRows * (kPad + 2 + D / 32);
     // a warp's own: the ring, scales, queries; the last partial goes over them, and behind it the scalars of a join
-    static constexpr int kScales = kStages * kStage, kQueries = kScales + D / 32 * (128 + 64);
+    static constexpr int kScales = kStages * kStage, kQueries = kScales + kHalves * (D / 32) * (128 + 64);
     static constexpr int kHeld = kQueries + RT * (D / 32) * 512;
     static constexpr int kJoin = (kPartial + (kMaxCtas + kWarps) / kWarps * 8 * (2 + D / 32)) * 4;   // kMaxCtas + 1 partials at most
     static constexpr int kRing = ((kHeld > kJoin ? kHeld : kJoin) + 127) / 128 * 128;
-    static constexpr int kSmem = kWarps * (kRing + kPartial * 4);   // without the sequences
+    static constexpr int kSmem = kWarps * kRing;   // without the sequences
+};
+
+constexpr int kMaxWarps = 16;
+
+// Of a unit's rows: their first and last position, the tokens that can be seen,
+// and the unit's index from which the job is counted.
+struct Span {
+    int pmin, pmax, seen, seg0;
 };
 
 struct FewArgs {
@@ -69,7 +78,7 @@ struct FewArgs {
     int G;                     // query heads per kv head
     int32_t *status;           // [2]
     uint32_t *tickets;         // [kMaxCtas], zero between calls
-    float *parts;              // [kMaxCtas][2][partial_floats]
+    float *parts, *heads;      // [kMaxCtas][2] and [kMaxCtas][kMaxWarps] partials
     int *seqs;                 // [3][n_seqs], or null: in shared memory
 };
 
@@ -120,26 +129,29 @@ __device__ __forceinline__ float2 row_factor(float m, float l, float N, float si
 }
 
 template <int D, int P, int RT>
-__global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel(const __grid_constant__ FewArgs f) {
-    typedef Few<D, RT> F;
+__global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_kernel(const __grid_constant__ FewArgs f) {
+    typedef Few<D, P, RT> F;
     constexpr int W = F::kWarps, NP = kTile / P, HP = P == 16 ? 2 : 1, NB = D / 32, ST = F::kStage, PAD = F::kPad, S = F::kStages;
-    constexpr int R = F::kUnitRows, PF = F::kPartial, PB = kv4_page_bytes(P, D), RING = F::kRing, SC = 8 * (2 + NB);   // (scalars of eight rows)
+    constexpr int HV = F::kHalves, R = F::kUnitRows, PF = F::kPartial, PB = kv4_page_bytes(P, D), RING = F::kRing, SC = 8 * (2 + NB);   // (scalars of eight rows)
     static_assert(F::kSmem + kSmemSeqs * 12 <= 230000, "shared memory");
     extern __shared__ __align__(128) unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[W][S];
     __shared__ int scan[W];
-    __shared__ Job jobs[W];                       // each warp's running job
+    __shared__ Span spans[W];                     // what each warp's rows see
+    __shared__ int row_pos[W][R], share[3];       // their positions; the CTA's first unit, the one behind its last; units of a kv head
+    __shared__ unsigned pages_at[W][S];           // the pages that are there, of each stage
+    __shared__ Job next_job[W], jobs[W][S];       // each warp's of the unit to be copied next, and of the stages
     __shared__ Seg segs[2 * W];                   // head and tail of each warp
     __shared__ int list[2 * W], group_at[2 * W + 1], group_seg[2 * W], shared_seg[2], s_first[2], s_count[2];
     const Kv4Attend &a = f.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     unsigned char *ring = smem_raw + (size_t)warp * RING;
-    float *part = reinterpret_cast<float *>(smem_raw + (size_t)W * RING);   // [W] head partials; tails go over the rings
+    float *part = f.heads + (size_t)blockIdx.x * (kMaxWarps * PF);   // [W] head partials (in memory, as few warps have one); tails go over the rings
     // per sequence: units of those before it (a kv head), index of its first unit in it, tokens that can be seen; of
     // many sequences in the workspace, where every CTA writes the same
     const uint32_t scratch = smem_u32(ring) + F::kScales;    // keys, floats [block][g][4]; values, fp16 pairs [block][t4][4]
     const uint32_t queries = smem_u32(ring) + F::kQueries;   // fp16 [block][row / 8][lane][8]
-    int *seq_s = reinterpret_cast<int *>(part + (size_t)W * PF);
+    int *seq_s = reinterpret_cast<int *>(smem_raw + (size_t)W * RING);
     auto seq = [&](int what, int b) { return f.seqs ? f.seqs[what * a.n_seqs + b] : seq_s[what * a.n_seqs + b]; };
     if (lane == 0)
         for (int s = 0; s < S; s++) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&bars[warp][s])));
@@ -183,6 +195,7 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
     __syncthreads();
     const int units = total * a.c.KVH, ctas = min((int)gridDim.x, (units + 3) / 4);
     if ((int)blockIdx.x >= ctas) return;
+    if (tid == 0) share[2] = total;
     // the job of unit u (0 <= u < units)
     auto job_of = [&](int u) {
         Job j;
@@ -197,7 +210,7 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
         j.b = lo;
         j.nt = max(1, (seq(2, lo) + kTile - 1) / kTile - seq(1, lo));
         const unsigned tile = (unsigned)(u - before) / (unsigned)j.nt;
-        const unsigned n_rt = ((lo + 1 < a.n_seqs ? seq(0, lo + 1) : total) - seq(0, lo)) / j.nt;
+        const unsigned n_rt = ((lo + 1 < a.n_seqs ? seq(0, lo + 1) : share[2]) - seq(0, lo)) / j.nt;
         j.h = tile / n_rt;
         j.rt = tile % n_rt;
         j.u0 = before + tile * j.nt;
@@ -206,48 +219,50 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
     // The CTA's share: the even cuts, each moved down to its job's first unit
     // where the job is at most 8 units long (a job that one CTA can take at
     // once is not worth joining across two).
+    __syncthreads();   // share[2]
     int cut = (int)((long long)units * (blockIdx.x + (lane & 1)) / ctas);
     if (cut > 0 && cut < units) {
         const Job j = job_of(cut);
         if (j.nt <= 8) cut = j.u0;
     }
-    const int c0 = __shfl_sync(0xffffffffu, cut, 0), c1 = __shfl_sync(0xffffffffu, cut, 1);
-    const int u0 = c0 + (c1 - c0) * warp / W, u1 = c0 + (c1 - c0) * (warp + 1) / W;   // c1 - c0 < 2^31 / 16 (host)
+    if (tid < 2) share[tid] = cut;
+    const int cta0 = __shfl_sync(0xffffffffu, cut, 0), cta1 = __shfl_sync(0xffffffffu, cut, 1);
+    const int u0 = cta0 + (cta1 - cta0) * warp / W, u1 = cta0 + (cta1 - cta0) * (warp + 1) / W;   // c1 - c0 < 2^31 / 16 (host)
 
-    // the issuing side: place of the next unit to copy, its pages read one unit ahead
-    Job ij = {0, 0, 0, 1, 0}, ji = ij;   // of unit iu, and of the one issued last
+    // the issuing side: the next unit to copy, its pages read one unit ahead
     int iu = u0;
     int pg = -1;
-    unsigned pages_at[S];   // per stage: the pages that are there
-#pragma unroll
-    for (int s = 0; s < S; s++) pages_at[s] = 0;
+    auto find_job = [&] {
+        const Job j = job_of(iu);
+        __syncwarp();
+        if (lane == 0) next_job[warp] = j;
+        __syncwarp();
+    };
     auto fetch_page = [&]() {   // lane p < NP: page of the unit iu
         pg = -1;
         if (iu < u1 && lane < NP) {
-            const int tile = seq(1, ij.b) + iu - ij.u0;
+            const int b = next_job[warp].b, tile = seq(1, b) + iu - next_job[warp].u0;
             const int t0 = tile * kTile + lane * P;
-            if (t0 < seq(2, ij.b)) pg = __ldg(a.table + (size_t)ij.b * a.width + t0 / P);
+            if (t0 < seq(2, b)) pg = __ldg(a.table + (size_t)b * a.width + t0 / P);
         }
     };
     auto issue = [&](int stage) {
         const bool ok = lane < NP && pg >= 0 && pg < a.c.n_pages;
         const unsigned okm = __ballot_sync(0xffffffffu, ok);
         const uint32_t bar = smem_u32(&bars[warp][stage]);
-        if (lane == 0)
+        if (lane == 0) {
+            jobs[warp][stage] = next_job[warp], pages_at[warp][stage] = okm;
             asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(bar),
                          "r"((uint32_t)(__popc(okm) * PB)) : "memory");
+        }
         __syncwarp();
-        if (ok) bulk_copy(smem_u32(ring + stage * ST) + lane * PB, a.c.c + ((size_t)pg * a.c.KVH + ij.h) * PB, PB, bar);
-#pragma unroll
-        for (int s = 0; s < S; s++)
-            if (s == stage) pages_at[s] = okm;
-        if (S > 1) ji = ij;
+        if (ok) bulk_copy(smem_u32(ring + stage * ST) + lane * PB, a.c.c + ((size_t)pg * a.c.KVH + next_job[warp].h) * PB, PB, bar);
         iu++;
-        if (iu < u1 && iu == ij.u0 + ij.nt) ij = job_of(iu);
+        if (iu < u1 && iu == next_job[warp].u0 + next_job[warp].nt) find_job();
         fetch_page();
     };
     if (u0 < u1) {
-        ij = job_of(u0);
+        find_job();
         fetch_page();
     }
     bool fine = true;
@@ -256,7 +271,6 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
     // 2 d + c of the tile [b][y][x]
     float acc[NB][2][RT][4], m[RT][2], l[RT][2];
     float rs[RT][2];       // turn a row's products into scores
-    float thr[RT][2];      // m in terms of the products
     bool large = false;    // of scores: products are rounded to scores first, as they are when compared
     // E of block vb, as a scale byte: where the lane's group of 8 has value scales (D = 64: lanes 16 ..)
     const int vb = D == 64 ? (lane >> 3) & 1 : lane >> 3;
@@ -264,24 +278,25 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
     auto of_block = [&](auto x, int b) { return __shfl_sync(0xffffffffu, x, 8 * b + (D == 64 ? 16 : 0)); };
     const float sc = a.scale * kLog2e;
     bool begun = false;
-    int pos[RT][2], pmin = 0, pmax = 0, seen = 0, at0 = 0, job_end = 0;   // the job's tokens, place of unit 0 in it, unit behind its last
-    int seg0 = u0;           // first unit of the running segment
-    static_assert(S <= 2, "the job of a unit that is issued and not begun is ji");
+    int at0 = 0, seg_end = 0, all_from = 0, all_to = 0;   // place of unit 0 in the job, unit behind the segment's last, tokens that all rows see
     for (int u = u0; u < u1 && fine; u++) {
         const int i = u - u0, stage = i % S;
         const bool fresh = !begun;
-        const Job j = S > 1 && iu > u ? ji : ij;   // the unit's, where it begins one
 #pragma unroll 1
         while (iu < u1 && iu < u + S) issue((iu - u0) % S);
         if (fresh) {
             // a new job: its rows' queries, while the unit's pages are on their way
-            if (lane == 0) jobs[warp] = j;
-            seen = seq(2, j.b), at0 = seq(1, j.b) - j.u0, job_end = j.u0 + j.nt;
-            begun = true, seg0 = u;
+            const Job j = jobs[warp][stage];
+            at0 = seq(1, j.b) - j.u0, seg_end = min(j.u0 + j.nt, u1);
+            begun = true;
             int row0, n, pos0;
             kv8_rows(a, j.b, row0, n, pos0);
-            pmin = pos0 + j.rt * R / f.G;
-            pmax = pos0 + min(n * f.G - 1, j.rt * R + R - 1) / f.G;
+            {
+                const int pmin = pos0 + j.rt * R / f.G, pmax = pos0 + min(n * f.G - 1, j.rt * R + R - 1) / f.G, seen = seq(2, j.b);
+                all_from = a.window ? max(pmax - a.window + 1, 0) : 0, all_to = min(seen - 1, pmin);
+                if (lane == 0) spans[warp] = {pmin, pmax, seen, u};
+                for (int r = lane; r < R; r += 32) row_pos[warp][r] = j.rt * R + r < n * f.G ? pos0 + (j.rt * R + r) / f.G : -1;
+            }
 #pragma unroll
             for (int x = 0; x < RT; x++) {
                 const int rr = j.rt * R + 8 * x + g, i2 = rr / f.G, head = j.h * f.G + rr - i2 * f.G;
@@ -311,10 +326,8 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
                 }
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    const int r2 = j.rt * R + 8 * x + 2 * t4 + c;
-                    pos[x][c] = r2 < n * f.G ? pos0 + r2 / f.G : -1;
                     rs[x][c] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4 * c);
-                    m[x][c] = thr[x][c] = -INFINITY, l[x][c] = 0.f;
+                    m[x][c] = -INFINITY, l[x][c] = 0.f;
                 }
             }
             E = 0, large = false;
@@ -326,43 +339,48 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
         const int u_at = (at0 + u) * kTile;
-        const unsigned here = S == 1 || stage == 0 ? pages_at[0] : pages_at[S - 1];
-        // 32 tokens at a time
+        const unsigned here = pages_at[warp][stage];
+        // HV halves of 32 tokens at a time
 #pragma unroll 1
-        for (int hf = 0; hf < 2; hf++) {
-            const int t0 = u_at + 32 * hf;
-            const unsigned pages = P == 64 ? here : here >> (hf * HP);   // bit p: of this half
-            const bool whole = t0 + 32 <= seen && t0 + 31 <= pmin && (a.window == 0 || t0 > pmax - a.window) && (pages & ((1u << HP) - 1)) == (1u << HP) - 1;
-            // this half's codes: a token's row of key block b
-            const uint32_t page = smem_u32(ring + stage * ST) + (P == 64 ? 0 : hf * HP * PB);
-            const uint32_t rows_at = page + (P == 16 ? (lane >> 4) * PB + (lane & 15) * 16 : P == 32 ? lane * 16 : hf * 512 + lane * 16);
-            // its scales: a lane the four tokens of a word, octets 2 kk and 2 kk + 1, of block vb
-            uint32_t vs;
-            {
+        for (int h0 = 0; h0 < 2; h0 += HV) {
+            const int t0 = u_at + 32 * h0;
+            constexpr int PV = HV * HP < NP ? HV * HP : NP;              // their pages
+            const unsigned pages = P == 64 ? here : here >> (h0 * HP);   // bit p: of these
+            const bool whole = t0 >= all_from && t0 + 32 * HV - 1 <= all_to && (pages & ((1u << PV) - 1)) == (1u << PV) - 1;
+            auto there = [&](int v, int n) { return pages >> ((4 * v + n) * PV / (4 * HV)) & 1; };   // of octet n of half v
+            // the codes of half v: a token's row of key block b; its scales: a lane the four tokens of a word, octets 2 kk and
+            // 2 kk + 1, of block vb
+            const uint32_t page = smem_u32(ring + stage * ST) + (P == 64 ? 0 : h0 * HP * PB);
+            const uint32_t rows_at = page + (P == 16 ? (lane >> 4) * PB + (lane & 15) * 16 : lane * 16) + (P == 64 ? h0 * 512 : 0);
+            constexpr int kRowsOn = P == 64 ? 512 : HP * PB;   // from half to half
+            uint32_t vs[HV], ends = 0;
+#pragma unroll
+            for (int v = 0; v < HV; v++) {
                 const int kk = (lane >> 2) & 1;
-                const uint32_t at = page + P * D + 4 * t4 + (P == 64 ? hf * 32 : 0) + (P == 16 ? kk * PB : kk * 16) + vb * P;
+                const uint32_t at = page + P * D + 4 * t4 + (P == 64 ? (h0 + v) * 32 : v * HP * PB) + (P == 16 ? kk * PB : kk * 16) + vb * P;
                 const uint32_t ks = lds32(at + (D == 64 && lane >= 16 ? NB * P : 0));
-                vs = D == 64 ? ks : lds32(at + NB * P);
+                vs[v] = D == 64 ? ks : lds32(at + NB * P);
                 if (D == 128 || lane < 16) {   // tokens 2 t4 and 2 t4 + 1 of the octets
-                    const uint32_t to = scratch + 128 * vb + 32 * t4 + 8 * kk;
+                    const uint32_t to = scratch + v * (NB * 192) + 128 * vb + 32 * t4 + 8 * kk;
                     sts64(to, byte_exp(ks, 0), byte_exp(ks, 2));
                     sts64(to + 16, byte_exp(ks, 1), byte_exp(ks, 3));
                 }
                 if (!whole) {
+                    const Span sp = spans[warp];
                     uint32_t keep = 0;   // values that some row sees
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        const int n = 2 * kk + (e >> 1), t = t0 + 8 * n + 2 * t4 + (e & 1);
-                        if (t < seen && (pages >> (n * HP / 4) & 1) && t <= pmax && t >= kv8_first(pmin, a.window)) keep |= 0xFFu << (8 * e);
+                        const int n = 2 * kk + (e >> 1), t = t0 + 32 * v + 8 * n + 2 * t4 + (e & 1);
+                        if (t < sp.seen && there(v, n) && t <= sp.pmax && t >= kv8_first(sp.pmin, a.window)) keep |= 0xFFu << (8 * e);
                     }
-                    vs &= keep;
+                    vs[v] &= keep;
                 }
-                if (D == 64 && lane < 16) vs = 0;
+                if (D == 64 && lane < 16) vs[v] = 0;
+                // the largest and (as 256 less it) the smallest value scale of each block
+                const uint32_t lo2 = vs[v] & 0x00FF00FFu, hi2 = vs[v] >> 8 & 0x00FF00FFu;
+                const uint32_t most = __vmaxu2(lo2, hi2), least = __vmaxu2((0x01000100u - lo2) & 0x00FF00FFu, (0x01000100u - hi2) & 0x00FF00FFu);
+                ends = __vmaxu2(ends, __vmaxu2(__byte_perm(most, least, 0x5410), __byte_perm(most, least, 0x7632)));
             }
-            // the largest and (as 256 less it) the smallest value scale of each block
-            const uint32_t lo2 = vs & 0x00FF00FFu, hi2 = vs >> 8 & 0x00FF00FFu;
-            const uint32_t most = __vmaxu2(lo2, hi2), least = __vmaxu2((0x01000100u - lo2) & 0x00FF00FFu, (0x01000100u - hi2) & 0x00FF00FFu);
-            uint32_t ends = __vmaxu2(__byte_perm(most, least, 0x5410), __byte_perm(most, least, 0x7632));
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) ends = __vmaxu2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
             const int E1 = max(E, (int)(ends & 0xFFFFu));
@@ -377,65 +395,73 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
                 }
                 E = E1;
             }
-            // the value scales of w, all within 4 of E: 2^(e - E) in fp16; nothing for what is not seen
-            auto scale_values = [&](uint32_t w, int E) {
+            // the value scales w of half v, all within 4 of E: 2^(e - E) in fp16; nothing for what is not seen
+            auto scale_values = [&](int v, uint32_t w, int E) {
                 const uint32_t some = (w | (w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u, keep = (some >> 7) * 255u;
                 const uint32_t by = (uint32_t)(15 - E) * 0x10001u;
                 w |= (uint32_t)E * 0x01010101u & ~keep;   // (no borrow from the neighbour)
                 const uint32_t x = (__byte_perm(w, 0, 0x4140) + by) << 10 & __byte_perm(keep, 0, 0x1100);
                 const uint32_t y = (__byte_perm(w, 0, 0x4342) + by) << 10 & __byte_perm(keep, 0, 0x3322);
-                if (D == 128 || lane >= 16) sts64(scratch + NB * 128 + 64 * vb + 16 * t4 + 2 * (lane & 4), x, y);
+                if (D == 128 || lane >= 16) sts64(scratch + v * (NB * 192) + NB * 128 + 64 * vb + 16 * t4 + 2 * (lane & 4), x, y);
             };
-            if (!wild) scale_values(vs, E);
-            __syncwarp();
-            // products: tokens 8 n + g, rows 2 t4 + c of the eights
-            float s[RT][4][2];
+            if (!wild) {
 #pragma unroll
-            for (int i = 0; i < RT * 8; i++) (&s[0][0][0])[i] = 0.f;
+                for (int v = 0; v < HV; v++) scale_values(v, vs[v], E);
+            }
+            __syncwarp();
+            // products: tokens 32 v + 8 n + g, rows 2 t4 + c of the eights
+            float s[RT][4 * HV][2];
+#pragma unroll
+            for (int i = 0; i < RT * 8 * HV; i++) (&s[0][0][0])[i] = 0.f;
 #pragma unroll 1
             for (int b = 0; b < NB; b++) {
-                uint32_t kw[4], ks[4], k0[2][4], k1[2][4];   // of two octets: dims 8 t4 .. + 3, + 4 .. + 7
-                ldsm4(kw, rows_at + b * (P * 16));
-                lds128(scratch + 128 * b + 16 * g, ks);
+                uint32_t q[RT][4];
 #pragma unroll
-                for (int n = 0; n < 4; n++) {
-                    uint32_t h[4];
-                    e2m1x8_to_f16(kw[n], h);
-                    k0[n >> 1][n & 1] = h[0], k0[n >> 1][2 + (n & 1)] = h[1];
-                    k1[n >> 1][n & 1] = h[2], k1[n >> 1][2 + (n & 1)] = h[3];
-                }
+                for (int x = 0; x < RT; x++) lds128(queries + (b * RT + x) * 512 + 16 * lane, q[x]);
 #pragma unroll
-                for (int x = 0; x < RT; x++) {
-                    uint32_t q[4];
-                    lds128(queries + (b * RT + x) * 512 + 16 * lane, q);
+                for (int v = 0; v < HV; v++) {
+                    uint32_t kw[4], ks[4], k0[2][4], k1[2][4];   // of two octets: dims 8 t4 .. + 3, + 4 .. + 7
+                    ldsm4(kw, rows_at + v * kRowsOn + b * (P * 16));
+                    lds128(scratch + v * (NB * 192) + 128 * b + 16 * g, ks);
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        float y[4];
-                        mma_f16_first(y, k0[h], q[0], q[1]);
-                        mma_f16(y, k1[h], q[2], q[3]);
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            s[x][2 * h + (e >> 1)][e & 1] = fmaf(y[e], __uint_as_float(ks[2 * h + (e >> 1)]), s[x][2 * h + (e >> 1)][e & 1]);
+                    for (int n = 0; n < 4; n++) {
+                        uint32_t h[4];
+                        e2m1x8_to_f16(kw[n], h);
+                        k0[n >> 1][n & 1] = h[0], k0[n >> 1][2 + (n & 1)] = h[1];
+                        k1[n >> 1][n & 1] = h[2], k1[n >> 1][2 + (n & 1)] = h[3];
                     }
+#pragma unroll
+                    for (int x = 0; x < RT; x++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            float y[4];
+                            mma_f16_first(y, k0[h], q[x][0], q[x][1]);
+                            mma_f16(y, k1[h], q[x][2], q[x][3]);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                float &to = s[x][4 * v + 2 * h + (e >> 1)][e & 1];
+                                to = fmaf(y[e], __uint_as_float(ks[2 * h + (e >> 1)]), to);
+                            }
+                        }
                 }
             }
             if (!whole) {
 #pragma unroll
-                for (int n = 0; n < 4; n++) {
-                    const int t = t0 + 8 * n + g;
-                    const bool there = t < seen && (pages >> (n * HP / 4) & 1);
+                for (int x = 0; x < RT; x++)
 #pragma unroll
-                    for (int x = 0; x < RT; x++)
+                    for (int c = 0; c < 2; c++) {
+                        // tokens from .. to of the thread's first one on
+                        const int pos = row_pos[warp][8 * x + 2 * t4 + c], from = (a.window ? max(pos - a.window + 1, 0) : 0) - t0 - g, to = min(spans[warp].seen - 1, pos) - t0 - g;
 #pragma unroll
-                        for (int c = 0; c < 2; c++)
-                            if (!(there && t <= pos[x][c] && (a.window == 0 || t > pos[x][c] - a.window))) s[x][n][c] = -INFINITY;
-                }
+                        for (int n = 0; n < 4 * HV; n++)
+                            if (8 * n < from || 8 * n > to || !there(n / 4, n % 4)) s[x][n][c] = -INFINITY;
+                    }
             }
             auto to_scores = [&] {
 #pragma unroll
                 for (int x = 0; x < RT; x++)
 #pragma unroll
-                    for (int i = 0; i < 8; i++) s[x][i >> 1][i & 1] = __fmul_rn(s[x][i >> 1][i & 1], rs[x][i & 1]);
+                    for (int i = 0; i < 8 * HV; i++) s[x][i >> 1][i & 1] = __fmul_rn(s[x][i >> 1][i & 1], rs[x][i & 1]);
             };
             if (large) to_scores();
             // a score above m: m moves
@@ -446,7 +472,9 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
                     mx[x][c] = fmaxf(fmaxf(s[x][0][c], s[x][1][c]), fmaxf(s[x][2][c], s[x][3][c]));
-                    above |= mx[x][c] > thr[x][c];
+                    if (HV == 2) mx[x][c] = fmaxf(mx[x][c], fmaxf(fmaxf(s[x][4 * HV - 4][c], s[x][4 * HV - 3][c]), fmaxf(s[x][4 * HV - 2][c], s[x][4 * HV - 1][c])));
+                    if (!large) mx[x][c] = __fmul_rn(mx[x][c], rs[x][c]);
+                    above |= mx[x][c] > m[x][c];
                 }
             if (__any_sync(0xffffffffu, above)) {
                 bool far = false;
@@ -458,7 +486,6 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
-                        if (!large) q = __fmul_rn(q, rs[x][c]);
                         if (q > m[x][c]) {
                             const float to = q + 4.f, corr = ex2(m[x][c] - to);
                             l[x][c] *= corr, m[x][c] = to;
@@ -473,31 +500,27 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
                     large = true;
                     to_scores();
                 }
-#pragma unroll
-                for (int x = 0; x < RT; x++)
-#pragma unroll
-                    for (int c = 0; c < 2; c++) thr[x][c] = large || m[x][c] == -INFINITY ? m[x][c] : __fdividef(m[x][c], rs[x][c]);
             }
-            uint32_t p[RT][4];   // weights times 2^15, of row g: tokens 8 n + 2 t4, + 1
+            uint32_t p[RT][4 * HV];   // weights times 2^15, of row g: tokens 8 n + 2 t4, + 1
 #pragma unroll
             for (int x = 0; x < RT; x++) {
-                float w[4][2];
+                float w[4 * HV][2];
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
                     const float k = large ? 1.f : rs[x][c], ms = m[x][c] == -INFINITY ? 0.f : m[x][c] - 15.f;
                     float sum = 0.f;
 #pragma unroll
-                    for (int n = 0; n < 4; n++) sum += w[n][c] = ex2(fmaf(s[x][n][c], k, -ms));
+                    for (int n = 0; n < 4 * HV; n++) sum += w[n][c] = ex2(fmaf(s[x][n][c], k, -ms));
                     l[x][c] += sum;
                 }
 #pragma unroll
-                for (int n = 0; n < 4; n++) p[x][n] = turn8(pack_f16(w[n][0], w[n][1]));
+                for (int n = 0; n < 4 * HV; n++) p[x][n] = turn8(pack_f16(w[n][0], w[n][1]));
             }
-            // block b's values times the weights, added to `to`
-            auto values = [&](int b, float (&to)[2][RT][4]) {
+            // block b's values of half v times the weights, added to `to`
+            auto values = [&](int v, int b, float (&to)[2][RT][4]) {
                 uint32_t sv[4], vw[4];
-                lds128(scratch + NB * 128 + 64 * b + 16 * t4, sv);
-                ldsm4t(vw, rows_at + P * D / 2 + b * (P * 16));
+                lds128(scratch + v * (NB * 192) + NB * 128 + 64 * b + 16 * t4, sv);
+                ldsm4t(vw, rows_at + v * kRowsOn + P * D / 2 + b * (P * 16));
 #pragma unroll
                 for (int kk = 0; kk < 2; kk++) {
                     // tokens of a word's halves side by side: dims 4 g and 4 g + 2 of two octets, 4 g + 1 and 4 g + 3
@@ -507,7 +530,7 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
                     e2m1x8_to_f16((lo >> 4 & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), h1);
 #pragma unroll
                     for (int x = 0; x < RT; x++) {
-                        const uint32_t p0 = mul_f16(p[x][2 * kk], sv[2 * kk]), p1 = mul_f16(p[x][2 * kk + 1], sv[2 * kk + 1]);
+                        const uint32_t p0 = mul_f16(p[x][4 * v + 2 * kk], sv[2 * kk]), p1 = mul_f16(p[x][4 * v + 2 * kk + 1], sv[2 * kk + 1]);
                         mma_f16(to[0][x], h0, p0, p1);
                         mma_f16(to[1][x], h1, p0, p1);
                     }
@@ -515,45 +538,50 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
             };
             if (!wild) {
 #pragma unroll
-                for (int b = 0; b < NB; b++) values(b, acc[b]);
+                for (int b = 0; b < NB; b++)
+#pragma unroll
+                    for (int v = 0; v < HV; v++) values(v, b, acc[b]);
             } else {
                 // classes of scales, the largest first; each one's products apart
-                uint32_t left = vs;
+#pragma unroll
+                for (int v = 0; v < HV; v++) {
+                    uint32_t left = vs[v];
 #pragma unroll 1
-                while (__any_sync(0xffffffffu, left)) {
-                    int top = 0;
+                    while (__any_sync(0xffffffffu, left)) {
+                        int top = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; e++) top = max(top, (int)(left >> (8 * e) & 255u));
+                        for (int e = 0; e < 4; e++) top = max(top, (int)(left >> (8 * e) & 255u));
 #pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    uint32_t in = 0;
+                        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        uint32_t in = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        if ((int)(left >> (8 * e) & 255u) >= max(top - 4, 1)) in |= 0xFFu << (8 * e);
-                    __syncwarp();   // the scales before are read
-                    scale_values(left & in, top);
-                    left &= ~in;
-                    __syncwarp();
-                    const float k = pow2i(top - E);
+                        for (int e = 0; e < 4; e++)
+                            if ((int)(left >> (8 * e) & 255u) >= max(top - 4, 1)) in |= 0xFFu << (8 * e);
+                        __syncwarp();   // the scales before are read
+                        scale_values(v, left & in, top);
+                        left &= ~in;
+                        __syncwarp();
+                        const float k = pow2i(top - E);
 #pragma unroll
-                    for (int b = 0; b < NB; b++) {
-                        float apart[2][RT][4];
-                        const float kb = of_block(k, b);
+                        for (int b = 0; b < NB; b++) {
+                            float apart[2][RT][4];
+                            const float kb = of_block(k, b);
 #pragma unroll
-                        for (int i = 0; i < 2 * RT * 4; i++) (&apart[0][0][0])[i] = 0.f;
-                        values(b, apart);
+                            for (int i = 0; i < 2 * RT * 4; i++) (&apart[0][0][0])[i] = 0.f;
+                            values(v, b, apart);
 #pragma unroll
-                        for (int i = 0; i < 2 * RT * 4; i++) (&acc[b][0][0][0])[i] = fmaf((&apart[0][0][0])[i], kb, (&acc[b][0][0][0])[i]);
+                            for (int i = 0; i < 2 * RT * 4; i++) (&acc[b][0][0][0])[i] = fmaf((&apart[0][0][0])[i], kb, (&acc[b][0][0][0])[i]);
+                        }
                     }
                 }
             }
             __syncwarp();   // the scales are read
         }
         __syncwarp();   // the stage is read: the next iteration fills it
-        if (u + 1 == job_end || u + 1 == u1) {
-            const Job j = jobs[warp];
+        if (u + 1 == seg_end) {
+            const Job j = jobs[warp][stage];
             begun = false;
-            const bool begins = seg0 == j.u0, ends = u + 1 == j.u0 + j.nt;
+            const bool begins = spans[warp].seg0 == j.u0, ends = u + 1 == j.u0 + j.nt;
 #pragma unroll
             for (int x = 0; x < RT; x++)
 #pragma unroll
@@ -616,6 +644,8 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
         for (int s = 0; s < S; s++)
             if (s < iu - u0) bar_wait(smem_u32(&bars[warp][s]), (uint32_t)((iu - u0 - 1 - s) / S) & 1, f.status, 96);
     __syncthreads();
+
+    const int c0 = share[0], c1 = share[1], all_units = share[2] * a.c.KVH, all_ctas = min((int)gridDim.x, (all_units + 3) / 4);   // (as above)
 
     // Joining: the CTA's segments in order, those of one job a group (they are
     // neighbours); then, of the jobs that other CTAs share (at most the first
@@ -705,7 +735,7 @@ __global__ void __launch_bounds__(Few<D, RT>::kWarps * 32, 1) moe_kv4_few_kernel
         if (shared_seg[tid] >= 0) {
             // the CTAs that share the job, by the even cuts (no cut inside it was moved)
             const Seg x = segs[shared_seg[tid]];
-            const int c_first = (int)(((long long)(x.u0 + 1) * ctas - 1) / units), c_last = (int)(((long long)(x.u0 + x.nt) * ctas - 1) / units);
+            const int c_first = (int)(((long long)(x.u0 + 1) * all_ctas - 1) / all_units), c_last = (int)(((long long)(x.u0 + x.nt) * all_ctas - 1) / all_units);
             if (atomicAdd(f.tickets + c_first, 1) == (uint32_t)(c_last - c_first)) {
                 f.tickets[c_first] = 0;   // as the next call finds it
                 s_first[tid] = c_first, s_count[tid] = c_last - c_first + 1;
@@ -736,22 +766,16 @@ constexpr size_t kPartOffset = kKv8ClearBytes + (size_t)kKv8MaxSeqs * 12;
 template <int D, int P, int RT>
 cudaError_t few_launch(FewArgs f, int ctas, cudaStream_t st) {
     if (f.a.n_seqs <= kSmemSeqs) f.seqs = nullptr;
-    const size_t smem = Few<D, RT>::kSmem + (f.seqs ? 0 : (size_t)f.a.n_seqs * 12);
+    const size_t smem = Few<D, P, RT>::kSmem + (f.seqs ? 0 : (size_t)f.a.n_seqs * 12);
     static PerDevice<bool> opted;
     cudaError_t e = smem_optin_once(moe_kv4_few_kernel<D, P, RT>, opted);
     if (e != cudaSuccess) return e;
-    return launch_pdl(moe_kv4_few_kernel<D, P, RT>, dim3(ctas), dim3(Few<D, RT>::kWarps * 32), smem, st, f);
+    return launch_pdl(moe_kv4_few_kernel<D, P, RT>, dim3(ctas), dim3(Few<D, P, RT>::kWarps * 32), smem, st, f);
 }
-constexpr int most_eights(int) { return 2; }   // of a unit's rows
+constexpr int kMostEights = 2;   // of a unit's rows
 template <int D, int P>
 cudaError_t few_rows(const FewArgs &f, int rows, int ctas, cudaStream_t st) {
-    const int eights = (rows + 7) / 8, tiles = (eights + most_eights(D) - 1) / most_eights(D);
-    switch ((eights + tiles - 1) / tiles) {
-        case 1: return few_launch<D, P, 1>(f, ctas, st);
-        case 2: return few_launch<D, P, 2>(f, ctas, st);
-        case 3: return few_launch<D, P, most_eights(D) < 3 ? 2 : 3>(f, ctas, st);
-        default: return few_launch<D, P, most_eights(D) < 4 ? 2 : 4>(f, ctas, st);
-    }
+    return rows <= 8 ? few_launch<D, P, 1>(f, ctas, st) : few_launch<D, P, kMostEights>(f, ctas, st);
 }
 template <int D>
 cudaError_t few_page(const FewArgs &f, int rows, int ctas, cudaStream_t st) {
@@ -761,9 +785,10 @@ cudaError_t few_page(const FewArgs &f, int rows, int ctas, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv4_workspace_bytes(int D) {
-    return kPartOffset + (size_t)kMaxCtas * 2 * (D == 64 ? Few<64, most_eights(64)>::kPartial : Few<128, most_eights(128)>::kPartial) * 4;
-}
+// Partials of a call: two a CTA, and one a warp.
+static size_t partial_bytes(int D) { return (size_t)(D == 64 ? Few<64, 16, kMostEights>::kPartial : Few<128, 16, kMostEights>::kPartial) * 4; }
+
+size_t kv4_workspace_bytes(int D) { return kPartOffset + (size_t)kMaxCtas * (2 + kMaxWarps) * partial_bytes(D); }
 
 cudaError_t launch_kv4_attend(const Kv4Attend &a, unsigned char *ws, cudaStream_t st) {
     const int G = a.QH / a.c.KVH;
@@ -774,6 +799,7 @@ cudaError_t launch_kv4_attend(const Kv4Attend &a, unsigned char *ws, cudaStream_
         f.tickets = reinterpret_cast<uint32_t *>(ws + 64);
         f.seqs = reinterpret_cast<int *>(ws + kKv8ClearBytes);
         f.parts = reinterpret_cast<float *>(ws + kPartOffset);
+        f.heads = reinterpret_cast<float *>(ws + kPartOffset + (size_t)kMaxCtas * 2 * partial_bytes(a.c.D));
         int ctas = 0;
         const cudaError_t e = sm_count(&ctas);
         if (e != cudaSuccess) return e;
