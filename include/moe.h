@@ -677,8 +677,8 @@ int moe_kv4_set_cache(moe_kv4 *plan, uint8_t *cache);
 int moe_kv4_set_sinks(moe_kv4 *plan, const float *sinks);
 size_t moe_kv4_workspace_bytes(const moe_kv4 *plan);
 int moe_kv4_set_workspace(moe_kv4 *plan, void *dev_ptr, size_t bytes);
-/* n_tokens tokens' keys and values (bf16, as moe_kv8_append takes them) into
- * the cache at slots (int32, device), in any order.  A slot outside 0 ..
+/* n_tokens (at most 2^30) tokens' keys and values (bf16, as moe_kv8_append
+ * takes them) into the cache at slots (int32, device), in any order.  A slot outside 0 ..
  * n_pages * P - 1 appends nothing; of one that a call names twice the contents
  * are unspecified.  A block's scale and codes are those of moe_mx_quantize_fp4
  * (k = ceil(log2(amax / 6)), the nearest E2M1 value to x / 2^k, ties to the
@@ -689,12 +689,15 @@ int moe_kv4_append(moe_kv4 *plan, const uint16_t *k, const uint16_t *v, long lon
 /* What the cache holds at slots (int32, device), as bf16 rows (exact) of the
  * form that append takes; k and v must not overlap (they may be places of the
  * same rows, at one stride).  Rows of slots outside 0 .. n_pages * P - 1 are
- * left as they are.  A scale byte that no append writes, 0 or above 252, counts
- * as a scale of 0 or as 252, here and in moe_kv4_attend. */
+ * left as they are.  Of a scale byte that no append writes, 0 counts as a scale
+ * of 0 and one above 252 as 252. */
 int moe_kv4_read(moe_kv4 *plan, const int32_t *slots, int n_tokens, uint16_t *k, uint16_t *v, long long k_stride,
                  long long v_stride, void *stream);
 /* Attention of new tokens over the cache: all of moe_kv8_attend's arguments,
- * rules and limits. */
+ * rules and limits.  What a row does not see does not touch its result,
+ * whatever codes and scale bytes lie there; a token that it sees must have been
+ * appended (one of zero bytes counts as zeros).  Weights are held in 11 bits or
+ * more, for many rows (the kernel for prompts) in 8, sums in 32. */
 int moe_kv4_attend(moe_kv4 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
                    const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
                    long long out_stride, void *stream);

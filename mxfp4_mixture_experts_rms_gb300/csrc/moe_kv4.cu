@@ -254,7 +254,7 @@ int moe_kv4_append(moe_kv4 *p, const uint16_t *k, const uint16_t *v, long long k
                    const int32_t *slots, int n_tokens, void *stream) {
     if (!p) return moe_fail_status(MOE_EINVAL, "NULL plan");
     if (!p->c.c) return moe_fail_status(MOE_ENOTREADY, "moe_kv4_set_cache has not been called");
-    if (n_tokens < 0) return moe_fail_status(MOE_EINVAL, "n_tokens must be >= 0");
+    if (n_tokens < 0 || n_tokens > (1 << 30)) return moe_fail_status(MOE_EINVAL, "n_tokens must be 0..2^30");
     if (n_tokens == 0) return MOE_OK;
     const int rc = rows_check(p, k, v, k_stride, v_stride, slots);
     if (rc) return rc;
@@ -268,7 +268,7 @@ int moe_kv4_read(moe_kv4 *p, const int32_t *slots, int n_tokens, uint16_t *k, ui
                  void *stream) {
     if (!p) return moe_fail_status(MOE_EINVAL, "NULL plan");
     if (!p->c.c) return moe_fail_status(MOE_ENOTREADY, "moe_kv4_set_cache has not been called");
-    if (n_tokens < 0) return moe_fail_status(MOE_EINVAL, "n_tokens must be >= 0");
+    if (n_tokens < 0 || n_tokens > (1 << 30)) return moe_fail_status(MOE_EINVAL, "n_tokens must be 0..2^30");
     if (n_tokens == 0) return MOE_OK;
     const int rc = rows_check(p, k, v, k_stride, v_stride, slots);
     if (rc) return rc;

@@ -4,6 +4,7 @@
 #include "moe_kv4.cuh"
 
 #include <algorithm>
+#include <climits>
 
 namespace {
 
@@ -32,13 +33,13 @@ namespace {
 // whose nibbles two masks bring side by side.  Weights come out of the scores'
 // layout by movmatrix.
 //
-// Softmax, per row, in units of log2: m at least every score so far, moved (to 4
-// above the largest) only when one passes it, so that the common step has no
-// exchange between lanes; l the sum of the weights w = 2^(s - m) <= 1.  The
-// accumulator of a block of values holds sum w 2^(15 + e - E) code over tokens
-// with scale 2^e, E the largest e so far, for all rows the same.  Where the e of
-// 32 tokens are all within 4 of E, w 2^(15 + e - E) is the fp16 operand: the row's
-// largest is then at least 2^6 and the others keep 11 bits down to 2^-20 of it.
+// Softmax, per row, in units of log2: weights w = 2^(s - m) <= 2^15, l their sum.
+// m moves (to 11 below the largest score) only when a score is more than 15 above
+// it, so that the common step has no exchange between lanes.  The accumulator of a
+// block of values holds sum w 2^(e - E) code over tokens with scale 2^e, E the
+// largest e so far, for all rows the same.  Where the e of 32 tokens are all within
+// 4 of E, w 2^(e - E) is the fp16 operand: the row's largest is then at least 2^7
+// and the others keep 11 bits down to 2^-21 of it.
 // Where they are not, tokens are multiplied in classes of e within 4 of one
 // another, each with its own reference, and added in fp32.
 // q is scaled per row by a power of two into fp16's range: exact for a bf16
@@ -49,7 +50,7 @@ namespace {
 // given to four at a time).
 template <int D, int P, int RT>
 struct Few {
-    static constexpr int kWarps = D == 64 ? 16 : (RT == 1 ? (P == 32 ? 16 : 12) : 8);
+    static constexpr int kWarps = D == 64 ? (RT == 2 && P == 16 ? 12 : 16) : RT == 2 ? 8 : P == 32 ? 16 : 12;
     static constexpr int kStages = D == 128 ? 1 : 2;
     static constexpr int kStage = kTile * D / 16 * 17;   // bytes of one unit
     static constexpr int kPad = D + 8;                   // floats of a partial's row
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                     for (int i = 0; i < 8 * HV; i++) s[x][i >> 1][i & 1] = __fmul_rn(s[x][i >> 1][i & 1], rs[x][i & 1]);
             };
             if (large) to_scores();
-            // a score above m: m moves
+            // a score too far above m: m moves
             float mx[RT][2];
             bool above = false;
 #pragma unroll
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                     mx[x][c] = fmaxf(fmaxf(s[x][0][c], s[x][1][c]), fmaxf(s[x][2][c], s[x][3][c]));
                     if (HV == 2) mx[x][c] = fmaxf(mx[x][c], fmaxf(fmaxf(s[x][4 * HV - 4][c], s[x][4 * HV - 3][c]), fmaxf(s[x][4 * HV - 2][c], s[x][4 * HV - 1][c])));
                     if (!large) mx[x][c] = __fmul_rn(mx[x][c], rs[x][c]);
-                    above |= mx[x][c] > m[x][c];
+                    above |= mx[x][c] - m[x][c] > 15.f;   // (-inf less -inf is not)
                 }
             if (__any_sync(0xffffffffu, above)) {
                 bool far = false;
@@ -486,8 +487,9 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
-                        if (q > m[x][c]) {
-                            const float to = q + 4.f, corr = ex2(m[x][c] - to);
+                        if (q - m[x][c] > 15.f) {
+                            const float near = q - 11.f, to = q - near > 15.f ? q : near;   // (where its rounding is 16)
+                            const float corr = ex2(m[x][c] - to);
                             l[x][c] *= corr, m[x][c] = to;
 #pragma unroll
                             for (int b = 0; b < NB; b++)
@@ -501,13 +503,13 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                     to_scores();
                 }
             }
-            uint32_t p[RT][4 * HV];   // weights times 2^15, of row g: tokens 8 n + 2 t4, + 1
+            uint32_t p[RT][4 * HV];   // weights, of row g: tokens 8 n + 2 t4, + 1
 #pragma unroll
             for (int x = 0; x < RT; x++) {
                 float w[4 * HV][2];
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    const float k = large ? 1.f : rs[x][c], ms = m[x][c] == -INFINITY ? 0.f : m[x][c] - 15.f;
+                    const float k = large ? 1.f : rs[x][c], ms = m[x][c] == -INFINITY ? 0.f : m[x][c];
                     float sum = 0.f;
 #pragma unroll
                     for (int n = 0; n < 4 * HV; n++) sum += w[n][c] = ex2(fmaf(s[x][n][c], k, -ms));
@@ -608,7 +610,7 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                         uint16_t *o = a.out + (long long)(row0 + rr / f.G) * a.o_stride + head * D + 4 * g;
 #pragma unroll
                         for (int b = 0; b < NB; b++) {
-                            const float2 k = row_factor(m[x][c] - 15.f, l[x][c], N[b], sink);
+                            const float2 k = row_factor(m[x][c], l[x][c], N[b], sink);
                             auto put = [&](float y, float z) {
                                 const __nv_bfloat162 v = __floats2bfloat162_rn(y * k.x * k.y, z * k.x * k.y);
                                 return *reinterpret_cast<const uint32_t *>(&v);
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                             *reinterpret_cast<float4 *>(to + r * PAD + 32 * b + 4 * g) = make_float4(acc[b][0][x][c], acc[b][1][x][c], acc[b][0][x][2 + c], acc[b][1][x][2 + c]);
                         float *ml = to + R * PAD + r;
                         if (g == 0) {
-                            ml[0] = m[x][c] - 15.f, ml[R] = l[x][c];   // l is of weights times 2^15
+                            ml[0] = m[x][c], ml[R] = l[x][c];
 #pragma unroll
                             for (int b = 0; b < NB; b++) ml[(2 + b) * R] = N[b];
                         }
@@ -791,8 +793,24 @@ static size_t partial_bytes(int D) { return (size_t)(D == 64 ? Few<64, 16, kMost
 size_t kv4_workspace_bytes(int D) { return kPartOffset + (size_t)kMaxCtas * (2 + kMaxWarps) * partial_bytes(D); }
 
 cudaError_t launch_kv4_attend(const Kv4Attend &a, unsigned char *ws, cudaStream_t st) {
+    // The streaming kernel's work grows by the unit of 16 rows, that of the kernel
+    // for prompts by 256 rows a CTA, which walks all keys.  Per 64 tokens of a
+    // kv head the first takes 0.23 us of an SM a unit (dims of 64; 0.44 with 128),
+    // the second 0.75 to 1.0 (0.95 to 1.1) a CTA of up to 128, 256 rows, in as many
+    // waves as its CTAs take; some 10 us are the joins'.  us with the first and the
+    // second, 8 kv heads of 64: one sequence of 32 K tokens, 128 rows 65 and 366,
+    // 512 rows 199 and 498; 4 of 8 K, 256 rows 112 and 130, 512 rows 205 and 129; 32
+    // of 4 K, 48 rows 93 and 116, 64 rows 116 and 109.  Of 128: one of 32 K, 512
+    // rows 385 and 558; 8 of 4 K, 40 rows 67 and 65, 64 rows 80 and 66.
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     const int G = a.QH / a.c.KVH;
-    if ((long long)a.max_new * G <= 64) {
+    const long long rows = (long long)a.max_new * G, heads = (long long)a.n_seqs * a.c.KVH, tiles = (rows + 15) / 16;
+    const long long waves = (heads * ((rows + 255) / 256) + sms - 1) / sms;
+    const int tenths = a.c.D == 64 ? (rows <= 128 ? 30 : 40) : (rows <= 128 ? 16 : 21);
+    const bool countable = ((long long)a.width * a.c.P / kTile + 2) * tiles * heads <= INT_MAX;   // the first's units
+    if (rows <= 16 || (countable && 10 * heads * tiles < waves * sms * tenths)) {
         FewArgs f{};
         f.a = a, f.G = G;
         f.status = reinterpret_cast<int32_t *>(ws);
@@ -800,11 +818,8 @@ cudaError_t launch_kv4_attend(const Kv4Attend &a, unsigned char *ws, cudaStream_
         f.seqs = reinterpret_cast<int *>(ws + kKv8ClearBytes);
         f.parts = reinterpret_cast<float *>(ws + kPartOffset);
         f.heads = reinterpret_cast<float *>(ws + kPartOffset + (size_t)kMaxCtas * 2 * partial_bytes(a.c.D));
-        int ctas = 0;
-        const cudaError_t e = sm_count(&ctas);
-        if (e != cudaSuccess) return e;
-        ctas = std::min(ctas, kMaxCtas);
-        return a.c.D == 64 ? few_page<64>(f, a.max_new * G, ctas, st) : few_page<128>(f, a.max_new * G, ctas, st);
+        const int ctas = std::min(sms, kMaxCtas), r = (int)std::min(rows, (long long)16);
+        return a.c.D == 64 ? few_page<64>(f, r, ctas, st) : few_page<128>(f, r, ctas, st);
     }
     return launch_kv4_prompt(a, reinterpret_cast<int32_t *>(ws), st);
 }

@@ -133,8 +133,8 @@ def attend(cache, P, q, starts, lens, table, window=0, sinks=None, scale=None, w
     moves numerator and denominator by at most A times it; `weight` for the rounding of p (half a step: 2^-11 and the
     power of two's own error in fp16, 2^-8 in bf16), and as much again for the sums; 2^-18 where 2 weight is nothing.
     F = max_t (p_t 2^(e_t)) sum_t |code_td| over a block of 32 dims, with e_t the token's exponent: fp16 weights
-    2^(s - m + 15 + e_t - E), E at most 4 above e_t, m at most 4 above the largest score so far, so 2^7 at least for the
-    token of that score; below 2^-14 they are off by up to half of fp16's smallest step, 2^-25: 2^-32 of the largest,
+    2^(s - m + e_t - E), E at most 4 above e_t, m at most 11 below the largest score when it was set and never more than
+    15 below one since, so 2^7 at least for the token of the largest score; below 2^-14 they are off by up to half of fp16's smallest step, 2^-25: 2^-32 of the largest,
     doubled for parts with references of their own.
     The last term: tokens of scales 2^126 below the largest add nothing, as fp32 ends there; 2^-120 for their number."""
     D, H = q.shape[2], q.shape[1]

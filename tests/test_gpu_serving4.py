@@ -34,7 +34,7 @@ def bf16(x):
 
 def close(got, ref, tol):
     nan = np.isnan(ref)
-    assert np.array_equal(np.isnan(got), nan)
+    assert not (np.isnan(got) != nan).any()
     far = (np.abs(got - ref) / tol)[~nan]
     assert not far.size or far.max() <= 1, far.max()
 
@@ -204,6 +204,16 @@ def test_append_odd_values_and_the_codes_of_the_activation_encoder():
 
 # ---------------------------------------------------------------- attention
 
+def for_prompts(seqs, kv, H, most, D):
+    """Does the kernel for prompts take a call (weights in bf16), or that for a few new tokens (in fp16)?  By the rule that the
+    choice is made by; where it is told otherwise a test fails by its tolerance or tests less."""
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows, heads = most * (H // kv), seqs * kv
+    tenths = (30 if rows <= 128 else 40) if D == 64 else (16 if rows <= 128 else 21)
+    return rows > 16 and 10 * heads * -(-rows // 16) >= -(-heads * -(-rows // 256) // sms) * sms * tenths
+
+
 def sequences(rng, P, lens, width, pages, kv, D, poison=True, **cache):
     """A cache with each sequence's tokens on pages of its own, anything everywhere else."""
     c = random_cache(rng, pages, kv, P, D, **cache)
@@ -226,7 +236,7 @@ def sequences(rng, P, lens, width, pages, kv, D, poison=True, **cache):
 
 
 def check_attend(rng, P, D, kv, H, lens, rows, window=0, sinks=True, width=None, pages=None, scale=None, spread=0.25,
-                 max_new=None, extra=0, poison=True, change=None, **cache):
+                 max_new=None, extra=0, poison=True, change=None, prompts=None, **cache):
     import torch
     lens, rows = list(lens), list(rows)
     width = width or max(1, -(-max(lens) // P))
@@ -243,7 +253,8 @@ def check_attend(rng, P, D, kv, H, lens, rows, window=0, sinks=True, width=None,
     out = torch.full((n, H, D), 7.5, dtype=torch.bfloat16, device="cuda")
     one = all(r == 1 for r in rows) and extra == 0
     most = max_new if max_new is not None else max(rows + [1])
-    many = most * (H // kv) > 64                         # of a kv head: the kernel for prompts, weights in bf16
+    many = for_prompts(len(lens), kv, H, most, D)        # weights in bf16
+    assert prompts is None or prompts == many
     for use in ([False, True] if one else [True]):      # with and without starts
         out.fill_(7.5)
         plan.attend(qd, dev(np.array(lens, np.int32)), dev(table), out, starts=dev(starts) if use else None, max_new=most)
@@ -283,6 +294,29 @@ def test_attend_several_tokens_a_sequence(P, D, kv, H):
     check_attend(rng, P, D, kv, H, [70, 33, 150, 9, 260], [70, 1, 37, 9, 130], sinks=False)       # prompts
 
 
+@pytest.mark.parametrize("P", [16, 32, 64])
+@pytest.mark.parametrize("D,kv,H,most", [(64, 8, 16, 100), (64, 2, 32, 200), (128, 8, 8, 17), (128, 4, 20, 40), (128, 1, 16, 260)])
+def test_attend_prompts(P, D, kv, H, most):
+    rng = np.random.default_rng(P + H + most)
+    n = {(64, 16): 6, (64, 32): 5, (128, 8): 31, (128, 20): 9, (128, 16): 6}[D, H]
+    rows = np.minimum(rng.integers(1, most + 1, n), rng.integers(1, 60, n))      # (the oracle is slow)
+    rows[0] = most
+    lens = rows + rng.integers(0, 150, n)
+    lens[0] = most
+    lens[1], rows[1] = rows[1] // 2, rows[1]                                     # rows before the sequence's beginning
+    check_attend(rng, P, D, kv, H, lens, rows, max_new=most, prompts=True, sinks=bool(P % 64))
+    check_attend(rng, P, D, kv, H, lens, rows, max_new=most, prompts=True, window=37, extra=3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_many_rows_over_few_keys_and_the_other_way_round(D):
+    # one sequence: the streaming kernel whatever its rows
+    rng = np.random.default_rng(D)
+    check_attend(rng, 32, D, 1, 8, [700], [90], prompts=False)
+    check_attend(rng, 32, D, 1, 16, [90], [90], prompts=False, window=20)
+    check_attend(rng, 16, D, 2, 2, [500, 30], [300, 7], prompts=False)
+
+
 def test_attend_long_contexts_and_many_sequences():
     rng = np.random.default_rng(11)
     check_attend(rng, 64, 64, 1, 8, [9000], [1])                       # one sequence over the whole GPU
@@ -314,7 +348,7 @@ def test_attend_lengths_and_starts_out_of_range(rows):
     # a length below 0 is none; the sequence between keeps its own
     plan.attend(qd, dev(np.array([-2 ** 31, 64, -5], np.int32)), dev(table), out, starts=dev(starts), max_new=max(rows))
     got = out.double().cpu().numpy()
-    close(got, *S4.attend(c, P, q, starts, [0, 64, 0], table, weight=2.0 ** -8))
+    close(got, *S4.attend(c, P, q, starts, [0, 64, 0], table))
     assert np.all(got[:starts[1]] == 0) and np.all(got[starts[2]:] == 0)
     # starts past the rows, before them and going back: nothing outside out's rows is written
     guard = torch.full((n + 40, H, D), 7.5, dtype=torch.bfloat16, device="cuda")
@@ -388,7 +422,7 @@ def test_attend_queries_that_are_not_finite_or_far_apart(rows):
     plan.attend(qd, dev(np.array(lens, np.int32)), dev(table), out, starts=dev(starts), max_new=max(rows))
     got = out.double().cpu().numpy()
     q[0, 1], q[1, 2] = 0, 0
-    ref, tol = S4.attend(c, P, q, starts, lens, table, weight=2.0 ** -8)
+    ref, tol = S4.attend(c, P, q, starts, lens, table)
     assert np.isnan(got[0, 1]).all() and np.isnan(got[1, 2]).all()
     got[0, 1], got[1, 2], ref[0, 1], ref[1, 2] = 0, 0, 0, 0
     close(got, ref, tol)
@@ -618,3 +652,100 @@ def test_verify_in_a_graph_and_on_two_streams():
         one, other = ids.clone(), (z(10) + 77, z(3))
         made[1][0].run(xd, dd, u, w, sd, *other, draft_probs=qd, top_k=k)
         assert torch.equal(one, other[0]) and torch.equal(acc, other[1])
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("D,H,kv", [(64, 16, 2), (128, 6, 2)])
+def test_a_run_with_drafted_tokens_and_its_graph(D, H, kv):
+    """Requests decode with drafted tokens: each step assigns pages, turns queries and keys, appends, attends, verifies, and
+    goes on behind the tokens that were accepted.  The whole run once call by call and once as a captured step replayed."""
+    import torch
+    m = moe()
+    P, n, W, V, steps, most, pages = 16, 5, 12, 300, 7, 5, 80
+    cap = n * most + 3
+    rng = np.random.default_rng(D)
+    rows_of = [rng.integers(1, most + 1, n) for _ in range(steps)]                # the drafts and one more
+    xs = [bf16(rng.normal(0, 1, (cap, H + 2 * kv, D)))[0] for _ in range(steps)]
+    extra = [[rng.random(cap), rng.random(n), rng.integers(0, V, cap)] for _ in range(steps)]
+    head = rng.normal(0, 0.3, (H * D, V)).astype(np.float32)
+    gamma, freqs = rng.normal(1, 0.1, (2, D)).astype(np.float32), 1e4 ** (-np.arange(D // 2) / (D // 2))
+
+    def run(graph):
+        z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device="cuda")   # noqa: E731
+        cache = m.Kv4(H, kv, D, P, pages, sliding_window=40)
+        rotary, verify = m.Rotary(D, freqs, q_gamma=dev(gamma[0]), k_gamma=dev(gamma[1])), m.Verify(cap)
+        free, counts, table = dev(np.arange(pages, dtype=np.int32)), dev(np.array([pages, 0], np.int32)), z(n, W)
+        have, fresh, lens, starts, slots, pos = z(n), z(n), z(n), z(n + 1), z(cap), z(cap)
+        x, q, k = z(cap, H + 2 * kv, D, t=torch.bfloat16), z(cap, H, D, t=torch.bfloat16), z(cap, kv, D, t=torch.bfloat16)
+        out, logits, hd = z(cap, H, D, t=torch.bfloat16), z(cap, V, t=torch.float32), dev(head)
+        u, draws, drafts, ids, accepted = z(cap, t=torch.float32), z(n, t=torch.float32), z(cap), z(cap), z(n)
+
+        def step():
+            m.pages_assign(P, have, fresh, free, counts, counts, table, starts, lens, slots, pos)
+            rotary.apply(x[:, :H], x[:, H:H + kv], pos, q, k)
+            cache.append(k, x[:, H + kv:], slots)
+            cache.attend(q, lens, table, out, starts=starts, max_new=most)
+            torch.mm(out.view(cap, -1).float(), hd, out=logits)
+            verify.run(logits, drafts, u, draws, starts, ids, accepted, top_k=None, temperature=None)
+            have.add_(accepted + 1)
+
+        kept_ = (have, free, counts, table, cache.cache, q, k, out, ids)
+        seen, g = [], None
+        for s in range(steps):
+            fresh.copy_(dev(rows_of[s].astype(np.int32)))
+            x.copy_(xs[s])
+            u.copy_(dev(extra[s][0].astype(np.float32))), draws.copy_(dev(extra[s][1].astype(np.float32)))
+            drafts.copy_(dev(extra[s][2].astype(np.int32)))
+            if s % 2:      # drafted tokens that the last step's logits like best
+                drafts.copy_(logits.argmax(-1))
+            q.zero_(), k.zero_(), out.zero_(), ids.zero_()
+            if graph and g is None:
+                side = torch.cuda.Stream()
+                side.wait_stream(torch.cuda.current_stream())
+                old = [t.clone() for t in kept_]
+                with torch.cuda.stream(side):
+                    step()                                       # a first run outside the capture
+                torch.cuda.current_stream().wait_stream(side)
+                for t, c in zip(kept_, old):
+                    t.copy_(c)
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    step()
+            g.replay() if graph else step()
+            seen.append([t.cpu().numpy().copy() for t in (table, starts, lens, slots, pos, counts, cache.cache, ids, accepted, drafts, logits, have)] +
+                        [t.double().cpu().numpy() for t in (q, k, out)])
+        return seen
+
+    eager, replayed = run(False), run(True)
+    for a, b in zip(eager, replayed):
+        assert all(np.array_equal(x, y) for x, y in zip(a, b))
+    free, n_free, table, have = np.arange(pages, dtype=np.int32), pages, np.zeros((n, W), np.int32), np.zeros(n, np.int64)
+    cache = np.zeros((pages, kv, S4.page_bytes(P, D)), np.uint8)
+    for s in range(steps):
+        t, starts, lens, slots, pos, counts, c, ids, accepted, drafts, logits, after, q, k, out = eager[s]
+        r = S.pages_assign(P, have, rows_of[s], free, n_free, table, cap)
+        free, n_free, table = r["free"], int(r["counts"][0]), r["table"]
+        for got, want in ((t, table), (starts, r["starts"]), (lens, r["lens"]), (slots, r["slots"]), (pos, r["positions"]), (counts, r["counts"])):
+            assert np.array_equal(got, want), s
+        e, x = int(starts[-1]), xs[s].double().cpu().numpy()
+        for got, src, ga in ((q, x[:, :H], gamma[0]), (k, x[:, H:H + kv], gamma[1])):
+            ref, tol = S4.rotate(src[:e], pos[None, :e], freqs, gamma=ga)
+            close(got[:e], ref, tol)
+            assert np.all(got[e:] == 0)                          # rows of no token
+        cache = S4.append(cache, P, k, x[:, H + kv:], slots)
+        assert np.array_equal(c, cache), s
+        ref, tol = S4.attend(cache, P, q, starts, lens, table, 40)
+        close(out[:e], ref[:e], tol[:e])
+        for b in range(n):
+            a, z = int(starts[b]), int(starts[b + 1])
+            ps = [S4.probabilities(logits[i], 1.0, 0, 1.0, 0.0) for i in range(a, z)]
+            took, rest, near = S4.verify(ps, drafts[a:z], None, extra[s][0][a:z].astype(np.float32), extra[s][1][b])
+            assert accepted[b] == took or near < 2.0 ** -18
+            if accepted[b] == took:
+                assert np.array_equal(ids[a:a + took], drafts[a:a + took]) and np.all(ids[a + took + 1:z] == -1)
+                cum, got = np.cumsum(rest), ids[a + took]
+                share = float(np.float32(extra[s][1][b])) * cum[-1]
+                assert cum[got] - rest[got] - 2.0 ** -18 <= share <= cum[got] + 2.0 ** -18
+        have = have + accepted + 1
+        assert np.array_equal(after, have)

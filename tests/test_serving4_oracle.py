@@ -180,7 +180,7 @@ def test_kv4_refusals(L):
         assert L.moe_kv4_set_f(h, b"softmax_scale", v) == moe.MOE_EINVAL
     assert L.moe_kv4_set_sinks(h, P(0x1002)) == moe.MOE_EINVAL and L.moe_kv4_set_sinks(h, None) == moe.MOE_OK
     assert app(n=0) == moe.MOE_OK and rd(n=0) == moe.MOE_OK
-    for bad in (dict(n=-1), dict(k=None), dict(v=None), dict(sl=None), dict(k=0x10008), dict(sl=P(0x30002)),
+    for bad in (dict(n=-1), dict(n=2 ** 30 + 1), dict(k=None), dict(v=None), dict(sl=None), dict(k=0x10008), dict(sl=P(0x30002)),
                 dict(ks=120), dict(vs=132), dict(ks=127)):
         assert app(**bad) == moe.MOE_EINVAL and rd(**bad) == moe.MOE_EINVAL, bad
     assert rd(v=x) == moe.MOE_EINVAL and rd(v=x + 128) == moe.MOE_EINVAL and rd(v=x + 128, ks=256, vs=256) == moe.MOE_EINVAL
