@@ -12,8 +12,9 @@
 //
 // Sums are whole numbers of units of 2^-52, at least one where there is anything:
 // of a lane's tokens, summed in two fp32 parts.  (64-bit floats are the GPU's
-// slowest numbers: sums and quotients in them took two thirds of the second
-// kernel's 76 us at 64 sequences of 128 K logits.)
+// slowest numbers: with sums and quotients in them the second kernel took 76 us
+// at 64 sequences, 282 rows of 128 K logits, in place of 38; the first takes 100,
+// as moe_sample would.)
 #include "moe_sample.cuh"
 #include "../../include/moe.h"
 
@@ -323,6 +324,16 @@ int moe_verify(const void *logits, int is_bf16, int n_rows, int vocab, long long
     if ((uintptr_t)workspace & 15u) return moe_fail_status(MOE_EINVAL, "the workspace must be 16-byte aligned");
     if (workspace_bytes < moe_verify_workspace_bytes(n_rows))
         return moe_fail_status(MOE_ENOMEM, "workspace of %zu bytes, %zu needed", workspace_bytes, moe_verify_workspace_bytes(n_rows));
+    // what one sequence's CTAs write others may still have to read
+    auto clash = [](const void *x, long long nx, const void *y, long long ny) {   // of 4-byte elements
+        return x && y && (uintptr_t)x < (uintptr_t)y + 4 * ny && (uintptr_t)y < (uintptr_t)x + 4 * nx;
+    };
+    if (clash(ids, n_rows, accepted, n_seqs)) return moe_fail_status(MOE_EINVAL, "ids and accepted must not overlap");
+    const struct { const void *p; long long n; } in[] = {{drafts, n_rows}, {u, n_rows}, {starts, n_seqs + 1}, {draws, n_seqs}, {temperature, n_seqs},
+                                                         {top_k, n_seqs}, {top_p, n_seqs}, {min_p, n_seqs}};
+    for (const auto &x : in)
+        if (clash(x.p, x.n, ids, n_rows) || clash(x.p, x.n, accepted, n_seqs))
+            return moe_fail_status(MOE_EINVAL, "ids and accepted must not overlap an input");
     VerifyArgs a{};
     a.s.x = logits, a.s.rows = n_rows, a.s.V = vocab, a.s.stride = row_stride;
     a.s.temperature = temperature, a.s.top_k = top_k, a.s.top_p = top_p, a.s.min_p = min_p;

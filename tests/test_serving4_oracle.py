@@ -203,7 +203,9 @@ def test_verify_refusals(L):
     for bad in (dict(n=-1), dict(n=2 ** 24 + 1), dict(V=0), dict(V=2 ** 24 + 1, st=2 ** 25), dict(st=9), dict(qs=9), dict(bf=2), dict(B=-1),
                 dict(B=65537), dict(x=None), dict(d=None), dict(starts=None), dict(u=None), dict(w=None), dict(ids=None), dict(acc=None),
                 dict(ws=None), dict(x=P(0x10002)), dict(bf=1, x=P(0x10001)), dict(d=P(2)), dict(q=P(2)), dict(starts=P(1)), dict(t=P(2)),
-                dict(k=P(1)), dict(p=P(3)), dict(mp=P(2)), dict(u=P(2)), dict(w=P(2)), dict(ids=P(2)), dict(acc=P(2)), dict(ws=P(0x10008))):
+                dict(k=P(1)), dict(p=P(3)), dict(mp=P(2)), dict(u=P(2)), dict(w=P(2)), dict(ids=P(2)), dict(acc=P(2)), dict(ws=P(0x10008)),
+                dict(ids=a[1]), dict(ids=P(0x20000 + 20)), dict(d=P(a[10].value - 20)), dict(ids=a[8]), dict(ids=a[3]), dict(acc=P(a[3].value + 8)),
+                dict(acc=a[9]), dict(acc=a[4]), dict(acc=P(a[10].value + 20)), dict(acc=P(a[10].value - 4)), dict(ids=a[7])):
         assert call(**bad) == moe.MOE_EINVAL, bad
         assert L.moe_last_error()
     assert call(size=6 * 24 - 1) == moe.MOE_ENOMEM
