@@ -628,7 +628,7 @@ int moe_sample(const void *logits, int is_bf16, int n_rows, int vocab, long long
  *             positions[axes[i]][token] * freqs[i]
  * rounded once, to bf16; dims in no pair are x'.  Pairs are dims i and
  * i + n_pairs, or 2 i and 2 i + 1 (interleaved = 1).  Angles are exact to
- * 2^-32 of a turn at any position. */
+ * 2^-32 of a turn and 2^-52 of themselves, wherever the position is. */
 typedef struct moe_rotary moe_rotary;
 /* head_dim 64, 128 or 256; n_pairs a multiple of 8, 0 .. head_dim / 2; n_axes
  * 1 .. 4 (time, height and width of images and video, say).  Defaults: no
@@ -696,7 +696,8 @@ int moe_kv4_read(moe_kv4 *plan, const int32_t *slots, int n_tokens, uint16_t *k,
 /* Attention of new tokens over the cache: all of moe_kv8_attend's arguments,
  * rules and limits.  What a row does not see does not touch its result,
  * whatever codes and scale bytes lie there; a token that it sees must have been
- * appended (one of zero bytes counts as zeros).  Weights are held in 11 bits or
+ * appended (one of zero bytes counts as zeros).  A seen key's scale of 2^100 or
+ * more may count as a score beyond fp32's range.  Weights are held in 11 bits or
  * more, for many rows (the kernel for prompts) in 8, sums in 32. */
 int moe_kv4_attend(moe_kv4 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
                    const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
@@ -727,7 +728,8 @@ void moe_kv4_destroy(moe_kv4 *plan);
  * and -1 behind it; rows of no sequence are left as they are.  Of a sequence of
  * one row the token is drawn as moe_sample would.  Weights are fp32, sums
  * within 2^-20 of their totals.  draft_probs is read at and beside tokens that
- * p keeps, never at a sequence's last row.  The workspace (device, 16-byte aligned) holds
+ * p keeps, never at a sequence's last row.  ids and accepted overlap nothing
+ * else.  The workspace (device, 16-byte aligned) holds
  * nothing between calls; calls that can overlap on the GPU need one each. */
 size_t moe_verify_workspace_bytes(int n_rows);
 int moe_verify(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride, const int32_t *drafts,

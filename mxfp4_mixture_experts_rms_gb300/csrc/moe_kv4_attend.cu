@@ -11,14 +11,17 @@ namespace {
 // ---- few new tokens a sequence: keys and values streamed once ----
 //
 // The work is cut, shared out and joined as in the kernel for the 8-bit cache
-// (moe_kv8_attend.cu): units of 64 tokens, one kv head and up to 32 rows (new
+// (moe_kv8_attend.cu): units of 64 tokens, one kv head and 8 or 16 rows (new
 // tokens x the kv head's query heads) in order of (sequence, kv head, row tile,
 // tokens), a contiguous share of them for each CTA and each of its warps; what a
 // share cuts apart is joined in a fixed order.
 //
 // A unit's pages are one bulk copy each, codes and scales together.  What bounds
-// the kernel is the integer pipe that turns codes into fp16 (two cycles a pair,
-// by the hardware's conversion), so everything else is arranged to spare it:
+// long calls is not HBM but issue slots (55 % taken) and the integer pipe (50 %),
+// which turns codes into fp16 (two cycles a pair, by the hardware's conversion),
+// so everything else is arranged to spare them: 96 ragged sequences, 598 K tokens,
+// 20 / 4 heads of 128 take 89 us, 49 at HBM's rate.  Short ones are latencies: of
+// 16 x 4096 tokens, 64 / 8 heads of 64, the bytes are 5 us of 23.
 //  * Both products have the cache's side as their 16-row operand, keys [tokens]
 //    [dims] and values [dims][tokens], and eight rows of queries or weights as
 //    the other, so that nothing is multiplied that is no row; a unit may have
@@ -45,9 +48,11 @@ namespace {
 // q is scaled per row by a power of two into fp16's range: exact for a bf16
 // row's values down to 2^-28 of its largest.
 
-// RT: eights of rows of a unit.  Warps, and units in each one's ring: as many
-// warps as registers and shared memory allow (a multiple of 4: registers are
-// given to four at a time).
+// RT: eights of rows of a unit; three or four, with the 8 warps that registers
+// then allow, were slower than two units of two.  Warps, and units in each one's
+// ring: as many warps as registers and shared memory allow (a multiple of 4:
+// registers are given to four at a time; the ragged sequences above: 12 warps 99
+// us, 16 94, and with both halves of a unit computed together 89).
 template <int D, int P, int RT>
 struct Few {
     static constexpr int kWarps = D == 64 ? (RT == 2 && P == 16 ? 12 : 16) : RT == 2 ? 8 : P == 32 ? 16 : 12;
@@ -315,8 +320,9 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                 }
                 am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
                 am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-                const int up = min(141 - (int)(am >> 7), 127);
-                const float mul = pow2i(up), back = fmaxf(pow2i(-up) * sc, 1e-37f);   // > 0: a hidden token's -inf stays
+                // (not so far that what undoes it is below 2^-120: a factor of 0 or less bits would make scores wrong)
+                const int up = min(141 - (int)(am >> 7), min((int)(__float_as_uint(sc) >> 23) - 7, 126));
+                const float mul = pow2i(up), back = pow2i(-up) * sc;
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
                     const uint32_t y[4] = {w[b].x, w[b].y, w[b].z, w[b].w};

@@ -111,6 +111,21 @@ def test_attend_large_scores_among_usual_ones():
 
 
 @pytest.mark.parametrize("rows", [[1, 1], [3, 2], [40, 33]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale,spread,lo", [(1e-25, 2.0 ** -40, 224), (None, 2.0 ** -118, 224), (2e-30, 2.0 ** -6, 222), (1e20, 2.0 ** -100, 124)])
+def test_attend_small_queries_and_large_keys(rows, D, scale, spread, lo):
+    # a row's scale, undone, times softmax_scale is far below fp32's smallest number, the scores are not
+    rng = np.random.default_rng(17)
+
+    def change(c, table):
+        codes, scales = S4.unpack(c, 16, D)
+        scales[1] = rng.integers(120, 130, scales[1].shape)
+        return S4.pack(codes, scales)
+
+    base.check_attend(rng, 16, D, 2, 8, [300, 64], rows, scale=scale, spread=spread, lo=lo, hi=lo + 3, change=change, poison=False)
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [3, 2], [40, 33]])
 def test_append_read_and_attend_past_32_bit_offsets(rows):
     # the last pages of a cache of 4.9 GB: byte offsets past 2^32, against a cache of those pages alone
     import torch
