@@ -57,8 +57,8 @@ __device__ __forceinline__ void mul2(float &y0, float &y1, float x0, float x1, f
 }
 // A block of 32 codes with its scale -> 64 bytes of bf16, exact, by way of fp32:
 // the conversions' pipe is what bounds the decoders, and this takes it twice a
-// pair (four times with fp16's bits shifted to bf16's places: 104 us where this
-// takes 95).
+// pair (four times with fp16's bits shifted to bf16's places: 4 x 900 rows over
+// 2700 tokens took 104 us, this takes 87).
 __device__ __forceinline__ void decode32(uint4 codes, float scale, uint4 (&out)[4]) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
