@@ -27,12 +27,11 @@ namespace {
 
 template <int D>
 struct Smem {   // offsets from a 1024-byte boundary
-    static constexpr int kStages = D == 64 ? 4 : 3, kRaw = D == 64 ? 4 : 2;   // operand tiles; steps of copied pages
+    static constexpr int kStages = 4, kRaw = D == 64 ? 4 : 2;   // operand tiles; steps of copied pages
     static constexpr int kStep = kT * D / 16 * 17;          // bytes of one
     static constexpr int kQ = 0;
-    static constexpr int kQ1 = kM * D * 2;                  // of a half: Q [128][D], P [128][64]
-    static constexpr int kP = 2 * kQ1, kP1 = kM * kT * 2;
-    static constexpr int kK = kP + 2 * kP1;                 // kStages x [64][D]
+    static constexpr int kQ1 = kM * D * 2;                  // of a half [128][D]
+    static constexpr int kK = 2 * kQ1;                      // kStages x [64][D]
     static constexpr int kV = kK + kStages * kT * D * 2;    // kStages x [64][D]
     static constexpr int kCodes = kV + kStages * kT * D * 2; // kRaw x pages
     static constexpr int kBytes = kCodes + kRaw * kStep;
@@ -50,6 +49,22 @@ struct PromptArgs {
     int32_t *status;
 };
 
+// 32 columns of the thread's TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32}; tcgen05.wait::st.sync.aligned;" ::"r"(at),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+        "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+// The first operand from tensor memory: a lane a row, a column two of K.
+template <bool ACC>
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
+}
 // (x0, x1) * k.
 __device__ __forceinline__ void mul2(float &y0, float &y1, float x0, float x1, float k) {
     asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
@@ -82,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
     constexpr int kStages = L::kStages, kRaw = L::kRaw;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2], drain[2];
+    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2][2], drain[2];
     __shared__ uint32_t rmeta[kRaw], meta[kStages];   // the pages that are there
     __shared__ uint32_t tmem_slot;
     __shared__ int job[2];
@@ -92,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
         for (int s = 0; s < kStages; s++) bar_init(&full[s], kLoaders / 32), bar_init(&empty[s], 2);
         for (int s = 0; s < kRaw; s++) bar_init(&raw[s], 2), bar_init(&raw_empty[s], kLoaders / 32);
         for (int h = 0; h < 2; h++)
-            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], kSoftmax / 2), bar_init(&p_full[h], kSoftmax / 2), bar_init(&o_done[h], 1), bar_init(&drain[h], 1);
+            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], kSoftmax / 2), bar_init(&p_full[h], kSoftmax / 2), bar_init(&o_done[h][0], 1), bar_init(&o_done[h][1], 1), bar_init(&drain[h], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kIssuer) {
@@ -163,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                 const float sc = a.scale * kLog2e;
                 float m = -INFINITY, l = 0.f;
                 const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * h;
-                unsigned char *pt = smem + L::kP + h * L::kP1;
                 bool ok = true;
                 for (int j = 0; j < steps; j++) {
                     const int st = j % kStages, t0 = (step0 + j) * kT;
@@ -210,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                         for (int c = 0; c < kT; c++) s[c] = __fmul_rn(s[c], sc);
                         ks = 1.f;
                     }
-                    // the products of the step before have read the P tile
-                    if (j > 0) ok = bar_wait(&o_done[h], (uint32_t)(j - 1) & 1, status, 101) && ok;
                     if (__any_sync(0xffffffffu, move || !ok)) {
+                        // the accumulator is that of the step before
+                        if (j > 0) ok = bar_wait(&o_done[h][(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1, status, 101) && ok;
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         fence_after();
@@ -222,25 +236,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                         }
                     }
                     float s0 = 0.f, s1 = 0.f;
+                    uint32_t y[kT / 2];
 #pragma unroll
-                    for (int c = 0; c < kT; c += 8) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            float w0, w1;
-                            fma2(w0, w1, s[c + 2 * e], s[c + 2 * e + 1], ks, -ms);
-                            w0 = ex2(w0), w1 = ex2(w1);
-                            add2(s0, s1, w0, w1);
-                            y[e] = bits_of(__floats2bfloat162_rn(w0, w1));
-                        }
-                        *reinterpret_cast<uint4 *>(pt + swizzled(r, c / 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    for (int c = 0; c < kT / 2; c++) {
+                        float w0, w1;
+                        fma2(w0, w1, s[2 * c], s[2 * c + 1], ks, -ms);
+                        w0 = ex2(w0), w1 = ex2(w1);
+                        add2(s0, s1, w0, w1);
+                        y[c] = bits_of(__floats2bfloat162_rn(w0, w1));
                     }
                     l += s0 + s1;
-                    fence_async();
+                    tmem_st32(lanes + (j & 1) * kT, y);   // over the scores
                     fence_before();
                     bar_arrive_warp(&p_full[h]);
                 }
-                if (ok) ok = bar_wait_warp(&o_done[h], (uint32_t)(steps - 1) & 1, status, 102);
+                if (ok) ok = bar_wait_warp(&o_done[h][(steps - 1) & 1], (uint32_t)((steps - 1) >> 1) & 1, status, 102);
                 if (ok) {
                     fence_after();
                     // (the row anew, so that no registers hold it meanwhile)
@@ -335,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
         } else {
             // ---- a half's products: the warp together, so that descriptors stay in uniform registers; one lane issues ----
             const int h = warp - kIssuer;
-            const uint64_t Q = tile_desc(smem_u32(smem + L::kQ + h * L::kQ1)), Pt = tile_desc(smem_u32(smem + L::kP + h * L::kP1));
+            const uint64_t Q = tile_desc(smem_u32(smem + L::kQ + h * L::kQ1));
             const uint64_t K0 = tile_desc(smem_u32(smem + L::kK)), V0 = turned_desc(smem_u32(smem + L::kV));
             const uint32_t S = tmem + 256 * h, O = S + 2 * kT;
             constexpr uint64_t kTile16 = kT * D * 2 / 16;   // descriptors count 16 bytes
@@ -362,21 +372,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
             if (ok) ok = scores(0, 0, 0);
             for (int j = 0; j < steps && ok; j++, st = st1) {
                 if (++st1 == kStages) st1 = 0, par1 ^= 1;
-                // the next scores go ahead of this step's values: their buffer was read before step j - 1's weights were
-                if (j + 1 < steps) ok = scores(j + 1, st1, par1);
+                // the next scores go ahead of this step's values: into the columns of step j - 1's weights, once its products are done
+                if (j > 0) ok = bar_wait_warp(&o_done[h][(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1, status, 111);
+                if (ok && j + 1 < steps) ok = scores(j + 1, st1, par1);
                 if (ok) ok = bar_wait_warp(&p_full[h], (uint32_t)j & 1, status, 106);
                 if (!ok) break;
                 fence_after();
                 const uint64_t V = V0 + st * kTile16;
                 if (elect_one()) {
                     // 16 tokens are two groups of eight rows of the tile, 1024 bytes each
-                    if (j == 0) mma<false>(O, Pt, V, inst_desc(D, true, true));
-                    else mma<true>(O, Pt, V, inst_desc(D, true, true));
+                    const uint32_t W = S + (j & 1) * kT;
+                    if (j == 0) mma_tmem<false>(O, W, V, inst_desc(D, true, true));
+                    else mma_tmem<true>(O, W, V, inst_desc(D, true, true));
 #pragma unroll
-                    for (int c = 1; c < kT / 16; c++) mma<true>(O, Pt + c * 2, V + c * 128, inst_desc(D, true, true));
+                    for (int c = 1; c < kT / 16; c++) mma_tmem<true>(O, W + c * 8, V + c * 128, inst_desc(D, true, true));
                     commit(&empty[st]);
                     if (halves == 1) commit(&empty[st]);   // the other half's
-                    commit(&o_done[h]);   // (last: the one that is waited for before the CTA ends)
+                    commit(&o_done[h][j & 1]);   // (last: the one that is waited for before the CTA ends)
                 }
                 __syncwarp();
             }
