@@ -22,6 +22,7 @@
 #include "moe_kv4.cuh"
 
 #include <algorithm>
+#include <climits>
 
 namespace {
 
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
     __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2][2], drain[2];
     __shared__ uint32_t rmeta[kRaw], meta[kStages];   // the pages that are there
     __shared__ uint32_t tmem_slot;
-    __shared__ int job[2];
+    __shared__ int job[5];   // sequence (-1: none), tile, and the sequence's first row, rows, first position
     const Kv4Attend &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kvh = blockIdx.x % a.c.KVH;
     if (tid == 0) {
@@ -116,29 +117,59 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
-        // a tile of 256 rows: sequences in order, a sequence's last (longest)
-        // tile first, its heads together, so that the last to start are short
-        int x = blockIdx.x / a.c.KVH, found = -1, rt = 0;
-        for (int b0 = 0; b0 < a.n_seqs && found < 0; b0 += 32) {
-            int row0, n = 0, pos0;
-            if (b0 + lane < a.n_seqs) kv8_rows(a, b0 + lane, row0, n, pos0);
-            const int mine = (n * f.G + 2 * kM - 1) / (2 * kM);
-            int inc = mine;
+        // a tile of 256 rows, its heads together
+        int x = blockIdx.x / a.c.KVH, found = -1, rt = 0, row0 = 0, n = 0, pos0 = 0;
+        auto take = [&](int at, int tile) {   // lane at's sequence
+            found = at, rt = __shfl_sync(0xffffffffu, tile, at);
+            row0 = __shfl_sync(0xffffffffu, row0, at), n = __shfl_sync(0xffffffffu, n, at), pos0 = __shfl_sync(0xffffffffu, pos0, at);
+        };
+        auto running = [&](int v) {
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
+                const int y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, x < inc);
-            if (hit) {
-                const int at = __ffs(hit) - 1;
-                found = b0 + at;
-                rt = __shfl_sync(0xffffffffu, inc, at) - 1 - x;
-            } else {
-                x -= __shfl_sync(0xffffffffu, inc, 31);
+            return v;
+        };
+        if (a.n_seqs <= 32) {
+            // the x-th by the steps up to its last row, longest first, so that the last to start are short (4 x 900 rows over
+            // 2700 tokens: 78 us; in the order below 78 to 85, as the sequences come)
+            if (lane < a.n_seqs) kv8_rows(a, lane, row0, n, pos0);
+            const int rows = n * f.G, tiles = (rows + 2 * kM - 1) / (2 * kM);
+            auto longer = [&](int k) {   // how many of the lane's have more than k + 1 steps (all: k < 0)
+                const long long r = k < 0 ? 0 : max(((long long)(k + 1) * kT - pos0) * f.G, 0ll);   // the first row that reaches as far
+                return r >= rows ? 0 : tiles - (int)(r / (2 * kM));
+            };
+            if (__reduce_add_sync(0xffffffffu, tiles) > x) {
+                // the least k that no more than x are longer than
+                int lo = -1, hi = (int)((long long)a.width * P / kT) + 1;
+                if (__reduce_add_sync(0xffffffffu, longer(hi)) > x) lo = hi, hi = INT_MAX / kT;   // (positions past the table)
+                while (hi - lo > 1) {
+                    const int mid = lo + (hi - lo) / 2;
+                    if (__reduce_add_sync(0xffffffffu, longer(mid)) > x) lo = mid;
+                    else hi = mid;
+                }
+                const int more = longer(hi), mine = longer(hi - 1) - more;
+                x -= __reduce_add_sync(0xffffffffu, more);
+                const int inc = running(mine);
+                take(__ffs(__ballot_sync(0xffffffffu, x < inc)) - 1, tiles - more - 1 - (x - (inc - mine)));
+            }
+        } else {
+            // sequences in order, a sequence's last (longest) tile first
+            for (int b0 = 0; b0 < a.n_seqs && found < 0; b0 += 32) {
+                n = 0;
+                if (b0 + lane < a.n_seqs) kv8_rows(a, b0 + lane, row0, n, pos0);
+                const int inc = running((n * f.G + 2 * kM - 1) / (2 * kM));
+                const unsigned hit = __ballot_sync(0xffffffffu, x < inc);
+                if (hit) {
+                    take(__ffs(hit) - 1, inc - 1 - x);
+                    found += b0;
+                } else {
+                    x -= __shfl_sync(0xffffffffu, inc, 31);
+                }
             }
         }
-        if (lane == 0) job[0] = found, job[1] = rt;
+        if (lane == 0) job[0] = found, job[1] = rt, job[2] = row0, job[3] = n, job[4] = pos0;
     }
     fence_before();
     __syncthreads();
@@ -149,8 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
     const uint32_t tmem = tmem_slot;
     const int b = job[0];
     if (b >= 0) {
-        int row0, n, pos0;
-        kv8_rows(a, b, row0, n, pos0);
+        const int row0 = job[2], n = job[3], pos0 = job[4];
         const int r0 = job[1] * 2 * kM, rows = min(2 * kM, n * f.G - r0), halves = rows > kM ? 2 : 1;
         const int p_first = pos0 + r0 / f.G, p_last = pos0 + (r0 + rows - 1) / f.G;
         // tokens that any row sees, and the steps over them (aligned to 64)
@@ -169,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                 const int to = on ? min(seen - 1, pos0 + i2) : -1, from = kv8_first(pos0 + i2, a.window);
                 {
                     const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (long long)(row0 + i2) * a.q_stride + head * D);
-#pragma unroll 8
+#pragma unroll
                     for (int c = 0; c < D / 8; c++)
                         *reinterpret_cast<uint4 *>(smem + L::kQ + h * L::kQ1 + (c / 8) * (kM * 128) + swizzled(r, c % 8)) = on ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
                     fence_async();
@@ -257,8 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                     uint32_t r;
                     asm volatile("mov.u32 %0, %%tid.x;" : "=r"(r));
                     r &= kM - 1;
-                    int row0, n, pos0;
-                    kv8_rows(a, *(volatile int *)&job[0], row0, n, pos0);
+                    const int row0 = *(volatile int *)&job[2], n = *(volatile int *)&job[3];
                     const int rr = (*(volatile int *)&job[1] * 2 + h) * kM + (int)r, i2 = rr / f.G, head = kvh * f.G + rr - i2 * f.G;
                     const bool on = rr < n * f.G;
                     const float sink = on && a.sinks ? a.sinks[head] * kLog2e : -INFINITY;

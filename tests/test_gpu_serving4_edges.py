@@ -95,6 +95,26 @@ def test_attend_large_scores(rows, kv, H, P, D, lo):
     base.check_attend(rng, P, D, kv, H, lens, rows, lo=lo, hi=lo + 3, change=change, spread=4.0, window=70, poison=False, prompts=many)
 
 
+@pytest.mark.parametrize("D,most", [(64, 12), (128, 6)])
+def test_attend_prompts_of_more_sequences_than_lanes(D, most):
+    rng = np.random.default_rng(18)
+    rows = np.minimum(rng.integers(0, most + 1, 40), 3)
+    rows[[5, 39]] = most
+    check = lambda lens, **kw: base.check_attend(rng, 16, D, 8, 64, lens, rows, max_new=most, prompts=True, **kw)
+    check(rows + rng.integers(0, 90, 40))
+    check(rows + rng.integers(-2, 200, 40).clip(0), window=50)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("width", [None, 3, 9])
+def test_attend_prompts_of_equal_sequences_and_past_the_table(D, width):
+    # tiles of the same length, of none, and of more tokens than their table has
+    rng = np.random.default_rng(19)
+    rows = [33, 33, 0, 33, 1, 33, 70] + [33] * 13
+    lens = [160, 160, 160, 20, 160, 160, 300] + [160] * 12 + [0]
+    base.check_attend(rng, 16, D, 8, 64, lens, rows, width=width, max_new=70, prompts=True)
+
+
 def test_attend_large_scores_among_usual_ones():
     # scores that pass 2^17 only behind the first tokens, and rows that do beside rows that do not
     rng = np.random.default_rng(7)
