@@ -697,8 +697,9 @@ int moe_kv4_read(moe_kv4 *plan, const int32_t *slots, int n_tokens, uint16_t *k,
  * rules and limits.  What a row does not see does not touch its result,
  * whatever codes and scale bytes lie there; a token that it sees must have been
  * appended (one of zero bytes counts as zeros).  A seen key's scale of 2^100 or
- * more may count as a score beyond fp32's range.  Weights are held in 11 bits or
- * more, for many rows (the kernel for prompts) in 8, sums in 32. */
+ * more may count as a score beyond fp32's range, and many seen values of such
+ * scales may add up to infinity.  Weights are held in 11 bits or more, for many
+ * rows (the kernel for prompts) in 8, sums in 32. */
 int moe_kv4_attend(moe_kv4 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
                    const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
                    long long out_stride, void *stream);

@@ -13,11 +13,19 @@
 //    with fp16 ones values would need a reference for each block of 32 dims.
 //    Results are 2.0e-3 from those in 64 bits (relative, over an output), 1.6e-3
 //    of it their own rounding to bf16; the sum of the weights is fp32's.
-//  * One softmax reference m, moved (to 8 above the largest score) only when a
+//  * One softmax reference m, moved (to 16 above the largest score) only when a
 //    score passes it, so that weights are at most 1 and the accumulator in tensor
-//    memory is rarely rescaled.
+//    memory is rarely rescaled (at 8 above, a tenth of a step's time was that).
+//  * Weights go back to tensor memory, over the scores they come from, and are an
+//    operand there: no tile of them in shared memory, and no wait for one.
 //  * The values of a block are finite whatever the cache holds, so that a token
 //    that a row does not see adds nothing to it.
+// 4 x 900 ragged rows over up to 2700 tokens, 32 / 8 heads of 128, take 76 us, 23
+// at the rate of large matrix products.  A step takes about 2050 cycles, in which
+// the tensor pipe is 80 % and issue 70 % busy; a CTA's start and end, 6 us, and
+// what 1.9 CTAs an SM leave idle are the rest.  Two score buffers or one and
+// weights beside it, eight warps to decode (83 us), and a table in place of the
+// conversions made no difference or a worse one.
 #include "moe_kv_prompt.cuh"
 #include "moe_kv4.cuh"
 
@@ -73,8 +81,8 @@ __device__ __forceinline__ void mul2(float &y0, float &y1, float x0, float x1, f
 }
 // A block of 32 codes with its scale -> 64 bytes of bf16, exact, by way of fp32:
 // the conversions' pipe is what bounds the decoders, and this takes it twice a
-// pair (four times with fp16's bits shifted to bf16's places: 4 x 900 rows over
-// 2700 tokens took 104 us, this takes 87).
+// pair (four times with fp16's bits shifted to bf16's places: the kernel took 104
+// us with that when it took 87 with this).
 __device__ __forceinline__ void decode32(uint4 codes, float scale, uint4 (&out)[4]) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                     float corr = 1.f;
                     const bool move = mx > m;
                     if (move) {
-                        const float mn = mx + 8.f;
+                        const float mn = mx + 16.f;
                         corr = ex2(m - mn);
                         l *= corr, m = mn;
                     }
