@@ -802,12 +802,12 @@ cudaError_t launch_kv4_attend(const Kv4Attend &a, unsigned char *ws, cudaStream_
     // The streaming kernel's work grows by the unit of 16 rows, that of the kernel
     // for prompts by 256 rows a CTA, which walks all keys.  Per 64 tokens of a
     // kv head the first takes 0.23 us of an SM a unit (dims of 64; 0.44 with 128),
-    // the second 0.75 to 1.0 (0.95 to 1.1) a CTA of up to 128, 256 rows, in as many
+    // the second 0.67 to 0.8 (0.95 to 1.05) a CTA of up to 128, 256 rows, in as many
     // waves as its CTAs take; some 10 us are the joins'.  us with the first and the
-    // second, 8 kv heads of 64: one sequence of 32 K tokens, 128 rows 65 and 366,
-    // 512 rows 199 and 498; 4 of 8 K, 256 rows 112 and 130, 512 rows 205 and 129; 32
-    // of 4 K, 48 rows 93 and 116, 64 rows 116 and 109.  Of 128: one of 32 K, 512
-    // rows 385 and 558; 8 of 4 K, 40 rows 67 and 65, 64 rows 80 and 66.
+    // second, 8 kv heads of 64: one sequence of 32 K tokens, 128 rows 65 and 344,
+    // 512 rows 198 and 414; 4 of 8 K, 256 rows 112 and 110, 512 rows 205 and 109; 32
+    // of 4 K, 48 rows 93 and 102, 64 rows 116 and 97.  Of 128: one of 32 K, 512
+    // rows 377 and 549; 8 of 4 K, 40 rows 67 and 66, 64 rows 80 and 66.
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;

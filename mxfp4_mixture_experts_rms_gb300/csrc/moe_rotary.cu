@@ -80,12 +80,15 @@ __device__ __forceinline__ void lds2(const float *p, u64 (&v)[4]) {   // eight f
     v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const RotaryArgs a) {
+// NORMS: is either side normed?  Where none is, three CTAs of 256 threads an SM
+// (80 registers: more rows in flight; 4099 tokens of 36 heads of 128 take 17.5
+// us, 19.6 with 120).
+template <int D, bool INTER, bool NORMS>
+__global__ void __launch_bounds__(kMaxThreads, NORMS ? 2 : 3) moe_rotary_kernel(const RotaryArgs a) {
     constexpr int L = D / 16, U = kHeads;                 // lanes of a head
     __shared__ u64 turns[D / 2];                          // of a position, in units of 2^-64
     __shared__ __align__(16) float cosines[kTokens][D / 2], sines[kTokens][D / 2];   // times the factor
-    __shared__ __align__(16) float gammas[2][D];
+    __shared__ __align__(16) float gammas[NORMS ? 2 : 1][NORMS ? D : 4];
     __shared__ int skip[kTokens];
     const int tid = threadIdx.x, threads = blockDim.x, t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - t0);
     asm volatile("griddepcontrol.launch_dependents;");
@@ -94,19 +97,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
     const bool turned = l < a.pairs / 8;
     int d0 = 16 * l, d1 = d0 + 8;   // (halves: what lies behind the pairs' dims, too)
     if (!INTER && turned) d0 = 8 * l, d1 = a.pairs + 8 * l;
-    const bool norms = a.qg || a.kg;
     // the group's heads, queries before keys, and where its lane's dims of the running token are
     const uint16_t *in[U];
     uint16_t *out[U];
-    long long in_step[U], out_step[U];
     int side[U];
     bool on[U], norm[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
         const int h = (blockIdx.y * U + u) * groups + g, x = h >= a.QH;
         side[u] = x, on[u] = h < a.QH + a.KVH, norm[u] = (x ? a.kg : a.qg) != nullptr;
-        in_step[u] = x ? a.ks : a.qs, out_step[u] = x ? a.kos : a.qos;
-        in[u] = (x ? a.k - a.QH * D : a.q) + t0 * in_step[u] + h * D, out[u] = (x ? a.ko - a.QH * D : a.qo) + t0 * out_step[u] + h * D;
+        in[u] = (x ? a.k - a.QH * D + t0 * a.ks : a.q + t0 * a.qs) + h * D, out[u] = (x ? a.ko - a.QH * D + t0 * a.kos : a.qo + t0 * a.qos) + h * D;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     uint4 next[U][2];
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
         for (int u = 0; u < U; u++) {
             next[u][0] = next[u][1] = make_uint4(0, 0, 0, 0);
             if (more && on[u]) next[u][0] = *reinterpret_cast<const uint4 *>(in[u] + d0), next[u][1] = *reinterpret_cast<const uint4 *>(in[u] + d1);
-            in[u] += in_step[u];
+            in[u] += side[u] ? a.ks : a.qs;
         }
     };
     load(true);
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
         t -= floor(t);
         turns[i] = __double2ull_rn(t * 18446744073709551616.0);
     }
-    if (norms)
+    if (NORMS)
         for (int i = tid; i < 2 * D; i += threads) {
             const float *gamma = i < D ? a.qg : a.kg;
             gammas[i / D][i % D] = gamma ? gamma[i % D] : 1.f;
@@ -152,12 +152,13 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
         load(t + 1 < nt);
         const bool live = !skip[t];
         u64 cs[4], sn[4];
-        if (turned) lds2(&cosines[t][8 * l], cs), lds2(&sines[t][8 * l], sn);
+        auto angles = [&] { lds2(&cosines[t][8 * l], cs), lds2(&sines[t][8 * l], sn); };
+        if (NORMS && turned) angles();
 #pragma unroll
         for (int u = 0; u < U; u++) {
             u64 x[4] = {unpack(w[u][0].x), unpack(w[u][0].y), unpack(w[u][0].z), unpack(w[u][0].w)};
             u64 y[4] = {unpack(w[u][1].x), unpack(w[u][1].y), unpack(w[u][1].z), unpack(w[u][1].w)};
-            if (norms) {
+            if constexpr (NORMS) {
                 auto squares = [&](unsigned lanes) {
                     u64 sq = mul2(x[0], x[0]), sr = mul2(y[0], y[0]);
 #pragma unroll
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
                 }
             }
             if (turned) {
+                if (!NORMS) angles();   // (once for each head, for the registers)
                 auto turn = [](u64 &a, u64 &b, u64 c, u64 s) {
                     const u64 y = fma2(b, s ^ 0x8000000080000000ull, mul2(a, c));
                     b = fma2(a, s, mul2(b, c));
@@ -213,15 +215,19 @@ __global__ void __launch_bounds__(kMaxThreads, 2) moe_rotary_kernel(const Rotary
                 *reinterpret_cast<uint4 *>(out[u] + d0) = make_uint4(pack(x[0]), pack(x[1]), pack(x[2]), pack(x[3]));
                 *reinterpret_cast<uint4 *>(out[u] + d1) = make_uint4(pack(y[0]), pack(y[1]), pack(y[2]), pack(y[3]));
             }
-            out[u] += out_step[u];
+            out[u] += side[u] ? a.kos : a.qos;
         }
     }
 }
 
+template <int D, bool INTER>
+cudaError_t rotary_launch(const RotaryArgs &a, dim3 grid, int threads, cudaStream_t st) {
+    return a.qg || a.kg ? launch_pdl(moe_rotary_kernel<D, INTER, true>, grid, dim3(threads), 0, st, a)
+                        : launch_pdl(moe_rotary_kernel<D, INTER, false>, grid, dim3(threads), 0, st, a);
+}
 template <int D>
 cudaError_t rotary_launch(const RotaryArgs &a, bool inter, dim3 grid, int threads, cudaStream_t st) {
-    return inter ? launch_pdl(moe_rotary_kernel<D, true>, grid, dim3(threads), 0, st, a)
-                 : launch_pdl(moe_rotary_kernel<D, false>, grid, dim3(threads), 0, st, a);
+    return inter ? rotary_launch<D, true>(a, grid, threads, st) : rotary_launch<D, false>(a, grid, threads, st);
 }
 
 }  // namespace
