@@ -469,9 +469,11 @@ void moe_attn_destroy(moe_attn *plan);
 
 /* ---------------------------------------------------------------------------
  * Serving: the page tables of a paged key/value cache, such a cache held in 8
- * bits with the attention over it, and the choice of the next token.  One
- * step of a serving loop is moe_pages_assign, then per layer moe_kv8_append
- * and moe_kv8_attend, then moe_sample on the logits.  All of it enqueues only,
+ * or 4 bits with the attention over it, norms and rotary positions before it,
+ * the choice of the next token and the check of drafted ones.  One step of a
+ * serving loop is moe_pages_assign, then per layer moe_rotary_apply,
+ * moe_kv8_append and moe_kv8_attend (or moe_kv4_append and moe_kv4_attend),
+ * then moe_sample or moe_verify on the logits.  All of it enqueues only,
  * is graph-capturable and reads lengths on the device; a captured call sees
  * the lengths of its replay.
  */
