@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 namespace {
 
@@ -82,6 +83,7 @@ struct Span {
 struct FewArgs {
     Kv4Attend a;
     int G;                     // query heads per kv head
+    int most_up;               // powers of two that a row is scaled by, at most
     int32_t *status;           // [2]
     uint32_t *tickets;         // [kMaxCtas], zero between calls
     float *parts, *heads;      // [kMaxCtas][2] and [kMaxCtas][kMaxWarps] partials
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
                 am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
                 am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
                 // (not so far that what undoes it is below 2^-120: a factor of 0 or less bits would make scores wrong)
-                const int up = min(141 - (int)(am >> 7), min((int)(__float_as_uint(sc) >> 23) - 7, 126));
+                const int up = min(141 - (int)(am >> 7), f.most_up);
                 const float mul = pow2i(up), back = pow2i(-up) * sc;
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
@@ -818,7 +820,7 @@ cudaError_t launch_kv4_attend(const Kv4Attend &a, unsigned char *ws, cudaStream_
     const bool countable = ((long long)a.width * a.c.P / kTile + 2) * tiles * heads <= INT_MAX;   // the first's units
     if (rows <= 16 || (countable && 10 * heads * tiles < waves * sms * tenths)) {
         FewArgs f{};
-        f.a = a, f.G = G;
+        f.a = a, f.G = G, f.most_up = std::min(126, 120 + std::ilogb(a.scale * kLog2e));
         f.status = reinterpret_cast<int32_t *>(ws);
         f.tickets = reinterpret_cast<uint32_t *>(ws + 64);
         f.seqs = reinterpret_cast<int *>(ws + kKv8ClearBytes);
