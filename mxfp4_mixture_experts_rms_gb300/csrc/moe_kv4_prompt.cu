@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
     constexpr int kStages = L::kStages, kRaw = L::kRaw;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2], o_done[2][2], drain[2];
+    __shared__ __align__(8) uint64_t raw[kRaw], raw_empty[kRaw], full[kStages], empty[kStages], s_full[2][2], q_full[2], p_full[2][2], o_done[2][2], drain[2];
     __shared__ uint32_t rmeta[kRaw], meta[kStages];   // the pages that are there
     __shared__ uint32_t tmem_slot;
     __shared__ int job[5];   // sequence (-1: none), tile, and the sequence's first row, rows, first position
@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
         for (int s = 0; s < kStages; s++) bar_init(&full[s], kLoaders / 32), bar_init(&empty[s], 2);
         for (int s = 0; s < kRaw; s++) bar_init(&raw[s], 2), bar_init(&raw_empty[s], kLoaders / 32);
         for (int h = 0; h < 2; h++)
-            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], kSoftmax / 2), bar_init(&p_full[h], kSoftmax / 2), bar_init(&o_done[h][0], 1), bar_init(&o_done[h][1], 1), bar_init(&drain[h], 1);
+            bar_init(&s_full[h][0], 1), bar_init(&s_full[h][1], 1), bar_init(&q_full[h], kSoftmax / 2), bar_init(&p_full[h][0], kSoftmax / 2),
+                bar_init(&p_full[h][1], kSoftmax / 2), bar_init(&o_done[h][0], 1), bar_init(&o_done[h][1], 1), bar_init(&drain[h], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kIssuer) {
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                     l += s0 + s1;
                     tmem_st32(lanes + (j & 1) * kT, y);   // over the scores
                     fence_before();
-                    bar_arrive_warp(&p_full[h]);
+                    bar_arrive_warp(&p_full[h][j & 1]);   // (the next step's may come before this one is waited for)
                 }
                 if (ok) ok = bar_wait_warp(&o_done[h][(steps - 1) & 1], (uint32_t)((steps - 1) >> 1) & 1, status, 102);
                 if (ok) {
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kv4_prompt_kernel(const __gri
                 // the next scores go ahead of this step's values: into the columns of step j - 1's weights, once its products are done
                 if (j > 0) ok = bar_wait_warp(&o_done[h][(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1, status, 111);
                 if (ok && j + 1 < steps) ok = scores(j + 1, st1, par1);
-                if (ok) ok = bar_wait_warp(&p_full[h], (uint32_t)j & 1, status, 106);
+                if (ok) ok = bar_wait_warp(&p_full[h][j & 1], (uint32_t)(j >> 1) & 1, status, 106);
                 if (!ok) break;
                 fence_after();
                 const uint64_t V = V0 + st * kTile16;
