@@ -697,7 +697,9 @@ int moe_kv4_read(moe_kv4 *plan, const int32_t *slots, int n_tokens, uint16_t *k,
                  long long v_stride, void *stream);
 /* Attention of new tokens over the cache: all of moe_kv8_attend's arguments,
  * rules and limits.  What a row does not see does not touch its result,
- * whatever codes and scale bytes lie there; a token that it sees must have been
+ * whatever codes and scale bytes lie there (in a call of a few new tokens, where
+ * another row sees values of scales above 2^25, this holds for values of 2^-84
+ * and more; smaller ones may lose bits); a token that it sees must have been
  * appended (one of zero bytes counts as zeros).  A seen key's scale of 2^100 or
  * more may count as a score beyond fp32's range, and many seen values of such
  * scales may add up to infinity.  Weights are held in 11 bits or more, for many

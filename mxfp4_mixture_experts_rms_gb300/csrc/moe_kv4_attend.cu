@@ -41,10 +41,13 @@ namespace {
 // m moves (to 11 below the largest score) only when a score is more than 15 above
 // it, so that the common step has no exchange between lanes.  The accumulator of a
 // block of values holds sum w 2^(e - E) code over tokens with scale 2^e, E the
-// largest e so far, for all rows the same.  Where the e of 32 tokens are all within
+// largest e so far that any row sees, for all rows the same, but 25 at most: a row
+// that sees none of the largest scales keeps its sum in fp32 (a row's largest
+// weight is at least 2^7, so values down to 2^-84 keep 24 bits of it; an exponent
+// of their own for each row's sums made decode steps 4 to 5 % slower).  Where the e of 32 tokens are all within
 // 4 of E, w 2^(e - E) is the fp16 operand: the row's largest is then at least 2^7
 // and the others keep 11 bits down to 2^-21 of it.
-// Where they are not, tokens are multiplied in classes of e within 4 of one
+// Where they are not, or above E, tokens are multiplied in classes of e within 4 of one
 // another, each with its own reference, and added in fp32.
 // q is scaled per row by a power of two into fp16's range: exact for a bf16
 // row's values down to 2^-28 of its largest.
@@ -73,6 +76,7 @@ struct Few {
 };
 
 constexpr int kMaxWarps = 16;
+constexpr int kMostE = 127 + 25;   // as a scale byte: a step's products with the largest scales, 2^100 units, are below 2^123
 
 // Of a unit's rows: their first and last position, the tokens that can be seen,
 // and the unit's index from which the job is counted.
@@ -392,9 +396,13 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
             }
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) ends = __vmaxu2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
-            const int E1 = max(E, (int)(ends & 0xFFFFu));
-            const bool wild = __any_sync(0xffffffffu, ends && E1 - 256 + (int)(ends >> 16) > 4);
+            int E1 = max(E, (int)(ends & 0xFFFFu));
+            bool wild = __any_sync(0xffffffffu, ends && E1 - 256 + (int)(ends >> 16) > 4);
             if (__any_sync(0xffffffffu, E1 > E)) {
+                wild = wild || __any_sync(0xffffffffu, E1 > kMostE);
+                E1 = min(E1, kMostE);
+#pragma unroll
+                for (int v = 0; v < HV; v++) vs[v] = __vminu4(vs[v], kKv4MaxByte * 0x01010101u);   // (bytes that no append writes)
                 const float k = ex2((float)(E - E1));
 #pragma unroll
                 for (int b = 0; b < NB; b++) {

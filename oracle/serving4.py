@@ -123,11 +123,11 @@ def read(cache, P, D, slots):
     return [values(codes[s][page, o], scales[s][page, o]) for s in range(2)]
 
 
-def attend(cache, P, q, starts, lens, table, window=0, sinks=None, scale=None, weight=2.0 ** -11, floor=2.0 ** -31):
+def attend(cache, P, q, starts, lens, table, window=0, sinks=None, scale=None, weight=2.0 ** -11, floor=2.0 ** -31, flush=2.0 ** -120):
     """-> (out, tol): out [rows][heads][D] float64 (NaN rows where no sequence has one), and how far a result may be
     off that holds probabilities to `weight` of themselves, scores and sums in 32 bits, and rounds once to bf16: with
     A = sum_t p_t |v_t| and B = max_t scale sum_d |q_d k_td|,
-        2^-8 |out| + A (2 weight + 2 (D + 8) 2^-24 B + 2^-18) + floor F + 2^-120 max_t 2^(e_t) sum_t |code_td|.
+        2^-8 |out| + A (2 weight + 2 (D + 8) 2^-24 B + 2^-18) + floor F + flush max_t 2^(e_t) sum_t |code_td|.
     A score is a sum of D products, off by at most (D + 4) 2^-24 B in 32 bits; turning it into a power of two and its
     argument's rounding add at most 4 * 2^-24 B, since |s| <= B.  Each p_t is off by that relative to itself, which
     moves numerator and denominator by at most A times it; `weight` for the rounding of p (half a step: 2^-11 and the
@@ -136,7 +136,9 @@ def attend(cache, P, q, starts, lens, table, window=0, sinks=None, scale=None, w
     2^(s - m + e_t - E), E at most 4 above e_t, m at most 11 below the largest score when it was set and never more than
     15 below one since, so 2^7 at least for the token of the largest score; below 2^-14 they are off by up to half of fp16's smallest step, 2^-25: 2^-32 of the largest,
     doubled for parts with references of their own.
-    The last term: tokens of scales 2^126 below the largest add nothing, as fp32 ends there; 2^-120 for their number."""
+    The last term, for weights of next to nothing on tokens of the largest scales (a weight 2^-31 of the row's largest may
+    count as none): 2^-120, where scales are within 2^120 of one another less than the floor.  0 where all of a row's
+    weights are of one size."""
     D, H = q.shape[2], q.shape[1]
     kv, n_pages = cache.shape[1], cache.shape[0]
     codes, scales = unpack(cache, P, D)
@@ -166,7 +168,7 @@ def attend(cache, P, q, starts, lens, table, window=0, sinks=None, scale=None, w
                 out[r, h] = w @ v[:, g]
                 B = scale * (np.abs(k[:, g]) @ np.abs(qv)).max()
                 F = (w[:, None] * ve[:, g]).max(0) * np.abs(E2M1[codes[1][pages, at, g]]).sum(0)
-                F = floor * F + 2.0 ** -120 * ve[:, g].max(0) * np.abs(E2M1[codes[1][pages, at, g]]).sum(0)
+                F = floor * F + flush * ve[:, g].max(0) * np.abs(E2M1[codes[1][pages, at, g]]).sum(0)
                 tol[r, h] = F + 2.0 ** -8 * np.abs(out[r, h]) + \
                     w @ np.abs(v[:, g]) * (2 * weight + 2 * (D + 8) * 2.0 ** -24 * B + 2.0 ** -18)
     return out, tol + 1e-30

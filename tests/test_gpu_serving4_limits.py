@@ -1,0 +1,77 @@
+"""The serving step's other operators at the limits that include/moe.h states, on the GPU.  Tolerances as in
+test_gpu_serving4.py, or derived at the test."""
+import numpy as np
+import pytest
+
+from oracle import serving4 as S4
+from tests import test_gpu_serving4 as base
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- attention
+
+def check_scales(rng, P, D, kv, H, lens, rows, scales_of, window=0, lo=118, hi=131, prompts=False, spread=0.1):
+    """Attention where scales_of (sequence, position, block or None, scale byte) says how large values are.  Scores are within
+    a few units of one another, so that no weight is next to nothing: what a row sees counts (flush = 0)."""
+    import torch
+    width, pages = -(-max(lens) // P), sum(-(-L // P) for L in lens) + 2
+    c, table = base.sequences(rng, P, lens, width, pages, kv, D, poison=False, lo=lo, hi=hi)
+    codes, scales = S4.unpack(c, P, D)
+    scales[0] = rng.integers(124, 128, scales[0].shape)
+    for b, t, block, byte in scales_of:
+        scales[1][table[b, t // P], t % P, :, slice(None) if block is None else block] = byte
+    c = S4.pack(codes, scales)
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    qd, q = base.bf16(rng.normal(0, spread, (starts[-1], H, D)))
+    plan = base.moe().Kv4(H, kv, D, P, pages, sliding_window=window, cache=base.dev(c))
+    out = torch.full((starts[-1], H, D), 7.5, dtype=torch.bfloat16, device="cuda")
+    assert base.for_prompts(len(lens), kv, H, max(rows), D) == prompts
+    plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out, starts=base.dev(starts), max_new=max(rows))
+    ref, tol = S4.attend(c, P, q, starts, lens, table, window, weight=2.0 ** -8 if prompts else 2.0 ** -11, flush=0.0)
+    base.close(out.double().cpu().numpy(), ref, tol)
+    assert plan.device_status() == 0
+
+
+@pytest.mark.parametrize("P,D", [(16, 64), (32, 128), (64, 64), (64, 128), (32, 64)])
+@pytest.mark.parametrize("kv,H", [(1, 1), (1, 8), (2, 6), (1, 16)])
+def test_attend_scales_that_only_some_rows_see(P, D, kv, H):
+    """Drafted rows of which the last one's values are as large as they can be, and tokens that slide out of the window."""
+    rng = np.random.default_rng(P + D + H)
+    for byte in (252, 255, 200):
+        check_scales(rng, P, D, kv, H, [230, 70], [5, 2], [(0, 229, None, byte), (1, 69, 0, byte)])
+        check_scales(rng, P, D, kv, H, [321, 70], [5, 2], [(0, 317, 1, byte), (0, 320, 0, byte)], lo=40, hi=60)
+    # positions 225 .. 229 see the last 100: 127 is seen by rows 0 and 1, 126 by row 0
+    check_scales(rng, P, D, kv, H, [230, 300], [5, 3], [(0, 127, None, 252), (0, 126, None, 250), (1, 199, 1, 252)], window=100)
+    check_scales(rng, P, D, kv, H, [230, 300], [5, 3], [(0, 127, None, 252), (0, 160, 0, 150), (0, 229, 0, 252)], window=100, lo=30, hi=50)
+
+
+@pytest.mark.parametrize("D,kv,H", [(64, 1, 8), (128, 1, 2), (128, 2, 8)])
+def test_attend_scales_that_only_some_rows_see_across_shares(D, kv, H):
+    """The same where a sequence is shared by many warps and CTAs: the joins' exponents are the rows' own."""
+    rng = np.random.default_rng(D + H)
+    check_scales(rng, 32, D, kv, H, [6000], [5], [(0, 5999, None, 252)])
+    check_scales(rng, 32, D, kv, H, [6000], [5], [(0, 3002, None, 252), (0, 4500, 0, 10), (0, 1500, 1, 190)], window=2995, lo=60, hi=70)
+    check_scales(rng, 32, D, kv, H, [2500, 90, 3000], [3, 2, 4], [(0, 2499, 0, 252), (1, 89, None, 252), (2, 2998, 1, 252)], lo=50, hi=60)
+
+
+@pytest.mark.parametrize("rows,H", [([1], 1), ([1], 8), ([3], 8)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_scales_of_every_size_in_one_row(rows, H, D):
+    """Every row sees them all: the largest ones are the result, whatever order they come in."""
+    rng = np.random.default_rng(H + D)
+    up = [(0, t, None, int(b)) for t, b in zip(range(700), np.linspace(1, 252, 700))]
+    for what in (up, [(0, 699 - t, None, b) for _, t, _, b in up], [(0, t, None, int(rng.integers(1, 253))) for t in range(700)],
+                 [(0, t, int(rng.integers(0, D // 32)), int(rng.integers(1, 253))) for t in range(0, 700, 3)]):
+        check_scales(rng, 16, D, 1, H, [700], rows, what)
+    check_scales(rng, 32, D, 1, H, [40], rows, [(0, t, None, int(rng.integers(1, 253))) for t in range(40)])
+
+
+@pytest.mark.parametrize("D,kv,H,most", [(64, 8, 16, 100), (128, 8, 8, 17)])
+def test_attend_scales_that_only_some_rows_of_prompts_see(D, kv, H, most):
+    rng = np.random.default_rng(most)
+    n = 6 if D == 64 else 31
+    rows = np.minimum(rng.integers(1, most + 1, n), 20)
+    rows[0] = most
+    lens = rows + rng.integers(0, 100, n)
+    check_scales(rng, 32, D, kv, H, lens, rows, [(b, int(L) - 1, None, 252) for b, L in enumerate(lens)] + [(0, int(lens[0]) - 40, 0, 250)], prompts=True)
