@@ -304,10 +304,11 @@ __global__ void __launch_bounds__(Few<D, P, RT>::kWarps * 32, 1) moe_kv4_few_ker
             int row0, n, pos0;
             kv8_rows(a, j.b, row0, n, pos0);
             {
-                const int pmin = pos0 + j.rt * R / f.G, pmax = pos0 + min(n * f.G - 1, j.rt * R + R - 1) / f.G, seen = seq(2, j.b);
+                // (rows far before the sequence are as near as the last of those: token - position stays in 32 bits)
+                const int pmin = max(pos0 + j.rt * R / f.G, -1), pmax = max(pos0 + min(n * f.G - 1, j.rt * R + R - 1) / f.G, -1), seen = seq(2, j.b);
                 all_from = a.window ? max(pmax - a.window + 1, 0) : 0, all_to = min(seen - 1, pmin);
                 if (lane == 0) spans[warp] = {pmin, pmax, seen, u};
-                for (int r = lane; r < R; r += 32) row_pos[warp][r] = j.rt * R + r < n * f.G ? pos0 + (j.rt * R + r) / f.G : -1;
+                for (int r = lane; r < R; r += 32) row_pos[warp][r] = j.rt * R + r < n * f.G ? max(pos0 + (j.rt * R + r) / f.G, -1) : -1;
             }
 #pragma unroll
             for (int x = 0; x < RT; x++) {

@@ -75,3 +75,20 @@ def test_attend_scales_that_only_some_rows_of_prompts_see(D, kv, H, most):
     rows[0] = most
     lens = rows + rng.integers(0, 100, n)
     check_scales(rng, 32, D, kv, H, lens, rows, [(b, int(L) - 1, None, 252) for b, L in enumerate(lens)] + [(0, int(lens[0]) - 40, 0, 250)], prompts=True)
+
+
+@pytest.mark.parametrize("D,H", [(64, 1), (64, 8), (128, 8)])
+@pytest.mark.parametrize("window", [0, 30, 2 ** 31 - 1])
+def test_attend_rows_far_before_their_sequence(D, H, window):
+    """starts that end at 2^31 - 1: the rows that are there stand almost 2^31 before the sequence's first token, and see nothing."""
+    import torch
+    rng = np.random.default_rng(H)
+    P, lens = 64, [67, 100]
+    c, table = base.sequences(rng, P, lens, 2, 6, 1, D)
+    qd, _ = base.bf16(rng.normal(0, 0.25, (7, H, D)))
+    out = torch.full((7, H, D), 7.5, dtype=torch.bfloat16, device="cuda")
+    plan = base.moe().Kv4(H, 1, D, P, 6, sliding_window=window, cache=base.dev(c))
+    for first in (0, 2):
+        out.fill_(7.5)
+        plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out, starts=base.dev(np.array([first, 2 ** 31 - 1, 2 ** 31 - 1], np.int32)), max_new=9)
+        assert bool((out[:first] == 7.5).all()) and bool((out[first:] == 0).all())
