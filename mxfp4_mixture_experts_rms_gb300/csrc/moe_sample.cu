@@ -98,6 +98,27 @@ __device__ __forceinline__ u64 fraction(float p) {
 }
 __device__ __forceinline__ u64 part_up(u64 sum, u64 f) { return __umul64hi(sum, f) + (sum * f != 0); }
 
+// A lane's weights, a vector's at a time.  Limits are told of sums in two parts:
+// 2^10 weights in one fp32 sum are off by up to 2^-16 where they are equal, as each
+// addition rounds the same way.  (lo is what hi's additions lost, but where one
+// added more than hi had, which is at most 2^-23 of the sum in all.  64 x up to 5
+// rows of 128 K bf16 take 146 us with it, 144 without.)
+template <bool LIMITS>
+struct LaneSum {
+    float hi = 0.f, lo = 0.f;
+    // a vector's weights are added to what this gives, and that is put back
+    __device__ __forceinline__ float take() const { return LIMITS ? 0.f : hi; }
+    __device__ __forceinline__ void put(float w) {
+        const float s = LIMITS ? hi + w : w;
+        if (LIMITS) lo += w - (s - hi);
+        hi = s;
+    }
+    __device__ __forceinline__ u64 fixed() const {   // in units of 2^-40
+        const u64 sum = __float2ull_rn(hi * 0x1p40f);
+        return LIMITS ? sum + (u64)__float2ll_rn(lo * 0x1p40f) : sum;
+    }
+};
+
 // What the CTAs of a row tell one another, each its slot.
 struct Told {
     uint32_t key;
@@ -224,7 +245,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     };
     // 0 - the bin of weight 1 - downwards; NaN is never asked for
     auto bin_of = [](float w) { return max((0x3F800000 >> kBinShift) - (int)(__float_as_uint(w) >> kBinShift), 0); };
-    auto fixed_sum = [](float sum) { return __float2ull_rn(sum * 0x1p40f); };
     auto warp_sum = [](u64 v) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -273,22 +293,23 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
         __syncthreads();
         for (int b = tid; b < kBins; b += NT) hist32[b] = 0;
         __syncthreads();
-        float sum = 0.f;
+        LaneSum<LIMITS> sum;
         const uint32_t half = (1u << a.drop) >> 1;
         d.each([&](float (&x)[VE], int) {
-            float w[VE];
+            float w[VE], here = sum.take();
             weights(x, w);
 #pragma unroll
             for (int e = 0; e < VE; e++) {
                 const bool in = x[e] > over;
                 const int b = bin_of(w[e]);
-                sum += in ? w[e] : 0.f;
+                here += in ? w[e] : 0.f;
                 if (in && b < kBins) atomicAdd(&hist32[b], by_weight ? (((__float_as_uint(w[e]) & 0x7FFFFFu) | 0x800000u) + half) >> a.drop : 1u);
             }
+            sum.put(here);
         });
         u64 goal = (u64)k, everything = 0;
         u64 drop = 0;   // weight that top-p may leave out, in units of 2^-64
-        tell({0, 0, 0, by_weight ? total(fixed_sum(sum)) : 0});   // and the histograms are there
+        tell({0, 0, 0, by_weight ? total(sum.fixed()) : 0});   // and the histograms are there
         if (by_weight) {
             for (int c = 0; c < C; c++) everything += told[turn][c].sum;
             if (T) {
@@ -331,23 +352,24 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
             __syncthreads();
             if (tid == 0) s_n = 0, s_lo = 0xFFFFFFFFu, s_hi = 0;
             __syncthreads();
-            float before = 0.f;
+            LaneSum<LIMITS> before;
             int count = 0;
             // the bin's weights: from w_in up to w_up; listed: from w_in, up to w_end (NaN nowhere)
             const bool first = span == kBinShift && from >= 0x3F800000u;   // with all weights of 1 and (by rounding) above
             const float w_in = __uint_as_float(from), w_up = first ? INFINITY : __uint_as_float(from + (1u << span));
             const float w_end = few ? INFINITY : w_up;
             d.each([&](float (&x)[VE], int i) {
-                float w[VE];
+                float w[VE], here = before.take();
                 weights(x, w);
                 uint32_t take = 0;
 #pragma unroll
                 for (int e = 0; e < VE; e++) {
                     const bool in = x[e] > over, up = in && w[e] >= w_up;
-                    before += up ? w[e] : 0.f;
+                    here += up ? w[e] : 0.f;
                     count += up;
                     take |= in && w[e] >= w_in && w[e] < w_end ? 1u << e : 0u;
                 }
+                before.put(here);
                 while (take) {
                     const int e = __ffs(take) - 1, at = atomicAdd(&s_n, 1);
                     take &= take - 1;
@@ -357,7 +379,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
                     if (at < kList) list[at] = make_uint2(order_key(v), i + e);
                 }
             });
-            const u64 mine = total(by_weight ? fixed_sum(before) : few ? 0 : (u64)count);
+            const u64 mine = total(by_weight ? before.fixed() : few ? 0 : (u64)count);
             tell({0, s_n, 0, mine});
             bool listed = true;
             int n = 0, base = 0;
@@ -604,18 +626,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) moe_sample_kernel(const SampleA
     const float xT = T ? key_logit(T) : -INFINITY;
     const float wT = T ? weight(xT) : 0.f;
     auto at_T = [&](u64 n) { return wT >= least ? units(min(n, r), wT) : 0; };
-    float sum = 0.f;
+    LaneSum<LIMITS> sum;
     int ties = 0;
     d.each([&](float (&x)[VE], int) {
-        float w[VE];
+        float w[VE], here = sum.take();
         weights(x, w);
 #pragma unroll
         for (int e = 0; e < VE; e++) {
-            sum += x[e] > xT && w[e] >= least ? w[e] : 0.f;
+            here += x[e] > xT && w[e] >= least ? w[e] : 0.f;
             ties += x[e] == xT;   // (-inf where no logit is at T: not counted below, as r is 0)
         }
+        sum.put(here);
     });
-    u64 mass = warp_sum(max(fixed_sum(sum), (u64)(sum > 0.f)));
+    u64 mass = warp_sum(max(sum.fixed(), (u64)(sum.hi > 0.f)));
     ties = __reduce_add_sync(0xffffffffu, ties);
     if (lane == 0) wmass[warp] = mass, wties[warp] = ties;
     __syncthreads();

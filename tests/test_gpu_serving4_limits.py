@@ -92,3 +92,19 @@ def test_attend_rows_far_before_their_sequence(D, H, window):
         out.fill_(7.5)
         plan.attend(qd, base.dev(np.array(lens, np.int32)), base.dev(table), out, starts=base.dev(np.array([first, 2 ** 31 - 1, 2 ** 31 - 1], np.int32)), max_new=9)
         assert bool((out[:first] == 7.5).all()) and bool((out[first:] == 0).all())
+
+
+# ---------------------------------------------------------------- verification
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("below", [0.90625, 0.69921875, 0.30078125])
+def test_verify_sums_of_the_largest_vocabulary(below, dtype):
+    """2^22 tokens of one weight, which 32-bit sums round the same way every time: a lane's 1024 are off by up to 2^-16.3.
+    Drafted tokens with u 2^-17.4 of p below p, and above it."""
+    V = 1 << 22
+    x = np.full((8, V), -below, np.float32)
+    x[:, 77] = 0.0
+    p = S4.probabilities(x[0], 1.0, 0, 1.0, 0.0)[5]
+    u = np.array([p * (1 - 2.0 ** -17.4), 0.5, p * (1 + 2.0 ** -17.4), 0.5] * 2)
+    ids, acc = base.check_verify(np.random.default_rng(1), x, [2, 2, 2, 2], np.array([5, 0, 9, 0, V - 1, 0, V // 2, 0]), None, u=u, dtype=dtype)
+    assert list(acc) == [1, 0, 1, 0]
