@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
                     y[e] = 0.f;
                     if (some[u] && (x[e] > xT || (x[e] == xT && i + e < cut))) {
                         const float w = weight(x[e]);
-                        if (mp < 1.f ? w >= lim.least : x[e] == weight.top) y[e] = fmaxf(fmaf(w, lim.inv, fmaf(w, lim.inv_lo, -used_prob(q[u][e]))), 0.f);
+                        // (what p and q have in common goes first, so that inv_lo still shows in what is left)
+                        if (mp < 1.f ? w >= lim.least : x[e] == weight.top) y[e] = fmaxf(fmaf(w, lim.inv_lo, fmaf(w, lim.inv, -used_prob(q[u][e]))), 0.f);
                     }
                     sum += y[e];
                 }

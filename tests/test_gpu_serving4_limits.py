@@ -108,3 +108,39 @@ def test_verify_sums_of_the_largest_vocabulary(below, dtype):
     u = np.array([p * (1 - 2.0 ** -17.4), 0.5, p * (1 + 2.0 ** -17.4), 0.5] * 2)
     ids, acc = base.check_verify(np.random.default_rng(1), x, [2, 2, 2, 2], np.array([5, 0, 9, 0, V - 1, 0, V // 2, 0]), None, u=u, dtype=dtype)
     assert list(acc) == [1, 0, 1, 0]
+
+
+def below_a_share(n):
+    """1 / n in fp32, which for these n is less than 1 / n: a residual of known size, some 2^-25 of it."""
+    q = np.float32(1.0 / n)
+    assert float(q) < 1.0 / n
+    return q
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n,step", [(11, 3), (1009, 7), (50021, 7), (100019, 3), (149993, 1000)])
+def test_verify_residuals_of_next_to_nothing(n, step, dtype):
+    """n equal logits, so that p is 1 / n to the last bit, and drafts' probabilities that are 1 / n rounded down at every
+    step-th token and more than 1 / n at the others: the residual is the rounding, the same at each of those tokens, and 0 at
+    the others.  Sums within 2^-20 of their totals choose the token of the middle of each share exactly, or one that is as
+    near as that."""
+    while float(np.float32(1.0 / n)) >= 1.0 / n:
+        n += 1
+    q = np.full(n, np.nextafter(below_a_share(n), np.float32(1)), np.float32)
+    some = np.arange(2 % n, n, step)
+    q[some] = below_a_share(n)
+    q[0] = 2.0 / n                                       # the drafted token: not accepted at u = 0.9
+    B = 24
+    pick = np.linspace(0, len(some) - 1, B).round().astype(int)
+    draws = ((pick + 0.5) / len(some)).astype(np.float32)
+    import torch
+    z = lambda k: torch.zeros(k, dtype=torch.int32, device="cuda")   # noqa: E731
+    ids, acc = z(2 * B), z(B)
+    x = torch.zeros((2 * B, n), dtype=getattr(torch, dtype), device="cuda")
+    base.moe().Verify(2 * B).run(x, z(2 * B), torch.full((2 * B,), 0.9, device="cuda"), base.dev(draws), base.dev(np.arange(0, 2 * B + 1, 2, dtype=np.int32)),
+                                 ids, acc, draft_probs=base.dev(np.tile(q, (2 * B, 1))))
+    got = ids.cpu().numpy()[::2]
+    assert not acc.any() and np.isin(got, some).all()
+    at = np.searchsorted(some, got)
+    slack = 2.0 ** -20 * len(some)
+    assert np.all(np.abs(at + 0.5 - draws.astype(np.float64) * len(some)) <= 0.5 + slack)
