@@ -11,10 +11,11 @@
 // q is read at kept tokens only.
 //
 // Sums are whole numbers of units of 2^-52, at least one where there is anything:
-// of a lane's tokens, summed in two fp32 parts.  (64-bit floats are the GPU's
-// slowest numbers: with sums and quotients in them the second kernel took 76 us
-// at 64 sequences, 282 rows of 128 K logits, in place of 38; the first takes 100,
-// as moe_sample would.)
+// of a lane's tokens, summed in two fp32 parts.  Where that comes to less than
+// 2^36 units (q is p but for last bits) the row is summed again in smaller ones.
+// (64-bit floats are the GPU's slowest numbers: with sums and quotients in them the
+// second kernel took 76 us at 64 sequences, 282 rows of 128 K logits, in place of
+// 38; the first takes 100, as moe_sample would.)
 #include "moe_sample.cuh"
 #include "../../include/moe.h"
 
@@ -46,12 +47,12 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// x (0 .. 1 and a little more) in units of 2^-52, at least one of them if it is not 0.
-__device__ __forceinline__ u64 units(float x) {
+// x (0 .. 1 and a little more) in units of 2^-(52 + up), at least one of them if it is not 0.
+__device__ __forceinline__ u64 units(float x, int up) {
     const uint32_t b = __float_as_uint(x);
-    const int s = (int)(b >> 23) - 98;   // mantissa times 2^(exponent - 150)
+    const int s = (int)(b >> 23) - 98 + up;   // mantissa times 2^(exponent - 150)
     const u64 m = (b & 0x7FFFFFu) | 0x800000u;
-    return x > 0.f ? max(s >= 0 ? m << min(s, 32) : m >> min(-s, 63), (u64)1) : 0;
+    return x > 0.f ? max(s >= 0 ? m << min(s, 38) : m >> min(-s, 63), (u64)1) : 0;
 }
 // u (0 .. 1 - 2^-24; NaN: 0) in units of 2^-64.
 __device__ __forceinline__ u64 fraction(float u) {
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
     const float t = used_temperature(a.s.temperature ? a.s.temperature[b] : 1.f);
     const float mp = a.s.min_p ? used_min_p(a.s.min_p[b]) : 0.f;
     const int n = s1 - s0;
-    const u64 draw = n > 0 ? fraction(a.draws[b]) : 0;
+    const float draw = n > 0 ? a.draws[b] : 0.f;
     // of row s0 + j: the drafted token (-1: none, or not in the vocabulary), its logit and probability, the random number
     struct Draft {
         int x;
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
             }
         }
     };
+    int up = 0;   // of the units
     for (int turn = 0; turn < 2; turn++) {
         float hi = 0.f, lo = 0.f;
         walk([&](int, const float (&)[VE], float sum) {
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
             return false;
         });
         // (lo is a correction of either sign, below half a unit in hi's last place)
-        const u64 mine = warp_sum(lo >= 0.f ? units(hi) + (lo > 0.f ? units(lo) : 0) : max(units(hi) - min(units(-lo), units(hi)), (u64)1));
+        const u64 mine = warp_sum(lo >= 0.f ? units(hi, up) + (lo > 0.f ? units(lo, up) : 0) : max(units(hi, up) - min(units(-lo, up), units(hi, up)), (u64)1));
         if (lane == 0) sums[warp] = mine;
         __syncthreads();
         u64 at = 0, all = 0;
@@ -236,15 +238,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
             if (c < rank) at += parts[turn][c];
             total += parts[turn][c];
         }
+        if (total < 1ull << 36 && minus && turn == 0) {
+            if (total == 0) minus = false;   // p is nowhere above q: from p
+            else up = __clzll((long long)total) - 2;   // a sum below 2^62
+            continue;
+        }
         if (total == 0) {
-            if (minus) {   // p is nowhere above q: from p
-                minus = false;
-                continue;
-            }
             if (rank == 0 && tid == 0) a.ids[row] = -1;
             return;
         }
-        const u64 target = __umul64hi(total, draw);   // below the total
+        const u64 target = __umul64hi(total, fraction(draw));   // below the total
         if (target < at || target >= at + mine) return;
         int last = -1, id = -1;
         walk([&](int i, const float (&y)[VE], float sum) {
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
             u64 s = 0;
 #pragma unroll
             for (int e = 0; e < VE; e++) {
-                s += units(y[e]);
+                s += units(y[e], up);
                 if (y[e] > 0.f) last = i + e;
             }
             u64 inc = s;
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
             if (hit)
 #pragma unroll
                 for (int e = 0; e < VE; e++) {
-                    const u64 one = units(y[e]);
+                    const u64 one = units(y[e], up);
                     if (target >= run && target < run + one) id = i + e;
                     run += one;
                 }

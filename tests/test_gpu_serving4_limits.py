@@ -118,7 +118,7 @@ def below_a_share(n):
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
-@pytest.mark.parametrize("n,step", [(11, 3), (1009, 7), (50021, 7), (100019, 3), (149993, 1000)])
+@pytest.mark.parametrize("n,step", [(11, 3), (1009, 7), (50021, 7), (100019, 3), (149993, 1000), (4100013, 3), (3333331, 1000)])
 def test_verify_residuals_of_next_to_nothing(n, step, dtype):
     """n equal logits, so that p is 1 / n to the last bit, and drafts' probabilities that are 1 / n rounded down at every
     step-th token and more than 1 / n at the others: the residual is the rounding, the same at each of those tokens, and 0 at
@@ -130,7 +130,7 @@ def test_verify_residuals_of_next_to_nothing(n, step, dtype):
     some = np.arange(2 % n, n, step)
     q[some] = below_a_share(n)
     q[0] = 2.0 / n                                       # the drafted token: not accepted at u = 0.9
-    B = 24
+    B = 24 if n < 1e6 else 9
     pick = np.linspace(0, len(some) - 1, B).round().astype(int)
     draws = ((pick + 0.5) / len(some)).astype(np.float32)
     import torch
