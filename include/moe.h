@@ -629,8 +629,8 @@ int moe_sample(const void *logits, int is_bf16, int n_rows, int vocab, long long
  *             for its n_pairs pairs (a, b), the angle of pair i being
  *             positions[axes[i]][token] * freqs[i]
  * rounded once, to bf16; dims in no pair are x'.  Pairs are dims i and
- * i + n_pairs, or 2 i and 2 i + 1 (interleaved = 1).  Angles are exact to
- * 2^-32 of a turn and 2^-52 of themselves, wherever the position is. */
+ * i + n_pairs, or 2 i and 2 i + 1 (interleaved = 1).  Angles are within 2^-25 of
+ * a turn and 2^-52 of themselves, wherever the position is. */
 typedef struct moe_rotary moe_rotary;
 /* head_dim 64, 128 or 256; n_pairs a multiple of 8, 0 .. head_dim / 2; n_axes
  * 1 .. 4 (time, height and width of images and video, say).  Defaults: no
@@ -638,7 +638,7 @@ typedef struct moe_rotary moe_rotary;
 moe_rotary *moe_rotary_create(int head_dim, int n_pairs, int n_axes, int interleaved);
 /* "eps" (0 .. 1e30), "factor" (1e-30 .. 1e30). */
 int moe_rotary_set_f(moe_rotary *plan, const char *key, double value);
-/* Radians a position (f64 [n_pairs], device, borrowed) and the axis of each
+/* Radians a position (finite, f64 [n_pairs], device, borrowed) and the axis of each
  * pair (uint8 [n_pairs], device, borrowed; NULL: the first; one past the last
  * counts as the last). */
 int moe_rotary_set_freqs(moe_rotary *plan, const double *freqs, const uint8_t *axes);

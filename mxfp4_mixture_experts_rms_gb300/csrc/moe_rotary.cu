@@ -8,7 +8,9 @@
 // Everything in fp32, rounded once, to bf16.  An angle is taken in turns: the
 // frequency's turns a position as a 64-bit fraction F, so that the low 64 bits
 // of position * F are the turn's fraction, exact to 2^-33 of a turn and 2^-52 of the
-// angle (an fp32 product is off by whole radians at 2^24).
+// angle (an fp32 product is off by whole radians at 2^24).  Its upper 32 bits are
+// what sine and cosine take, as fp32: within 2^-26 of a turn near half a turn,
+// nearer where it is less.
 //
 // Bound by HBM: 4 bytes an element.  A CTA takes its tokens' angles first, once
 // for all heads, then a group of D / 16 lanes has two heads of each token: a lane
@@ -120,9 +122,12 @@ __global__ void __launch_bounds__(kMaxThreads, NORMS ? 2 : 3) moe_rotary_kernel(
     };
     load(true);
     for (int i = tid; i < a.pairs; i += threads) {
-        double t = a.freqs[i] * 0.15915494309189533577;
+        // (a negative one by its magnitude: next to 1 a fraction has no bits for it)
+        const double freq = a.freqs[i];
+        double t = fabs(freq) * 0.15915494309189533577;
         t -= floor(t);
-        turns[i] = __double2ull_rn(t * 18446744073709551616.0);
+        const u64 turn = __double2ull_rn(t * 18446744073709551616.0);
+        turns[i] = freq < 0. ? 0 - turn : turn;
     }
     if (NORMS)
         for (int i = tid; i < 2 * D; i += threads) {

@@ -144,3 +144,21 @@ def test_verify_residuals_of_next_to_nothing(n, step, dtype):
     at = np.searchsorted(some, got)
     slack = 2.0 ** -20 * len(some)
     assert np.all(np.abs(at + 0.5 - draws.astype(np.float64) * len(some)) <= 0.5 + slack)
+
+
+# ---------------------------------------------------------------- angles
+
+def test_rotate_negative_frequencies_keep_their_angles():
+    """Far positions whose angles are whole turns but for their frequencies' last bits: sines of next to nothing show the
+    angle's error, which is at most 2^-25 of a turn.  (The frequency's own product with the position is exact to 2^-40.)"""
+    import torch
+    pos = 2 ** 31 - 1
+    turns = np.array([256, 768, 1280, 1792, 2304, 2816, 1, 12345] * 4)
+    freqs = np.where(np.arange(32) % 16 < 8, -1, 1) * 2 * np.pi * turns / pos
+    x = np.zeros((1, 1, 64))
+    x[..., 32:] = 1.0                                     # (0, 1) -> (-sin, cos)
+    xd, _ = base.bf16(x)
+    base.moe().Rotary(64, freqs).apply(xd, None, base.dev(np.array([pos], np.int32)))
+    got, angle = xd.double().cpu().numpy()[0, 0], freqs * pos
+    assert np.all(np.abs(got[:32] + np.sin(angle)) <= 2 * np.pi * 2.0 ** -25)
+    assert np.all(got[32:] == 1.0)
