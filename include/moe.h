@@ -733,9 +733,10 @@ void moe_kv4_destroy(moe_kv4 *plan);
  * and -1 behind it; rows of no sequence are left as they are.  Of a sequence of
  * one row the token is drawn as moe_sample would.  Weights are fp32, sums
  * within 2^-20 of their totals.  draft_probs is read at and beside tokens that
- * p keeps, never at a sequence's last row.  ids and accepted overlap nothing
- * else.  The workspace (device, 16-byte aligned) holds
- * nothing between calls; calls that can overlap on the GPU need one each. */
+ * p keeps, never at a sequence's last row.  ids, accepted and the workspace
+ * overlap nothing else (they may lie between rows that are apart).  The workspace
+ * (device, 16-byte aligned) holds nothing between calls; calls that can overlap
+ * on the GPU need one each. */
 size_t moe_verify_workspace_bytes(int n_rows);
 int moe_verify(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride, const int32_t *drafts,
                const float *draft_probs, long long probs_stride, const int32_t *starts, int n_seqs, const float *temperature,

@@ -328,16 +328,30 @@ int moe_verify(const void *logits, int is_bf16, int n_rows, int vocab, long long
     if ((uintptr_t)workspace & 15u) return moe_fail_status(MOE_EINVAL, "the workspace must be 16-byte aligned");
     if (workspace_bytes < moe_verify_workspace_bytes(n_rows))
         return moe_fail_status(MOE_ENOMEM, "workspace of %zu bytes, %zu needed", workspace_bytes, moe_verify_workspace_bytes(n_rows));
-    // what one sequence's CTAs write others may still have to read
-    auto clash = [](const void *x, long long nx, const void *y, long long ny) {   // of 4-byte elements
-        return x && y && (uintptr_t)x < (uintptr_t)y + 4 * ny && (uintptr_t)y < (uintptr_t)x + 4 * nx;
+    // what one row's or sequence's CTAs write others may still have to read
+    struct Array {
+        const void *p;
+        long long row, stride, n;   // bytes of a row, from row to row; rows
     };
-    if (clash(ids, n_rows, accepted, n_seqs)) return moe_fail_status(MOE_EINVAL, "ids and accepted must not overlap");
-    const struct { const void *p; long long n; } in[] = {{drafts, n_rows}, {u, n_rows}, {starts, n_seqs + 1}, {draws, n_seqs}, {temperature, n_seqs},
-                                                         {top_k, n_seqs}, {top_p, n_seqs}, {min_p, n_seqs}};
-    for (const auto &x : in)
-        if (clash(x.p, x.n, ids, n_rows) || clash(x.p, x.n, accepted, n_seqs))
-            return moe_fail_status(MOE_EINVAL, "ids and accepted must not overlap an input");
+    auto clash = [](const Array &x, const Array &y) {   // y: one row
+        if (!x.p || !y.p || x.n <= 0 || y.n <= 0 || !y.row) return false;
+        const uintptr_t xa = (uintptr_t)x.p, ya = (uintptr_t)y.p;
+        if (ya + y.row <= xa || xa + (x.n - 1) * x.stride + x.row <= ya) return false;
+        const long long at = ya < xa ? 0 : (long long)((ya - xa) % x.stride);   // in a row, or behind its end
+        return at < x.row || at + y.row > x.stride;
+    };
+    auto flat = [](const void *p, long long n) { return Array{p, 4 * n, 4 * n, n > 0}; };
+    const long long size = is_bf16 ? 2 : 4;
+    const Array out[] = {flat(ids, n_rows), flat(accepted, n_seqs), {workspace, (long long)moe_verify_workspace_bytes(n_rows), 1, n_rows > 0}};
+    const Array in[] = {flat(drafts, n_rows), flat(u, n_rows), flat(starts, n_seqs + 1), flat(draws, n_seqs), flat(temperature, n_seqs),
+                        flat(top_k, n_seqs), flat(top_p, n_seqs), flat(min_p, n_seqs), {logits, vocab * size, row_stride * size, n_rows},
+                        {draft_probs, vocab * 4ll, probs_stride * 4, n_rows}};
+    for (int o = 0; o < 3; o++) {
+        for (int i = 0; i < o; i++)
+            if (clash(out[i], out[o])) return moe_fail_status(MOE_EINVAL, "ids, accepted and the workspace must not overlap");
+        for (const Array &x : in)
+            if (clash(x, out[o])) return moe_fail_status(MOE_EINVAL, "ids, accepted and the workspace must not overlap an input");
+    }
     VerifyArgs a{};
     a.s.x = logits, a.s.rows = n_rows, a.s.V = vocab, a.s.stride = row_stride;
     a.s.temperature = temperature, a.s.top_k = top_k, a.s.top_p = top_p, a.s.min_p = min_p;
