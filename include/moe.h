@@ -731,12 +731,13 @@ void moe_kv4_destroy(moe_kv4 *plan);
  * accepted[b] (int32 [n_seqs]) is the number of accepted tokens; ids (int32
  * [n_rows]) gets those, the drawn token (-1 where the row has none to choose)
  * and -1 behind it; rows of no sequence are left as they are.  Of a sequence of
- * one row the token is drawn as moe_sample would.  Weights are fp32, sums
- * within 2^-20 of their totals.  draft_probs is read at and beside tokens that
- * p keeps, never at a sequence's last row.  ids, accepted and the workspace
- * overlap nothing else (they may lie between rows that are apart).  The workspace
- * (device, 16-byte aligned) holds nothing between calls; calls that can overlap
- * on the GPU need one each. */
+ * one row the token is drawn as moe_sample would, to within what both say of
+ * their sums.  Weights are fp32, sums within 2^-20 of their totals.  draft_probs
+ * is read at the drafted tokens, and at and beside tokens that p keeps, never at
+ * a sequence's last row.  ids, accepted and the workspace overlap nothing else
+ * (they may lie between rows that are apart).  The workspace (device, 16-byte
+ * aligned) holds nothing between calls; calls that can overlap on the GPU need
+ * one each. */
 size_t moe_verify_workspace_bytes(int n_rows);
 int moe_verify(const void *logits, int is_bf16, int n_rows, int vocab, long long row_stride, const int32_t *drafts,
                const float *draft_probs, long long probs_stride, const int32_t *starts, int n_seqs, const float *temperature,

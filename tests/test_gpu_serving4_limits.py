@@ -146,6 +146,30 @@ def test_verify_residuals_of_next_to_nothing(n, step, dtype):
     assert np.all(np.abs(at + 0.5 - draws.astype(np.float64) * len(some)) <= 0.5 + slack)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_verify_of_single_rows_draws_what_sample_draws(dtype):
+    """Rows without drafts against the sampler at the same random numbers: the same token, but where the share lies within the
+    two sums' bounds (2^-19) of a border."""
+    import torch
+    rng = np.random.default_rng(9)
+    n, V = 300, 4001
+    x = torch.from_numpy(rng.normal(0, 2.5, (n, V)).astype(np.float32)).to(getattr(torch, dtype)).cuda()
+    t, k = rng.choice([0.0, 0.6, 1.0, 1.4], n).astype(np.float32), rng.choice([0, 1, 40, 900], n).astype(np.int32)
+    p, mp = rng.choice([1.0, 0.95, 0.5], n).astype(np.float32), rng.choice([0.0, 0.02], n).astype(np.float32)
+    u = rng.random(n).astype(np.float32)
+    z = lambda k: torch.zeros(k, dtype=torch.int32, device="cuda")   # noqa: E731
+    a, b, acc = z(n), z(n), z(n)
+    opt = dict(temperature=base.dev(t), top_k=base.dev(k), top_p=base.dev(p), min_p=base.dev(mp))
+    base.moe().sample(x, base.dev(u), a, **opt)
+    base.moe().Verify(n).run(x, z(n), base.dev(u), base.dev(u), base.dev(np.arange(n + 1, dtype=np.int32)), b, acc, **opt)
+    a, b, x = a.cpu().numpy(), b.cpu().numpy(), x.double().cpu().numpy()
+    assert not acc.any()
+    for i in np.flatnonzero(a != b):
+        c = np.cumsum(S4.probabilities(x[i], float(t[i]), int(k[i]), float(p[i]), float(mp[i])))
+        lo, hi = sorted((a[i], b[i]))
+        assert abs(float(u[i]) - c[lo]) <= 2.0 ** -19 and c[hi - 1] - c[lo] <= 2.0 ** -19, i
+
+
 # ---------------------------------------------------------------- angles
 
 def test_rotate_negative_frequencies_keep_their_angles():
