@@ -200,6 +200,16 @@ inline cudaError_t current_device_slot(int *dev) {
     return e;
 }
 
+// SMs of the current device.
+inline cudaError_t sm_count(int *n) {
+    static PerDevice<int> sms;
+    int dev = 0;
+    cudaError_t e = current_device_slot(&dev);
+    if (e == cudaSuccess && !sms.v[dev]) e = cudaDeviceGetAttribute(&sms.v[dev], cudaDevAttrMultiProcessorCount, dev);
+    *n = sms.v[dev];
+    return e;
+}
+
 // Raise a kernel's dynamic shared memory limit to the device maximum, once per
 // device (host-side setup; kept out of the per-forward launch sequence).
 template <class F>

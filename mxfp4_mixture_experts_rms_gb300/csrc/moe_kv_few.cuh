@@ -79,13 +79,4 @@ struct Seg {
     int nt, b, h, rt;
 };
 
-inline cudaError_t sm_count(int *n) {
-    static PerDevice<int> sms;
-    int dev = 0;
-    cudaError_t e = current_device_slot(&dev);
-    if (e == cudaSuccess && !sms.v[dev]) e = cudaDeviceGetAttribute(&sms.v[dev], cudaDevAttrMultiProcessorCount, dev);
-    *n = sms.v[dev];
-    return e;
-}
-
 }  // namespace

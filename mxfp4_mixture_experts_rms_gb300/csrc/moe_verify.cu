@@ -287,8 +287,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_verify_kernel(const VerifyArg
 template <bool BF16>
 cudaError_t verify_launch(const VerifyArgs &a, cudaStream_t st) {
     const long long vecs = ((long long)a.s.V + (BF16 ? 7 : 3)) / (BF16 ? 8 : 4) + 1;
-    int C = kMaxCluster;
-    while (C > 1 && ((long long)a.s.n_seqs * C > 2 * 152 || vecs / C < 256)) C /= 2;
+    int sms = 0, C = kMaxCluster;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    while (C > 1 && ((long long)a.s.n_seqs * C > 2 * sms || vecs / C < 256)) C /= 2;   // (two CTAs an SM)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.s.n_seqs * C);
     cfg.blockDim = dim3(kThreads);
