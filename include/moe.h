@@ -611,8 +611,8 @@ void moe_kv8_destroy(moe_kv8 *plan);
  *   3. min_p (above 1: 1) keeps those with w >= min_p
  *   4. the token is the first, in order of index, at which the running sum of
  *      the kept weights exceeds u times their total
- * Weights are fp32 (one below 2^-126 is 0), sums of them within 2^-20 of the
- * row's total; however little a kept token weighs next to the others, it has its
+ * Weights are fp32 (one below 2^-126 is 0), sums of them within 2^-19 of the
+ * row's total (2^-15 for more than 2^17 tokens, where many are equal); however little a kept token weighs next to the others, it has its
  * share of u.
  * t <= 0 (or NaN) takes the first token in descending order.  temperature, top_k,
  * top_p, min_p: device arrays [n_rows], each may be NULL (1, all, 1, 0); a NaN
@@ -701,9 +701,12 @@ int moe_kv4_read(moe_kv4 *plan, const int32_t *slots, int n_tokens, uint16_t *k,
  * another row sees values of scales above 2^25, this holds for values of 2^-84
  * and more; smaller ones may lose bits); a token that it sees must have been
  * appended (one of zero bytes counts as zeros).  A seen key's scale of 2^100 or
- * more may count as a score beyond fp32's range, and many seen values of such
- * scales may add up to infinity.  Weights are held in 11 bits or more, for many
- * rows (the kernel for prompts) in 8, sums in 32. */
+ * more may count as a score beyond fp32's range, as may a query of a magnitude of
+ * 2^140 / softmax_scale, and many seen values of such scales may add up to
+ * infinity.  Weights are held in 11 bits for a few new tokens (one below 2^-21 of a
+ * row's largest in fewer, below 2^-31 perhaps as 0), in 8 for many rows (the kernel
+ * for prompts), sums in 32; which it is goes by the call's sizes, so a row's last
+ * bits can change with the batch that it is in. */
 int moe_kv4_attend(moe_kv4 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
                    const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
                    long long out_stride, void *stream);

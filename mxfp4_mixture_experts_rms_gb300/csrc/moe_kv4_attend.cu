@@ -17,12 +17,13 @@ namespace {
 // tokens), a contiguous share of them for each CTA and each of its warps; what a
 // share cuts apart is joined in a fixed order.
 //
-// A unit's pages are one bulk copy each, codes and scales together.  What bounds
-// long calls is not HBM but issue slots (55 % taken) and the integer pipe (50 %),
-// which turns codes into fp16 (two cycles a pair, by the hardware's conversion),
-// so everything else is arranged to spare them: 96 ragged sequences, 598 K tokens,
-// 20 / 4 heads of 128 take 89 us, 49 at HBM's rate.  Short ones are latencies: of
-// 16 x 4096 tokens, 64 / 8 heads of 64, the bytes are 5 us of 23.
+// A unit's pages are one bulk copy each, codes and scales together.  Long calls are
+// bound by no one pipe: issue slots, the integer pipe, which turns codes into fp16
+// (two cycles a pair, by the hardware's conversion), and HBM are about half busy
+// each, and 16 warps an SM wait for instructions of fixed latency and for loads
+// most.  So instructions are spared: 96 ragged sequences, 598 K tokens, 20 / 4 heads
+// of 128 take 89 us, 49 at HBM's rate.  Short ones are latencies: of 16 x 4096
+// tokens, 64 / 8 heads of 64, the bytes are 5 us of 23.5.
 //  * Both products have the cache's side as their 16-row operand, keys [tokens]
 //    [dims] and values [dims][tokens], and eight rows of queries or weights as
 //    the other, so that nothing is multiplied that is no row; a unit may have
@@ -46,7 +47,7 @@ namespace {
 // weight is at least 2^7, so values down to 2^-84 keep 24 bits of it; an exponent
 // of their own for each row's sums made decode steps 4 to 5 % slower).  Where the e of 32 tokens are all within
 // 4 of E, w 2^(e - E) is the fp16 operand: the row's largest is then at least 2^7
-// and the others keep 11 bits down to 2^-21 of it.
+// and the others keep 11 bits down to 2^-21 of it, some down to 2^-31.
 // Where they are not, or above E, tokens are multiplied in classes of e within 4 of one
 // another, each with its own reference, and added in fp32.
 // q is scaled per row by a power of two into fp16's range: exact for a bf16

@@ -11,8 +11,9 @@
 //    Both tiles are [token][D], the same conversion; V's is read turned.
 //  * Weights are bf16, 8 bits where a sum takes fp32 weights in the plain form:
 //    with fp16 ones values would need a reference for each block of 32 dims.
-//    Results are 2.0e-3 from those in 64 bits (relative, over an output), 1.6e-3
-//    of it their own rounding to bf16; the sum of the weights is fp32's.
+//    Results are 2.0e-3 to 2.2e-3 from those in 64 bits (relative, over an
+//    output), 1.6e-3 of it their own rounding to bf16; the sum of the weights is
+//    fp32's.
 //  * One softmax reference m, moved (to 16 above the largest score) only when a
 //    score passes it, so that weights are at most 1 and the accumulator in tensor
 //    memory is rarely rescaled (at 8 above, a tenth of a step's time was that).

@@ -33,6 +33,7 @@ namespace {
 // output), as is a form in fp32 that is rounded to bf16 at its end.
 // q is scaled per row by a power of two into fp16's range: exact for a bf16
 // row's values down to 2^-28 of its largest.
+constexpr int kRows = 16;   // rows of a unit
 
 // Measured: 16 x 4096 tokens of 8 heads of 64 (67 MB) 23.8 us: lengths and
 // table 1.4, the first pages 2.8, units 8.0 (HBM's rate), joins 4.7, the launch
@@ -67,6 +68,15 @@ struct FewArgs {
     float *parts;              // [kMaxCtas][2][partial_floats]
     int *seqs;                 // [3][n_seqs], or null: in shared memory
 };
+
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
 
 // What turns a row's accumulator into its output (sink: the head's logit in
 // units of log2, -inf without one): two factors, as their product may be below

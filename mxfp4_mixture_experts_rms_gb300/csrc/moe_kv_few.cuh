@@ -7,7 +7,6 @@
 namespace {
 
 constexpr int kTile = 64;             // tokens of a unit
-constexpr int kRows = 16;             // rows of a unit
 constexpr int kMaxCtas = 160;         // the tickets and partials there are room for
 constexpr int kSmemSeqs = 512;       // sequences whose lengths are held in shared memory
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -58,14 +57,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
 struct Job {

@@ -18,9 +18,10 @@
 // is the only exchange.  As many groups as the heads need; a head's places move on
 // by a stride from token to token, and the next token is loaded before this one
 // is computed.  fp32 by twos.  15 001 tokens of 32 heads of 128 take 55 us, 37 at
-// HBM's rate, 44 without norms and rotation: a warp's instructions are the next
-// bound (with eight dims a lane and heads' places found anew for each, 71; tokens
-// by asynchronous copies through shared memory, 72).
+// HBM's rate, 44 without norms and rotation: HBM and issue slots are 45 % busy
+// each, a CTA's waits before its first row (angles, barriers) are the rest.  (With
+// eight dims a lane and heads' places found anew for each, 71; tokens by
+// asynchronous copies through shared memory, 72.)
 #include "moe_common.cuh"
 #include "../../include/moe.h"
 

@@ -136,9 +136,10 @@ def attend(cache, P, q, starts, lens, table, window=0, sinks=None, scale=None, w
     2^(s - m + e_t - E), E at most 4 above e_t, m at most 11 below the largest score when it was set and never more than
     15 below one since, so 2^7 at least for the token of the largest score; below 2^-14 they are off by up to half of fp16's smallest step, 2^-25: 2^-32 of the largest,
     doubled for parts with references of their own.
-    The last term, for weights of next to nothing on tokens of the largest scales (a weight 2^-31 of the row's largest may
-    count as none): 2^-120, where scales are within 2^120 of one another less than the floor.  0 where all of a row's
-    weights are of one size."""
+    F counts on a weight of 2^-21 of the largest or more for the token that counts most in a dim: one of 2^-31 may be taken
+    as 0, and a result that such tokens alone make up (the others' codes being 0) is none.
+    The last term, for such weights on tokens of the largest scales: 2^-120, where scales are within 2^120 of one another
+    less than the floor.  0 where all of a row's weights are of one size."""
     D, H = q.shape[2], q.shape[1]
     kv, n_pages = cache.shape[1], cache.shape[0]
     codes, scales = unpack(cache, P, D)
