@@ -696,17 +696,17 @@ int moe_kv4_append(moe_kv4 *plan, const uint16_t *k, const uint16_t *v, long lon
 int moe_kv4_read(moe_kv4 *plan, const int32_t *slots, int n_tokens, uint16_t *k, uint16_t *v, long long k_stride,
                  long long v_stride, void *stream);
 /* Attention of new tokens over the cache: all of moe_kv8_attend's arguments,
- * rules and limits.  What a row does not see does not touch its result,
- * whatever codes and scale bytes lie there (in a call of a few new tokens, where
- * another row sees values of scales above 2^25, this holds for values of 2^-84
- * and more; smaller ones may lose bits); a token that it sees must have been
- * appended (one of zero bytes counts as zeros).  A seen key's scale of 2^100 or
- * more may count as a score beyond fp32's range, as may a query of a magnitude of
- * 2^140 / softmax_scale, and many seen values of such scales may add up to
- * infinity.  Weights are held in 11 bits for a few new tokens (one below 2^-21 of a
- * row's largest in fewer, below 2^-31 perhaps as 0), in 8 for many rows (the kernel
- * for prompts), sums in 32; which it is goes by the call's sizes, so a row's last
- * bits can change with the batch that it is in. */
+ * rules and limits.  What a row does not see does not touch its result, whatever
+ * codes and scale bytes lie there (for a few new tokens this holds for values of
+ * 2^-84 and more: smaller ones may lose bits where the call's rows meet scales
+ * above 2^25); a token that it sees must have been appended (one of zero bytes
+ * counts as zeros).  A seen key's scale of 2^100 or more may count as a score
+ * beyond fp32's range, as may a query of a magnitude of 2^140 / softmax_scale, and
+ * many seen values of such scales may add up to infinity.  Weights are held in 11
+ * bits for a few new tokens (one below 2^-21 of a row's largest in fewer, below
+ * 2^-31 perhaps as 0), in 8 for many rows (the kernel for prompts), sums in 32;
+ * which it is goes by the call's sizes, so a row's last bits can change with the
+ * batch that it is in. */
 int moe_kv4_attend(moe_kv4 *plan, const uint16_t *q, long long q_stride, const int32_t *starts, const int32_t *lens,
                    const int32_t *table, int table_width, int n_seqs, int max_new, int n_rows, uint16_t *out,
                    long long out_stride, void *stream);
